@@ -168,6 +168,58 @@ swa_status swa_append_verify_attn(const void *q, const void *k_new, const void *
                                   float scale, void *out, float *lse, const swa_dims *dims,
                                   swa_stream_t stream);
 
+/* Norms of the query and key heads and the position rotation, the step
+ * between a layer's fused projection and its attention, in one pass over the
+ * block's rows.  The pages name no such kernel; it produces what
+ * swa_verify_attn and swa_append_verify_attn take.
+ *
+ * Per token at position p = q_pos[b] + i, for every head row x of q and k:
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ *   (y_a, y_b) <- (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
+ *       t = p * inv_freq[n], n < rot_dim / 2, over the pairs
+ *       (a, b) = (n, n + rot_dim / 2), or (2n, 2n + 1) if interleaved;
+ *       dims from rot_dim on are not rotated (rot_dim 0: none are)
+ * in fp32 (the angle modulo a turn exactly, at any position), rounded to bf16
+ * once.  Value rows are copied bit by bit. */
+typedef struct {
+    int64_t q_row, k_row, v_row; /* elements from one token's rows to the next in q, k and v
+                                    (at least heads * D, a multiple of 8): views of one fused
+                                    projection are taken as they are                        */
+    const float *q_weight;       /* fp32 [D] device, 16-byte aligned, or NULL: no norm of q */
+    const float *k_weight;       /* the same for k                                          */
+    const float *inv_freq;       /* fp32 [rot_dim / 2] device; may be NULL when rot_dim is 0 */
+    float eps;                   /* > 0 and finite where a weight is given                  */
+    int32_t rot_dim;             /* 0 or a multiple of 16 up to D                           */
+    int32_t interleaved;         /* 0: pairs (n, n + rot_dim / 2); 1: pairs (2n, 2n + 1)    */
+} swa_rope;
+
+/*   q        bf16, token t = b * q_len + i at q + t * q_row: [Hq, D], 16-byte aligned
+ *   k, v     bf16, the same with Hkv heads
+ *   q_pos    int32 [B] device
+ *   q_out    bf16 [B, q_len, Hq, D]   device, 16-byte aligned, written
+ *   k_out, v_out  bf16 [B, q_len, Hkv, D], written: k_new / v_new of
+ *            swa_append_verify_attn
+ *   dims     batch, q_len, num_q_heads, num_kv_heads and head_dim (limits as for
+ *            swa_verify_attn, but any number of rows per KV head); the rest is not read
+ * The outputs must not overlap the inputs.  Asynchronous on `stream`, no
+ * workspace, no state: calls on several streams may overlap.  Errors as for
+ * swa_verify_attn, before any CUDA call. */
+swa_status swa_qk_norm_rope(const void *q, const void *k, const void *v, const swa_rope *rope,
+                            const int32_t *q_pos, void *q_out, void *k_out, void *v_out,
+                            const swa_dims *dims, swa_stream_t stream);
+
+/* The same with the key and value rows written into the cache, contiguous
+ * [B, Hkv, max_len, D] (paged == NULL) or paged (see swa_verify_attn_paged),
+ * at positions q_pos[b] + i < min(seq_lens[b], max_len); rows at other
+ * positions are dropped and no other cache byte changes.  swa_verify_attn on
+ * the result sees the block's own rows.  dims->max_len is the cache's, and the
+ * device preconditions are those of swa_append_verify_attn. */
+swa_status swa_qk_norm_rope_append(const void *q, const void *k, const void *v,
+                                   const swa_rope *rope, void *k_cache, void *v_cache,
+                                   const swa_paged *paged, const int32_t *seq_lens,
+                                   const int32_t *q_pos, void *q_out, const swa_dims *dims,
+                                   swa_stream_t stream);
+
 /* Upper bound, in bytes, of the split-partial workspace any call with these
  * dims and window may need on any device (pure host arithmetic; 0 if the
  * arguments are invalid).  Layout: fp32 acc [B, Hkv, splits, R, D] followed

@@ -38,6 +38,14 @@ class SwaPlanInfo(ctypes.Structure):
                 ("merge", ctypes.c_int32), ("workspace_bytes", ctypes.c_int64)]
 
 
+class SwaRope(ctypes.Structure):
+    """swa_rope of include/swa.h."""
+    _fields_ = [("q_row", ctypes.c_int64), ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 class SwaDebugOptions(ctypes.Structure):
     """swa_debug_options of include/swa.h (test and sweep controls)."""
     _fields_ = [("force_kernel", ctypes.c_int32), ("pdl", ctypes.c_int32),
@@ -99,6 +107,13 @@ def load_library(path=LIB_PATH):
     lib.swa_append_verify_attn.restype = ctypes.c_int
     lib.swa_greedy_accept.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp]
     lib.swa_greedy_accept.restype = ctypes.c_int
+    lib.swa_qk_norm_rope.argtypes = [vp, vp, vp, ctypes.POINTER(SwaRope), vp, vp, vp, vp,
+                                     ctypes.POINTER(SwaDims), vp]
+    lib.swa_qk_norm_rope.restype = ctypes.c_int
+    lib.swa_qk_norm_rope_append.argtypes = [vp, vp, vp, ctypes.POINTER(SwaRope), vp, vp,
+                                            ctypes.POINTER(SwaPaged), vp, vp, vp,
+                                            ctypes.POINTER(SwaDims), vp]
+    lib.swa_qk_norm_rope_append.restype = ctypes.c_int
     lib.swa_set_debug_options.argtypes = [ctypes.POINTER(SwaDebugOptions)]
     lib.swa_set_debug_options.restype = ctypes.c_int
     lib.swa_get_debug_options.argtypes = [ctypes.POINTER(SwaDebugOptions)]
@@ -170,6 +185,157 @@ def swa_verify_attn_paged(q, k_pages, v_pages, block_table, seq_lens, q_pos, win
 def _issue(entry, args, keep, result):
     _check(getattr(load_library(), entry)(*args))
     return result
+
+
+def _issue_on(device, entry, args, keep, result):
+    """_issue with the tensors' device current: the C entry points launch on
+    the current device."""
+    with torch.cuda.device(device):
+        return _issue(entry, args, keep, result)
+
+
+def _one_device(**tensors):
+    """The device all given tensors (None: absent) share."""
+    given = {n: t for n, t in tensors.items() if t is not None}
+    first = next(iter(given))
+    for n, t in given.items():
+        if t.device != given[first].device:
+            raise ValueError(f"{n} is on {t.device}, {first} on {given[first].device}")
+    return given[first].device
+
+
+def _head_rows(t, name, shape):
+    """Pointer and token stride of a bf16 [B, q_len, H, D] tensor whose
+    tokens' [H, D] blocks are contiguous and evenly spaced (a contiguous
+    tensor, or a view of a fused projection's output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device (got {t.device})")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
+    B, q_len, H, D = t.shape
+    sb, sq, sh, sd = t.stride()
+    row = sq if q_len > 1 else sb if B > 1 else H * D
+    if sd != 1 or (H > 1 and sh != D) or (B > 1 and sb != q_len * row):
+        raise ValueError(f"{name}: a token's heads must be contiguous and its tokens evenly spaced "
+                         f"(strides {tuple(t.stride())})")
+    return t.data_ptr(), row
+
+
+def _marshal_rope(q, k, v, q_weight, k_weight, eps, inv_freq, q_pos, interleaved, cache,
+                  outs, stream):
+    """swa_qk_norm_rope (cache None, outs (q_out, k_out, v_out)) or
+    swa_qk_norm_rope_append (cache (k_cache, v_cache, seq_lens, block_table),
+    outs (q_out,))."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be [B, q_len, heads, D]")
+    B, q_len, Hq, D = q.shape
+    Hkv = k.shape[2]
+    pq, rq = _head_rows(q, "q", (B, q_len, Hq, D))
+    pk, rk = _head_rows(k, "k", (B, q_len, Hkv, D))
+    pv, rv = _head_rows(v, "v", (B, q_len, Hkv, D))
+    weights = []
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        weights.append(None if t is None else _dev_tensor(t, name, torch.float32, 1))
+        if t is not None and t.numel() != D:
+            raise ValueError(f"{name} must be [D] = [{D}]")
+    pf = None if inv_freq is None else _dev_tensor(inv_freq, "inv_freq", torch.float32, 1)
+    pp = _dev_tensor(q_pos, "q_pos", torch.int32, 1)
+    if q_pos.numel() != B:
+        raise ValueError("q_pos needs one entry per sequence")
+    rope = SwaRope(rq, rk, rv, weights[0], weights[1], pf, float(eps),
+                   0 if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)))
+    dev = _one_device(q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq,
+                      q_pos=q_pos)
+    shapes = ((B, q_len, Hq, D), (B, q_len, Hkv, D), (B, q_len, Hkv, D))
+    outs = [torch.empty(s, dtype=torch.bfloat16, device=dev) if t is None else t
+            for t, s in zip(outs, shapes)]
+    po = []
+    for t, s, name in zip(outs, shapes, ("q_out", "k_out", "v_out")):
+        po.append(_dev_tensor(t, name, torch.bfloat16, 4))
+        if tuple(t.shape) != s:
+            raise ValueError(f"{name} must be {s} (got {tuple(t.shape)})")
+        _one_device(q=q, **{name: t})
+    handle = _stream_handle(stream, dev)
+    keep = (q, k, v, q_weight, k_weight, inv_freq, q_pos, cache, outs, rope)
+    if cache is None:
+        dims = make_dims(B, q_len, Hq, Hkv, D, 0)
+        args = (pq, pk, pv, ctypes.byref(rope), pp, *po, ctypes.byref(dims), handle)
+        return "swa_qk_norm_rope", args, keep + (dims,), tuple(outs)
+    k_cache, v_cache, seq_lens, block_table = cache
+    pkc = _dev_tensor(k_cache, "k_cache", torch.bfloat16, 4)
+    pvc = _dev_tensor(v_cache, "v_cache", torch.bfloat16, 4)
+    if v_cache.shape != k_cache.shape or k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
+        raise ValueError("k_cache / v_cache shapes do not match each other or k")
+    ps = _dev_tensor(seq_lens, "seq_lens", torch.int32, 1)
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens needs one entry per sequence")
+    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, seq_lens=seq_lens, block_table=block_table)
+    paged, max_len = _paged_of(k_cache, block_table, B)
+    dims = make_dims(B, q_len, Hq, Hkv, D, max_len)
+    args = (pq, pk, pv, ctypes.byref(rope), pkc, pvc,
+            ctypes.byref(paged) if paged is not None else None, ps, pp, po[0],
+            ctypes.byref(dims), handle)
+    return "swa_qk_norm_rope_append", args, keep + (paged, dims), outs[0]
+
+
+def _paged_of(k_cache, block_table, B):
+    """(SwaPaged, logical length) of a page pool, or (None, cache length)."""
+    if block_table is None:
+        if k_cache.shape[0] != B:
+            raise ValueError("the caches need one slab per sequence")
+        return None, k_cache.shape[2]
+    pt = _dev_tensor(block_table, "block_table", torch.int32, 2)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table needs one row per sequence")
+    paged = SwaPaged(pt, block_table.shape[1], k_cache.shape[2], k_cache.shape[0])
+    return paged, block_table.shape[1] * k_cache.shape[2]
+
+
+def _marshal_rope_rows(q, k, v, q_weight, k_weight, eps, inv_freq, q_pos, interleaved=False,
+                       q_out=None, k_out=None, v_out=None, stream=None):
+    return _marshal_rope(q, k, v, q_weight, k_weight, eps, inv_freq, q_pos, interleaved, None,
+                         (q_out, k_out, v_out), stream)
+
+
+def swa_qk_norm_rope(q, k, v, q_weight, k_weight, eps, inv_freq, q_pos, interleaved=False,
+                     q_out=None, k_out=None, v_out=None, stream=None):
+    """RMS norm of the query and key heads and the position rotation through
+    the C entry point swa_qk_norm_rope.
+
+    q bf16 [B, q_len, Hq, D], k and v bf16 [B, q_len, Hkv, D], contiguous or
+    views of one fused projection [B, q_len, Hq + 2 Hkv, D]; weights fp32 [D]
+    or None (that norm is left out); inv_freq fp32 [rot_dim / 2] or None (no
+    rotation); q_pos int32 [B].  Returns (q_out, k_out, v_out), contiguous:
+    q, k_new and v_new of swa_append_verify_attn.  Enqueued on `stream`
+    (default: torch's current stream); does not synchronise.
+    """
+    return _issue_on(q.device, *_marshal_rope_rows(q, k, v, q_weight, k_weight, eps, inv_freq,
+                                                   q_pos, interleaved, q_out, k_out, v_out,
+                                                   stream))
+
+
+def _marshal_rope_append(q, k, v, q_weight, k_weight, eps, inv_freq, k_cache, v_cache, seq_lens,
+                         q_pos, interleaved=False, block_table=None, q_out=None, stream=None):
+    return _marshal_rope(q, k, v, q_weight, k_weight, eps, inv_freq, q_pos, interleaved,
+                         (k_cache, v_cache, seq_lens, block_table), (q_out,), stream)
+
+
+def swa_qk_norm_rope_append(q, k, v, q_weight, k_weight, eps, inv_freq, k_cache, v_cache,
+                            seq_lens, q_pos, interleaved=False, block_table=None, q_out=None,
+                            stream=None):
+    """swa_qk_norm_rope with the key and value rows written into the cache
+    (C entry point swa_qk_norm_rope_append): [B, Hkv, max_len, D], or page
+    pools [num_pages, Hkv, page_size, D] with block_table int32
+    [B, max_blocks].  Returns q_out; the caches are modified in place, and
+    swa_verify_attn / swa_verify_attn_paged on them sees the block's rows.
+    """
+    return _issue_on(q.device, *_marshal_rope_append(q, k, v, q_weight, k_weight, eps, inv_freq,
+                                                     k_cache, v_cache, seq_lens, q_pos,
+                                                     interleaved, block_table, q_out, stream))
 
 
 def _marshal_append(q, k_new, v_new, k_cache, v_cache, seq_lens, q_pos, window, scale,
@@ -341,13 +507,17 @@ class PreparedCall:
 
 
 _MARSHAL = {"swa_verify_attn": _marshal_verify, "swa_verify_attn_noalloc": _marshal_noalloc,
-            "swa_verify_attn_paged": _marshal_paged, "swa_append_verify_attn": _marshal_append}
+            "swa_verify_attn_paged": _marshal_paged, "swa_append_verify_attn": _marshal_append,
+           "swa_qk_norm_rope": _marshal_rope_rows,
+           "swa_qk_norm_rope_append": _marshal_rope_append}
 
 
 def prepare(fn, *args, **kwargs):
     """Validate and marshal a call of swa_verify_attn, swa_verify_attn_noalloc,
-    swa_verify_attn_paged or swa_append_verify_attn once, with the same
-    arguments the function takes, and return a PreparedCall that issues it.
+    swa_verify_attn_paged, swa_append_verify_attn, swa_qk_norm_rope or
+    swa_qk_norm_rope_append once, with the same arguments the function takes,
+    and return a PreparedCall that issues it (on the device that is current
+    then: the tensors').
 
     The per-call host cost is then one C call: no tensor checks, no struct
     building, no stream lookup (the stream is the one given, or torch's

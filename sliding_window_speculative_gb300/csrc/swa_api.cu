@@ -12,6 +12,7 @@
 #include "../../include/swa.h"
 #include "swa_simt.cuh"
 #include "swa_accept.cuh"
+#include "swa_host.h"
 #include "swa_tc_host.h"
 
 // Fault word of each device that loads the library; kernels receive its
@@ -26,9 +27,9 @@ constexpr int kMaxSplits = 64;
 constexpr int kTcKeysPerTile = 128;  // keys per tensor-core tile (MMA M)
 static_assert(kMaxSplits <= swa::kMergeMaxSplits, "the merge kernel weighs at most 64 splits");
 constexpr int kMaxQLen = 64;      // SPLITKV_VERIFY_MAX_Q: draft rows of a greedy verification
-constexpr int kMaxBlockLen = 512; // MAX_NUM_BATCHED_TOKENS: rows of an attention call
-                                  // (verify blocks up to 64, prefill chunks up to 512)
-constexpr int kMaxDevices = 64;
+// rows of an attention call: verify blocks up to 64, prefill chunks up to 512
+using swa::kMaxBlockLen;
+using swa::kMaxDevices;
 
 thread_local char t_last_error[512] = "";
 
@@ -819,6 +820,38 @@ swa_status swa_get_debug_options(swa_debug_options *opt) {
 }
 
 }  // extern "C"
+
+// ------------------------------------------- shared with the other units
+
+swa_status swa::api_fail(swa_status st, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(t_last_error, sizeof t_last_error, fmt, ap);
+    va_end(ap);
+    return st;
+}
+
+swa_status swa::api_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+
+swa_status swa::api_ok() {
+    t_last_error[0] = '\0';
+    return SWA_OK;
+}
+
+swa_status swa::api_device(int *dev, uint32_t **fault) {
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (*dev >= kMaxDevices) return fail(SWA_ERR_UNSUPPORTED, "device ordinal %d too large", *dev);
+    *fault = fault_word_ptr(*dev);
+    if (*fault == nullptr) return fail(SWA_ERR_CUDA, "cannot resolve the device fault word");
+    return SWA_OK;
+}
+
+int swa::api_device_sms(int dev) { return device_sms(dev); }
+
+swa_status swa::api_check_paged(const swa_paged *paged, const swa_dims *dims) {
+    return check_paged(paged, dims);
+}
 
 bool swa::pdl_enabled() { return g_opt_pdl.load(std::memory_order_relaxed) != 0; }
 
