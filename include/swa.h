@@ -352,6 +352,61 @@ swa_status swa_greedy_accept(const void *logits, const int32_t *keep_ids, const 
                              int32_t *argmax_out, int32_t *accepted, int32_t batch,
                              int32_t q_len, int32_t vocab, swa_stream_t stream);
 
+/* Sampled verification of a draft block: per verify row one token drawn from
+ * its logits with a random number that the caller gives, and the number of
+ * drafted tokens accepted; what swa_greedy_accept does for requests that ask for
+ * sampling.  The pages decode greedily only.
+ *
+ * Per row, with T, k, p, m the settings of its sequence, x_j the logits and M
+ * the largest of them:
+ *   candidates    the columns with x_j > -inf (a NaN is none), ordered by
+ *                 falling x_j, equal ones by rising column
+ *   weight        w_j = exp((x_j - M) / T); M = +inf: 1 where x_j = M, else 0
+ *   top-k         the first k candidates (k <= 0: all)
+ *   top-p         of these the shortest prefix whose weights reach p times
+ *                 the weights of all of these (p >= 1 or NaN: all of them;
+ *                 p <= 0: the first)
+ *   min-p         of these the candidates with w_j >= m (m <= 0 or NaN: all;
+ *                 m > 1 counts as 1), never fewer than the first
+ *   token         with S the weights left, the first column at which the
+ *                 running weight passes u * S, u its random number (below 0
+ *                 or NaN counts as 0, 1 and above as the largest float below
+ *                 1); logprob = ln(w / S)
+ *   T <= 0 or NaN is greedy: the first candidate, logprob 0.  A row without
+ *   candidates gives column 0, logprob 0.
+ * Weights are computed to 2^-44 relative and summed exactly, so results do not
+ * depend on the launch; columns more than 50 T below M are left out (together
+ * under 2^-41 of S up to 2^31 columns), and logits smaller in magnitude than
+ * 2^-32 times the row's largest of their sign (at most |M - 50 T|) weigh like
+ * 0, within 2^-26 of their weight. */
+typedef struct {
+    const float *temperature; /* fp32 [batch] device                           */
+    const int32_t *top_k;     /* int32 [batch] device or NULL: no top-k        */
+    const float *top_p;       /* fp32 [batch] device or NULL: no top-p         */
+    const float *min_p;       /* fp32 [batch] device or NULL: no min-p         */
+} swa_sampling;
+
+/*   logits     bf16 [batch, q_len, vocab]  device, 2-byte aligned, as for
+ *              swa_greedy_accept
+ *   keep_ids   int32 [vocab]  device or NULL: column j is token keep_ids[j]
+ *   draft      int32 [batch, q_len - 1]  device (may be NULL when q_len == 1)
+ *   uniforms   fp32 [batch, q_len]  device: the random numbers, one per row
+ *   tokens     int32 [batch, q_len]  device, written
+ *   logprobs   fp32 [batch, q_len]  device or NULL, written
+ *   accepted   int32 [batch]  device, written: the largest n <= q_len - 1 with
+ *              tokens[b][i] == draft[b][i] for every i < n; the step emits
+ *              draft[b][0 .. n) and then tokens[b][n].  For drafted tokens that
+ *              were fixed before the uniforms were drawn, that follows the
+ *              target's filtered distribution exactly.
+ *   batch 1..65535, q_len 1..64, vocab >= 1.
+ * Asynchronous on `stream`; no workspace and no state, so calls on several
+ * streams may overlap and be captured.  SWA_ERR_INVALID_ARG on bad arguments
+ * before any CUDA call. */
+swa_status swa_sample_accept(const void *logits, const int32_t *keep_ids, const int32_t *draft,
+                             const float *uniforms, const swa_sampling *sampling, int32_t *tokens,
+                             float *logprobs, int32_t *accepted, int32_t batch, int32_t q_len,
+                             int32_t vocab, swa_stream_t stream);
+
 /* Bytes of the fixed device scratch used by swa_verify_attn_noalloc. */
 #define SWA_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)
 

@@ -32,3 +32,55 @@ def norm_rope(x, weight, eps, inv_freq, pos, interleaved=False):
     out[..., ia], out[..., ib] = a * c - b * s, b * c + a * s
     size[..., ia] = size[..., ib] = np.abs(a) + np.abs(b)
     return out, size
+
+
+def sample_order(x):
+    """Candidate columns of one row of logits: by falling value, then rising
+    column; neither NaN nor -inf."""
+    x = np.asarray(x, np.float64)
+    cols = np.flatnonzero(x > -np.inf)
+    return cols[np.lexsort((cols, -x[cols]))]
+
+
+def sample_weights(x, order, T):
+    """Weights of the ordered candidates."""
+    v = np.asarray(x, np.float64)[order]
+    if np.isinf(v[0]):
+        return (v == v[0]).astype(np.float64)
+    with np.errstate(over="ignore", invalid="ignore"):
+        return np.exp((v - v[0]) / T)
+
+
+def sample_row(x, u, T, top_k=0, top_p=1.0, min_p=0.0):
+    """(column, logprob) of one row: the definition, on sorted columns."""
+    order = sample_order(x)
+    if order.size == 0:
+        return 0, 0.0
+    if not T > 0:
+        return int(order[0]), 0.0
+    w = sample_weights(x, order, T)
+    n = order.size
+    if top_k > 0:
+        n = min(n, int(top_k))
+    if top_p < 1:
+        need = top_p * w[:n].sum()
+        before = np.concatenate([[0.0], np.cumsum(w[:n])[:-1]])
+        n_p = int(np.count_nonzero(before < need))
+    else:
+        n_p = n
+    n = max(1, min(n, n_p, int(np.count_nonzero(w >= min(min_p, 1.0))) if min_p > 0 else n))
+    cum = np.cumsum(w[:n])
+    u = 0.0 if not u > 0 else min(float(u), 1 - 2.0 ** -24)
+    m = min(int(np.count_nonzero(cum <= u * cum[-1])), n - 1)
+    return int(order[m]), float(np.log(w[m] / cum[-1]))
+
+
+def accepted_prefix(tokens, draft):
+    """Per sequence the drafted tokens that equal the sampled ones in front."""
+    out = []
+    for t, d in zip(np.asarray(tokens), np.asarray(draft)):
+        n = 0
+        while n < len(d) and t[n] == d[n]:
+            n += 1
+        out.append(n)
+    return np.array(out)

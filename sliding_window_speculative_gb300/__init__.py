@@ -7,11 +7,12 @@ build raises: there is no CPU path.
 """
 from ._binding import (SWA_ERR_CUDA, SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED,  # noqa: F401
                        SWA_ERR_WORKSPACE, SWA_OK, PreparedCall, SwaDebugOptions, SwaDims,
-                       SwaError, SwaPaged, SwaRope, dims_of, load_library, make_dims, swa_append_verify_attn,
+                       SwaError, SwaPaged, SwaRope, SwaSampling, dims_of, load_library,
+                       make_dims, swa_append_verify_attn,
                        swa_get_debug_options, swa_greedy_accept, swa_last_error, swa_plan,
                        swa_qk_norm_rope, swa_qk_norm_rope_append,
                        swa_read_debug_checks, swa_read_device_errors, swa_release_workspace,
-                       swa_set_debug_options,
+                       swa_sample_accept, swa_set_debug_options,
                        swa_set_workspace, swa_verify_attn, swa_verify_attn_noalloc,
                        swa_verify_attn_paged, swa_version, swa_workspace_bytes, prepare)
 
@@ -23,11 +24,13 @@ __all__ = [
     "swa_read_debug_checks", "swa_version",
     # the step before: head norms and the position rotation
     "swa_qk_norm_rope", "swa_qk_norm_rope_append",
+    # drafts verified by sampling
+    "swa_sample_accept",
     # a call validated once and re-issued (serving loops)
     "prepare", "PreparedCall",
     # test and sweep controls
     "swa_set_debug_options", "swa_get_debug_options",
     # structs and helpers
-    "SwaDims", "SwaPaged", "SwaRope", "SwaDebugOptions", "SwaError", "make_dims", "dims_of",
+    "SwaDims", "SwaPaged", "SwaRope", "SwaSampling", "SwaDebugOptions", "SwaError", "make_dims", "dims_of",
     "load_library",
 ]

@@ -46,6 +46,12 @@ class SwaRope(ctypes.Structure):
                 ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class SwaSampling(ctypes.Structure):
+    """swa_sampling of include/swa.h."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
+
+
 class SwaDebugOptions(ctypes.Structure):
     """swa_debug_options of include/swa.h (test and sweep controls)."""
     _fields_ = [("force_kernel", ctypes.c_int32), ("pdl", ctypes.c_int32),
@@ -114,6 +120,9 @@ def load_library(path=LIB_PATH):
                                             ctypes.POINTER(SwaPaged), vp, vp, vp,
                                             ctypes.POINTER(SwaDims), vp]
     lib.swa_qk_norm_rope_append.restype = ctypes.c_int
+    lib.swa_sample_accept.argtypes = [vp, vp, vp, vp, ctypes.POINTER(SwaSampling), vp, vp, vp,
+                                      i32, i32, i32, vp]
+    lib.swa_sample_accept.restype = ctypes.c_int
     lib.swa_set_debug_options.argtypes = [ctypes.POINTER(SwaDebugOptions)]
     lib.swa_set_debug_options.restype = ctypes.c_int
     lib.swa_get_debug_options.argtypes = [ctypes.POINTER(SwaDebugOptions)]
@@ -483,14 +492,71 @@ def swa_verify_attn_noalloc(q, k_cache, v_cache, seq_lens, q_pos, window, scale,
                                     lse, num_splits, stream))
 
 
+def _marshal_sample(logits, uniforms, temperature, top_k=None, top_p=None, min_p=None, draft=None,
+                    keep_ids=None, tokens=None, logprobs=None, accepted=None, stream=None,
+                    want_logprobs=True):
+    pl = _dev_tensor(logits, "logits", torch.bfloat16, 3)
+    B, q_len, V = logits.shape
+    dev = _one_device(logits=logits, uniforms=uniforms, temperature=temperature, top_k=top_k,
+                      top_p=top_p, min_p=min_p, draft=draft, keep_ids=keep_ids, tokens=tokens,
+                      logprobs=logprobs, accepted=accepted)
+
+    def ptr(t, name, dtype, *shape):
+        if t is None:
+            return None
+        p = _dev_tensor(t, name, dtype, len(shape))
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)} (got {tuple(t.shape)})")
+        return p
+
+    f32, i32 = torch.float32, torch.int32
+    if q_len > 1 and draft is None:
+        raise ValueError("draft must be [B, q_len - 1]")
+    if tokens is None:
+        tokens = torch.empty((B, q_len), dtype=i32, device=dev)
+    if accepted is None:
+        accepted = torch.empty((B,), dtype=i32, device=dev)
+    if logprobs is None and want_logprobs:
+        logprobs = torch.empty((B, q_len), dtype=f32, device=dev)
+    if temperature is None:
+        raise ValueError("temperature must be [B]")
+    settings = SwaSampling(ptr(temperature, "temperature", f32, B), ptr(top_k, "top_k", i32, B),
+                           ptr(top_p, "top_p", f32, B), ptr(min_p, "min_p", f32, B))
+    args = (pl, ptr(keep_ids, "keep_ids", i32, V), ptr(draft, "draft", i32, B, q_len - 1),
+            ptr(uniforms, "uniforms", f32, B, q_len), ctypes.byref(settings),
+            ptr(tokens, "tokens", i32, B, q_len), ptr(logprobs, "logprobs", f32, B, q_len),
+            ptr(accepted, "accepted", i32, B), B, q_len, V, _stream_handle(stream, dev))
+    keep = (logits, keep_ids, draft, uniforms, temperature, top_k, top_p, min_p, tokens, logprobs,
+            accepted, settings)
+    return "swa_sample_accept", args, keep, (tokens, accepted, logprobs)
+
+
+def swa_sample_accept(logits, uniforms, temperature, top_k=None, top_p=None, min_p=None,
+                      draft=None, keep_ids=None, tokens=None, logprobs=None, accepted=None,
+                      stream=None, want_logprobs=True):
+    """Sampled verification through the C entry point swa_sample_accept.
+
+    logits bf16 [B, q_len, V]; uniforms fp32 [B, q_len] in [0, 1);
+    temperature fp32 [B] (<= 0: greedy); top_k int32 [B], top_p and min_p
+    fp32 [B], each or None; draft int32 [B, q_len - 1] (None when q_len ==
+    1); keep_ids int32 [V] or None.  Returns (tokens int32 [B, q_len],
+    accepted int32 [B], logprobs fp32 [B, q_len] or None), allocated if not
+    given.  Enqueued on `stream` (default: torch's current stream); does not
+    synchronise.
+    """
+    return _issue_on(logits.device, *_marshal_sample(logits, uniforms, temperature, top_k, top_p,
+                                                     min_p, draft, keep_ids, tokens, logprobs,
+                                                     accepted, stream, want_logprobs))
+
+
 class PreparedCall:
-    """One attention call validated and marshalled once (see prepare()).
+    """One call validated and marshalled once (see prepare()).
 
     Calling the object re-issues the same C call with the same pointers,
     shapes, window, scale and stream; the tensors' contents may change
     between calls (a serving loop writes the next step's rows into the same
-    buffers).  Returns the (out, lse) tensors the call writes.  The object
-    keeps every tensor it points at alive."""
+    buffers).  Returns the tensors the call writes.  The object keeps
+    every tensor it points at alive."""
 
     def __init__(self, entry, args, keep, result):
         self._fn = getattr(load_library(), entry)
@@ -509,15 +575,16 @@ class PreparedCall:
 _MARSHAL = {"swa_verify_attn": _marshal_verify, "swa_verify_attn_noalloc": _marshal_noalloc,
             "swa_verify_attn_paged": _marshal_paged, "swa_append_verify_attn": _marshal_append,
            "swa_qk_norm_rope": _marshal_rope_rows,
-           "swa_qk_norm_rope_append": _marshal_rope_append}
+           "swa_qk_norm_rope_append": _marshal_rope_append,
+           "swa_sample_accept": _marshal_sample}
 
 
 def prepare(fn, *args, **kwargs):
     """Validate and marshal a call of swa_verify_attn, swa_verify_attn_noalloc,
-    swa_verify_attn_paged, swa_append_verify_attn, swa_qk_norm_rope or
-    swa_qk_norm_rope_append once, with the same arguments the function takes,
-    and return a PreparedCall that issues it (on the device that is current
-    then: the tensors').
+    swa_verify_attn_paged, swa_append_verify_attn, swa_qk_norm_rope,
+    swa_qk_norm_rope_append or swa_sample_accept once, with the same arguments
+    the function takes, and return a PreparedCall that issues it (on the
+    device that is current then: the tensors').
 
     The per-call host cost is then one C call: no tensor checks, no struct
     building, no stream lookup (the stream is the one given, or torch's

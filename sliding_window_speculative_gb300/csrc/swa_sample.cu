@@ -1,0 +1,102 @@
+// Entry point of the sampled verification: argument checks and launches.
+#include <cuda_runtime.h>
+
+#include "../../include/swa.h"
+#include "swa_host.h"
+#include "swa_sample.cuh"
+#include "swa_tc_host.h"
+
+namespace {
+
+using swa::aligned_to;
+using swa::api_fail;
+
+constexpr int kMaxQLen = 64;  // SPLITKV_VERIFY_MAX_Q: draft rows of a verification
+
+template <int C, bool REG>
+cudaError_t launch(const swa::SampleParams &A, long long rows, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(rows * C));
+    cfg.blockDim = dim3(swa::kSampThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = swa::pdl_enabled() ? 2 : 1;
+    if (swa::launch_fault_due()) return cudaErrorLaunchOutOfResources;
+    return cudaLaunchKernelEx(&cfg, swa::swa_sample_kernel<C, REG>, A);
+}
+
+cudaError_t launch_rows(const swa::SampleParams &A, long long rows, int sms, cudaStream_t s) {
+    // the fewest CTAs whose registers hold a row, more while SMs would idle
+    const long long nvec = ((long long)A.V + 14) / 8;
+    const long long held = (long long)swa::kSampThreads * swa::kSampVpt;
+    if (nvec > swa::kSampMaxCluster * held) return launch<swa::kSampMaxCluster, false>(A, rows, s);
+    int c = 1;
+    while (c * held < nvec) c *= 2;
+    while (c < swa::kSampMaxCluster && rows * c * 2 <= sms && nvec > 2LL * c * swa::kSampThreads)
+        c *= 2;
+    switch (c) {
+        case 1: return launch<1, true>(A, rows, s);
+        case 2: return launch<2, true>(A, rows, s);
+        case 4: return launch<4, true>(A, rows, s);
+        default: return launch<8, true>(A, rows, s);
+    }
+}
+
+}  // namespace
+
+extern "C" swa_status swa_sample_accept(const void *logits, const int32_t *keep_ids,
+                                        const int32_t *draft, const float *uniforms,
+                                        const swa_sampling *sampling, int32_t *tokens,
+                                        float *logprobs, int32_t *accepted, int32_t batch,
+                                        int32_t q_len, int32_t vocab, swa_stream_t stream) {
+    if (batch < 1 || batch > 65535)
+        return api_fail(SWA_ERR_INVALID_ARG, "batch %d outside [1, 65535]", batch);
+    if (q_len < 1 || q_len > kMaxQLen)
+        return api_fail(SWA_ERR_INVALID_ARG, "q_len %d outside [1, %d]", q_len, kMaxQLen);
+    if (vocab < 1) return api_fail(SWA_ERR_INVALID_ARG, "vocab %d < 1", vocab);
+    if (!logits || !uniforms || !sampling || !sampling->temperature || !tokens || !accepted ||
+        (q_len > 1 && !draft))
+        return api_fail(SWA_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned_to(logits, 2))
+        return api_fail(SWA_ERR_INVALID_ARG, "logits must be 2-byte aligned");
+    const void *words[] = {keep_ids, draft, uniforms, sampling->temperature, sampling->top_k,
+                           sampling->top_p, sampling->min_p, tokens, logprobs, accepted};
+    for (const void *p : words)
+        if (!aligned_to(p, 4))
+            return api_fail(SWA_ERR_INVALID_ARG, "the int32 and fp32 arrays must be 4-byte aligned");
+    int dev = 0;
+    uint32_t *fault = nullptr;
+    const swa_status st = swa::api_device(&dev, &fault);
+    if (st != SWA_OK) return st;
+    swa::SampleParams A{};
+    A.logits = static_cast<const uint16_t *>(logits);
+    A.keep = keep_ids;
+    A.uniforms = uniforms;
+    A.temperature = sampling->temperature;
+    A.top_k = sampling->top_k;
+    A.top_p = sampling->top_p;
+    A.min_p = sampling->min_p;
+    A.tokens = tokens;
+    A.logprobs = logprobs;
+    A.accepted = accepted;
+    A.q_len = q_len;
+    A.V = vocab;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_rows(A, (long long)batch * q_len, swa::api_device_sms(dev), s);
+    if (e != cudaSuccess) return swa::api_cuda_fail(e, "sampling kernel launch");
+    if (q_len > 1) {
+        constexpr int kSeqs = swa::kPrefixThreads / 32;
+        e = swa::launch_kernel(swa::swa_prefix_kernel, dim3((unsigned)((batch + kSeqs - 1) / kSeqs)),
+                               dim3(swa::kPrefixThreads), 0, s, (const int32_t *)tokens, draft,
+                               accepted, batch, q_len);
+        if (e != cudaSuccess) return swa::api_cuda_fail(e, "accepted prefix kernel launch");
+    }
+    return swa::api_ok();
+}
