@@ -168,6 +168,26 @@ swa_status swa_append_verify_attn(const void *q, const void *k_new, const void *
                                   float scale, void *out, float *lse, const swa_dims *dims,
                                   swa_stream_t stream);
 
+/* swa_verify_attn in which the first num_sinks positions of a sequence stay
+ * visible however far the window has moved on ("sinks": a few first tokens, or
+ * a short pinned prefix).  The pages attend to the most recent tokens only.
+ * For the row at position p the key set becomes
+ *   K(p) = { j : 0 <= j <= p, j < seq_len[b], j < max_len,
+ *                and (j > p - W or j < num_sinks) }
+ * and everything else is as for swa_verify_attn (paged == NULL),
+ * swa_verify_attn_paged, and with k_new / v_new (both or neither NULL)
+ * swa_append_verify_attn.  A paged cache has to keep the pages of the first
+ * num_sinks positions: a ring's block table lists pages of their own for them.
+ * num_sinks 0..128 (0: the windowed call itself); SWA_ERR_INVALID_ARG below,
+ * SWA_ERR_UNSUPPORTED above.  swa_workspace_bytes bounds the workspace as for
+ * the windowed call; swa_plan describes it too, but for its kernel 4: these
+ * calls take kernel 3 instead. */
+swa_status swa_sink_verify_attn(const void *q, const void *k_new, const void *v_new, void *k_cache,
+                                void *v_cache, const swa_paged *paged, const int32_t *seq_lens,
+                                const int32_t *q_pos, int32_t window, int32_t num_sinks,
+                                float scale, void *out, float *lse, const swa_dims *dims,
+                                swa_stream_t stream);
+
 /* Norms of the query and key heads and the position rotation, the step
  * between a layer's fused projection and its attention, in one pass over the
  * block's rows.  The pages name no such kernel; it produces what
@@ -242,8 +262,8 @@ typedef struct {
     int32_t kernel;        /* 1 = CUDA-core (SIMT) chunk kernel, 2 = key-major tensor-core
                               (tcgen05) kernel, 3 = rows-major tensor-core kernel, 4 = the
                               rows-major kernel on CTA pairs (clusters of two CTAs, 2 x 128
-                              packed rows per item; swa_verify_attn only: a paged or fused-
-                              append call with these dims takes kernel 3 instead) */
+                              packed rows per item; swa_verify_attn only: a paged, fused-
+                              append or sink call with these dims takes kernel 3 instead) */
     int32_t num_splits;    /* chunks per (sequence, KV head)                    */
     int32_t chunk_keys;    /* keys per chunk                                    */
     int32_t row_tiles;     /* work items along the packed rows R = q_len * G    */

@@ -84,3 +84,33 @@ def accepted_prefix(tokens, draft):
             n += 1
         out.append(n)
     return np.array(out)
+
+
+def sink_attention(q, k, v, seq_len, q_pos, window, sinks, scale):
+    """Windowed attention of one sequence whose first `sinks` positions stay
+    visible.
+
+    q [q_len, Hq, D], k and v [Hkv, L, D].  Returns (out, lse, absv, mag): per
+    row and head the result, and for error bounds the weighted sum of |v| per
+    dim and the largest of scale * sum_d |q_d k_jd| over its visible keys.
+    """
+    q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
+    q_len, Hq, D = q.shape
+    Hkv, L = k.shape[:2]
+    out, absv = np.zeros((q_len, Hq, D)), np.zeros((q_len, Hq, D))
+    lse, mag = np.full((q_len, Hq), -np.inf), np.zeros((q_len, Hq))
+    for i in range(q_len):
+        p = q_pos + i
+        js = [j for j in range(max(0, min(p + 1, seq_len, L))) if j > p - window or j < sinks]
+        if not js:
+            continue
+        for h in range(Hq):
+            kk, vv = k[h // (Hq // Hkv)][js], v[h // (Hq // Hkv)][js]
+            s = scale * (kk @ q[i, h])
+            m = s.max()
+            e = np.exp(s - m)
+            out[i, h] = e @ vv / e.sum()
+            absv[i, h] = e @ np.abs(vv) / e.sum()
+            lse[i, h] = m + np.log(e.sum())
+            mag[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * abs(scale)
+    return out, lse, absv, mag

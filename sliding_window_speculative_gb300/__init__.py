@@ -12,7 +12,7 @@ from ._binding import (SWA_ERR_CUDA, SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED,  
                        swa_get_debug_options, swa_greedy_accept, swa_last_error, swa_plan,
                        swa_qk_norm_rope, swa_qk_norm_rope_append,
                        swa_read_debug_checks, swa_read_device_errors, swa_release_workspace,
-                       swa_sample_accept, swa_set_debug_options,
+                       swa_sample_accept, swa_set_debug_options, swa_sink_verify_attn,
                        swa_set_workspace, swa_verify_attn, swa_verify_attn_noalloc,
                        swa_verify_attn_paged, swa_version, swa_workspace_bytes, prepare)
 
@@ -22,6 +22,8 @@ __all__ = [
     "swa_append_verify_attn", "swa_greedy_accept", "swa_workspace_bytes", "swa_set_workspace",
     "swa_release_workspace", "swa_plan", "swa_last_error", "swa_read_device_errors",
     "swa_read_debug_checks", "swa_version",
+    # the windowed attention with sinks
+    "swa_sink_verify_attn",
     # the step before: head norms and the position rotation
     "swa_qk_norm_rope", "swa_qk_norm_rope_append",
     # drafts verified by sampling

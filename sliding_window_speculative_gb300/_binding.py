@@ -113,6 +113,10 @@ def load_library(path=LIB_PATH):
     lib.swa_append_verify_attn.restype = ctypes.c_int
     lib.swa_greedy_accept.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp]
     lib.swa_greedy_accept.restype = ctypes.c_int
+    lib.swa_sink_verify_attn.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(SwaPaged), vp, vp,
+                                         i32, i32, ctypes.c_float, vp, vp,
+                                         ctypes.POINTER(SwaDims), vp]
+    lib.swa_sink_verify_attn.restype = ctypes.c_int
     lib.swa_qk_norm_rope.argtypes = [vp, vp, vp, ctypes.POINTER(SwaRope), vp, vp, vp, vp,
                                      ctypes.POINTER(SwaDims), vp]
     lib.swa_qk_norm_rope.restype = ctypes.c_int
@@ -400,6 +404,66 @@ def swa_append_verify_attn(q, k_new, v_new, k_cache, v_cache, seq_lens, q_pos, w
                                    scale, block_table, out, lse, num_splits, stream))
 
 
+def _marshal_sink(q, k_cache, v_cache, seq_lens, q_pos, window, num_sinks, scale, k_new=None,
+                  v_new=None, block_table=None, out=None, lse=None, num_splits=0, stream=None,
+                  want_lse=True):
+    pq = _dev_tensor(q, "q", torch.bfloat16, 4)
+    B, q_len, Hq, D = q.shape
+    pk = _dev_tensor(k_cache, "k_cache", torch.bfloat16, 4)
+    pv = _dev_tensor(v_cache, "v_cache", torch.bfloat16, 4)
+    Hkv = k_cache.shape[1]
+    if v_cache.shape != k_cache.shape or k_cache.shape[3] != D:
+        raise ValueError("k_cache / v_cache shapes do not match each other or q")
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new must both be given")
+    pn = [None, None]
+    if k_new is not None:
+        pn = [_dev_tensor(k_new, "k_new", torch.bfloat16, 4),
+              _dev_tensor(v_new, "v_new", torch.bfloat16, 4)]
+        if tuple(k_new.shape) != (B, q_len, Hkv, D) or v_new.shape != k_new.shape:
+            raise ValueError("k_new / v_new must be [B, q_len, Hkv, D] = %s" % ((B, q_len, Hkv, D),))
+    ps = _dev_tensor(seq_lens, "seq_lens", torch.int32, 1)
+    pp = _dev_tensor(q_pos, "q_pos", torch.int32, 1)
+    if seq_lens.numel() != B or q_pos.numel() != B:
+        raise ValueError("seq_lens and q_pos need one entry per sequence")
+    paged, max_len = _paged_of(k_cache, block_table, B)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, q_len, Hq), dtype=torch.float32, device=q.device)
+    dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new,
+                      seq_lens=seq_lens, q_pos=q_pos, block_table=block_table, out=out, lse=lse)
+    po = _dev_tensor(out, "out", torch.bfloat16, 4)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    pl = None if lse is None else _dev_tensor(lse, "lse", torch.float32, 3)
+    if lse is not None and tuple(lse.shape) != (B, q_len, Hq):
+        raise ValueError("lse must be [B, q_len, Hq]")
+    dims = make_dims(B, q_len, Hq, Hkv, D, max_len, num_splits)
+    args = (pq, *pn, pk, pv, ctypes.byref(paged) if paged is not None else None, ps, pp,
+            int(window), int(num_sinks), float(scale), po, pl, ctypes.byref(dims),
+            _stream_handle(stream, dev))
+    keep = (q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, q_pos, out, lse, paged, dims)
+    return "swa_sink_verify_attn", args, keep, (out, lse)
+
+
+def swa_sink_verify_attn(q, k_cache, v_cache, seq_lens, q_pos, window, num_sinks, scale,
+                         k_new=None, v_new=None, block_table=None, out=None, lse=None,
+                         num_splits=0, stream=None, want_lse=True):
+    """Windowed verify attention whose first num_sinks positions stay visible
+    (C entry point swa_sink_verify_attn).
+
+    Tensors as for swa_verify_attn; with block_table int32 [B, max_blocks]
+    the caches are page pools as in swa_verify_attn_paged; with k_new / v_new
+    bf16 [B, q_len, Hkv, D] the block's rows are written into the cache first,
+    as in swa_append_verify_attn.  Returns (out, lse).  Enqueued on `stream`
+    (default: torch's current stream); does not synchronise.
+    """
+    return _issue_on(q.device, *_marshal_sink(q, k_cache, v_cache, seq_lens, q_pos, window,
+                                              num_sinks, scale, k_new, v_new, block_table, out,
+                                              lse, num_splits, stream, want_lse))
+
+
 def make_dims(batch, q_len, num_q_heads, num_kv_heads, head_dim, max_len, num_splits=0):
     return SwaDims(batch, q_len, num_q_heads, num_kv_heads, head_dim, max_len, num_splits)
 
@@ -576,14 +640,14 @@ _MARSHAL = {"swa_verify_attn": _marshal_verify, "swa_verify_attn_noalloc": _mars
             "swa_verify_attn_paged": _marshal_paged, "swa_append_verify_attn": _marshal_append,
            "swa_qk_norm_rope": _marshal_rope_rows,
            "swa_qk_norm_rope_append": _marshal_rope_append,
-           "swa_sample_accept": _marshal_sample}
+           "swa_sample_accept": _marshal_sample, "swa_sink_verify_attn": _marshal_sink}
 
 
 def prepare(fn, *args, **kwargs):
     """Validate and marshal a call of swa_verify_attn, swa_verify_attn_noalloc,
-    swa_verify_attn_paged, swa_append_verify_attn, swa_qk_norm_rope,
-    swa_qk_norm_rope_append or swa_sample_accept once, with the same arguments
-    the function takes, and return a PreparedCall that issues it (on the
+    swa_verify_attn_paged, swa_append_verify_attn, swa_sink_verify_attn,
+    swa_qk_norm_rope, swa_qk_norm_rope_append or swa_sample_accept once, with
+    the same arguments the function takes, and return a PreparedCall that issues it (on the
     device that is current then: the tensors').
 
     The per-call host cost is then one C call: no tensor checks, no struct

@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libswa.so")
 DEBUG_LIB = os.path.join(HERE, "libswa_debug.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
-SOURCES = ["swa_api.cu", "swa_tc.cu", "swa_rope.cu", "swa_sample.cu"]
+SOURCES = ["swa_api.cu", "swa_tc.cu", "swa_sinks.cu", "swa_rope.cu", "swa_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]

@@ -13,6 +13,7 @@
 #include "swa_simt.cuh"
 #include "swa_accept.cuh"
 #include "swa_host.h"
+#include "swa_simt_launch.cuh"
 #include "swa_tc_host.h"
 
 // Fault word of each device that loads the library; kernels receive its
@@ -373,32 +374,6 @@ swa_status ensure_workspace(int dev, size_t need, cudaStream_t stream, void **ou
     return SWA_OK;
 }
 
-template <int D, int RPW, int NRG, bool AP>
-cudaError_t launch_simt_ap(const swa::AttnParams &P, cudaStream_t stream) {
-    using C = swa::SimtCfg<D, RPW, NRG>;
-    auto kern = swa::swa_simt_kernel<D, RPW, NRG, AP>;
-    static std::atomic<bool> attr_done[kMaxDevices];
-    cudaError_t e = swa::raise_smem_limit(kern, C::SMEM_BYTES, attr_done);
-    if (e != cudaSuccess) return e;
-    dim3 grid(P.splits, P.Hkv * P.row_tiles, P.B);
-    return swa::launch_kernel(kern, grid, dim3(swa::kSimtThreads), C::SMEM_BYTES, stream, P);
-}
-
-// The plain kernel, or (fused append) its variant.
-template <int D, int RPW, int NRG>
-cudaError_t launch_simt(const swa::AttnParams &P, cudaStream_t stream) {
-    return P.k_new != nullptr ? launch_simt_ap<D, RPW, NRG, true>(P, stream)
-                              : launch_simt_ap<D, RPW, NRG, false>(P, stream);
-}
-
-template <int D>
-cudaError_t launch_simt_d(const Plan &pl, const swa::AttnParams &P, cudaStream_t s) {
-    if (pl.rpw == 4) return launch_simt<D, 4, 1>(P, s);
-    if (pl.nrg == 1) return launch_simt<D, 8, 1>(P, s);
-    if (pl.nrg == 2) return launch_simt<D, 8, 2>(P, s);
-    return launch_simt<D, 8, 4>(P, s);
-}
-
 template <int D>
 cudaError_t launch_merge(const swa::AttnParams &P, cudaStream_t s) {
     const long long blocks = (long long)P.B * P.Hkv * P.R;  // one per packed row
@@ -449,11 +424,8 @@ swa_status launch_plan(const Plan &pl, const swa_dims *dims, const swa::AttnPara
             return msg[0] ? fail(SWA_ERR_CUDA, "%s", msg)
                           : cuda_fail(e, "tensor-core kernel launch");
     } else {
-        switch (dims->head_dim) {
-            case 64: e = launch_simt_d<64>(pl, P, s); break;
-            case 128: e = launch_simt_d<128>(pl, P, s); break;
-            default: e = launch_simt_d<256>(pl, P, s); break;
-        }
+        e = P.sinks > 0 ? swa::simt_launch_sinks(P, dims->head_dim, pl.rpw, pl.nrg, s)
+                        : swa::launch_simt_kernel<false>(P, dims->head_dim, pl.rpw, pl.nrg, s);
         if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
     }
     if (pl.splits > 1) {
@@ -547,12 +519,13 @@ swa_status noalloc_scratch(int dev, void **ptr) {
 // (paged == NULL) or a paged one; with k_new / v_new non-NULL the kernels
 // first write the new rows into the cache (swa_append_verify_attn).  With
 // `noalloc` the split partials go to the fixed scratch array above
-// (swa_verify_attn_noalloc) and nothing is ever allocated.
+// (swa_verify_attn_noalloc) and nothing is ever allocated.  The first `sinks`
+// positions stay visible behind the window (swa_sink_verify_attn).
 swa_status verify_impl(const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *seq_lens, const int32_t *q_pos, int32_t window, float scale,
                        void *out, float *lse, const swa_dims *dims, swa_stream_t stream,
                        const swa_paged *paged, const void *k_new = nullptr,
-                       const void *v_new = nullptr, bool noalloc = false) {
+                       const void *v_new = nullptr, bool noalloc = false, int32_t sinks = 0) {
     swa_status st = validate_dims(dims, window);
     if (st != SWA_OK) return st;
     if (!q || !k_cache || !v_cache || !seq_lens || !q_pos || !out)
@@ -576,8 +549,9 @@ swa_status verify_impl(const void *q, const void *k_cache, const void *v_cache,
 
     uint32_t *fault = fault_word_ptr(dev);
     if (fault == nullptr) return fail(SWA_ERR_CUDA, "cannot resolve the device fault word");
-    // the CTA-pair kernel reads a contiguous cache without a fused append
-    const Plan pl = make_plan(dims, window, device_sms(dev), paged == nullptr && k_new == nullptr);
+    // the CTA-pair kernel reads a contiguous cache without a fused append or sinks
+    const Plan pl = make_plan(dims, window, device_sms(dev),
+                              paged == nullptr && k_new == nullptr && sinks == 0);
     swa::AttnParams P{};
     P.q = static_cast<const __nv_bfloat16 *>(q);
     P.k = static_cast<const __nv_bfloat16 *>(k_cache);
@@ -593,6 +567,7 @@ swa_status verify_impl(const void *q, const void *k_cache, const void *v_cache,
     P.G = dims->num_q_heads / dims->num_kv_heads;
     P.L = dims->max_len;
     P.window = window;
+    P.sinks = sinks;
     P.R = P.q_len * P.G;
     P.splits = pl.splits;
     P.chunk = pl.chunk;
@@ -673,6 +648,22 @@ swa_status swa_append_verify_attn(const void *q, const void *k_new, const void *
     }
     return verify_impl(q, k_cache, v_cache, seq_lens, q_pos, window, scale, out, lse, dims, stream,
                        paged, k_new, v_new);
+}
+
+swa_status swa_sink_verify_attn(const void *q, const void *k_new, const void *v_new, void *k_cache,
+                                void *v_cache, const swa_paged *paged, const int32_t *seq_lens,
+                                const int32_t *q_pos, int32_t window, int32_t num_sinks,
+                                float scale, void *out, float *lse, const swa_dims *dims,
+                                swa_stream_t stream) {
+    if (num_sinks < 0) return fail(SWA_ERR_INVALID_ARG, "num_sinks %d < 0", num_sinks);
+    if (num_sinks > kTcKeysPerTile)
+        return fail(SWA_ERR_UNSUPPORTED, "num_sinks %d > %d", num_sinks, kTcKeysPerTile);
+    if (paged != nullptr) {
+        const swa_status st = check_paged(paged, dims);
+        if (st != SWA_OK) return st;
+    }
+    return verify_impl(q, k_cache, v_cache, seq_lens, q_pos, window, scale, out, lse, dims, stream,
+                       paged, k_new, v_new, /*noalloc=*/false, num_sinks);
 }
 
 size_t swa_workspace_bytes(const swa_dims *dims, int32_t window) {

@@ -86,7 +86,7 @@ struct RowsCfg {
     static_assert(STG_OFF % 16 == 0 && BAR_OFF % 8 == 0 && META_OFF % 8 == 0, "alignment");
 };
 
-template <int D, int QR, int NT, int QB, bool AP>
+template <int D, int QR, int NT, int QB, bool AP, bool SK = false>
 __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
     swa_rows_kernel(const __grid_constant__ TcParams T, const __grid_constant__ TcMaps M) {
     using C = RowsCfg<D, QR, NT, QB>;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
     grid_dep_wait();
     grid_dep_trigger();
     for (int j = tid; j < kTcMetaItems; j += NTHR)
-        if (j < cta_items(T)) meta[j] = tc_decode_global<AP>(T, cta_item(T, j));
+        if (j < cta_items(T)) meta[j] = tc_decode_global<AP, SK>(T, cta_item(T, j));
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
 
     if (warp == 0) {
         // ======================================================= producer
-        tile_producer<C, NT, QB, AP>(T, M, meta, ftab, ring, qs, bars, false);
+        tile_producer<C, NT, QB, AP, SK>(T, M, meta, ftab, ring, qs, bars, false);
     } else if (warp == 1) {
         // ============================================================ MMA
         // Two cursors over the tile sequence: S = Q K^T of the next tile and
@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
                 int item, j, t, n_tiles;
                 int last_keys;  // keys of the item's last tile
                 int head;       // key rows before the chunk in its first tile (paged cache)
+                int z_lo, z_hi; // (SK) key slots that hold no key in front of the last one
                 uint32_t k, g;
                 bool valid;
                 int slot;       // this cursor's fill: slot, parity (-1: not yet looked up)
@@ -195,11 +196,16 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
             auto seek = [&](Cursor &c) {
                 for (; c.j < n_items; ++c.j) {
                     c.item = cta_item(T, c.j);
-                    const TcItem it = tc_decode<AP>(T, c.item, c.j, meta);
+                    const TcItem it = tc_decode<AP, SK>(T, c.item, c.j, meta);
                     if (it.n_tiles > 0) {
                         c.n_tiles = it.n_tiles;
                         c.last_keys = it.cr.c_hi - it.t0 - kTcTileKeys * (it.n_tiles - 1);
                         c.head = it.cr.c_lo - it.t0;
+                        if constexpr (SK) {
+                            const int end = item_end(it);
+                            c.last_keys = end - kTcTileKeys * (it.n_tiles - 1);
+                            gap_slots(P, it, c.z_lo, c.z_hi);
+                        }
                         c.t = 0;
                         c.valid = true;
                         return;
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
                 ++c.j;
                 seek(c);
             };
-            Cursor qc{0, 0, 0, 0, 0, 0, 0u, 0u, false, -1, 0u};
+            Cursor qc{0, 0, 0, 0, 0, 0, 0, 0, 0u, 0u, false, -1, 0u};
             seek(qc);
             Cursor pc = qc;
             bool ok = true;
@@ -256,7 +262,17 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
-                        if (pc.t == 0 && pc.head > 0) {
+                        if constexpr (SK) {
+                            // (the fill of the last sink's atom, and the rows
+                            // before the chunk in its first window atom)
+                            const int lo = max(pc.z_lo - kTcTileKeys * pc.t, 0);
+                            const int hi = min(pc.z_hi - kTcTileKeys * pc.t, kTcTileKeys);
+                            if (lo < hi) {
+                                zero_v_rows<C>(vt, lo, hi, lane);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                        } else if (pc.t == 0 && pc.head > 0) {
                             // (paged cache) the rows before the chunk in its first
                             // tile: P is 0 there, but they may hold anything
                             const int row = lane >> 3, q = lane & 7;
@@ -367,7 +383,7 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
             bool ok = true;
             const int n_items = cta_items(T);
             for (int j = 0; j < n_items && ok; ++j) {
-                const TcItem it = tc_decode<AP>(T, cta_item(T, j), j, meta);
+                const TcItem it = tc_decode<AP, SK>(T, cta_item(T, j), j, meta);
                 const bool live = r < it.rows;
                 const int rg = it.row0 + r;  // packed row of the (sequence, KV head)
                 const int i = rg / P.G, gg = rg - i * P.G;
@@ -405,6 +421,9 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
                     jlo = 1;
                     jhi = 0;
                 }
+                // (SK) the last of the first P.sinks positions it sees among the
+                // window keys; the sinks in front it sees all
+                const long long jsink = SK && jhi > P.sinks - 1 ? P.sinks - 1 : jhi;
                 const uint32_t ob = k % OB;
                 float mref = kNoRef, lsum = 0.f;
                 for (int t = 0; t < it.n_tiles; ++t, ++g) {
@@ -415,16 +434,32 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
                     fence_after_sync();
                     // this thread's 64 scores (keys kh .. kh + 63 of the tile), masked
                     // to the row's keys, in log2 units
-                    const long long j0 = (long long)it.t0 + (long long)kTcTileKeys * t + kh;
+                    const long long j0 =
+                        (long long)it.t0 + (long long)kTcTileKeys * t + kh - (SK ? it.vs() : 0);
                     const long long ca_l = jlo - j0, cb_l = jhi - j0;
                     const int ca = ca_l < 0 ? 0 : (ca_l > 64 ? 64 : (int)ca_l);
                     const int cb = cb_l < -1 ? -1 : (cb_l > 63 ? 63 : (int)cb_l);
+                    uint64_t seen = ~0ull;  // (SK) bit c: the row sees key kh + c
+                    if constexpr (SK) {
+                        // keys [a, b] of this thread's 64
+                        auto keys = [](long long a, long long b) -> uint64_t {
+                            if (a < 0) a = 0;
+                            if (b > 63) b = 63;
+                            return a > b ? 0ull : (~0ull >> (63 - (int)(b - a))) << (int)a;
+                        };
+                        seen = keys(ca_l, cb_l);
+                        if (live) {
+                            const long long v0 = (long long)kTcTileKeys * t + kh;
+                            seen |= keys(-v0, it.sink - 1 - v0);
+                            seen |= keys(it.cr.c_lo - j0, jsink - j0);
+                        }
+                    }
                     uint32_t sraw[64];
                     tmem_ld32(tl + sb * 128 + kh, *reinterpret_cast<uint32_t(*)[32]>(sraw));
                     tmem_ld32(tl + sb * 128 + kh + 32, *reinterpret_cast<uint32_t(*)[32]>(sraw + 32));
                     tmem_wait_ld();
                     float m4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-                    if (ca == 0 && cb == 63) {
+                    if (SK ? seen == ~0ull : ca == 0 && cb == 63) {
                         const uint64_t sc2 = f2_pack(sc, sc);
 #pragma unroll
                         for (int c = 0; c < 64; c += 2) {
@@ -439,10 +474,10 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
                     } else {
 #pragma unroll
                         for (int c = 0; c < 64; c += 2) {
-                            const float x0 =
-                                (c >= ca && c <= cb) ? __uint_as_float(sraw[c]) * sc : NEG_INF;
-                            const float x1 =
-                                (c + 1 >= ca && c + 1 <= cb) ? __uint_as_float(sraw[c + 1]) * sc : NEG_INF;
+                            const bool s0 = SK ? (seen >> c) & 1 : c >= ca && c <= cb;
+                            const bool s1 = SK ? (seen >> (c + 1)) & 1 : c + 1 >= ca && c + 1 <= cb;
+                            const float x0 = s0 ? __uint_as_float(sraw[c]) * sc : NEG_INF;
+                            const float x1 = s1 ? __uint_as_float(sraw[c + 1]) * sc : NEG_INF;
                             sraw[c] = __float_as_uint(x0);
                             sraw[c + 1] = __float_as_uint(x1);
                             m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], x0, x1);
@@ -640,7 +675,7 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
         }
     } else if constexpr (AP) {
         // ================================================= append worker
-        append_worker<C, D>(T, meta, ftab, ring, bars);
+        append_worker<C, D, SK>(T, meta, ftab, ring, bars);
     }
 
     // ---------------------------------------------------------- teardown
@@ -649,7 +684,7 @@ __global__ void __launch_bounds__(AP ? kRowsThreads + 32 : kRowsThreads, 1)
     fence_after_sync();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
     if constexpr (AP) {
-        if (cta_items(T) > 2) append_flush<D>(T, meta, ring, NT * C::TILE_BYTES, NTHR);
+        if (cta_items(T) > 2) append_flush<D, SK>(T, meta, ring, NT * C::TILE_BYTES, NTHR);
     }
 }
 

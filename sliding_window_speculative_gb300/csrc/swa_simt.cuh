@@ -46,6 +46,7 @@ struct AttnParams {
     const __nv_bfloat16 *k_new;
     const __nv_bfloat16 *v_new;
     int B, q_len, Hq, Hkv, G, L, window, R;
+    int sinks;  // first positions that stay visible behind the window (0: none)
     int splits, chunk, row_tiles, rows_per_tile;
     float qk_scale;   // scale * log2(e)
     // bounded waits give up after this many SM cycles (kWaitLimitCycles
@@ -101,6 +102,20 @@ __device__ __forceinline__ ChunkRange chunk_range(const AttnParams &P, int b, in
     if (lo > c.c_lo) c.c_lo = (int)(lo < c.c_hi ? lo : c.c_hi);
     if (hi < c.c_hi) c.c_hi = (int)(hi > c.c_lo ? hi : c.c_lo);
     return c;
+}
+
+// The sink positions [0, n) in front of the window keys of a work item whose
+// first draft row is i_first: those of the sequence's first P.sinks positions
+// that lie before every window of the item (a sink inside a window is one of
+// its keys), read with the first chunk only.
+__device__ __forceinline__ int sink_keys(const AttnParams &P, int b, int split, int i_first) {
+    if (split != 0) return 0;
+    const long long qp = P.q_pos[b];
+    long long n = qp + i_first - P.window + 1;  // the item's first window key
+    const long long hi = min(min(qp + P.q_len, (long long)P.seq_lens[b]), (long long)P.L);
+    if (n > hi) n = hi;
+    if (n > P.sinks) n = P.sinks;
+    return n > 0 ? (int)n : 0;
 }
 
 // A block-table page, checked in SWA_DEBUG_CHECKS builds: one outside
@@ -197,7 +212,10 @@ struct SimtCfg {
     static_assert(KB % KPG == 0, "key block must hold whole butterfly groups");
 };
 
-template <int D, int RPW, int NRG, bool AP>
+// SK: the first P.sinks positions stay visible.  The keys of a work item are
+// then its sinks followed by its window keys: the CTA's key v is position v
+// while v < n_sink, else c_lo + v - n_sink.
+template <int D, int RPW, int NRG, bool AP, bool SK = false>
 __global__ void __launch_bounds__(kSimtThreads) swa_simt_kernel(const AttnParams P) {
     using C = SimtCfg<D, RPW, NRG>;
     constexpr int DPL = C::DPL;
@@ -223,9 +241,10 @@ __global__ void __launch_bounds__(kSimtThreads) swa_simt_kernel(const AttnParams
     const int i_first = rt * C::RPT / P.G;
     const int i_last = (min(P.R, rt * C::RPT + C::RPT) - 1) / P.G;
     const ChunkRange cr = chunk_range(P, b, split, i_first, i_last);
-    const int n_keys = cr.c_hi - cr.c_lo;
+    int n_sink = 0;
+    if constexpr (SK) n_sink = sink_keys(P, b, split, i_first);
+    const int n_keys = cr.c_hi - cr.c_lo + n_sink;
     const int n_tiles = n_keys > 0 ? (n_keys + kSimtTileKeys - 1) / kSimtTileKeys : 0;
-
 
     // keys read from k_new / v_new (every position >= q_pos under an append)
     // and the new rows this CTA stores to the cache; both empty in the plain
@@ -239,11 +258,36 @@ __global__ void __launch_bounds__(kSimtThreads) swa_simt_kernel(const AttnParams
     auto issue = [&](int t) {
         const int s = t % C::STAGES;
         const int j0 = cr.c_lo + t * kSimtTileKeys;
-        const int n = min(kSimtTileKeys, cr.c_hi - j0);
+        const int n = SK ? min(kSimtTileKeys, n_keys - t * kSimtTileKeys)
+                         : min(kSimtTileKeys, cr.c_hi - j0);
         const uint32_t bytes = (uint32_t)n * D * 2;
         uint8_t *dst = ring + s * C::STAGE_BYTES;
         mbar_arrive_expect_tx(&full[s], 2 * bytes);
         if (P.withhold_fill == t && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) return;
+        if constexpr (SK) {
+            // as below, with a run ending at the last sink too
+            for (int v = t * kSimtTileKeys; v < t * kSimtTileKeys + n;) {
+                const int j = v < n_sink ? v : cr.c_lo + v - n_sink;
+                const uint32_t off = (uint32_t)(v - t * kSimtTileKeys) * D * 2;
+                if (AP && j >= cr.qp) {
+                    const size_t src = (((size_t)b * P.q_len + (j - cr.qp)) * P.Hkv + h) * D;
+                    bulk_copy_g2s(dst + off, P.k_new + src, D * 2, &full[s]);
+                    bulk_copy_g2s(dst + C::TILE_BYTES + off, P.v_new + src, D * 2, &full[s]);
+                    ++v;
+                    continue;
+                }
+                int run = t * kSimtTileKeys + n - v;
+                if (v < n_sink) run = min(run, n_sink - v);
+                if (AP) run = min(run, cr.qp - j);
+                if (P.block_table != nullptr) run = min(run, P.page_size - j % P.page_size);
+                const size_t row = (size_t)cache_row(P, b, h, j);
+                const uint32_t rb = (uint32_t)run * D * 2;
+                bulk_copy_g2s(dst + off, P.k + row * D, rb, &full[s]);
+                bulk_copy_g2s(dst + C::TILE_BYTES + off, P.v + row * D, rb, &full[s]);
+                v += run;
+            }
+            return;
+        }
         // one copy per run of rows contiguous in the cache (a page's rows, or
         // the whole tile of a contiguous cache); a new row of a fused append
         // is one copy from k_new / v_new
@@ -304,6 +348,8 @@ __global__ void __launch_bounds__(kSimtThreads) swa_simt_kernel(const AttnParams
         jlo_own = max(max(cr.c_lo, p - P.window + 1), 0);
         jhi_own = min(p, cr.c_hi - 1);
     }
+    // (SK) the row's last visible sink among the window keys
+    const int jsink_own = SK ? min(P.sinks - 1, jhi_own) : -1;
 
     float m_own = NEG_INF, l_own = 0.f;
     float acc[RPW][DPL];
@@ -331,8 +377,9 @@ __global__ void __launch_bounds__(kSimtThreads) swa_simt_kernel(const AttnParams
         }
         const __nv_bfloat16 *Ks = reinterpret_cast<const __nv_bfloat16 *>(ring + s * C::STAGE_BYTES);
         const __nv_bfloat16 *Vs = Ks + kSimtTileKeys * D;
-        const int j0 = cr.c_lo + t * kSimtTileKeys;
-        const int n = min(kSimtTileKeys, cr.c_hi - j0);
+        const int v0 = t * kSimtTileKeys;
+        const int j0 = cr.c_lo + v0 - n_sink;  // position of the tile's key 0 past the sinks
+        const int n = min(kSimtTileKeys, n_keys - v0);
         if constexpr (AP) {
             // the fused append's new rows of this tile that this CTA owns, from
             // the stage to the cache
@@ -368,8 +415,16 @@ __global__ void __launch_bounds__(kSimtThreads) swa_simt_kernel(const AttnParams
                 }
             }
             const float red = warp_reduce_scatter32(v);
-            const int j = j0 + kb0 + grp * C::KPG + lane / RPW;
-            sc[grp] = (j >= jlo_own && j <= jhi_own) ? red : NEG_INF;
+            const int kt = kb0 + grp * C::KPG + lane / RPW;
+            const int j = j0 + kt;
+            bool vis = j >= jlo_own && j <= jhi_own;
+            if constexpr (SK) {
+                if (v0 + kt < n_sink)
+                    vis = r_own < P.R;  // (before every window of the item)
+                else
+                    vis = vis || (j >= cr.c_lo && j <= jsink_own);
+            }
+            sc[grp] = vis ? red : NEG_INF;
         }
 
         // online softmax for the row this lane holds

@@ -11,24 +11,10 @@
 #include "swa_rows.cuh"
 #include "swa_tc.cuh"
 #include "swa_tc_host.h"
+#include "swa_tc_launch.cuh"
 
 namespace swa {
 namespace {
-
-// Per (head_dim, padded rows): ring slots of one 128-key tile and Q / P
-// buffer counts, sized to one CTA per SM (at most 227 KB of shared memory).
-template <int D, int N>
-struct Conf {
-    // A ring of three K-or-V tiles lets V(t+1) load while V(t) waits for its
-    // PV; at head_dim 256 (64 KB tiles) that leaves room for one Q and one P
-    // buffer beside it (two at 16 rows).  O^T (2N columns per head-dim half)
-    // is double-buffered unless TMEM runs out (head_dim 256, 64 rows).
-    static constexpr int NT = D == 256 ? (N <= 32 ? 3 : 2) : 5;
-    static constexpr int QB = (D == 256 && N >= 32) ? 1 : (D == 128 && N == 64) ? 1 : 2;
-    static constexpr int PB = (D == 256 && N >= 32) ? 1 : (N == 64) ? 1 : 2;
-    static constexpr int OB = (D == 256 && N == 64) ? 1 : 2;
-    using C = TcCfg<D, N, NT, QB, PB, OB>;
-};
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
@@ -43,62 +29,6 @@ bool load_encode() {
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
     return g_encode != nullptr;
-}
-
-template <int D, int N, bool AP>
-cudaError_t launch_ap(const TcLaunch &L, const TcMaps &maps, cudaStream_t stream) {
-    using Cf = Conf<D, N>;
-    using C = typename Cf::C;
-    auto kern = swa_tc_kernel<D, N, Cf::NT, Cf::QB, Cf::PB, Cf::OB, AP>;
-    static std::atomic<bool> attr_done[64];
-    cudaError_t e = raise_smem_limit(kern, C::SMEM_BYTES, attr_done);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3(L.grid), dim3(AP ? kTcThreads + 32 : kTcThreads),
-                         C::SMEM_BYTES, stream, L.T, maps);
-}
-
-// The plain kernel, or (fused append) its variant with the append warp.
-template <int D, int N>
-cudaError_t launch(const TcLaunch &L, const TcMaps &maps, cudaStream_t stream) {
-    return L.T.a.k_new != nullptr ? launch_ap<D, N, true>(L, maps, stream)
-                                  : launch_ap<D, N, false>(L, maps, stream);
-}
-
-// Rows-major kernel: per (head_dim, Q rows) the ring tiles and Q buffers
-// that fit one CTA per SM.
-template <int D, int QR>
-struct RowsConf {
-    static constexpr int NT = D == 256 ? (QR == 32 ? 3 : 2) : (QR == 128 ? 5 : 6);
-    static constexpr int QB = D == 256 ? (QR == 64 ? 2 : 1) : (QR == 32 ? 2 : 1);
-    using C = RowsCfg<D, QR, NT, QB>;
-};
-
-template <int D, int QR, bool AP>
-cudaError_t launch_rows_ap(const TcLaunch &L, const TcMaps &maps, cudaStream_t stream) {
-    using Cf = RowsConf<D, QR>;
-    using C = typename Cf::C;
-    auto kern = swa_rows_kernel<D, QR, Cf::NT, Cf::QB, AP>;
-    static std::atomic<bool> attr_done[64];
-    cudaError_t e = raise_smem_limit(kern, C::SMEM_BYTES, attr_done);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3(L.grid), dim3(AP ? kRowsThreads + 32 : kRowsThreads),
-                         C::SMEM_BYTES, stream, L.T, maps);
-}
-
-template <int D, int QR>
-cudaError_t launch_rows(const TcLaunch &L, const TcMaps &maps, cudaStream_t stream) {
-    return L.T.a.k_new != nullptr ? launch_rows_ap<D, QR, true>(L, maps, stream)
-                                  : launch_rows_ap<D, QR, false>(L, maps, stream);
-}
-
-template <int D>
-cudaError_t launch_rows_d(const TcLaunch &L, const TcMaps &maps, cudaStream_t s) {
-    switch (L.N) {
-        case 32: return launch_rows<D, 32>(L, maps, s);
-        case 64: return launch_rows<D, 64>(L, maps, s);
-        case 128: return launch_rows<D, 128>(L, maps, s);
-        default: return cudaErrorInvalidConfiguration;
-    }
 }
 
 // CTA-pair kernel: clusters of two CTAs, as many pairs as the plan's grid
@@ -141,16 +71,6 @@ cudaError_t launch_pairs(const TcLaunch &L, const TcMaps &maps, const PairMaps &
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     if (launch_fault_due()) return cudaErrorLaunchOutOfResources;
     return cudaLaunchKernelEx(&cfg, kern, L.T, maps, pm);
-}
-
-template <int D>
-cudaError_t launch_d(const TcLaunch &L, const TcMaps &maps, cudaStream_t s) {
-    switch (L.N) {
-        case 16: return launch<D, 16>(L, maps, s);
-        case 32: return launch<D, 32>(L, maps, s);
-        case 64: return launch<D, 64>(L, maps, s);
-        default: return cudaErrorInvalidConfiguration;
-    }
 }
 
 template <int D, int N>
@@ -295,12 +215,7 @@ cudaError_t tc_launch(const TcLaunch &L, cudaStream_t stream, char *err, size_t 
         }
         return launch_pairs<256>(L, maps, pm, stream);
     }
-    if (L.rows_major) {
-        if (D == 256) return launch_rows_d<256>(L, maps, stream);
-        return launch_rows_d<128>(L, maps, stream);
-    }
-    if (D == 256) return launch_d<256>(L, maps, stream);
-    return launch_d<128>(L, maps, stream);
+    return P.sinks > 0 ? tc_launch_sinks(L, maps, stream) : launch_kernels<false>(L, maps, stream);
 }
 
 }  // namespace swa

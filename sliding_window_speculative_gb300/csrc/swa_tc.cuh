@@ -82,8 +82,11 @@ struct TcItem {
                // q_pos mod 8 (fused append: new rows start on an atom)
     int n_tiles;
     int row0;  // first packed row of the item
-    int rows;  // packed rows of the item
-    int i0;    // first draft row
+    int16_t rows;  // packed rows of the item (at most 128)
+    int16_t sink;  // sink positions [0, sink) in front of the window keys (SK kernels)
+    int i0;        // first draft row
+    // key slots the sinks take: whole 8-key atoms
+    __device__ __forceinline__ int vs() const { return (sink + 7) & ~7; }
 };
 
 template <int D, int N, int NT, int QB, int PB, int OB>
@@ -146,8 +149,63 @@ __device__ __forceinline__ int cta_item(const TcParams &T, int j) {
     return (int)blockIdx.x + j * (int)gridDim.x;
 }
 
+// Keys of the SK kernels (the first P.sinks positions stay visible): an item's
+// key slot v holds position v while v < it.vs() (a sink; slots from it.sink to
+// it.vs(), the last sink's atom filled up, count for nothing), else t0 + v - vs.
+// So a few sinks share a tile with the first window keys, at the cost of one
+// atom; positions rise with the slot.  An item whose sinks would run into its
+// window's first atoms takes all keys from position 0 on instead (sink 0).
+// Without SK sink = vs = 0 and slot v is position t0 + v.
+//
+// One past the last slot that holds a key.
+__device__ __forceinline__ int item_end(const TcItem &it) {
+    return it.cr.c_hi > it.cr.c_lo ? it.vs() + it.cr.c_hi - it.t0 : it.sink;
+}
+
+// Slots [lo, hi) in front of the window keys that no row of the item sees: the
+// rest of the last sink's atom and the rows before the chunk in its first
+// window atom, or, all keys taken from position 0 on, those between the sinks
+// and the item's first window.
+__device__ __forceinline__ void gap_slots(const AttnParams &P, const TcItem &it, int &lo, int &hi) {
+    const int first = it.cr.qp + it.i0 - P.window + 1;
+    if (it.cr.c_lo < first && it.cr.c_hi > it.cr.c_lo) {
+        lo = min(P.sinks, first);
+        hi = min(first, it.cr.c_hi);
+    } else {
+        lo = it.sink;
+        hi = min(it.vs() + it.cr.c_lo - it.t0, item_end(it));
+    }
+}
+
+// What tile t holds: sa atoms of sinks (n_sink of them keys), then n window
+// keys from position p on.
+struct TileKeys {
+    int sa, n_sink, p, n;
+};
+template <bool SK>
+__device__ __forceinline__ TileKeys tile_keys(const TcItem &it, int t) {
+    TileKeys k;
+    k.sa = k.n_sink = 0;
+    k.p = it.t0 + kTcTileKeys * t;
+    if constexpr (SK) {
+        if (t == 0) {
+            k.sa = it.vs() >> 3;
+            k.n_sink = it.sink;
+        } else {
+            k.p -= it.vs();
+        }
+    }
+    k.n = min(kTcTileKeys - 8 * k.sa, it.cr.c_hi - k.p);
+    if (SK && it.cr.c_hi <= it.cr.c_lo) k.n = 0;  // no window key: sinks only
+    return k;
+}
+// Position of the first key slot of atom a of a tile.
+__device__ __forceinline__ int atom_pos(const TileKeys &k, int a) {
+    return a < k.sa ? 8 * a : k.p + 8 * (a - k.sa);
+}
+
 // Work item `item` (its sequence's seq_len / q_pos read from global memory).
-template <bool AP>
+template <bool AP, bool SK = false>
 __device__ __forceinline__ TcItem tc_decode_global(const TcParams &T, int item) {
     const AttnParams &P = T.a;
     TcItem it;
@@ -159,7 +217,7 @@ __device__ __forceinline__ TcItem tc_decode_global(const TcParams &T, int item) 
     it.h = rest % P.Hkv;
     it.b = rest / P.Hkv;
     it.row0 = it.rt * T.rows_per_tile;
-    it.rows = min(P.R - it.row0, T.rows_per_tile);
+    it.rows = (int16_t)min(P.R - it.row0, T.rows_per_tile);
     it.i0 = it.rt * T.q_rows_per_tile;
     it.cr = chunk_range(P, it.b, it.split, it.i0, (it.row0 + it.rows - 1) / P.G);
     // a contiguous cache under a fused append: rounded down to q_pos mod 8,
@@ -169,18 +227,28 @@ __device__ __forceinline__ TcItem tc_decode_global(const TcParams &T, int item) 
     it.t0 = P.block_table != nullptr ? (it.cr.c_lo & ~7)
             : AP                     ? max(it.cr.c_lo - ((it.cr.c_lo - it.cr.qp) & 7), 0)
                                      : it.cr.c_lo;
-    const int nk = it.cr.c_hi - it.t0;
-    it.n_tiles = it.cr.c_hi > it.cr.c_lo ? (nk + kTcTileKeys - 1) / kTcTileKeys : 0;
+    it.sink = 0;
+    if constexpr (SK) {
+        it.sink = (int16_t)sink_keys(P, it.b, it.split, it.i0);
+        if (it.cr.c_hi > it.cr.c_lo && it.t0 < it.vs()) {
+            it.sink = 0;
+            it.t0 = it.cr.c_lo = 0;
+        }
+        it.n_tiles = (item_end(it) + kTcTileKeys - 1) / kTcTileKeys;
+    } else {
+        const int nk = it.cr.c_hi - it.t0;
+        it.n_tiles = it.cr.c_hi > it.cr.c_lo ? (nk + kTcTileKeys - 1) / kTcTileKeys : 0;
+    }
     return it;
 }
 
 // Work item `item`, the j-th of this CTA: the first kTcMetaItems were
 // decoded once at set-up into shared memory.
-template <bool AP>
+template <bool AP, bool SK = false>
 __device__ __forceinline__ TcItem tc_decode(const TcParams &T, int item, int j,
                                             const TcItem *meta) {
     if (j < kTcMetaItems) return meta[j];
-    return tc_decode_global<AP>(T, item);
+    return tc_decode_global<AP, SK>(T, item);
 }
 
 // Barrier of one softmax warpgroup (128 threads), ids 1 / 3.
@@ -338,6 +406,53 @@ __device__ __forceinline__ void append_split(const AttnParams &P, int qp, int p,
     a_n = qp > p && ((qp - p) & 7) ? a_m + 1 : a_m;
 }
 
+// append_split over a whole tile: positions rise with the atom, and at most
+// one atom of an item holds both cache rows and new rows (sinks reach past
+// q_pos only where every window atom starts behind it).
+template <bool SK>
+__device__ __forceinline__ void tile_split(const AttnParams &P, int qp, const TileKeys &k,
+                                           int &a_m, int &a_n) {
+    if constexpr (SK) {
+        if (k.n_sink > 0 && P.k_new != nullptr && k.n_sink > qp) {
+            a_m = qp > 0 ? qp >> 3 : 0;
+            a_n = qp > 0 && (qp & 7) ? a_m + 1 : a_m;
+            return;
+        }
+        if (k.n == 0) {
+            a_m = a_n = k.sa;
+            return;
+        }
+    }
+    append_split(P, qp, k.p, k.n, a_m, a_n);
+    a_m += k.sa;
+    a_n += k.sa;
+}
+
+// The cache rows of a tile's atoms [0, atoms): tile_copies of its sinks and of
+// its window keys.
+template <int AB, bool SK>
+__device__ __forceinline__ void tile_copies_of(const AttnParams &P, const TcMaps &M, int kv, int b,
+                                               int h, const TileKeys &k, int atoms, uint8_t *dst,
+                                               uint64_t *bar, uint64_t policy, int lane) {
+    if (SK && k.sa > 0)
+        tile_copies<AB>(P, M, kv, b, h, 0, atoms < k.sa ? 8 * atoms : k.n_sink, dst, bar, policy,
+                        lane);
+    if (atoms > k.sa)
+        tile_copies<AB>(P, M, kv, b, h, k.p, min(8 * (atoms - k.sa), k.n), dst + k.sa * AB, bar,
+                        policy, lane);
+}
+
+// Zeroes the V rows of a tile's key slots [lo, hi), whose P is 0 but which may
+// hold anything (one warp; the caller fences).
+template <class C>
+__device__ __forceinline__ void zero_v_rows(uint8_t *vt, int lo, int hi, int lane) {
+    for (int r = lo + (lane >> 3); r < hi; r += 4)
+#pragma unroll
+        for (int s = 0; s < C::SLABS; ++s)
+            reinterpret_cast<uint4 *>(vt + (r >> 3) * C::ATOM_BYTES + s * 1024 +
+                                      (r & 7) * 128)[lane & 7] = make_uint4(0, 0, 0, 0);
+}
+
 // Fills of the CTA's first work item issued ahead of the producer loop:
 // its first min(NT, early_max, 2 * n_tiles) K/V fills (fill 2t + kv into
 // ring slot 2t + kv) and its Q rows; 0 if none (paged cache, fused append,
@@ -357,14 +472,14 @@ __device__ __forceinline__ int early_fills(const TcParams &T, const TcItem &it) 
 // other thread writes the bytes these copies land in (the Q rows TMA writes
 // are never zeroed).  A withheld fill (tests of the bounded waits) is
 // posted on its barrier but not copied.
-template <class C, int NT, bool AP>
+template <class C, int NT, bool AP, bool SK = false>
 __device__ __forceinline__ void issue_early_fills(const TcParams &T, const TcMaps &M,
                                                   volatile uint32_t *ftab, uint8_t *ring,
                                                   uint8_t *qs, uint64_t *bars, int warp) {
     using namespace tc;
     const AttnParams &P = T.a;
     if (AP || P.block_table != nullptr || warp > NT || cta_items(T) < 1) return;
-    const TcItem it = tc_decode_global<AP>(T, cta_item(T, 0));
+    const TcItem it = tc_decode_global<AP, SK>(T, cta_item(T, 0));
     const int n = early_fills<NT, AP>(T, it);
     if (n == 0) return;
     if (warp == NT) {
@@ -376,14 +491,14 @@ __device__ __forceinline__ void issue_early_fills(const TcParams &T, const TcMap
     }
     if (warp >= n) return;
     const int t = warp >> 1, kv = warp & 1;
-    const int p = it.t0 + kTcTileKeys * t;
-    const int n_valid = min(kTcTileKeys, it.cr.c_hi - p);
+    const TileKeys tk = tile_keys<SK>(it, t);
+    const int natoms = tk.sa + ((tk.n + 7) >> 3);
     ftab[warp] = ((uint32_t)warp << 8) | (uint32_t)warp;  // fill w -> slot w, use parity 0
-    mbar_arrive_expect_tx(&bars[C::B_FULL + warp], (uint32_t)((n_valid + 7) >> 3) * C::ATOM_BYTES);
+    mbar_arrive_expect_tx(&bars[C::B_FULL + warp], (uint32_t)natoms * C::ATOM_BYTES);
     if (P.withhold_fill == warp && blockIdx.x == 0) return;
     const uint64_t policy = P.row_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-    tile_copies<C::ATOM_BYTES>(P, M, kv, it.b, it.h, p, n_valid, ring + warp * C::TILE_BYTES,
-                               &bars[C::B_FULL + warp], policy, 0);
+    tile_copies_of<C::ATOM_BYTES, SK>(P, M, kv, it.b, it.h, tk, natoms, ring + warp * C::TILE_BYTES,
+                                      &bars[C::B_FULL + warp], policy, 0);
 }
 
 // The TMA producer (warp 0) of both tensor-core kernels: lane 0 runs the
@@ -397,7 +512,7 @@ __device__ __forceinline__ void issue_early_fills(const TcParams &T, const TcMap
 // B_MIX, for the append worker to complete the fill.  With `early`, the
 // first item's first early_fills() fills and its Q rows were issued already
 // (issue_early_fills).  Waits for every copy it issued before returning.
-template <class C, int NT, int QB, bool AP>
+template <class C, int NT, int QB, bool AP, bool SK = false>
 __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M,
                                               const TcItem *meta, volatile uint32_t *ftab,
                                               uint8_t *ring, uint8_t *qs, uint64_t *bars,
@@ -422,14 +537,14 @@ __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M
 #pragma unroll
     for (int s2 = 0; s2 < NT; ++s2) uses[s2] = 0;
     const int n_items = cta_items(T);
-    const int n_early = early && n_items > 0 ? early_fills<NT, AP>(T, tc_decode<AP>(T, cta_item(T, 0), 0, meta)) : 0;
+    const int n_early = early && n_items > 0 ? early_fills<NT, AP>(T, tc_decode<AP, SK>(T, cta_item(T, 0), 0, meta)) : 0;
 #pragma unroll
     for (int s2 = 0; s2 < NT; ++s2)
         if (s2 < n_early) uses[s2] = 1;  // fill s2 went to slot s2
     f = (uint32_t)n_early;
     bool ok = true;
     for (int j = 0; j < n_items && ok; ++j) {
-        const TcItem it = tc_decode<AP>(T, cta_item(T, j), j, meta);
+        const TcItem it = tc_decode<AP, SK>(T, cta_item(T, j), j, meta);
         if (it.n_tiles == 0) continue;
         const uint32_t qb = k % QB, quse = k / QB;
         auto load_q = [&]() -> bool {
@@ -444,11 +559,10 @@ __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M
         };
         ++k;
         for (int t = 0; t < it.n_tiles && ok; ++t) {
-            const int p = it.t0 + kTcTileKeys * t;
-            const int n_valid = min(kTcTileKeys, it.cr.c_hi - p);
-            const int natoms = (n_valid + 7) >> 3;
+            const TileKeys tk = tile_keys<SK>(it, t);
+            const int natoms = tk.sa + ((tk.n + 7) >> 3);
             int a_m = natoms, a_n = natoms;
-            if constexpr (AP) append_split(P, it.cr.qp, p, n_valid, a_m, a_n);
+            if constexpr (AP) tile_split<SK>(P, it.cr.qp, tk, a_m, a_n);
             const bool worker_full = AP && a_n > a_m;  // the append worker completes a mixed atom
             for (int kv = 0; kv < 2 && ok; ++kv) {
                 if (j == 0 && 2 * t + kv < n_early) continue;  // issued ahead of the loop
@@ -503,13 +617,12 @@ __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M
                     continue;
                 }
                 if (a_m > 0)
-                    tile_copies<C::ATOM_BYTES>(P, M, kv, it.b, it.h, p,
-                                               a_m < natoms ? 8 * a_m : n_valid, dst, bar,
-                                               policy, lane);
+                    tile_copies_of<C::ATOM_BYTES, SK>(P, M, kv, it.b, it.h, tk, a_m, dst, bar,
+                                                      policy, lane);
                 if (lane == 0) {
                     for (int a = a_n; a < natoms; ++a)
                         tma_load_5d(dst + a * C::ATOM_BYTES, kv ? &M.vn_atom : &M.kn_atom, 0,
-                                    p + 8 * a - it.cr.qp, 0, it.h, it.b, bar);
+                                    atom_pos(tk, a) - it.cr.qp, 0, it.h, it.b, bar);
                     if (worker_full) {
                         // the mixed atom from the cache, on its own barrier
                         uint64_t *mb = &bars[C::B_MIX + slot];
@@ -517,7 +630,7 @@ __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M
                         mix_n ^= 1u << slot;
                         mbar_arrive_expect_tx(mb, C::ATOM_BYTES);
                         tma_load_3d_hint(dst + a_m * C::ATOM_BYTES, kv ? &M.v_atom : &M.k_atom,
-                                         0, (int)cache_row(P, it.b, it.h, p + 8 * a_m), 0, mb,
+                                         0, (int)cache_row(P, it.b, it.h, atom_pos(tk, a_m)), 0, mb,
                                          policy);
                     } else if (AP) {
                         mbar_arrive(bar);
@@ -558,7 +671,7 @@ __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M
 // (append_flush).
 // It runs in a warp of its own: lanes of the TMA warp blocked on their
 // loads would hold back the other, diverged path of that warp.
-template <class C, int D>
+template <class C, int D, bool SK = false>
 __device__ __forceinline__ void append_worker(const TcParams &T, const TcItem *meta,
                                               const volatile uint32_t *ftab, uint8_t *ring,
                                               uint64_t *bars) {
@@ -570,19 +683,18 @@ __device__ __forceinline__ void append_worker(const TcParams &T, const TcItem *m
     uint32_t f = 0, mixpar = 0;                 // fills seen; use parity of B_MIX per slot
     const int n_items = cta_items(T);
     for (int j = 0; j < n_items; ++j) {
-        const TcItem it = tc_decode<true>(T, cta_item(T, j), j, meta);
+        const TcItem it = tc_decode<true, SK>(T, cta_item(T, j), j, meta);
         if (it.n_tiles == 0) continue;
         int ap_lo, ap_hi;
         append_range(P, it.cr, it.i0, (it.row0 + it.rows - 1) / P.G, ap_lo, ap_hi);
         const long long row_b = (long long)it.b * P.q_len;  // k_new row of draft row 0
         for (int tt = 0; tt < it.n_tiles; ++tt, f += 2) {
-            const int p = it.t0 + kTcTileKeys * tt;
-            const int n_valid = min(kTcTileKeys, it.cr.c_hi - p);
+            const TileKeys tk = tile_keys<SK>(it, tt);
             int a_m, a_n;
-            append_split(P, it.cr.qp, p, n_valid, a_m, a_n);
+            tile_split<SK>(P, it.cr.qp, tk, a_m, a_n);
             if (a_n == a_m) continue;
             // the mixed atom's new rows (rows [m_lo, 8) of atom a_m), loaded early
-            const int p_m = p + 8 * a_m;
+            const int p_m = atom_pos(tk, a_m);
             const int m_lo = it.cr.qp - p_m;
             const int np = (8 - m_lo) * PR;
             uint4 w[2][MP];
@@ -686,7 +798,7 @@ struct AppendChunk {
     int b, h, lo, qp, n, first;
 };
 
-template <int D>
+template <int D, bool SK = false>
 __device__ __forceinline__ void append_flush(const TcParams &T, const TcItem *meta,
                                              uint8_t *scratch, int scratch_bytes, int nthreads) {
     const AttnParams &P = T.a;
@@ -700,7 +812,7 @@ __device__ __forceinline__ void append_flush(const TcParams &T, const TcItem *me
         const int nk = min(cap, n_items - k0);
         for (int k = tid; k < nk; k += nthreads) {
             const int j = k0 + k;
-            const TcItem it = tc_decode<true>(T, cta_item(T, j), j, meta);
+            const TcItem it = tc_decode<true, SK>(T, cta_item(T, j), j, meta);
             int lo, hi;
             append_range(P, it.cr, it.i0, (it.row0 + it.rows - 1) / P.G, lo, hi);
             const bool own = lo < hi;
@@ -751,7 +863,7 @@ __device__ __forceinline__ void append_flush(const TcParams &T, const TcItem *me
     }
 }
 
-template <int D, int N, int NT, int QB, int PB, int OB, bool AP>
+template <int D, int N, int NT, int QB, int PB, int OB, bool AP, bool SK = false>
 __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
     swa_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ TcMaps M) {
     using C = TcCfg<D, N, NT, QB, PB, OB>;
@@ -839,9 +951,9 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
     grid_dep_trigger();
     // the first item's first fills and Q rows go out before anything else,
     // one warp each; then the metadata of this CTA's first items
-    if (lane == 0) issue_early_fills<C, NT, AP>(T, M, ftab, ring, qs, bars, warp);
+    if (lane == 0) issue_early_fills<C, NT, AP, SK>(T, M, ftab, ring, qs, bars, warp);
     for (int j = tid; j < kTcMetaItems; j += NTHR)
-        if (j < cta_items(T)) meta[j] = tc_decode_global<AP>(T, cta_item(T, j));
+        if (j < cta_items(T)) meta[j] = tc_decode_global<AP, SK>(T, cta_item(T, j));
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -849,7 +961,7 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
 
     if (warp == 0) {
         // ======================================================= producer
-        tile_producer<C, NT, QB, AP>(T, M, meta, ftab, ring, qs, bars, true);
+        tile_producer<C, NT, QB, AP, SK>(T, M, meta, ftab, ring, qs, bars, true);
     } else if (warp == 1) {
         // ============================================================ MMA
         // An event loop over two cursors on the same tile sequence: S = K Q^T
@@ -870,6 +982,7 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
                 int item, j, t, n_tiles;
                 int last_keys;  // keys of the item's last tile
                 int head;       // key rows before the chunk in its first tile (paged cache)
+                int z_lo, z_hi; // (SK) key slots that hold no key in front of the last one
                 uint32_t k, g;
                 bool valid;
                 int slot;       // this cursor's fill: slot, parity (-1: not yet looked up)
@@ -888,11 +1001,16 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
             auto seek = [&](Cursor &c) {
                 for (; c.j < n_items; ++c.j) {
                     c.item = cta_item(T, c.j);
-                    const TcItem it = tc_decode<AP>(T, c.item, c.j, meta);
+                    const TcItem it = tc_decode<AP, SK>(T, c.item, c.j, meta);
                     if (it.n_tiles > 0) {
                         c.n_tiles = it.n_tiles;
                         c.last_keys = it.cr.c_hi - it.t0 - kTcTileKeys * (it.n_tiles - 1);
                         c.head = it.cr.c_lo - it.t0;
+                        if constexpr (SK) {
+                            const int end = item_end(it);
+                            c.last_keys = end - kTcTileKeys * (it.n_tiles - 1);
+                            gap_slots(P, it, c.z_lo, c.z_hi);
+                        }
                         c.t = 0;
                         c.valid = true;
                         return;
@@ -908,7 +1026,7 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
                 ++c.j;
                 seek(c);
             };
-            Cursor qc{0, 0, 0, 0, 0, 0, 0u, 0u, false, -1, 0u};
+            Cursor qc{0, 0, 0, 0, 0, 0, 0, 0, 0u, 0u, false, -1, 0u};
             seek(qc);
             Cursor pc = qc;
             bool ok = true;
@@ -952,7 +1070,17 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
-                        if (pc.t == 0 && pc.head > 0) {
+                        if constexpr (SK) {
+                            // (the fill of the last sink's atom, and the rows
+                            // before the chunk in its first window atom)
+                            const int lo = max(pc.z_lo - kTcTileKeys * pc.t, 0);
+                            const int hi = min(pc.z_hi - kTcTileKeys * pc.t, kTcTileKeys);
+                            if (lo < hi) {
+                                zero_v_rows<C>(vt, lo, hi, lane);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                        } else if (pc.t == 0 && pc.head > 0) {
                             // (paged cache) the rows before the chunk in its first
                             // tile: P is 0 there, but they may hold anything
                             const int row = lane >> 3, q = lane & 7;
@@ -1082,7 +1210,7 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
         bool ok = true;
         const int n_items = cta_items(T);
         for (int j = 0; j < n_items && ok; ++j) {
-            const TcItem it = tc_decode<AP>(T, cta_item(T, j), j, meta);
+            const TcItem it = tc_decode<AP, SK>(T, cta_item(T, j), j, meta);
             const size_t bh = (size_t)it.b * P.Hkv + it.h;
             const int my_rows = min(HN, it.rows - r0);  // rows of this group in the item
             if (it.n_tiles == 0) {
@@ -1123,19 +1251,25 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
                 const bool got = mbar_wait_bounded(&bars[C::B_SFULL + sb], suse & 1, P.fault,
                                                    kFaultCopyTimeout, P.wait_limit);
                 fence_after_sync();
-                const int j0 = it.t0 + kTcTileKeys * t;
+                const int j0 = it.t0 + kTcTileKeys * t - (SK ? it.vs() : 0);
                 const int n_valid = min(kTcTileKeys, it.cr.c_hi - j0);
                 const int jk = j0 + lk;
                 // packed rows [ra, rb) of this item whose window holds key jk:
                 // draft row i sees jk iff p_i - W < jk <= p_i, p_i = qp_i0 + i;
                 // shifted to this group's rows
                 int ra = 0, rb = 0;
-                if (lk < n_valid && jk >= it.cr.c_lo) {
+                if (SK && kTcTileKeys * t + lk < it.vs()) {
+                    // a sink before every window of the item
+                    if (kTcTileKeys * t + lk < it.sink) {
+                        ra = -r0;
+                        rb = it.rows - r0;
+                    }
+                } else if (lk < n_valid && jk >= it.cr.c_lo) {
                     const long long lo_i = (long long)jk - qp_i0;
                     const long long hi_i = (long long)jk + P.window - qp_i0;
                     const long long a = lo_i < 0 ? 0 : lo_i * P.G;
                     long long bnd = hi_i < 0 ? 0 : hi_i * P.G;
-                    if (bnd > it.rows) bnd = it.rows;
+                    if (bnd > it.rows || (SK && jk < P.sinks)) bnd = it.rows;
                     ra = (int)(a < it.rows ? a : it.rows) - r0;
                     rb = (int)bnd - r0;
                 }
@@ -1409,7 +1543,7 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
         }
     } else if constexpr (AP) {
         // ================================================= append worker
-        append_worker<C, D>(T, meta, ftab, ring, bars);
+        append_worker<C, D, SK>(T, meta, ftab, ring, bars);
     }
 
     // ---------------------------------------------------------- teardown
@@ -1418,7 +1552,7 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
     fence_after_sync();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
     if constexpr (AP) {
-        if (cta_items(T) > 2) append_flush<D>(T, meta, ring, NT * C::TILE_BYTES, NTHR);
+        if (cta_items(T) > 2) append_flush<D, SK>(T, meta, ring, NT * C::TILE_BYTES, NTHR);
     }
 }
 

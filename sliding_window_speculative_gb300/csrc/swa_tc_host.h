@@ -112,6 +112,11 @@ cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, dim3 block, size_t
 // Constants of the (head_dim, padded rows) configuration; false if none.
 bool tc_conf(int D, int N, TcConfInfo *c);
 
+// The launch of a call whose first positions stay visible (P.sinks > 0), with
+// the maps tc_launch encoded; and the CUDA-core kernel of such a call.
+cudaError_t tc_launch_sinks(const TcLaunch &L, const TcMaps &maps, cudaStream_t stream);
+cudaError_t simt_launch_sinks(const AttnParams &P, int D, int rpw, int nrg, cudaStream_t stream);
+
 // Encodes the TMA tensor maps and launches; on failure writes a message.
 cudaError_t tc_launch(const TcLaunch &L, cudaStream_t stream, char *err, size_t errlen);
 
