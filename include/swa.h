@@ -396,9 +396,9 @@ swa_status swa_greedy_accept(const void *logits, const int32_t *keep_ids, const 
  *   candidates gives column 0, logprob 0.
  * Weights are computed to 2^-44 relative and summed exactly, so results do not
  * depend on the launch; columns more than 50 T below M are left out (together
- * under 2^-41 of S up to 2^31 columns), and logits smaller in magnitude than
- * 2^-32 times the row's largest of their sign (at most |M - 50 T|) weigh like
- * 0, within 2^-26 of their weight. */
+ * under 2^-41 of S up to 2^31 columns), and of many candidates those of
+ * vanishing magnitude (below 2^-28 of the row's largest) may weigh like 0,
+ * within 2^-22 of their weight. */
 typedef struct {
     const float *temperature; /* fp32 [batch] device                           */
     const int32_t *top_k;     /* int32 [batch] device or NULL: no top-k        */
