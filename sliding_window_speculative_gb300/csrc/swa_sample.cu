@@ -13,16 +13,16 @@ using swa::api_fail;
 
 constexpr int kMaxQLen = 64;  // SPLITKV_VERIFY_MAX_Q: draft rows of a verification
 
-template <int C>
+template <int C, int NT, bool HOLD>
 cudaError_t launch(const swa::SampleParams &A, long long rows, cudaStream_t s) {
     static std::atomic<bool> attr_done[swa::kMaxDevices];
-    const cudaError_t e = swa::raise_smem_limit(swa::swa_sample_kernel<C>,
+    const cudaError_t e = swa::raise_smem_limit(swa::swa_sample_kernel<C, NT, HOLD>,
                                                 (int)sizeof(swa::SampShared), attr_done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.dynamicSmemBytes = sizeof(swa::SampShared);
     cfg.gridDim = dim3((unsigned)(rows * C));
-    cfg.blockDim = dim3(swa::kSampThreads);
+    cfg.blockDim = dim3(NT);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -34,22 +34,22 @@ cudaError_t launch(const swa::SampleParams &A, long long rows, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = swa::pdl_enabled() ? 2 : 1;
     if (swa::launch_fault_due()) return cudaErrorLaunchOutOfResources;
-    return cudaLaunchKernelEx(&cfg, swa::swa_sample_kernel<C>, A);
+    return cudaLaunchKernelEx(&cfg, swa::swa_sample_kernel<C, NT, HOLD>, A);
 }
 
 cudaError_t launch_rows(const swa::SampleParams &A, long long rows, int sms, cudaStream_t s) {
-    // one CTA per row; more share a row while SMs would idle and each still
-    // has two vectors per thread
+    // one CTA per row, four to an SM; more share a row while SMs would idle and
+    // each still has two vectors per thread
     const long long nvec = ((long long)A.V + 14) / 8;
     int c = 1;
-    while (c < swa::kSampMaxCluster && rows * c * 2 <= 2LL * sms &&
-           nvec > 2LL * c * swa::kSampThreads)
-        c *= 2;
+    while (c < swa::kSampMaxCluster && rows * c * 2 <= 2LL * sms && nvec > 1024LL * c) c *= 2;
     switch (c) {
-        case 1: return launch<1>(A, rows, s);
-        case 2: return launch<2>(A, rows, s);
-        case 4: return launch<4>(A, rows, s);
-        default: return launch<8>(A, rows, s);
+        case 1: return launch<1, 256, false>(A, rows, s);
+        case 2: return launch<2, 512, false>(A, rows, s);
+        case 4: return launch<4, 512, false>(A, rows, s);
+        default:
+            return rows * c <= sms ? launch<8, 512, true>(A, rows, s)
+                                   : launch<8, 512, false>(A, rows, s);
     }
 }
 

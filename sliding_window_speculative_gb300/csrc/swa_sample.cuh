@@ -21,11 +21,13 @@
 // read.
 //
 // Histogram: else (or when the list overflows) every CTA counts its columns by
-// value into its own histogram; the CTAs sum the histograms over the cluster
-// (each a slice of the bins, through distributed shared memory), agree on the
-// cut-offs slice by slice, and the CTA that holds the r-th column of the
-// chosen value finds it in a second look at its part.  One shared memory
-// increment per column bounds this way.
+// value into its own histogram; the CTAs weigh and sum the histograms over the
+// cluster in blocks of 32 bins (each CTA a slice of the blocks, through
+// distributed shared memory) and tell each other the blocks' sums.  From these
+// every CTA finds the cut-offs and the draw for itself, looking into a block
+// only where one falls, and the CTA that holds the r-th column of the chosen
+// value finds it in a second look at its part.  One shared memory increment
+// per column bounds this way (about six cycles per 32 of them).
 //
 // Weights and masses are integers, so sums do not depend on any order and
 // comparisons are exact: w = 2^-((max - x) log2(e) / T) in units of 2^-62 (the
@@ -33,11 +35,13 @@
 // quartic; relative error below 2^-44), masses as 128-bit sums of count * w.
 //
 // Bins: for each sign 4096 values downwards from a top magnitude, i.e. 32
-// octaves; the top is a few octaves above the first chunk's largest, and a row
-// that exceeds it is counted again.  What is smaller still shares the last bin
-// and weighs like 0 (kept columns lie within 50 T of the maximum, so that is
-// within 2^-22 of their weight), and its order is resolved by value when the
-// draw lands in it.
+// octaves.  The top of the positive values is a few octaves above the first
+// chunk's largest, and a row that exceeds it is counted again; that of the
+// negative ones is the lowest value that can weigh anything.  What is smaller
+// still shares the last bin and weighs like 0 (within 2^-22 of its weight:
+// kept columns lie within 50 T of the maximum), and its order is resolved by
+// value when the draw lands in it.  The first bin of each sign takes what does
+// not count: NaN, and everything below the line.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -46,13 +50,14 @@
 
 namespace swa {
 
-constexpr int kSampThreads = 512;
-constexpr int kSampWarps = kSampThreads / 32;
+constexpr int kSampMaxWarps = 16;
 constexpr int kSampHalf = 4096;            // bins per sign
 constexpr int kSampBins = 2 * kSampHalf;
-constexpr int kSampChunk = 8 * kSampThreads;  // 16-byte vectors of a CTA's first chunk
+constexpr int kSampVpt = 8;                // 16-byte vectors of the first chunk per thread
+constexpr int kSampBlocks = kSampBins / 32;  // of 32 bins
 constexpr int kSampList = kSampBins / 2;   // columns the list holds
-constexpr int kSampListK = kSampThreads / 2;  // largest top-k taken by list
+constexpr int kSampKeys = 512;             // maxima the top-k bound is taken from
+constexpr int kSampListK = kSampKeys / 2;  // largest top-k taken by list
 constexpr int kSampMaxCluster = 8;
 constexpr int kSampRoom = 4 << 7;          // four octaves above the first chunk's largest
 constexpr float kSampCut = 50.f;           // columns 50 T below the maximum weigh under 2^-72
@@ -98,6 +103,15 @@ __device__ __forceinline__ u128 shfl_up128(u128 x, int d) {
     const uint64_t lo = __shfl_up_sync(0xffffffffu, (uint64_t)x, d);
     const uint64_t hi = __shfl_up_sync(0xffffffffu, (uint64_t)(x >> 64), d);
     return ((u128)hi << 64) | lo;
+}
+__device__ __forceinline__ u128 sum128(u128 x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t lo = __shfl_xor_sync(0xffffffffu, (uint64_t)x, o);
+        const uint64_t hi = __shfl_xor_sync(0xffffffffu, (uint64_t)(x >> 64), o);
+        x += ((u128)hi << 64) | lo;
+    }
+    return x;
 }
 __device__ __forceinline__ u128 shfl128(u128 x, int src) {
     const uint64_t lo = __shfl_sync(0xffffffffu, (uint64_t)x, src);
@@ -177,7 +191,7 @@ __device__ __forceinline__ uint64_t samp_weight(uint64_t y, const uint64_t *tabl
 // What one row's columns are counted by.
 struct SampRow {
     float cut;     // columns below are left out (also NaN and -inf)
-    int pt, nt;    // top magnitudes (bf16 bits) of the columns >= 0 and < 0
+    int pt, nt;    // top magnitudes (bf16 bits) of the columns >= 0 and < 0, exclusive
 };
 
 // A logit as fp32, -0 as 0.
@@ -185,15 +199,29 @@ __device__ __forceinline__ float samp_value(uint32_t bits) {
     return __uint_as_float(bits << 16) + 0.f;
 }
 
-// The bin of a kept value; outside [0, kSampBins) above a top magnitude.
-__device__ __forceinline__ int samp_bin(const SampRow &r, float x) {
-    const int m = (int)(__float_as_uint(x) >> 16);
-    return m < 0x8000 ? min(r.pt - m, kSampHalf - 1)
-                      : max(kSampBins - 1 - r.nt + (m - 0x8000), kSampHalf);
+// Byte offsets into the histogram of the bins of two packed logits, by packed
+// 16-bit arithmetic: d = top - (the magnitude clamped to 4096 values below the
+// top of its sign), bin d for positive values and 8191 - d = d ^ 8191 for
+// negative ones.
+struct SampBins {
+    uint32_t pt, plo, nt, nlo;  // tops and lowest magnitudes, in both halves
+};
+__device__ __forceinline__ SampBins samp_bins(const SampRow &r) {
+    auto both = [](int x) { return (uint32_t)x * 0x10001u; };
+    return SampBins{both(r.pt), both(max(r.pt - kSampHalf + 1, 0)), both(r.nt),
+                    both(max(r.nt - kSampHalf + 1, 0))};
+}
+__device__ __forceinline__ uint32_t samp_offsets(const SampBins &b, uint32_t w) {
+    uint32_t neg, x = w & 0x7fff7fffu;
+    asm("prmt.b32 %0, %1, %1, 0xbb99;" : "=r"(neg) : "r"(w));  // sign of each half, spread
+    const uint32_t top = (b.pt & ~neg) | (b.nt & neg), low = (b.plo & ~neg) | (b.nlo & neg);
+    asm("max.u16x2 %0, %0, %1;" : "+r"(x) : "r"(low));
+    asm("min.u16x2 %0, %0, %1;" : "+r"(x) : "r"(top));
+    return ((top - x) ^ (neg & 0x1fff1fffu)) << 2;
 }
 
-// Largest magnitude a bin's columns can have: their only one, but in the two
-// shared bins.
+// The magnitude a bin stands for: its only one, but in the two shared bins
+// their largest.
 __device__ __forceinline__ int samp_bin_mk(const SampRow &r, int bin) {
     return max(0, bin < kSampHalf ? r.pt - bin : r.nt - (kSampBins - 1 - bin));
 }
@@ -202,56 +230,59 @@ __device__ __forceinline__ bool samp_shared_bin(int bin) {
     return bin == kSampHalf - 1 || bin == kSampHalf;
 }
 
-// A list entry: larger is earlier in the row's order (value, then column).
-__device__ __forceinline__ uint64_t samp_entry(float x, uint32_t column) {
+// A value's place in the order, larger first (its bits, made monotone).
+__device__ __forceinline__ uint32_t samp_key(float x) {
     const uint32_t u = __float_as_uint(x) >> 16;
-    const uint32_t key = u & 0x8000u ? 0xffffu - u : u | 0x8000u;
-    return ((uint64_t)key << 32) | (0xffffffffu - column);
+    return u & 0x8000u ? 0xffffu - u : u | 0x8000u;
 }
 
-// Shared memory of a CTA.  The members marked * are written by other CTAs of
-// the cluster, each between two cluster barriers that separate it from its
-// reads.
+// A list entry: larger is earlier in the row's order (value, then column).
+__device__ __forceinline__ uint64_t samp_entry(float x, uint32_t column) {
+    return ((uint64_t)samp_key(x) << 32) | (0xffffffffu - column);
+}
+
+// Shared memory of a CTA.  The members marked * are written by the CTAs of the
+// cluster, each between two cluster barriers that separate it from its reads.
 struct SampShared {
     union {
         uint32_t hist[kSampBins];
-        uint64_t list[kSampList];                        // * (first CTA)
+        uint64_t list[kSampList];                        // * (first CTA's)
     };
-    uint32_t merged[kSampBins / 2];                      // this CTA's slice (C > 1)
     uint64_t table[256];
-    float max_[kSampMaxCluster], min_[kSampMaxCluster];  // *
-    uint32_t bound[kSampMaxCluster];                     // * float bits
-    uint32_t list_n;                                     // * (first CTA)
-    float max2[2][kSampMaxCluster], min2[2][kSampMaxCluster];  // *
-    uint32_t cnt[kSampMaxCluster], cnt_mp[kSampMaxCluster];  // *
-    uint64_t mass[kSampMaxCluster][2];                   // *
-    uint64_t cut_mass[3][2];                             // * after top-k, min-p, top-p
-    uint32_t bin, rank;                                  // *
-    float lp;                                            // *
-    uint32_t refine[17][kSampMaxCluster];                // *
-    float red[2][kSampWarps];
-    uint32_t wcnt[kSampWarps], wmp[kSampWarps];
-    uint64_t wmass[kSampWarps][2];
-    uint32_t found[2][kSampWarps];
+    uint32_t blk_cnt[kSampBlocks], blk_mp[kSampBlocks];  // *
+    uint64_t blk_mass[kSampBlocks][2];                   // *
+    float max_[kSampMaxCluster];                         // *
+    uint32_t bound[2][kSampMaxCluster];                  // * float bits
+    uint32_t list_n[kSampMaxCluster];                    // *
+    float max2[2][kSampMaxCluster];                      // *
+    uint32_t refine[18][kSampMaxCluster];                // *
+    float red[kSampMaxWarps];
+    uint32_t wcnt[kSampMaxWarps], wmp[kSampMaxWarps];
+    uint64_t wmass[kSampMaxWarps][2];
+    uint64_t cut_mass[3][2];                             // after top-k, min-p, top-p
+    uint32_t found[2][kSampMaxWarps];
+    uint32_t keys[kSampKeys];
     uint64_t cut64;
+    uint32_t listed, bin, rank;
+    float lp;
     SampScale scale;
 };
 
-// The largest and smallest of eight bf16 logits (NaN left out), folded in.
-__device__ __forceinline__ void samp_minmax(const uint4 &w, __nv_bfloat162 &hi, __nv_bfloat162 &lo) {
+// The largest of eight bf16 logits (NaN left out), folded into both halves of hi.
+__device__ __forceinline__ void samp_max(const uint4 &w, __nv_bfloat162 &hi) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&u[e]);
-        hi = __hmax2(hi, x);  // (the other operand of a NaN)
-        lo = __hmin2(lo, x);
-    }
+    for (int e = 0; e < 4; ++e)  // (the other operand of a NaN)
+        hi = __hmax2(hi, *reinterpret_cast<const __nv_bfloat162 *>(&u[e]));
 }
 
-template <int C>
-__global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const SampleParams A) {
+// C CTAs of NT threads per row; HOLD: the first chunk stays in registers.
+template <int C, int NT, bool HOLD>
+__global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(const SampleParams A) {
     namespace cg = cooperative_groups;
-    constexpr int BPT = kSampBins / (C * kSampThreads);  // bins a thread sums over the cluster
+    constexpr int kWarps = NT / 32;
+    constexpr int kChunk = kSampVpt * NT;      // vectors of the first chunk
+    constexpr uint32_t kPart = kSampList / C;  // list entries of one CTA
     const float INF = __int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     SampShared &sh = *reinterpret_cast<SampShared *>(smem_raw);
@@ -276,17 +307,12 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
     auto cluster_wait = [&]() {
         if constexpr (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     };
-    // one thread's value to every CTA of the cluster
-    auto publish = [&](auto *slot, auto value) {
-#pragma unroll
-        for (int r = 0; r < C; ++r) *at(slot, r) = value;
-    };
     if (tid < 256) sh.table[tid] = kSampTable.v[tid];
     if (tid == 0) {
-        sh.list_n = sh.bin = sh.rank = 0;
+        sh.listed = sh.bin = sh.rank = 0;
         sh.lp = 0.f;
     }
-    for (int i = tid; i < kSampBins / 4; i += kSampThreads)
+    for (int i = tid; i < kSampBins / 4; i += NT)
         reinterpret_cast<uint4 *>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
     cluster_arrive();  // (every CTA runs before another writes to its shared memory)
 
@@ -315,15 +341,24 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
         }
         return make_uint4(h[0], h[1], h[2], h[3]);
     };
+    uint4 held[HOLD ? kSampVpt : 1];
+    if constexpr (HOLD) {
+#pragma unroll
+        for (int v = 0; v < kSampVpt; ++v) held[v] = load(g0 + tid + v * NT);
+    }
     // f(vector number, vector) over this thread's vectors of [g0, end), four
     // loads at a time; every thread of the CTA takes the same number of steps
     auto each = [&](int end, auto f) {
-        for (int g = g0 + tid; g - tid < end; g += 4 * kSampThreads) {
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int v = 0; v < kSampVpt; ++v) f(g0 + tid + v * NT, held[v]);
+        }
+        for (int g = g0 + tid + (HOLD ? kChunk : 0); g - tid < end; g += 4 * NT) {
             uint4 w[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) w[v] = load(g + v * kSampThreads);
+            for (int v = 0; v < 4; ++v) w[v] = load(g + v * NT);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) f(g + v * kSampThreads, w[v]);
+            for (int v = 0; v < 4; ++v) f(g + v * NT, w[v]);
         }
     };
 
@@ -344,71 +379,91 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
     float u = A.uniforms[row];
     if (!(u > 0.f)) u = 0.f;
     if (u >= 1.f) u = 0.99999994f;
-    if (tid == kSampThreads - 1) sh.scale = samp_scale(T);
+    if (tid == NT - 1) sh.scale = samp_scale(T);
     auto finish = [&](long long column, float lp) {
         A.tokens[row] = A.keep != nullptr ? A.keep[column] : (int32_t)column;
         if (A.logprobs != nullptr) A.logprobs[row] = lp;
         if (A.q_len == 1) A.accepted[b] = 0;
     };
 
-    // ---- the largest and smallest logit of the first chunk
-    const bool rest = cv > kSampChunk;  // there are columns behind it
-    float mx, mn;
+    // ---- the largest logit of the first chunk
+    const bool rest = cv > kChunk;  // there are columns behind it
+    float mx = -INF;
     {
-        __nv_bfloat162 hi2 = __floats2bfloat162_rn(-INF, -INF), lo2 = __floats2bfloat162_rn(INF, INF);
-        each(min(g1, g0 + kSampChunk), [&](int, const uint4 &w) { samp_minmax(w, hi2, lo2); });
-        mx = fmaxf(__low2float(hi2), __high2float(hi2));
-        mn = fminf(__low2float(lo2), __high2float(lo2));
-    }
-    const float own_max = mx;  // this thread's
-    auto block_minmax = [&](float &hi, float &lo) {  // in warp 0 afterwards
+        // (a thread's maxima of several parts of the chunk, as many as there
+        // are keys)
+        constexpr int kParts = kSampKeys / NT;
+        static_assert(kParts == 1 || kParts == 2, "one or two maxima per thread");
+        const __nv_bfloat162 none = __floats2bfloat162_rn(-INF, -INF);
+        __nv_bfloat162 hi2[kParts];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        for (int i = 0; i < kParts; ++i) hi2[i] = none;
+        each(min(g1, g0 + kChunk), [&](int g, const uint4 &w) {
+            if constexpr (kParts == 1) {
+                samp_max(w, hi2[0]);
+            } else {
+                __nv_bfloat162 x = none;
+                samp_max(w, x);
+                const bool second = g - g0 >= kChunk / 2;
+                hi2[0] = __hmax2(hi2[0], second ? none : x);
+                hi2[kParts - 1] = __hmax2(hi2[kParts - 1], second ? x : none);
+            }
+        });
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const float x = fmaxf(__low2float(hi2[i]), __high2float(hi2[i]));
+            sh.keys[i * NT + tid] = samp_key(x);
+            mx = fmaxf(mx, x);
         }
-        if (lane == 0) {
-            sh.red[0][warp] = hi;
-            sh.red[1][warp] = lo;
-        }
+    }
+    auto block_max = [&](float hi) {  // in warp 0 afterwards
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        if (lane == 0) sh.red[warp] = hi;
         __syncthreads();
         if (warp == 0) {
-            hi = lane < kSampWarps ? sh.red[0][lane] : -INF;
-            lo = lane < kSampWarps ? sh.red[1][lane] : INF;
+            hi = sh.red[lane % kWarps];
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
+            for (int o = kWarps / 2; o > 0; o >>= 1)
                 hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            }
         }
+        return hi;
     };
-    // top-k: of the threads' maxima the k-th largest is a bound that at least
-    // k of this CTA's columns reach; bisected on ordered 16-bit keys
-    float bound = -INF;
-    if (k <= kSampListK) {
-        const uint32_t key = (uint32_t)(samp_entry(own_max, 0) >> 32);
-        uint32_t lo = 0;
-        for (uint32_t bit = 0x8000u; bit > 0; bit >>= 1)
-            if (__syncthreads_count(key >= (lo | bit)) >= (int)k) lo |= bit;
-        bound = __uint_as_float((lo & 0x8000u ? lo & 0x7fffu : 0xffffu - lo) << 16);
-        if (!(bound > -INF)) bound = -INF;
-    }
-    block_minmax(mx, mn);
+    mx = block_max(mx);
     cluster_wait();
-    if (tid < C) {
-        *at(&sh.max_[rank], tid) = mx;
-        *at(&sh.min_[rank], tid) = mn;
-        *at(&sh.bound[rank], tid) = __float_as_uint(bound);
+    if (tid < C) *at(&sh.max_[rank], tid) = mx;
+    // top-k: of the chunk's part maxima the k-th largest is a bound that at
+    // least k of this CTA's columns reach, and where every CTA has a k/C-th
+    // largest, k of the cluster's reach the smallest of those; a warp for each
+    // bisects 16-bit keys
+    if (warp == 1 || (C > 1 && warp == 2)) {
+        float x = -INF;
+        if (k <= kSampListK) {
+            const int n = warp == 1 ? (int)k : (int)((k + C - 1) / C);
+            uint32_t key[kSampKeys / 32], lo = 0;
+#pragma unroll
+            for (int i = 0; i < kSampKeys / 32; ++i) key[i] = sh.keys[i * 32 + lane];
+            for (uint32_t bit = 0x8000u; bit > 0; bit >>= 1) {
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < kSampKeys / 32; ++i) c += key[i] >= (lo | bit);
+                if (__reduce_add_sync(0xffffffffu, c) >= n) lo |= bit;
+            }
+            x = __uint_as_float((lo & 0x8000u ? lo & 0x7fffu : 0xffffu - lo) << 16);
+            if (!(x > -INF)) x = -INF;
+        }
+        if (lane < C) *at(&sh.bound[warp - 1][rank], lane) = __float_as_uint(x);
     }
     cluster_sync();
+    float bound = -INF, share = INF;
     mx = -INF;
-    mn = INF;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
         mx = fmaxf(mx, sh.max_[r]);
-        mn = fminf(mn, sh.min_[r]);
-        bound = fmaxf(bound, __uint_as_float(sh.bound[r]));
+        bound = fmaxf(bound, __uint_as_float(sh.bound[0][r]));
+        if (C > 1) share = fminf(share, __uint_as_float(sh.bound[1][r]));
     }
+    if (C > 1) bound = fmaxf(bound, share);
     if (mx == -INF && !rest) {
         // nothing to choose from: column 0
         if (rank == 0 && tid == 0) finish(0, 0.f);
@@ -443,79 +498,122 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
     if (mx > -INF && (bound > -INF || (mp > 0.f && !has_p))) {
         // ================================================= by list
         each(g1, [&](int g, const uint4 &w) {
-            __nv_bfloat162 hi2 = __floats2bfloat162_rn(-INF, -INF), lo2 = hi2;
-            samp_minmax(w, hi2, lo2);
+            __nv_bfloat162 hi2 = __floats2bfloat162_rn(-INF, -INF);
+            samp_max(w, hi2);
             if (!(fmaxf(__low2float(hi2), __high2float(hi2)) >= R.cut)) return;
             const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float x = samp_value(e & 1 ? h[e >> 1] >> 16 : h[e >> 1] & 0xffffu);
                 if (x >= R.cut) {
-                    const uint32_t n = atomicAdd(at(&sh.list_n, 0), 1u);
-                    if (n < kSampList)
-                        *at(&sh.list[n], 0) = samp_entry(x, (uint32_t)(8LL * g - off + e));
+                    const uint32_t n = atomicAdd(&sh.listed, 1u);
+                    if (n < kPart)
+                        *at(&sh.list[rank * kPart + n], 0) =
+                            samp_entry(x, (uint32_t)(8LL * g - off + e));
                 }
             }
         });
+        __syncthreads();
+        if (tid < C) *at(&sh.list_n[rank], tid) = sh.listed;
         cluster_sync();
-        uint32_t n = *at(&sh.list_n, 0);
-        if (n <= kSampList) {
-            // (the first CTA stays until every CTA has read the count)
-            cluster_arrive();
-            if (rank != 0) return;
-            if (n > 160 && k < (long long)n) {
-                // more than top-k's: those that reach the k-th largest value
-                uint32_t lo = 0;
-                for (uint32_t bit = 0x8000u; bit > 0; bit >>= 1) {
-                    int c = 0;
-                    for (uint32_t i = tid; i < n; i += kSampThreads)
-                        c += (uint32_t)(sh.list[i] >> 32) >= (lo | bit);
-                    c = __reduce_add_sync(0xffffffffu, c);
-                    __syncthreads();
-                    if (lane == 0) sh.wcnt[warp] = c;
-                    __syncthreads();
-                    uint32_t all = 0;
+        uint32_t n = 0;
+        bool fits = true;
 #pragma unroll
-                    for (int w = 0; w < kSampWarps; ++w) all += sh.wcnt[w];
-                    if (all >= (uint32_t)k) lo |= bit;
+        for (int r = 0; r < C; ++r) {
+            n += sh.list_n[r];
+            fits = fits && sh.list_n[r] <= kPart;
+        }
+        if (fits) {
+            if (rank != 0) return;
+            if constexpr (C > 1) {
+                // the CTAs' parts moved together
+                uint64_t mine[kSampList / NT];
+#pragma unroll
+                for (int i = 0; i < kSampList / NT; ++i) {
+                    uint32_t from = tid + i * NT, part = 0;
+#pragma unroll
+                    for (int r = 0; r < C - 1; ++r)
+                        if (part == (uint32_t)r && from >= sh.list_n[r]) {
+                            from -= sh.list_n[r];
+                            ++part;
+                        }
+                    mine[i] = tid + i * NT < n ? sh.list[part * kPart + from] : 0;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kSampList / NT; ++i)
+                    if (tid + i * NT < n) sh.list[tid + i * NT] = mine[i];
+                __syncthreads();
+            }
+            if (n > 160 && k < (long long)n) {
+                // more than top-k's: those that reach the k-th largest value, found
+                // by counting the keys' upper, then their lower bytes
+                uint32_t lo = 0, left = (uint32_t)k;  // left: still to find
+                for (int half = 1; half >= 0; --half) {
+                    if (tid < 256) sh.blk_cnt[tid] = 0;
+                    __syncthreads();
+                    for (uint32_t i = tid; i < n; i += NT) {
+                        const uint32_t key = (uint32_t)(sh.list[i] >> 32);
+                        if (half == 1 || (key >> 8) == (lo >> 8))
+                            atomicAdd(&sh.blk_cnt[half == 1 ? key >> 8 : key & 255u], 1u);
+                    }
+                    __syncthreads();
+                    // thread t: digit 255 - t, and the larger ones
+                    const uint32_t c = tid < 256 ? sh.blk_cnt[255 - tid] : 0;
+                    uint32_t upto = c;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += x;
+                    }
+                    if (lane == 31) sh.wcnt[warp] = upto;
+                    __syncthreads();
+                    for (int w = 0; w < warp; ++w) upto += sh.wcnt[w];
+                    if (tid < 256 && upto - c < left && left <= upto) {
+                        sh.found[0][0] = 255 - tid;
+                        sh.found[0][1] = left - (upto - c);
+                    }
+                    __syncthreads();
+                    lo |= sh.found[0][0] << (8 * half);
+                    left = sh.found[0][1];
                 }
                 // (each thread's entries first, then all of them packed anew)
-                uint64_t mine[kSampList / kSampThreads];
+                uint64_t mine[kSampList / NT];
                 int c = 0;
 #pragma unroll
-                for (int i = 0; i < kSampList / kSampThreads; ++i) {
-                    const uint32_t at_i = tid + i * kSampThreads;
+                for (int i = 0; i < kSampList / NT; ++i) {
+                    const uint32_t at_i = tid + i * NT;
                     mine[i] = at_i < n ? sh.list[at_i] : 0;
                     if ((uint32_t)(mine[i] >> 32) < lo) mine[i] = 0;
                     c += mine[i] != 0;
                 }
+                if (tid == 0) sh.listed = 0;
                 __syncthreads();
-                if (tid == 0) sh.list_n = 0;
-                __syncthreads();
-                uint32_t to = c > 0 ? atomicAdd(&sh.list_n, (uint32_t)c) : 0;
+                uint32_t to = c > 0 ? atomicAdd(&sh.listed, (uint32_t)c) : 0;
 #pragma unroll
-                for (int i = 0; i < kSampList / kSampThreads; ++i)
+                for (int i = 0; i < kSampList / NT; ++i)
                     if (mine[i] != 0) sh.list[to++] = mine[i];
                 __syncthreads();
-                n = sh.list_n;
+                n = sh.listed;
             }
-            if (n <= kSampThreads) {
+            if (n <= NT) {
                 // every entry's place is the number of larger ones
                 const uint64_t e = (uint32_t)tid < n ? sh.list[tid] : 0;
                 uint32_t place = 0;
                 if ((uint32_t)(tid & ~31) < n)
+    #pragma unroll 4
                     for (uint32_t i = 0; i < n; ++i) place += sh.list[i] > e;
                 __syncthreads();
                 if ((uint32_t)tid < n) sh.list[place] = e;
             } else {
                 // many equal values: a bitonic network over the list
-                uint32_t size = kSampThreads;
+                uint32_t size = NT;
                 while (size < n) size *= 2;
-                for (uint32_t i = n + tid; i < size; i += kSampThreads) sh.list[i] = 0;
+                for (uint32_t i = n + tid; i < size; i += NT) sh.list[i] = 0;
                 __syncthreads();
                 for (uint32_t span = 2; span <= size; span *= 2)
                     for (uint32_t d = span / 2; d > 0; d /= 2) {
-                        for (uint32_t i = tid; i < size / 2; i += kSampThreads) {
+                        for (uint32_t i = tid; i < size / 2; i += NT) {
                             const uint32_t x = 2 * i - (i & (d - 1)), y = x + d;
                             const uint64_t p = sh.list[x], q = sh.list[y];
                             if ((p < q) == ((x & span) == 0)) {
@@ -530,7 +628,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
             // ---- in order: weights in units of 2^-50, running sums; eight
             // consecutive places per thread where there are many
             const uint32_t kept = k < (long long)n ? (uint32_t)k : n;
-            const int per = kept <= kSampThreads ? 1 : kSampList / kSampThreads;
+            const int per = kept <= NT ? 1 : kSampList / NT;
             auto value_of = [&](uint64_t e) {
                 const uint32_t key = (uint32_t)(e >> 32);
                 return __uint_as_float((key & 0x8000u ? key & 0x7fffu : 0xffffu - key) << 16);
@@ -556,7 +654,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
             pre -= sum;
             uint64_t S = 0;
 #pragma unroll
-            for (int w = 0; w < kSampWarps; ++w) {
+            for (int w = 0; w < kWarps; ++w) {
                 if (w < warp) pre += sh.wmass[w][0];
                 S += sh.wmass[w][0];
             }
@@ -592,117 +690,92 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
                     m += w;
                 }
             }
-            cluster_wait();
             return;
         }
         // too many: count them (the first CTA's list gives way to its histogram)
-        cluster_sync();
-        for (int i = tid; i < kSampBins / 4; i += kSampThreads)
+        for (int i = tid; i < kSampBins / 4; i += NT)
             reinterpret_cast<uint4 *>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
 
     // ===================================================== by histogram
-    {
-        const float top = mx > 0.f ? mx : 0.f;
-        R.pt = top == INF ? 0x7f80
-                          : min((int)(__float_as_uint(fmaxf(top, T)) >> 16) + kSampRoom, 0x7f7f);
-        const float low = fminf(fabsf(fminf(mn, 0.f)), 3.4028234e38f);
-        R.nt = min((int)(__float_as_uint(fmaxf(low, T)) >> 16) + kSampRoom,
-                   (int)(__float_as_uint(fabsf(fminf(fmaxf(R.cut, -3.4028234e38f), 0.f))) >> 16));
-    }
+    auto top_key = [](float x) { return (int)(__float_as_uint(fmaxf(x, 0.f)) >> 16); };
+    // (never so low that 0 and -0 fall outside the shared bins)
+    auto at_least = [](int top) { return max(top, kSampHalf); };
+    R.pt = at_least(min(top_key(fmaxf(mx, T)) + kSampRoom, 0x7f81));
     float full_max;
     for (int round = 0;; ++round) {
-        // count; a column above its top magnitude shows in the largest logit or
-        // the lowest kept one
+        R.nt = at_least(top_key(-fmaxf(R.cut, -3.4028234e38f)) + 1);
+        const SampBins bins = samp_bins(R);
         __nv_bfloat162 hi2 = __floats2bfloat162_rn(-INF, -INF);
-        float lowest = 0.f;
         each(g1, [&](int, const uint4 &w) {
+            samp_max(w, hi2);
             const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                hi2 = __hmax2(hi2, *reinterpret_cast<const __nv_bfloat162 *>(&h[e]));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = samp_value(e & 1 ? h[e >> 1] >> 16 : h[e >> 1] & 0xffffu);
-                if (x >= R.cut) {
-                    const int bin = samp_bin(R, x);
-                    if ((unsigned)bin < (unsigned)kSampBins)
-                        atomicAdd(&sh.hist[bin], 1u);
-                    else
-                        lowest = fminf(lowest, x);  // (the positive ones leave it 0)
-                }
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t o = samp_offsets(bins, h[e]);
+                uint8_t *base = reinterpret_cast<uint8_t *>(sh.hist);
+                atomicAdd(reinterpret_cast<uint32_t *>(base + (o & 0xffffu)), 1u);
+                atomicAdd(reinterpret_cast<uint32_t *>(base + (o >> 16)), 1u);
             }
         });
-        float hi = fmaxf(__low2float(hi2), __high2float(hi2));
-        block_minmax(hi, lowest);
-        if (tid < C) {
-            *at(&sh.max2[round & 1][rank], tid) = hi;
-            *at(&sh.min2[round & 1][rank], tid) = lowest;
-        }
+        const float hi = block_max(fmaxf(__low2float(hi2), __high2float(hi2)));
+        if (tid < C) *at(&sh.max2[round][rank], tid) = hi;
         cluster_sync();
         full_max = -INF;
-        lowest = 0.f;
 #pragma unroll
-        for (int r = 0; r < C; ++r) {
-            full_max = fmaxf(full_max, sh.max2[round & 1][r]);
-            lowest = fminf(lowest, sh.min2[round & 1][r]);
-        }
-        const bool over = lowest < 0.f || (full_max > 0.f &&
-                                           (int)(__float_as_uint(full_max) >> 16) > R.pt);
-        if (!over || round > 0) break;
-        // a column above its top magnitude: once more, with tops that hold all
-        mx = full_max;
-        R.cut = cut_of(mx);
-        R.pt = mx > 0.f ? (int)(__float_as_uint(mx) >> 16) : 0;
-        R.nt = (int)(__float_as_uint(fabsf(fminf(fmaxf(R.cut, -3.4028234e38f), 0.f))) >> 16);
+        for (int r = 0; r < C; ++r) full_max = fmaxf(full_max, sh.max2[round][r]);
+        if (round > 0 || top_key(full_max) < R.pt) break;
+        // a column above the top: once more, from the row's own maximum
+        R.cut = cut_of(full_max);
+        R.pt = at_least(top_key(full_max) + 1);
         cluster_sync();
-        for (int i = tid; i < kSampBins / 4; i += kSampThreads)
+        for (int i = tid; i < kSampBins / 4; i += NT)
             reinterpret_cast<uint4 *>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
     const uint64_t ymax = falling_of(full_max + 0.f);
     const float cut = fmaxf(R.cut, cut_of(full_max));  // (the row's own, now)
 
-    // ---- sum this CTA's slice of the bins over the cluster; weights
-    const int bin0 = rank * (kSampBins / C) + tid * BPT;
-    uint32_t *slice = C > 1 ? sh.merged + tid * BPT : sh.hist + tid * BPT;
-    if constexpr (C > 1) {
-        uint32_t cnt[BPT];
-#pragma unroll
-        for (int i = 0; i < BPT; ++i) cnt[i] = 0;
-#pragma unroll
-        for (int r = 0; r < C; ++r) {
-            const uint32_t *h = at(sh.hist, r) + bin0;
-#pragma unroll
-            for (int i = 0; i < BPT; i += 2) {
-                const uint2 x = *reinterpret_cast<const uint2 *>(h + i);
-                cnt[i] += x.x;
-                cnt[i + 1] += x.y;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < BPT; ++i) slice[i] = cnt[i];
-    }
+    // ---- this CTA's slice of the blocks: counts over the cluster, weights
     auto bin_weight = [&](int bin) {
         const int mk = samp_shared_bin(bin) ? 0 : samp_bin_mk(R, bin);
         const float x = __uint_as_float((uint32_t)mk << 16);
-        if (!((bin >= kSampHalf ? -x : x) >= cut)) return (uint64_t)0;
+        if (bin == 0 || bin == kSampBins - 1 || !((bin >= kSampHalf ? -x : x) >= cut))
+            return (uint64_t)0;
         return samp_weight(falling(bin >= kSampHalf, mk) - ymax, sh.table);
+    };
+    auto bin_count = [&](int bin) {
+        uint32_t c = 0;
+        if (bin == 0) return c;  // no columns
+#pragma unroll
+        for (int r = 0; r < C; ++r) c += at(sh.hist, r)[bin];
+        return c;
     };
     // min-p as a weight
     const uint64_t mp_w = (uint64_t)scale_down((u128)1 << 63, 0.5f * mp, true);
-    uint32_t c_sum = 0, c_mp = 0;
-    u128 m_sum = 0;
-    for (int i = 0; i < BPT; ++i) {
-        const uint32_t c = slice[i];
-        if (c == 0) continue;
-        const uint64_t w = bin_weight(bin0 + i);
-        c_sum += c;
-        if (w >= mp_w) c_mp += c;
-        m_sum += (u128)w * c;
+    for (int i = warp; i < kSampBlocks / C; i += kWarps) {
+        const int blk = rank * (kSampBlocks / C) + i, bin = blk * 32 + lane;
+        uint32_t c = bin_count(bin), c_mp = 0;
+        u128 m = 0;
+        if (__any_sync(0xffffffffu, c > 0)) {
+            const uint64_t w = c > 0 ? bin_weight(bin) : 0;
+            c_mp = __reduce_add_sync(0xffffffffu, w >= mp_w ? c : 0);
+            m = sum128((u128)w * c);
+            c = __reduce_add_sync(0xffffffffu, c);
+        }
+        if (lane < C) {
+            *at(&sh.blk_cnt[blk], lane) = c;
+            *at(&sh.blk_mp[blk], lane) = c_mp;
+            *at(&sh.blk_mass[blk][0], lane) = (uint64_t)m;
+            *at(&sh.blk_mass[blk][1], lane) = (uint64_t)(m >> 64);
+        }
     }
-    // exclusive prefix (count, mass) over the CTA's threads, then the cluster
+    cluster_sync();
+    // ---- one thread per block: its sums, and those of the blocks before it
+    const bool holds = tid < kSampBlocks;
+    const uint32_t c_sum = holds ? sh.blk_cnt[tid] : 0;
+    const u128 m_sum = holds ? ((u128)sh.blk_mass[tid][1] << 64) | sh.blk_mass[tid][0] : 0;
     uint32_t c_pre = c_sum;
     u128 m_pre = m_sum;
 #pragma unroll
@@ -714,10 +787,10 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
             m_pre += m;
         }
     }
-    c_mp = __reduce_add_sync(0xffffffffu, c_mp);
+    const uint32_t w_mp = __reduce_add_sync(0xffffffffu, holds ? sh.blk_mp[tid] : 0);
     if (lane == 31) {
         sh.wcnt[warp] = c_pre;
-        sh.wmp[warp] = c_mp;
+        sh.wmp[warp] = w_mp;
         sh.wmass[warp][0] = (uint64_t)m_pre;
         sh.wmass[warp][1] = (uint64_t)(m_pre >> 64);
     }
@@ -727,7 +800,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
     uint32_t n_all = 0, n_mp = 0;
     u128 S = 0;
 #pragma unroll
-    for (int w = 0; w < kSampWarps; ++w) {
+    for (int w = 0; w < kSampBlocks / 32; ++w) {
         const u128 m = ((u128)sh.wmass[w][1] << 64) | sh.wmass[w][0];
         if (w < warp) {
             c_pre += sh.wcnt[w];
@@ -737,47 +810,24 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
         n_mp += sh.wmp[w];
         S += m;
     }
-    if constexpr (C > 1) {
-        if (tid < C) {
-            *at(&sh.cnt[rank], tid) = n_all;
-            *at(&sh.cnt_mp[rank], tid) = n_mp;
-            *at(&sh.mass[rank][0], tid) = (uint64_t)S;
-            *at(&sh.mass[rank][1], tid) = (uint64_t)(S >> 64);
-        }
-        cluster_sync();
-        n_all = n_mp = 0;
-        S = 0;
-#pragma unroll
-        for (int r = 0; r < C; ++r) {
-            const u128 m = ((u128)sh.mass[r][1] << 64) | sh.mass[r][0];
-            if (r < rank) {
-                c_pre += sh.cnt[r];
-                m_pre += m;
-            }
-            n_all += sh.cnt[r];
-            n_mp += sh.cnt_mp[r];
-            S += m;
-        }
-    }
-    if (n_all == 0) {
+    if (full_max == -INF) {
         if (rank == 0 && tid == 0) finish(0, 0.f);
-        if constexpr (C > 1) cluster_sync();
         return;
     }
-    // f(bin, count, weight, columns before, mass before) for the bins of the
-    // one thread of the cluster that `mine` names, a lane per bin
+    // f(bin, count, weight, columns before, mass before), a lane per bin, for
+    // the block of the one thread that `mine` names
     auto expand = [&](bool mine, auto f) {
-        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        const uint32_t who = __ballot_sync(0xffffffffu, holds && mine);
         if (who == 0) return;
         const int src = __ffs(who) - 1;
-        const int bin = __shfl_sync(0xffffffffu, bin0, src) + lane;
-        const uint32_t c = lane < BPT ? (slice - (lane - src) * BPT)[lane] : 0;
+        const int bin = 32 * (tid - lane + src) + lane;
+        const uint32_t c = bin_count(bin);
         const uint64_t w = c > 0 ? bin_weight(bin) : 0;
         const u128 m = (u128)w * c;
         uint32_t cp = c;
         u128 mpre = m;
 #pragma unroll
-        for (int o = 1; o < BPT; o <<= 1) {
+        for (int o = 1; o < 32; o <<= 1) {
             const uint32_t x = __shfl_up_sync(0xffffffffu, cp, o);
             const u128 y = shfl_up128(mpre, o);
             if (lane >= o) {
@@ -789,16 +839,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
         mpre += shfl128(m_pre, src) - m;
         if (c > 0) f(bin, c, w, cp, mpre);
     };
-    auto publish_cut = [&](int slot, u128 s) {
-        publish(&sh.cut_mass[slot][0], (uint64_t)s);
-        publish(&sh.cut_mass[slot][1], (uint64_t)(s >> 64));
+    auto put_cut = [&](int slot, u128 s) {
+        sh.cut_mass[slot][0] = (uint64_t)s;
+        sh.cut_mass[slot][1] = (uint64_t)(s >> 64);
     };
     auto cut_mass = [&](int slot) { return ((u128)sh.cut_mass[slot][1] << 64) | sh.cut_mass[slot][0]; };
     // the mass of the first n columns
     auto mass_of = [&](uint32_t n, int slot) {
         expand(c_pre < n && n <= c_pre + c_sum,
                [&](int, uint32_t c, uint64_t w, uint32_t c0, u128 m0) {
-                   if (c0 < n && n <= c0 + c) publish_cut(slot, m0 + (u128)w * (n - c0));
+                   if (c0 < n && n <= c0 + c) put_cut(slot, m0 + (u128)w * (n - c0));
                });
     };
     const uint32_t n_k = k < (long long)n_all ? (uint32_t)k : n_all;
@@ -806,7 +856,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
     if (n_k < n_all || n_mp < n_all) {
         mass_of(n_k, 0);
         mass_of(n_mp, 1);
-        cluster_sync();
+        __syncthreads();
         S = cut_mass(0);
     }
     if (has_p) {
@@ -816,9 +866,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
         expand(m_pre < X && X <= m_pre + m_sum,
                [&](int, uint32_t c, uint64_t w, uint32_t, u128 m0) {
                    if (m0 < X && X <= m0 + (u128)w * c)
-                       publish_cut(2, m0 + (u128)w * (small_quotient(X - m0 - 1, w) + 1));
+                       put_cut(2, m0 + (u128)w * (small_quotient(X - m0 - 1, w) + 1));
                });
-        cluster_sync();
+        __syncthreads();
         const u128 s = cut_mass(2);
         if (s < S) S = s;
     }
@@ -831,40 +881,36 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
     expand(m_pre <= target && target < m_pre + m_sum,
            [&](int bin, uint32_t c, uint64_t w, uint32_t, u128 m0) {
                if (m0 <= target && target < m0 + (u128)w * c) {
-                   publish(&sh.bin, (uint32_t)bin);
-                   publish(&sh.rank, small_quotient(target - m0, w));
+                   sh.bin = (uint32_t)bin;
+                   sh.rank = small_quotient(target - m0, w);
                    // ln(w / S), by the rest's share where w is most of S
                    const float sf = to_float(S);
-                   publish(&sh.lp, 2 * (u128)w > S ? log1pf(-(to_float(S - w) / sf))
-                                                   : logf(__ull2float_rn(w) / sf));
+                   sh.lp = 2 * (u128)w > S ? log1pf(-(to_float(S - w) / sf))
+                                           : logf(__ull2float_rn(w) / sf);
                }
            });
-    cluster_sync();
+    __syncthreads();
     const int bin = (int)sh.bin;
     uint32_t r = sh.rank;
 
     // ---- its place: the r-th column, in column order, of the bin's value
-    int mk = samp_bin_mk(R, bin);
-    const bool neg = bin >= kSampHalf;
-    // (the magnitude of) a kept column of the bin's sign, else -1
-    auto magnitude = [&](uint32_t bits) {
-        const float x = samp_value(bits);
-        const int m = (int)(__float_as_uint(x) >> 16);
-        return x >= R.cut && (m >= 0x8000) == neg ? m & 0x7fff : -1;
-    };
+    uint32_t value = (uint32_t)samp_bin_mk(R, bin) | (bin >= kSampHalf ? 0x8000u : 0u);
+    bool zero = false;  // the value is 0: of either sign
     uint32_t before = 0, here;
     if (samp_shared_bin(bin)) {
-        // a bin of several values: the value first, by bisection of its 15
-        // bits (values >= 0 fall with the magnitude, others rise)
-        const int top = mk;  // no column of the bin has a larger magnitude
+        // the two bins of many values, in order one after the other: the value
+        // first, by bisection of its 16 bits
+        if (bin == kSampHalf) r += bin_count(kSampHalf - 1);
+        const float plo = __uint_as_float((uint32_t)max(R.pt - kSampHalf + 1, 0) << 16);
+        const float nlo = __uint_as_float((uint32_t)max(R.nt - kSampHalf + 1, 0) << 16);
         auto count = [&](auto pred, int slot) {
             uint32_t n = 0;
             each(g1, [&](int, const uint4 &w) {
                 const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    n += pred(magnitude(h[e] & 0xffffu)) ? 1 : 0;
-                    n += pred(magnitude(h[e] >> 16)) ? 1 : 0;
+                for (int e = 0; e < 8; ++e) {
+                    const float x = samp_value(e & 1 ? h[e >> 1] >> 16 : h[e >> 1] & 0xffffu);
+                    n += x <= plo && x >= -nlo && pred(samp_key(x)) ? 1 : 0;
                 }
             });
             n = __reduce_add_sync(0xffffffffu, n);
@@ -872,32 +918,29 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
             if (lane == 0) sh.found[0][warp] = n;
             __syncthreads();
             if (tid < C) {
-                uint32_t s = 0;
-                for (int w = 0; w < kSampWarps; ++w) s += sh.found[0][w];
-                *at(&sh.refine[slot][rank], tid) = s;
+                uint32_t all = 0;
+                for (int w = 0; w < kWarps; ++w) all += sh.found[0][w];
+                *at(&sh.refine[slot][rank], tid) = all;
             }
             cluster_sync();
-        };
-        int v = 0;  // the value: magnitudes from the bin's first one with at most r columns before
-        uint32_t skipped = 0;
-        for (int bit = 14; bit >= 0; --bit) {
-            const int t = v | (1 << bit);
-            count([&](int m) { return m >= 0 && m <= top && (neg ? m < t : top - m < t); }, bit);
-            uint32_t n = 0;
+            n = 0;
 #pragma unroll
-            for (int q = 0; q < C; ++q) n += sh.refine[bit][q];
-            if (n <= r) {
-                v = t;
-                skipped = n;
-            }
+            for (int q = 0; q < C; ++q) n += sh.refine[slot][q];
+            return n;
+        };
+        uint32_t key = 0;  // the largest that more than r columns reach
+        for (int bit = 15; bit >= 0; --bit) {
+            const uint32_t t = key | (1u << bit);
+            if (count([&](uint32_t x) { return x >= t; }, bit) > r) key = t;
         }
-        mk = neg ? v : top - v;
-        r -= skipped;
-        count([&](int m) { return m == mk; }, 15);
+        r -= count([&](uint32_t x) { return x > key; }, 16);
+        count([&](uint32_t x) { return x == key; }, 17);
 #pragma unroll
         for (int q = 0; q < C; ++q)
-            if (q < rank) before += sh.refine[15][q];
-        here = sh.refine[15][rank];
+            if (q < rank) before += sh.refine[17][q];
+        here = sh.refine[17][rank];
+        value = key & 0x8000u ? key & 0x7fffu : 0xffffu - key;
+        zero = value == 0;
     } else {
 #pragma unroll
         for (int q = 0; q < C; ++q)
@@ -907,40 +950,74 @@ __global__ void __launch_bounds__(kSampThreads, 2) swa_sample_kernel(const Sampl
     cluster_arrive();  // no CTA leaves while its shared memory is read
     if (r >= before && r < before + here) {
         r -= before;
-        // vectors in column order: one step of the CTA after the other
-        for (int g = g0 + tid, step = 0; g - tid < g1; g += kSampThreads, ++step) {
-            const uint4 w = load(g);
-            const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-            uint32_t m8 = 0;
+        // vectors in column order, eight of a thread's per step
+        const uint32_t both = value * 0x10001u;
+        const __nv_bfloat162 want = *reinterpret_cast<const __nv_bfloat162 *>(&both);
+        (void)zero;  // (0 equals -0 as a number)
+        constexpr int U = 8;
+        for (int g = g0 + tid, step = 0; g - tid < g1; g += U * NT, ++step) {
+            uint32_t hit[U];  // bit 2 e (2 e + 1): the lower (upper) half of word e
+            {
+                uint4 w[U];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                m8 |= (magnitude(e & 1 ? h[e >> 1] >> 16 : h[e >> 1] & 0xffffu) == mk ? 1u : 0u) << e;
-            const uint32_t n = __popc(m8);
-            uint32_t *f = sh.found[step & 1];
-            const uint32_t all = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0) f[warp] = all;
-            __syncthreads();
-            uint32_t total = 0, first = 0;
+                for (int v = 0; v < U; ++v) w[v] = load(g + v * NT);
 #pragma unroll
-            for (int q = 0; q < kSampWarps; ++q) {
-                if (q < warp) first += f[q];
-                total += f[q];
+                for (int v = 0; v < U; ++v) {
+                    const uint32_t h[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+                    hit[v] = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t m =
+                            __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&h[e]), want);
+                        hit[v] |= ((m & 1u) | ((m >> 15) & 2u)) << (2 * e);
+                    }
+                }
             }
+            auto block_sum = [&](uint32_t n, uint32_t *f, uint32_t &first) {
+                n = __reduce_add_sync(0xffffffffu, n);
+                if (lane == 0) f[warp] = n;
+                __syncthreads();
+                uint32_t total = 0;
+                first = 0;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q) {
+                    if (q < warp) first += f[q];
+                    total += f[q];
+                }
+                return total;
+            };
+            uint32_t n = 0, first;
+#pragma unroll
+            for (int v = 0; v < U; ++v) n += __popc(hit[v]);
+            const uint32_t total = block_sum(n, sh.found[step & 1], first);
             if (r >= total) {
                 r -= total;
                 continue;
             }
-            if (r >= first && r < first + all) {
-                uint32_t pre = n;
+            // in this step: its vectors one after the other
+            bool done = false;
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                if (done) continue;
+                __syncthreads();
+                const uint32_t c = __popc(hit[v]);
+                const uint32_t all = block_sum(c, sh.found[v & 1], first);
+                if (r >= all) {
+                    r -= all;
+                    continue;
+                }
+                done = true;
+                uint32_t upto = c;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
-                    if (lane >= o) pre += x;
+                    const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += x;
                 }
-                uint32_t left = r - first - (pre - n);
-                if (left < n) {
-                    while (left-- > 0) m8 &= m8 - 1;
-                    finish(8LL * g - off + (__ffs(m8) - 1), sh.lp);
+                uint32_t skip = r - first - (upto - c);
+                if (r >= first && skip < c) {
+                    uint32_t m = hit[v];
+                    while (skip-- > 0) m &= m - 1;
+                    finish(8LL * (g + v * NT) - off + (__ffs(m) - 1), sh.lp);
                 }
             }
             break;
