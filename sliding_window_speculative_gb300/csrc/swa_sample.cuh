@@ -183,8 +183,13 @@ __device__ __forceinline__ uint64_t samp_weight(uint64_t y, const uint64_t *tabl
     if (n >= 62) return 0;
     const uint64_t t = table[(y >> 42) & 255];
     const uint64_t z = __umul64hi((y & 0x3ffffffffffull) << 14, 12786308645202655660ull);  // ln 2
-    const uint64_t z2 = __umul64hi(z, z), z3 = __umul64hi(z2, z), z4 = __umul64hi(z2, z2);
-    const uint64_t s = z - (z2 >> 1) + z3 / 6 - z4 / 24;
+    // 1 - e^-z = z - z^2 / 2 + z^3 / 6 - z^4 / 24, z < 2^-8.5: the powers from
+    // 32-bit pieces, a = z in units of 2^-40 and b = z^2 in units of 2^-48
+    const uint32_t a = (uint32_t)(z >> 24);
+    const uint64_t z2 = ((uint64_t)a * a) >> 16;
+    const uint32_t b = (uint32_t)(z2 >> 16);
+    const uint64_t s = z - (z2 >> 1) + (((uint64_t)a * __umulhi(b, 715827883u)) >> 24) -
+                       (((uint64_t)b * __umulhi(b, 178956971u)) >> 32);
     return (t - __umul64hi(t, s)) >> (n + 1);
 }
 
@@ -326,18 +331,20 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     const int nvec = (int)(((long long)A.V + off + 7) >> 3);
     const int cv = (nvec + C - 1) / C;
     const int g0 = min(nvec, rank * cv), g1 = min(nvec, g0 + cv);
+    // (those of the first and last column may reach over the row's ends)
+    const uint4 *vp = reinterpret_cast<const uint4 *>(rp - off);
+    const int in0 = off > 0 ? 1 : 0, in1 = (int)(((long long)A.V + off) >> 3);
     auto load = [&](int g) -> uint4 {
-        uint4 w = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);  // NaN: no column
-        if (g >= g1) return w;
-        const long long j = 8LL * g - off;
-        if (j >= 0 && j + 8 <= A.V) return __ldg(reinterpret_cast<const uint4 *>(rp + j));
-        uint32_t h[4];
+        if (g >= in0 && g < min(g1, in1)) return __ldg(vp + g);
+        uint32_t h[4] = {0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu};  // NaN: no column
+        if (g < g1) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const long long a = j + 2 * e;
-            const uint32_t lo = a >= 0 && a < A.V ? rp[a] : 0x7fffu;
-            const uint32_t hi = a + 1 >= 0 && a + 1 < A.V ? rp[a + 1] : 0x7fffu;
-            h[e] = lo | (hi << 16);
+            for (int e = 0; e < 8; ++e) {
+                const long long a = 8LL * g - off + e;
+                if (a >= 0 && a < A.V)
+                    h[e >> 1] = e & 1 ? (h[e >> 1] & 0xffffu) | ((uint32_t)rp[a] << 16)
+                                      : (h[e >> 1] & 0xffff0000u) | rp[a];
+            }
         }
         return make_uint4(h[0], h[1], h[2], h[3]);
     };
@@ -346,19 +353,26 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
 #pragma unroll
         for (int v = 0; v < kSampVpt; ++v) held[v] = load(g0 + tid + v * NT);
     }
-    // f(vector number, vector) over this thread's vectors of [g0, end), four
+    // f(vector number, vector) over this thread's vectors of [g0, end), eight
     // loads at a time; every thread of the CTA takes the same number of steps
     auto each = [&](int end, auto f) {
         if constexpr (HOLD) {
 #pragma unroll
             for (int v = 0; v < kSampVpt; ++v) f(g0 + tid + v * NT, held[v]);
         }
-        for (int g = g0 + tid + (HOLD ? kChunk : 0); g - tid < end; g += 4 * NT) {
-            uint4 w[4];
+        constexpr int U = kSampVpt;
+        for (int s = g0 + (HOLD ? kChunk : 0); s < end; s += U * NT) {
+            const int g = s + tid;
+            uint4 w[U];
+            if (s >= in0 && s + U * NT <= min(g1, in1)) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) w[v] = load(g + v * NT);
+                for (int v = 0; v < U; ++v) w[v] = __ldg(vp + g + v * NT);
+            } else {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) f(g + v * NT, w[v]);
+                for (int v = 0; v < U; ++v) w[v] = load(g + v * NT);
+            }
+#pragma unroll
+            for (int v = 0; v < U; ++v) f(g + v * NT, w[v]);
         }
     };
 
@@ -497,20 +511,27 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
 
     if (mx > -INF && (bound > -INF || (mp > 0.f && !has_p))) {
         // ================================================= by list
+        const __nv_bfloat162 line = __bfloat162bfloat162(__float2bfloat16_ru(R.cut));
         each(g1, [&](int g, const uint4 &w) {
-            __nv_bfloat162 hi2 = __floats2bfloat162_rn(-INF, -INF);
-            samp_max(w, hi2);
-            if (!(fmaxf(__low2float(hi2), __high2float(hi2)) >= R.cut)) return;
+            __nv_bfloat162 hi2 = *reinterpret_cast<const __nv_bfloat162 *>(&w.x);
+            hi2 = __hmax2(hi2, *reinterpret_cast<const __nv_bfloat162 *>(&w.y));
+            hi2 = __hmax2(hi2, *reinterpret_cast<const __nv_bfloat162 *>(&w.z));
+            hi2 = __hmax2(hi2, *reinterpret_cast<const __nv_bfloat162 *>(&w.w));
+            if (__hge2_mask(hi2, line) == 0) return;  // (false for NaN)
             const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+            uint32_t hit = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = samp_value(e & 1 ? h[e >> 1] >> 16 : h[e >> 1] & 0xffffu);
-                if (x >= R.cut) {
-                    const uint32_t n = atomicAdd(&sh.listed, 1u);
-                    if (n < kPart)
-                        *at(&sh.list[rank * kPart + n], 0) =
-                            samp_entry(x, (uint32_t)(8LL * g - off + e));
-                }
+            for (int e = 0; e < 8; ++e)
+                hit |= (samp_value(e & 1 ? h[e >> 1] >> 16 : h[e >> 1] & 0xffffu) >= R.cut ? 1u : 0u)
+                       << e;
+            uint32_t n = atomicAdd(&sh.listed, (uint32_t)__popc(hit));
+            for (; hit != 0; hit &= hit - 1, ++n) {
+                const int e = __ffs(hit) - 1;
+                const uint32_t pair = e < 4 ? (e < 2 ? h[0] : h[1]) : (e < 6 ? h[2] : h[3]);
+                if (n < kPart)
+                    *at(&sh.list[rank * kPart + n], 0) =
+                        samp_entry(samp_value(e & 1 ? pair >> 16 : pair & 0xffffu),
+                                   (uint32_t)(8LL * g - off + e));
             }
         });
         __syncthreads();
@@ -741,9 +762,9 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     auto bin_weight = [&](int bin) {
         const int mk = samp_shared_bin(bin) ? 0 : samp_bin_mk(R, bin);
         const float x = __uint_as_float((uint32_t)mk << 16);
-        if (bin == 0 || bin == kSampBins - 1 || !((bin >= kSampHalf ? -x : x) >= cut))
-            return (uint64_t)0;
-        return samp_weight(falling(bin >= kSampHalf, mk) - ymax, sh.table);
+        const bool none = bin == 0 || bin == kSampBins - 1 || !((bin >= kSampHalf ? -x : x) >= cut);
+        const uint64_t w = samp_weight(falling(bin >= kSampHalf, mk) - ymax, sh.table);
+        return none ? (uint64_t)0 : w;
     };
     auto bin_count = [&](int bin) {
         uint32_t c = 0;
@@ -754,21 +775,50 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     };
     // min-p as a weight
     const uint64_t mp_w = (uint64_t)scale_down((u128)1 << 63, 0.5f * mp, true);
-    for (int i = warp; i < kSampBlocks / C; i += kWarps) {
-        const int blk = rank * (kSampBlocks / C) + i, bin = blk * 32 + lane;
-        uint32_t c = bin_count(bin), c_mp = 0;
-        u128 m = 0;
-        if (__any_sync(0xffffffffu, c > 0)) {
-            const uint64_t w = c > 0 ? bin_weight(bin) : 0;
-            c_mp = __reduce_add_sync(0xffffffffu, w >= mp_w ? c : 0);
-            m = sum128((u128)w * c);
-            c = __reduce_add_sync(0xffffffffu, c);
-        }
-        if (lane < C) {
-            *at(&sh.blk_cnt[blk], lane) = c;
-            *at(&sh.blk_mp[blk], lane) = c_mp;
-            *at(&sh.blk_mass[blk][0], lane) = (uint64_t)m;
-            *at(&sh.blk_mass[blk][1], lane) = (uint64_t)(m >> 64);
+    {
+        constexpr int kMine = (kSampBlocks / C + kWarps - 1) / kWarps;  // blocks of this warp
+        auto block_of = [&](int i) { return rank * (kSampBlocks / C) + warp + i * kWarps; };
+        auto tell = [&](int blk, uint32_t c, uint32_t c_mp, u128 m) {
+            if (lane < C) {
+                *at(&sh.blk_cnt[blk], lane) = c;
+                *at(&sh.blk_mp[blk], lane) = c_mp;
+                *at(&sh.blk_mass[blk][0], lane) = (uint64_t)m;
+                *at(&sh.blk_mass[blk][1], lane) = (uint64_t)(m >> 64);
+            }
+        };
+        uint32_t full = 0;  // those with columns
+#pragma unroll 8
+        for (int i = 0; i < kMine; ++i)
+            if (warp + i * kWarps < kSampBlocks / C) {
+                if (__any_sync(0xffffffffu, bin_count(block_of(i) * 32 + lane) > 0))
+                    full |= 1u << i;
+                else
+                    tell(block_of(i), 0, 0, 0);
+            }
+        // (two at a time: a weight is a long chain of multiplications)
+        while (full != 0) {
+            const int i = __ffs(full) - 1;
+            full &= full - 1;
+            const int j = full != 0 ? __ffs(full) - 1 : i;
+            full &= full - 1;
+            int blk[2] = {block_of(i), block_of(j)};
+            uint32_t c[2], c_mp[2];
+            u128 m[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                c[v] = bin_count(blk[v] * 32 + lane);
+                const uint64_t w = bin_weight(blk[v] * 32 + lane);
+                c_mp[v] = w >= mp_w ? c[v] : 0;
+                m[v] = (u128)w * c[v];
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                c[v] = __reduce_add_sync(0xffffffffu, c[v]);
+                c_mp[v] = __reduce_add_sync(0xffffffffu, c_mp[v]);
+                m[v] = sum128(m[v]);
+            }
+            tell(blk[0], c[0], c_mp[0], m[0]);
+            tell(blk[1], c[1], c_mp[1], m[1]);
         }
     }
     cluster_sync();
