@@ -776,7 +776,8 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     // min-p as a weight
     const uint64_t mp_w = (uint64_t)scale_down((u128)1 << 63, 0.5f * mp, true);
     {
-        constexpr int kMine = (kSampBlocks / C + kWarps - 1) / kWarps;  // blocks of this warp
+        constexpr int kMine = kSampBlocks / C / kWarps;  // blocks of this warp
+        static_assert(kMine % 2 == 0 && kMine * kWarps * C == kSampBlocks, "whole pairs of blocks");
         auto block_of = [&](int i) { return rank * (kSampBlocks / C) + warp + i * kWarps; };
         auto tell = [&](int blk, uint32_t c, uint32_t c_mp, u128 m) {
             if (lane < C) {
@@ -786,27 +787,13 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 *at(&sh.blk_mass[blk][1], lane) = (uint64_t)(m >> 64);
             }
         };
-        uint32_t full = 0;  // those with columns
-#pragma unroll 8
-        for (int i = 0; i < kMine; ++i)
-            if (warp + i * kWarps < kSampBlocks / C) {
-                if (__any_sync(0xffffffffu, bin_count(block_of(i) * 32 + lane) > 0))
-                    full |= 1u << i;
-                else
-                    tell(block_of(i), 0, 0, 0);
-            }
-        // (two at a time: a weight is a long chain of multiplications)
-        while (full != 0) {
-            const int i = __ffs(full) - 1;
-            full &= full - 1;
-            const int j = full != 0 ? __ffs(full) - 1 : i;
-            full &= full - 1;
-            int blk[2] = {block_of(i), block_of(j)};
-            uint32_t c[2], c_mp[2];
+        // two blocks at a time: a weight is a long chain of multiplications
+        auto weigh = [&](int blk0, int blk1, uint32_t c0, uint32_t c1) {
+            const int blk[2] = {blk0, blk1};
+            uint32_t c[2] = {c0, c1}, c_mp[2];
             u128 m[2];
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-                c[v] = bin_count(blk[v] * 32 + lane);
                 const uint64_t w = bin_weight(blk[v] * 32 + lane);
                 c_mp[v] = w >= mp_w ? c[v] : 0;
                 m[v] = (u128)w * c[v];
@@ -816,9 +803,40 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 c[v] = __reduce_add_sync(0xffffffffu, c[v]);
                 c_mp[v] = __reduce_add_sync(0xffffffffu, c_mp[v]);
                 m[v] = sum128(m[v]);
+                tell(blk[v], c[v], c_mp[v], m[v]);
             }
-            tell(blk[0], c[0], c_mp[0], m[0]);
-            tell(blk[1], c[1], c_mp[1], m[1]);
+        };
+        if constexpr (C > 1) {
+            // (the counts come from afar: read once)
+            uint32_t c[kMine];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) c[i] = bin_count(block_of(i) * 32 + lane);
+#pragma unroll
+            for (int i = 0; i < kMine; i += 2) {
+                if (__any_sync(0xffffffffu, (c[i] | c[i + 1]) != 0)) {
+                    weigh(block_of(i), block_of(i + 1), c[i], c[i + 1]);
+                } else {
+                    tell(block_of(i), 0, 0, 0);
+                    tell(block_of(i + 1), 0, 0, 0);
+                }
+            }
+        } else {
+            static_assert(kMine <= 32, "a bit per block of a warp");
+            uint32_t full = 0;  // those with columns
+#pragma unroll 8
+            for (int i = 0; i < kMine; ++i)
+                if (__any_sync(0xffffffffu, bin_count(block_of(i) * 32 + lane) > 0))
+                    full |= 1u << i;
+                else
+                    tell(block_of(i), 0, 0, 0);
+            while (full != 0) {
+                const int i = __ffs(full) - 1;
+                full &= full - 1;
+                const int j = full != 0 ? __ffs(full) - 1 : i;
+                full &= full - 1;
+                weigh(block_of(i), block_of(j), bin_count(block_of(i) * 32 + lane),
+                      bin_count(block_of(j) * 32 + lane));
+            }
         }
     }
     cluster_sync();
