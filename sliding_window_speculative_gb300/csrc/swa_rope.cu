@@ -57,13 +57,14 @@ template <int D>
 cudaError_t launch(swa::RopeParams &R, int sms, cudaStream_t s) {
     constexpr int kWarps = swa::kRopeThreads / 32;
     const int steps = (R.Hq + 2 * R.Hkv + 512 / D - 1) / (512 / D);  // warp steps per token
-    // one warp per token; a token's heads go to several warps while the
-    // launch would leave SMs with fewer than eight warps
-    const long long want = 8LL * sms;
+    // one warp per token; a token's heads go to several warps while the launch
+    // would leave SMs with fewer than four (measured on GB300, 64 x 8 tokens
+    // into pages, us, 2 / 4 / 8 / 16 warps: 6.2 / 6.0 / 6.2 / 7.7)
+    const long long want = 4LL * sms;
     long long parts = R.tokens < want ? (want + R.tokens - 1) / R.tokens : 1;
     R.parts = (int)(parts < steps ? parts : steps);
     long long blocks = ((long long)R.tokens * R.parts + kWarps - 1) / kWarps;
-    const long long cap = 8LL * sms;
+    const long long cap = (long long)swa::kRopeBlocksPerSm * sms;
     if (blocks > cap) blocks = cap;
     return swa::launch_kernel(swa::swa_rope_kernel<D>, dim3((unsigned)blocks),
                               dim3(swa::kRopeThreads), 0, s, R);
@@ -148,8 +149,8 @@ swa_status swa_qk_norm_rope_append(const void *q, const void *k, const void *v,
         R.cache.max_blocks = paged->max_blocks;
         R.cache.num_pages = paged->num_pages;
     }
-    R.cache.k = static_cast<const __nv_bfloat16 *>(k_cache);
-    R.cache.v = static_cast<const __nv_bfloat16 *>(v_cache);
+    R.k_out = static_cast<__nv_bfloat16 *>(k_cache);
+    R.v_out = static_cast<__nv_bfloat16 *>(v_cache);
     R.cache.seq_lens = seq_lens;
     R.cache.L = dims->max_len;
     R.to_cache = 1;
