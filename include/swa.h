@@ -90,7 +90,8 @@ typedef struct {
  * Workspace: when the chosen split count needs split partials in global
  * memory, they go to the workspace set with swa_set_workspace() for the
  * current device, or else to a library-owned buffer grown on demand with
- * cudaMalloc (never while `stream` is capturing: then SWA_ERR_WORKSPACE).
+ * cudaMalloc (never while `stream` is capturing: then SWA_ERR_WORKSPACE; an
+ * outgrown buffer stays allocated, so that captured calls keep theirs).
  * All calls on one device share that buffer, so calls that may run at the
  * same time on different streams race on it; order them on one stream or
  * give each its own device.
@@ -252,8 +253,10 @@ size_t swa_workspace_bytes(const swa_dims *dims, int32_t window);
  * library-owned buffer.  The memory must stay valid until replaced. */
 swa_status swa_set_workspace(void *dev_ptr, size_t bytes);
 
-/* Release the library-owned workspace of the current device (synchronises
- * the device through cudaFree). */
+/* Release the library-owned workspace of the current device, outgrown buffers
+ * too (synchronises the device through cudaFree).  Graphs that captured calls
+ * with split partials must not be replayed afterwards; the same holds for
+ * swa_set_workspace. */
 swa_status swa_release_workspace(void);
 
 /* What the library would launch for these dims on a GPU with `num_sms`

@@ -330,13 +330,39 @@ Plan make_plan(const swa_dims *d, int32_t window, int num_sms, bool pairs_ok) {
 
 // ------------------------------------------------------------- workspace
 
+// A library-owned buffer that was outgrown stays allocated (a captured graph
+// may replay calls that use it) until the workspace is released or replaced;
+// each is over a quarter larger than the one before, so a few slots hold any
+// number of bytes.
+constexpr int kMaxRetired = 256;
+
 struct Workspace {
     void *ptr = nullptr;
     size_t bytes = 0;
     bool owned = false;
+    void *retired[kMaxRetired] = {};
+    int n_retired = 0;
 };
 std::mutex g_ws_mutex;
 Workspace g_ws[kMaxDevices];
+
+// Frees the library-owned buffers of a device, outgrown ones too.
+swa_status free_owned(Workspace &w) {
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < w.n_retired; ++i) {
+        const cudaError_t f = cudaFree(w.retired[i]);
+        if (e == cudaSuccess) e = f;
+    }
+    w.n_retired = 0;
+    if (w.owned && w.ptr) {
+        const cudaError_t f = cudaFree(w.ptr);
+        if (e == cudaSuccess) e = f;
+        w.ptr = nullptr;
+        w.bytes = 0;
+        w.owned = false;
+    }
+    return e == cudaSuccess ? SWA_OK : cuda_fail(e, "cudaFree(workspace)");
+}
 
 swa_status ensure_workspace(int dev, size_t need, cudaStream_t stream, void **out) {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
@@ -356,18 +382,15 @@ swa_status ensure_workspace(int dev, size_t need, cudaStream_t stream, void **ou
                     "stream is capturing and the workspace (%zu bytes) is below the %zu needed; "
                     "run one call outside capture first or set a workspace",
                     w.bytes, need);
-    if (w.ptr) {
-        e = cudaFree(w.ptr);
-        w.ptr = nullptr;
-        w.bytes = 0;
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFree(workspace)");
-    }
+    if (w.n_retired == kMaxRetired)
+        return fail(SWA_ERR_WORKSPACE, "the workspace was outgrown %d times; release it", kMaxRetired);
     size_t grow = need + need / 4;
-    e = cudaMalloc(&w.ptr, grow);
-    if (e != cudaSuccess) {
-        w.ptr = nullptr;
-        return cuda_fail(e, "cudaMalloc(workspace)");
-    }
+    if (w.ptr != nullptr && grow < w.bytes + w.bytes / 4) grow = w.bytes + w.bytes / 4;
+    void *ptr = nullptr;
+    e = cudaMalloc(&ptr, grow);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
+    if (w.ptr != nullptr) w.retired[w.n_retired++] = w.ptr;
+    w.ptr = ptr;
     w.bytes = grow;
     w.owned = true;
     *out = w.ptr;
@@ -696,10 +719,8 @@ swa_status swa_set_workspace(void *dev_ptr, size_t bytes) {
     if (dev >= kMaxDevices) return fail(SWA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);
     std::lock_guard<std::mutex> lock(g_ws_mutex);
     Workspace &w = g_ws[dev];
-    if (w.owned && w.ptr) {
-        e = cudaFree(w.ptr);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFree(workspace)");
-    }
+    const swa_status st = free_owned(w);
+    if (st != SWA_OK) return st;
     w.ptr = dev_ptr;
     w.bytes = bytes;
     w.owned = false;
@@ -712,13 +733,7 @@ swa_status swa_release_workspace(void) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     if (dev >= kMaxDevices) return fail(SWA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace &w = g_ws[dev];
-    if (w.owned && w.ptr) {
-        e = cudaFree(w.ptr);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFree(workspace)");
-        w = Workspace{};
-    }
-    return SWA_OK;
+    return free_owned(g_ws[dev]);
 }
 
 swa_status swa_plan(const swa_dims *dims, int32_t window, int32_t num_sms, swa_plan_info *plan) {

@@ -497,17 +497,20 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     auto min_p_line = [&](float top) {
         return top + T * (__logf(mp) * 1.0001f - 1e-5f) - fabsf(top) * 1e-6f;
     };
-    // columns that the filters cannot keep need no look: those far below the
-    // maximum, those below the top-k bound, and without top-p those below
-    // min-p's line (the first chunk's maximum stands in for the row's: lower)
+    // columns that weigh nothing lie far below the maximum
+    auto line_of = [&](float top) {
+        return top == INF ? INF : fmaxf(top - kSampCut * T, -3.4028234e38f);
+    };
+    // and those that the filters cannot keep below the top-k bound, or without
+    // top-p below min-p's line (the first chunk's maximum stands in for the
+    // row's: lower)
     auto cut_of = [&](float top) {
-        float cut = top == INF ? INF : fmaxf(top - kSampCut * T, -3.4028234e38f);
-        cut = fmaxf(cut, bound);
+        float cut = fmaxf(line_of(top), bound);
         if (mp > 0.f && !has_p) cut = fmaxf(cut, min_p_line(top));
         return cut;
     };
     SampRow R;
-    R.cut = cut_of(mx);
+    R.cut = cut_of(mx);  // (by list)
 
     if (mx > -INF && (bound > -INF || (mp > 0.f && !has_p))) {
         // ================================================= by list
@@ -720,6 +723,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     }
 
     // ===================================================== by histogram
+    R.cut = line_of(mx);
     auto top_key = [](float x) { return (int)(__float_as_uint(fmaxf(x, 0.f)) >> 16); };
     // (never so low that 0 and -0 fall outside the shared bins)
     auto at_least = [](int top) { return max(top, kSampHalf); };
@@ -746,9 +750,16 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
         full_max = -INF;
 #pragma unroll
         for (int r = 0; r < C; ++r) full_max = fmaxf(full_max, sh.max2[round][r]);
-        if (round > 0 || top_key(full_max) < R.pt) break;
-        // a column above the top: once more, from the row's own maximum
-        R.cut = cut_of(full_max);
+        if (round > 0) break;
+        // the first chunk may mislead: a column above the positive top, or a
+        // line so far below the row's own that values a weight apart share
+        // the negative values' last bin.  Then once more, from the row's own
+        // maximum
+        const float own = line_of(full_max);
+        const float shared = __uint_as_float((uint32_t)max(R.nt - kSampHalf + 1, 0) << 16);
+        const bool coarse = own < 0.f && 2.f * own > R.cut && shared > T * 2.3841858e-7f;  // 2^-22
+        if (top_key(full_max) < R.pt && !coarse) break;
+        R.cut = own;
         R.pt = at_least(top_key(full_max) + 1);
         cluster_sync();
         for (int i = tid; i < kSampBins / 4; i += NT)
@@ -756,14 +767,22 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
         __syncthreads();
     }
     const uint64_t ymax = falling_of(full_max + 0.f);
-    const float cut = fmaxf(R.cut, cut_of(full_max));  // (the row's own, now)
+    const float cut = line_of(full_max);  // (the row's own, now)
 
     // ---- this CTA's slice of the blocks: counts over the cluster, weights
+    const float shared_max = __uint_as_float((uint32_t)max(R.pt - kSampHalf + 1, 0) << 16);
     auto bin_weight = [&](int bin) {
-        const int mk = samp_shared_bin(bin) ? 0 : samp_bin_mk(R, bin);
+        // (the shared bins' values as 0, or as the maximum if that is one of them)
+        const bool shared = samp_shared_bin(bin);
+        const int mk = shared ? 0 : samp_bin_mk(R, bin);
         const float x = __uint_as_float((uint32_t)mk << 16);
-        const bool none = bin == 0 || bin == kSampBins - 1 || !((bin >= kSampHalf ? -x : x) >= cut);
-        const uint64_t w = samp_weight(falling(bin >= kSampHalf, mk) - ymax, sh.table);
+        const bool none = bin == 0 || bin == kSampBins - 1 ||
+                          !(bin == kSampHalf - 1 ? cut <= shared_max
+                            : shared             ? cut <= 0.f
+                                                 : (bin >= kSampHalf ? -x : x) >= cut);
+        const uint64_t y =
+            shared && full_max <= shared_max ? 0 : falling(bin >= kSampHalf, mk) - ymax;
+        const uint64_t w = samp_weight(y, sh.table);
         return none ? (uint64_t)0 : w;
     };
     auto bin_count = [&](int bin) {

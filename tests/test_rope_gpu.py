@@ -223,3 +223,32 @@ def test_binding_refuses_uneven_strides():
     ref = swa.swa_qk_norm_rope(**{**c, **{n: t.contiguous() for n, t in e.items()}})
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_offsets_past_32_bits():
+    """Rows written past element 2^31 of a cache, and inputs whose token
+    stride takes them there."""
+    import sliding_window_speculative_gb300 as swa
+    D, n = 256, 4
+    L = (1 << 31) // D + 1024
+    c = _case(1, n, 2, 1, D, D, seed=15, pos=[L - n - 3])
+    q_ref, k_ref, v_ref = swa.swa_qk_norm_rope(**c)
+    kc = torch.zeros((1, 1, L, D), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    q = swa.swa_qk_norm_rope_append(**c, k_cache=kc, v_cache=vc,
+                                    seq_lens=torch.tensor([L], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    p = L - n - 3
+    assert torch.equal(q, q_ref)
+    for cache, rows in ((kc, k_ref), (vc, v_ref)):
+        assert torch.equal(cache[0, 0, p:p + n], rows[0, :, 0])
+        assert not cache[0, 0, p + n:].any() and not cache[0, 0, p - 1000:p].any()
+    # one token every 2^30 elements
+    flat = vc.view(-1)
+    step = 1 << 30
+    strided = flat.as_strided((1, 2, 2, D), (2 * step, step, D, 1), 512)
+    strided.copy_(c["q"][:, :2])
+    got = swa.swa_qk_norm_rope(strided, c["k"][:, :2], c["v"][:, :2], c["q_weight"], c["k_weight"],
+                               1e-6, c["inv_freq"], c["q_pos"])[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got, q_ref[:, :2])

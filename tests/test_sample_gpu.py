@@ -291,3 +291,77 @@ def test_launch_failures_are_reported():
     assert swa.swa_get_debug_options()["fail_launch"] == 0
     swa.swa_sample_accept(x, u, T, draft=d)
     torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    """The last rows of logits with more than 2^31 elements."""
+    import sliding_window_speculative_gb300 as swa
+    V, rows, last = 262147, 8210, 24
+    x = torch.empty((rows, 1, V), dtype=torch.bfloat16, device="cuda")
+    x[:-last] = 0
+    x[-last:] = _logits("peaked", (last, 1, V), seed=3).cuda()
+    u = torch.rand((rows, 1), device="cuda")
+    T = torch.full((rows,), 0.9, device="cuda")
+    k = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    k[:-last] = 1
+    k[-last::2] = 50
+    t, _, lp = swa.swa_sample_accept(x, u, T, top_k=k)
+    want = swa.swa_sample_accept(x[-last:].contiguous(), u[-last:].contiguous(),
+                                 T[-last:].contiguous(), top_k=k[-last:].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(t[-last:], want[0])
+    assert (lp[-last:] - want[2]).abs().max().item() <= 2.0 ** -19 * want[2].abs().max().item()
+    assert not t[:-last].any()
+
+
+def test_rows_that_outgrow_their_first_chunk():
+    """The largest logit far above the first chunk's (the histogram's top is
+    raised and the row counted again), or only behind it; lists that overflow
+    (equal logits above the bound) fall back to the histogram."""
+    V = 70001
+    base = _logits("normal", (1, 1, V), seed=21)[0, 0]
+    rows = []
+    for kind in range(12):
+        x = base.clone()
+        if kind == 0:
+            x[60000:60005] = 3.0e4             # far above 16 times the first chunk's largest
+        elif kind == 1:
+            x[:40000] = float("-inf")          # nothing in the first chunk
+        elif kind == 2:
+            x[:40000] = float("nan")
+            x[69999] = float("inf")
+        elif kind == 3:
+            x[:] = 1.5                         # one value everywhere
+        elif kind == 4:
+            x[:40000] = -300.0                 # negative first, positive behind
+        elif kind == 5:
+            x[:] = -1.0e30
+            x[65000] = -9.0e29
+        elif kind == 6:
+            x[30000:] = 7.0                    # more columns at the bound than the list holds
+        elif kind == 7:
+            x[:] = float("-inf")
+            x[V - 1] = -5.0
+        elif kind == 8:
+            x[:40000] = torch.finfo(torch.bfloat16).min   # a masked half, finite
+        elif kind == 9:
+            x[:40000] = -1.0e6
+            x[40000:] *= 1e-3
+        elif kind == 10:
+            x[:] = -1.0e-12                    # the maximum itself vanishes beside T
+        else:
+            x[:] = 1.0e-12
+            x[5] = -1.0e-12
+        rows.append(x)
+    n = len(rows)
+    xs = torch.stack(rows).view(n, 1, V)
+    u = np.random.default_rng(2).random((n, 1)).astype(np.float32)
+    for mode in ("none", "k", "p", "m", "all"):
+        for T in (0.8, 40.0):
+            s = _settings(n, 17, mode)
+            s["temperature"] = np.full(n, T, np.float32)
+            _check(xs, s, u, what=f"{mode} T{T}")
+    # as many rows as make every CTA take a row for itself
+    many = xs.repeat(40, 1, 1)
+    s = _settings(40 * n, 19, "all")
+    _check(many, s, np.random.default_rng(4).random((40 * n, 1)).astype(np.float32), what="one CTA per row")

@@ -286,3 +286,56 @@ def test_captured_split_plan_and_prepared_call():
     graph.replay()
     torch.cuda.synchronize()
     cs[1].check(go, gl, "captured")
+
+
+def test_a_captured_split_survives_a_larger_call():
+    """The split workspace grows while a graph that uses the old one lives:
+    the replay still finds its own."""
+    import sliding_window_speculative_gb300 as swa
+    swa.swa_release_workspace()
+    small = Case(4, 8, 2, 128, 200, 5, [300], 512, seed=12)
+    big = Case(8, 8, 2, 256, 300, 5, [400, 700, 500, 650], 1024, seed=13)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    k, v, _, _, _ = small.device()
+    args = (small.q.cuda(), k, v, i32(small.lens), i32(small.pos), 200, 5, small.scale)
+    swa.swa_sink_verify_attn(*args, num_splits=2)
+    out, lse = torch.empty_like(small.q).cuda(), torch.empty((1, 4, 8)).cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        swa.swa_sink_verify_attn(*args, out=out, lse=lse, num_splits=2)
+    big.check(*big.run(8), "the larger call")
+    filler = torch.full((1 << 22,), 3.0e4, device="cuda")   # whatever is free now is overwritten
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    small.check(out, lse, "the captured call")
+    del graph, filler
+    swa.swa_release_workspace()
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^31 elements: the last rows are attended and
+    written where they are."""
+    import sliding_window_speculative_gb300 as swa
+    D, q_len, W, S = 256, 8, 40, 4
+    L = (1 << 31) // D + 4096
+    small = Case(q_len, 8, 1, D, W, S, [300], 512, append=True, seed=14)
+    p0 = L - q_len - 100
+    shift = p0 - 300
+    caches = []
+    for src in small.device()[:2]:
+        c = torch.empty((1, 1, L, D), dtype=torch.bfloat16, device="cuda")
+        c[:, :, :S] = src[:, :, :S]
+        lo = 300 - W + 1
+        c[:, :, lo + shift:300 + shift] = src[:, :, lo:300]
+        caches.append(c)
+    _, _, _, kn, vn = small.device()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    for kernel in ("plan", "simt", "rows"):
+        with forced_kernel(kernel):
+            out, lse = swa.swa_sink_verify_attn(small.q.cuda(), *caches, i32([p0 + q_len]), i32([p0]),
+                                                W, S, small.scale, k_new=kn, v_new=vn)
+            torch.cuda.synchronize()
+        small.check(out, lse, f"far rows, {kernel}")
+        for c, n in zip(caches, (kn, vn)):
+            assert torch.equal(c[0, :, p0:p0 + q_len].transpose(0, 1), n[0])
