@@ -14,7 +14,8 @@
 // columns, by one of two ways.
 //
 // List: where a bound is known below which nothing can be kept (small top-k:
-// at least k of the first chunk's columns reach it; min-p alone), the columns
+// at least k of the first chunk's columns reach it; min-p alone), and for rows
+// short enough to be sorted whole, the columns
 // that reach it go to a list in the first CTA's shared memory, which sorts
 // them and finishes the row by itself.  Almost every 16-byte vector of the row
 // is dismissed by one packed maximum, so this way runs at the speed of the
@@ -56,6 +57,7 @@ constexpr int kSampBins = 2 * kSampHalf;
 constexpr int kSampVpt = 8;                // 16-byte vectors of the first chunk per thread
 constexpr int kSampBlocks = kSampBins / 32;  // of 32 bins
 constexpr int kSampList = kSampBins / 2;   // columns the list holds
+constexpr int kSampSmall = 1024;           // rows up to here are always taken by list
 constexpr int kSampKeys = 512;             // maxima the top-k bound is taken from
 constexpr int kSampListK = kSampKeys / 2;  // largest top-k taken by list
 constexpr int kSampMaxCluster = 8;
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     SampRow R;
     R.cut = cut_of(mx);  // (by list)
 
-    if (mx > -INF && (bound > -INF || (mp > 0.f && !has_p))) {
+    if (mx > -INF && (bound > -INF || (mp > 0.f && !has_p) || A.V <= kSampSmall)) {
         // ================================================= by list
         const __nv_bfloat162 line = __bfloat162bfloat162(__float2bfloat16_ru(R.cut));
         each(g1, [&](int g, const uint4 &w) {
