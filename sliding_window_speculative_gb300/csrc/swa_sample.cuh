@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 uint64_t mine[kSampList / NT];
 #pragma unroll
                 for (int i = 0; i < kSampList / NT; ++i) {
+                    if ((uint32_t)(i * NT) >= n) break;
                     uint32_t from = tid + i * NT, part = 0;
 #pragma unroll
                     for (int r = 0; r < C - 1; ++r)
@@ -622,8 +623,19 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 __syncthreads();
                 n = sh.listed;
             }
-            if (n <= NT) {
-                // every entry's place is the number of larger ones
+            if (n <= NT / 4) {
+                // every entry's place is the number of larger ones: four
+                // threads count for one
+                const uint32_t who = tid >> 2;
+                const uint64_t e = who < n ? sh.list[who] : 0;
+                uint32_t place = 0;
+#pragma unroll 4
+                for (uint32_t i = tid & 3; i < n; i += 4) place += sh.list[i] > e;
+                place += __shfl_xor_sync(0xffffffffu, place, 1);
+                place += __shfl_xor_sync(0xffffffffu, place, 2);
+                __syncthreads();
+                if (who < n && (tid & 3) == 0) sh.list[place] = e;
+            } else if (n <= NT) {
                 const uint64_t e = (uint32_t)tid < n ? sh.list[tid] : 0;
                 uint32_t place = 0;
                 if ((uint32_t)(tid & ~31) < n)
