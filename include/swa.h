@@ -397,7 +397,7 @@ swa_status swa_greedy_accept(const void *logits, const int32_t *keep_ids, const 
  *                 1); logprob = ln(w / S)
  *   T <= 0 or NaN is greedy: the first candidate, logprob 0.  A row without
  *   candidates gives column 0, logprob 0.
- * Weights are computed to 2^-44 relative and summed exactly, so results do not
+ * Weights are computed to 2^-39 relative and summed exactly, so results do not
  * depend on the launch; columns more than 50 T below M are left out (together
  * under 2^-41 of S up to 2^31 columns), and of many candidates those of
  * vanishing magnitude (below 2^-28 of the row's largest) may weigh like 0,

@@ -33,7 +33,7 @@
 // Weights and masses are integers, so sums do not depend on any order and
 // comparisons are exact: w = 2^-((max - x) log2(e) / T) in units of 2^-62 (the
 // exponent in fixed point to 2^-50, the power from a table of 2^(-j/256) and a
-// quartic; relative error below 2^-44), masses as 128-bit sums of count * w.
+// quartic; relative error below 2^-39), masses as 128-bit sums of count * w.
 //
 // Bins: for each sign 4096 values downwards from a top magnitude, i.e. 32
 // octaves.  The top of the positive values is a few octaves above the first
@@ -51,15 +51,15 @@
 
 namespace swa {
 
-constexpr int kSampMaxWarps = 16;
+constexpr int kSampMaxWarps = 32;
 constexpr int kSampHalf = 4096;            // bins per sign
 constexpr int kSampBins = 2 * kSampHalf;
 constexpr int kSampVpt = 8;                // 16-byte vectors of the first chunk per thread
 constexpr int kSampBlocks = kSampBins / 32;  // of 32 bins
 constexpr int kSampList = kSampBins / 2;   // columns the list holds
 constexpr int kSampSmall = 1024;           // rows up to here are always taken by list
-constexpr int kSampKeys = 512;             // maxima the top-k bound is taken from
-constexpr int kSampListK = kSampKeys / 2;  // largest top-k taken by list
+constexpr int kSampKeys = 1024;            // maxima the top-k bound is taken from, at most
+constexpr int kSampListK = 256;            // largest top-k taken by list
 constexpr int kSampMaxCluster = 8;
 constexpr int kSampRoom = 4 << 7;          // four octaves above the first chunk's largest
 constexpr float kSampCut = 50.f;           // columns 50 T below the maximum weigh under 2^-72
@@ -106,14 +106,14 @@ __device__ __forceinline__ u128 shfl_up128(u128 x, int d) {
     const uint64_t hi = __shfl_up_sync(0xffffffffu, (uint64_t)(x >> 64), d);
     return ((u128)hi << 64) | lo;
 }
+// Sum over the warp of x < 2^104: its 26-bit pieces by one reduction each.
 __device__ __forceinline__ u128 sum128(u128 x) {
+    constexpr uint32_t kLow = (1u << 26) - 1;
+    u128 sum = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t lo = __shfl_xor_sync(0xffffffffu, (uint64_t)x, o);
-        const uint64_t hi = __shfl_xor_sync(0xffffffffu, (uint64_t)(x >> 64), o);
-        x += ((u128)hi << 64) | lo;
-    }
-    return x;
+    for (int i = 0; i < 4; ++i)
+        sum += (u128)__reduce_add_sync(0xffffffffu, (uint32_t)(x >> (26 * i)) & kLow) << (26 * i);
+    return sum;
 }
 __device__ __forceinline__ u128 shfl128(u128 x, int src) {
     const uint64_t lo = __shfl_sync(0xffffffffu, (uint64_t)x, src);
@@ -184,15 +184,19 @@ __device__ __forceinline__ uint64_t samp_weight(uint64_t y, const uint64_t *tabl
     const uint32_t n = (uint32_t)(y >> 50);
     if (n >= 62) return 0;
     const uint64_t t = table[(y >> 42) & 255];
-    const uint64_t z = __umul64hi((y & 0x3ffffffffffull) << 14, 12786308645202655660ull);  // ln 2
-    // 1 - e^-z = z - z^2 / 2 + z^3 / 6 - z^4 / 24, z < 2^-8.5: the powers from
-    // 32-bit pieces, a = z in units of 2^-40 and b = z^2 in units of 2^-48
+    // 1 - e^-z = z - z^2 / 2 + z^3 / 6 - z^4 / 24, z < 2^-8.5, from 32-bit
+    // pieces: z in units of 2^-64 (ln 2 to 32 bits), a = z in units of 2^-40,
+    // b = z^2 in units of 2^-48
+    const uint64_t z = ((uint64_t)(uint32_t)(y >> 10) * 2977044472u) >> 8;
     const uint32_t a = (uint32_t)(z >> 24);
     const uint64_t z2 = ((uint64_t)a * a) >> 16;
     const uint32_t b = (uint32_t)(z2 >> 16);
     const uint64_t s = z - (z2 >> 1) + (((uint64_t)a * __umulhi(b, 715827883u)) >> 24) -
                        (((uint64_t)b * __umulhi(b, 178956971u)) >> 32);
-    return (t - __umul64hi(t, s)) >> (n + 1);
+    // t s, s in units of 2^-40
+    const uint32_t s40 = (uint32_t)(s >> 24);
+    const uint64_t ts = ((uint64_t)(uint32_t)(t >> 32) * s40 + (((uint64_t)(uint32_t)t * s40) >> 32)) >> 8;
+    return (t - ts) >> (n + 1);
 }
 
 // What one row's columns are counted by.
@@ -289,6 +293,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     namespace cg = cooperative_groups;
     constexpr int kWarps = NT / 32;
     constexpr int kChunk = kSampVpt * NT;      // vectors of the first chunk
+    constexpr int kKeys = NT < 512 ? 512 : NT;  // maxima the top-k bound is taken from
     constexpr uint32_t kPart = kSampList / C;  // list entries of one CTA
     const float INF = __int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     {
         // (a thread's maxima of several parts of the chunk, as many as there
         // are keys)
-        constexpr int kParts = kSampKeys / NT;
+        constexpr int kParts = kKeys / NT;
         static_assert(kParts == 1 || kParts == 2, "one or two maxima per thread");
         const __nv_bfloat162 none = __floats2bfloat162_rn(-INF, -INF);
         __nv_bfloat162 hi2[kParts];
@@ -456,13 +461,13 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
         float x = -INF;
         if (k <= kSampListK) {
             const int n = warp == 1 ? (int)k : (int)((k + C - 1) / C);
-            uint32_t key[kSampKeys / 32], lo = 0;
+            uint32_t key[kKeys / 32], lo = 0;
 #pragma unroll
-            for (int i = 0; i < kSampKeys / 32; ++i) key[i] = sh.keys[i * 32 + lane];
+            for (int i = 0; i < kKeys / 32; ++i) key[i] = sh.keys[i * 32 + lane];
             for (uint32_t bit = 0x8000u; bit > 0; bit >>= 1) {
                 int c = 0;
 #pragma unroll
-                for (int i = 0; i < kSampKeys / 32; ++i) c += key[i] >= (lo | bit);
+                for (int i = 0; i < kKeys / 32; ++i) c += key[i] >= (lo | bit);
                 if (__reduce_add_sync(0xffffffffu, c) >= n) lo |= bit;
             }
             x = __uint_as_float((lo & 0x8000u ? lo & 0x7fffu : 0xffffu - lo) << 16);

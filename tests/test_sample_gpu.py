@@ -7,8 +7,8 @@ function's own 2 units: within 2^-21 of the value.  Elsewhere the logarithm of
 such a quotient: its argument's 2^-22 as an absolute error, and 2 units, on a
 value of at least ln 2.  Together within 2^-20 of the value.  To that come
 errors that do not shrink with the value: a relative error e of w / S moves
-ln(w / S) by e however near 0 that is.  The weights' 2^-44 (numerator and sum)
-make 2^-43, the fp64 side's running sum of up to 2^18 terms, 2^-53 each, at
+ln(w / S) by e however near 0 that is.  The weights' 2^-39 (numerator and sum)
+make 2^-38, the fp64 side's running sum of up to 2^18 terms, 2^-53 each, at
 most 2^-35: together below 2^-34."""
 import numpy as np
 import pytest
