@@ -38,15 +38,20 @@ cudaError_t launch(const swa::SampleParams &A, long long rows, cudaStream_t s) {
 }
 
 cudaError_t launch_rows(const swa::SampleParams &A, long long rows, int sms, cudaStream_t s) {
-    // one CTA per row, four to an SM; more share a row while SMs would idle and
-    // each still has two vectors per thread
+    // One CTA per row, four to an SM; clusters share a row while SMs would be
+    // left without two CTAs and each still has two vectors per thread.  Measured
+    // on GB300, rows of 262144, us, unfiltered / top-k 50: 64 rows 4 CTAs of
+    // 256 threads 30.6 / 18.5, of 512 32.8 / 18.5, 8 of 256 32.8; 128 rows 2 of
+    // 512 47.1 / 22.6, 2 of 256 43.7 / 26.0, 1 of 256 - / 32.9; 512 rows 1 of
+    // 256 135 / 67, 1 of 512 133 / 69, 2 of 512 140 / 86.  8 rows, 8 CTAs:
+    // the first chunk held in registers 12.5, read again 16.3.
     const long long nvec = ((long long)A.V + 14) / 8;
     int c = 1;
     while (c < swa::kSampMaxCluster && rows * c * 2 <= 2LL * sms && nvec > 1024LL * c) c *= 2;
     switch (c) {
         case 1: return launch<1, 256, false>(A, rows, s);
         case 2: return launch<2, 512, false>(A, rows, s);
-        case 4: return launch<4, 512, false>(A, rows, s);
+        case 4: return launch<4, 256, false>(A, rows, s);
         default:
             return rows * c <= sms ? launch<8, 512, true>(A, rows, s)
                                    : launch<8, 512, false>(A, rows, s);

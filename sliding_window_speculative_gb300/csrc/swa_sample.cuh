@@ -5,21 +5,24 @@
 // rising column, keeps a prefix of that order and draws from it by the inverse
 // of the cumulative weights.  Logits are bf16, so a row of V columns holds few
 // distinct values, and columns of one value share one weight: how often each
-// value occurs is all the order and the weights depend on.  So a row is read
-// once into registers and counted into a histogram of its values; every
-// cut-off is then a prefix sum over bins, and the chosen token is the r-th
-// column, in column order, whose value is the chosen bin's.
+// value occurs is all the order and the weights depend on.  Counted into a
+// histogram of its values, a row's every cut-off is a prefix sum over bins, and
+// the chosen token is the r-th column, in column order, whose value is the
+// chosen bin's.
 //
 // One cluster of C CTAs works on one row, each CTA on a contiguous part of its
-// columns, by one of two ways.
+// columns, by one of two ways.  What the columns must be compared with is not
+// known before they are read, so the first chunk (8 vectors per thread) is read
+// twice, the second time from L1 or L2 (or held in registers); the rest once.
 //
 // List: where a bound is known below which nothing can be kept (small top-k:
 // at least k of the first chunk's columns reach it; min-p alone), and for rows
-// short enough to be sorted whole, the columns
-// that reach it go to a list in the first CTA's shared memory, which sorts
-// them and finishes the row by itself.  Almost every 16-byte vector of the row
-// is dismissed by one packed maximum, so this way runs at the speed of the
-// read.
+// short enough to be sorted whole, the columns that reach it go to a list in
+// the first CTA's shared memory, which sorts them and finishes the row by
+// itself.  Almost every 16-byte vector of the row is dismissed by one packed
+// maximum: 512 rows of 262,144 under top-k 50 take 67 us (4.0 TB/s; the first
+// chunk's and the list's latencies and the fourth row of some SMs are the
+// rest), 8 rows 10.8 us, all latency (two cluster barriers, the list).
 //
 // Histogram: else (or when the list overflows) every CTA counts its columns by
 // value into its own histogram; the CTAs weigh and sum the histograms over the
@@ -28,7 +31,10 @@
 // every CTA finds the cut-offs and the draw for itself, looking into a block
 // only where one falls, and the CTA that holds the r-th column of the chosen
 // value finds it in a second look at its part.  One shared memory increment
-// per column bounds this way (about six cycles per 32 of them).
+// per column bounds this way, 3.4 cycles per 32 of them with random bank
+// conflicts (on average half a row is read again besides): 512 rows of 262,144
+// unfiltered take 135 us (2.0 TB/s), 64 rows 28 us; the blocks' weights are a
+// fifth of that.
 //
 // Weights and masses are integers, so sums do not depend on any order and
 // comparisons are exact: w = 2^-((max - x) log2(e) / T) in units of 2^-62 (the
@@ -51,15 +57,15 @@
 
 namespace swa {
 
-constexpr int kSampMaxWarps = 32;
+constexpr int kSampMaxWarps = 16;
 constexpr int kSampHalf = 4096;            // bins per sign
 constexpr int kSampBins = 2 * kSampHalf;
 constexpr int kSampVpt = 8;                // 16-byte vectors of the first chunk per thread
 constexpr int kSampBlocks = kSampBins / 32;  // of 32 bins
 constexpr int kSampList = kSampBins / 2;   // columns the list holds
 constexpr int kSampSmall = 1024;           // rows up to here are always taken by list
-constexpr int kSampKeys = 1024;            // maxima the top-k bound is taken from, at most
-constexpr int kSampListK = 256;            // largest top-k taken by list
+constexpr int kSampKeys = 512;             // maxima the top-k bound is taken from
+constexpr int kSampListK = kSampKeys / 2;  // largest top-k taken by list
 constexpr int kSampMaxCluster = 8;
 constexpr int kSampRoom = 4 << 7;          // four octaves above the first chunk's largest
 constexpr float kSampCut = 50.f;           // columns 50 T below the maximum weigh under 2^-72
@@ -274,7 +280,7 @@ struct SampShared {
     uint32_t found[2][kSampMaxWarps];
     uint32_t keys[kSampKeys];
     uint64_t cut64;
-    uint32_t listed, bin, rank;
+    uint32_t listed, most, bin, rank;
     float lp;
     SampScale scale;
 };
@@ -293,7 +299,6 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     namespace cg = cooperative_groups;
     constexpr int kWarps = NT / 32;
     constexpr int kChunk = kSampVpt * NT;      // vectors of the first chunk
-    constexpr int kKeys = NT < 512 ? 512 : NT;  // maxima the top-k bound is taken from
     constexpr uint32_t kPart = kSampList / C;  // list entries of one CTA
     const float INF = __int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     };
     if (tid < 256) sh.table[tid] = kSampTable.v[tid];
     if (tid == 0) {
-        sh.listed = sh.bin = sh.rank = 0;
+        sh.listed = sh.most = sh.bin = sh.rank = 0;
         sh.lp = 0.f;
     }
     for (int i = tid; i < kSampBins / 4; i += NT)
@@ -361,11 +366,13 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
         for (int v = 0; v < kSampVpt; ++v) held[v] = load(g0 + tid + v * NT);
     }
     // f(vector number, vector) over this thread's vectors of [g0, end), eight
-    // loads at a time; every thread of the CTA takes the same number of steps
-    auto each = [&](int end, auto f) {
+    // loads at a time; every thread of the CTA takes the same number of steps,
+    // and more(step) says after each whether to go on
+    auto each = [&](int end, auto f, auto more) {
         if constexpr (HOLD) {
 #pragma unroll
             for (int v = 0; v < kSampVpt; ++v) f(g0 + tid + v * NT, held[v]);
+            if (!more(0)) return;
         }
         constexpr int U = kSampVpt;
         for (int s = g0 + (HOLD ? kChunk : 0); s < end; s += U * NT) {
@@ -380,8 +387,10 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
             }
 #pragma unroll
             for (int v = 0; v < U; ++v) f(g + v * NT, w[v]);
+            if (!more((s - g0) / kChunk)) return;
         }
     };
+    auto always = [](int) { return true; };
 
     // ---- the request's settings
     const int b = (int)(row / A.q_len);
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     {
         // (a thread's maxima of several parts of the chunk, as many as there
         // are keys)
-        constexpr int kParts = kKeys / NT;
+        constexpr int kParts = kSampKeys / NT;
         static_assert(kParts == 1 || kParts == 2, "one or two maxima per thread");
         const __nv_bfloat162 none = __floats2bfloat162_rn(-INF, -INF);
         __nv_bfloat162 hi2[kParts];
@@ -429,7 +438,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 hi2[0] = __hmax2(hi2[0], second ? none : x);
                 hi2[kParts - 1] = __hmax2(hi2[kParts - 1], second ? x : none);
             }
-        });
+        }, always);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             const float x = fmaxf(__low2float(hi2[i]), __high2float(hi2[i]));
@@ -461,13 +470,13 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
         float x = -INF;
         if (k <= kSampListK) {
             const int n = warp == 1 ? (int)k : (int)((k + C - 1) / C);
-            uint32_t key[kKeys / 32], lo = 0;
+            uint32_t key[kSampKeys / 32], lo = 0;
 #pragma unroll
-            for (int i = 0; i < kKeys / 32; ++i) key[i] = sh.keys[i * 32 + lane];
+            for (int i = 0; i < kSampKeys / 32; ++i) key[i] = sh.keys[i * 32 + lane];
             for (uint32_t bit = 0x8000u; bit > 0; bit >>= 1) {
                 int c = 0;
 #pragma unroll
-                for (int i = 0; i < kKeys / 32; ++i) c += key[i] >= (lo | bit);
+                for (int i = 0; i < kSampKeys / 32; ++i) c += key[i] >= (lo | bit);
                 if (__reduce_add_sync(0xffffffffu, c) >= n) lo |= bit;
             }
             x = __uint_as_float((lo & 0x8000u ? lo & 0x7fffu : 0xffffu - lo) << 16);
@@ -543,6 +552,16 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                         samp_entry(samp_value(e & 1 ? pair >> 16 : pair & 0xffffu),
                                    (uint32_t)(8LL * g - off + e));
             }
+        }, [&](int step) {
+            // (a list that the first chunk shows to overflow is given up at once:
+            // 512 rows of 262144, min-p 0.05 alone, 201 -> 130 us)
+            const uint32_t listed = *(volatile uint32_t *)&sh.listed;
+            if (step > 0 || !rest) return listed <= kPart;
+            __syncthreads();
+            const bool on = (uint64_t)sh.listed * (uint32_t)cv <= (uint64_t)kPart * kChunk;
+            __syncthreads();
+            if (!on && tid == 0) sh.listed = kPart + 1;
+            return on;
         });
         __syncthreads();
         if (tid < C) *at(&sh.list_n[rank], tid) = sh.listed;
@@ -577,11 +596,26 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                     if (tid + i * NT < n) sh.list[tid + i * NT] = mine[i];
                 __syncthreads();
             }
-            if (n > 160 && k < (long long)n) {
-                // more than top-k's: those that reach the k-th largest value, found
-                // by counting the keys' upper, then their lower bytes
+            auto value_of = [&](uint32_t key) {
+                return __uint_as_float((key & 0x8000u ? key & 0x7fffu : 0xffffu - key) << 16);
+            };
+            const bool by_line = mp > 0.f && !has_p, by_count = k < (long long)n;
+            if (n > 160 && (by_line || by_count)) {
+                // fewer to sort: those on min-p's line of the row's own maximum
+                float low = R.cut;
+                if (by_line) {
+                    uint32_t most = 0;
+                    for (uint32_t i = tid; i < n; i += NT)
+                        most = max(most, (uint32_t)(sh.list[i] >> 32));
+                    most = __reduce_max_sync(0xffffffffu, most);
+                    if (lane == 0) atomicMax(&sh.most, most);
+                    __syncthreads();
+                    low = fmaxf(low, cut_of(value_of(sh.most)));
+                }
+                // and those that reach the k-th largest value, found by counting the
+                // keys' upper, then their lower bytes
                 uint32_t lo = 0, left = (uint32_t)k;  // left: still to find
-                for (int half = 1; half >= 0; --half) {
+                for (int half = 1; by_count && half >= 0; --half) {
                     if (tid < 256) sh.blk_cnt[tid] = 0;
                     __syncthreads();
                     for (uint32_t i = tid; i < n; i += NT) {
@@ -616,7 +650,8 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 for (int i = 0; i < kSampList / NT; ++i) {
                     const uint32_t at_i = tid + i * NT;
                     mine[i] = at_i < n ? sh.list[at_i] : 0;
-                    if ((uint32_t)(mine[i] >> 32) < lo) mine[i] = 0;
+                    const uint32_t key = (uint32_t)(mine[i] >> 32);
+                    if (key < lo || !(value_of(key) >= low)) mine[i] = 0;
                     c += mine[i] != 0;
                 }
                 if (tid == 0) sh.listed = 0;
@@ -644,7 +679,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 const uint64_t e = (uint32_t)tid < n ? sh.list[tid] : 0;
                 uint32_t place = 0;
                 if ((uint32_t)(tid & ~31) < n)
-    #pragma unroll 4
+#pragma unroll 4
                     for (uint32_t i = 0; i < n; ++i) place += sh.list[i] > e;
                 __syncthreads();
                 if ((uint32_t)tid < n) sh.list[place] = e;
@@ -672,15 +707,11 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
             // consecutive places per thread where there are many
             const uint32_t kept = k < (long long)n ? (uint32_t)k : n;
             const int per = kept <= NT ? 1 : kSampList / NT;
-            auto value_of = [&](uint64_t e) {
-                const uint32_t key = (uint32_t)(e >> 32);
-                return __uint_as_float((key & 0x8000u ? key & 0x7fffu : 0xffffu - key) << 16);
-            };
-            const float top = value_of(sh.list[0]);
+            const float top = value_of((uint32_t)(sh.list[0] >> 32));
             const float cut = fmaxf(R.cut, cut_of(top));  // (the row's own, now)
             const uint64_t ymax = falling_of(top);
             auto weight_at = [&](uint32_t i) -> uint64_t {
-                const float x = i < kept ? value_of(sh.list[i]) : -INF;
+                const float x = i < kept ? value_of((uint32_t)(sh.list[i] >> 32)) : -INF;
                 return x >= cut ? samp_weight(falling_of(x) - ymax, sh.table) >> 12 : 0;
             };
             uint64_t sum = 0;
@@ -762,7 +793,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 atomicAdd(reinterpret_cast<uint32_t *>(base + (o & 0xffffu)), 1u);
                 atomicAdd(reinterpret_cast<uint32_t *>(base + (o >> 16)), 1u);
             }
-        });
+        }, always);
         const float hi = block_max(fmaxf(__low2float(hi2), __high2float(hi2)));
         if (tid < C) *at(&sh.max2[round][rank], tid) = hi;
         cluster_sync();
@@ -825,19 +856,19 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 *at(&sh.blk_mass[blk][1], lane) = (uint64_t)(m >> 64);
             }
         };
-        // two blocks at a time: a weight is a long chain of multiplications
-        auto weigh = [&](int blk0, int blk1, uint32_t c0, uint32_t c1) {
-            const int blk[2] = {blk0, blk1};
-            uint32_t c[2] = {c0, c1}, c_mp[2];
-            u128 m[2];
+        // several blocks at a time: a weight is a long chain of multiplications
+        auto weigh = [&](const auto &blk, auto &c) {
+            constexpr int n = sizeof(c) / sizeof(c[0]);
+            uint32_t c_mp[n];
+            u128 m[n];
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
+            for (int v = 0; v < n; ++v) {
                 const uint64_t w = bin_weight(blk[v] * 32 + lane);
                 c_mp[v] = w >= mp_w ? c[v] : 0;
                 m[v] = (u128)w * c[v];
             }
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
+            for (int v = 0; v < n; ++v) {
                 c[v] = __reduce_add_sync(0xffffffffu, c[v]);
                 c_mp[v] = __reduce_add_sync(0xffffffffu, c_mp[v]);
                 m[v] = sum128(m[v]);
@@ -852,7 +883,9 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
 #pragma unroll
             for (int i = 0; i < kMine; i += 2) {
                 if (__any_sync(0xffffffffu, (c[i] | c[i + 1]) != 0)) {
-                    weigh(block_of(i), block_of(i + 1), c[i], c[i + 1]);
+                    const int blk[2] = {block_of(i), block_of(i + 1)};
+                    uint32_t pair[2] = {c[i], c[i + 1]};
+                    weigh(blk, pair);
                 } else {
                     tell(block_of(i), 0, 0, 0);
                     tell(block_of(i + 1), 0, 0, 0);
@@ -868,12 +901,18 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 else
                     tell(block_of(i), 0, 0, 0);
             while (full != 0) {
-                const int i = __ffs(full) - 1;
-                full &= full - 1;
-                const int j = full != 0 ? __ffs(full) - 1 : i;
-                full &= full - 1;
-                weigh(block_of(i), block_of(j), bin_count(block_of(i) * 32 + lane),
-                      bin_count(block_of(j) * 32 + lane));
+                constexpr int n = 4;  // (the last of them over again where fewer are left)
+                int blk[n];
+                uint32_t c[n];
+                int i = 0;
+#pragma unroll
+                for (int v = 0; v < n; ++v) {
+                    if (full != 0) i = __ffs(full) - 1;
+                    full &= full - 1;
+                    blk[v] = block_of(i);
+                    c[v] = bin_count(blk[v] * 32 + lane);
+                }
+                weigh(blk, c);
             }
         }
     }
@@ -1018,7 +1057,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                     const float x = samp_value(e & 1 ? h[e >> 1] >> 16 : h[e >> 1] & 0xffffu);
                     n += x <= plo && x >= -nlo && pred(samp_key(x)) ? 1 : 0;
                 }
-            });
+            }, always);
             n = __reduce_add_sync(0xffffffffu, n);
             __syncthreads();
             if (lane == 0) sh.found[0][warp] = n;

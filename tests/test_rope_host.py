@@ -19,7 +19,7 @@ def lib():
 
 
 GOOD_DIMS = (2, 8, 8, 2, 256, 4096, 0)
-GOOD_ROPE = dict(q_row=12 * 256, k_row=12 * 256, v_row=12 * 256, q_weight=1024, k_weight=2048,
+GOOD_ROPE = dict(q_row=13 * 256, k_row=13 * 256, v_row=13 * 256, q_weight=1024, k_weight=2048,
                  inv_freq=4096, eps=1e-6, rot_dim=256, interleaved=0)
 PTRS = dict(q=16, k=32, v=48, q_pos=64, q_out=80, k_out=96, v_out=112)
 
@@ -60,7 +60,7 @@ def test_bad_dims(lib, call, dims, code):
 @pytest.mark.parametrize("rope", [
     {"rot_dim": 24}, {"rot_dim": 272}, {"rot_dim": -16}, {"interleaved": 2}, {"inv_freq": None},
     {"eps": 0.0}, {"eps": float("nan")}, {"eps": float("inf")}, {"q_row": 8 * 256 - 8},
-    {"k_row": 12 * 256 + 4}, {"v_row": 0}, {"q_weight": 1028}, {"inv_freq": 4098},
+    {"k_row": 13 * 256 + 4}, {"v_row": 0}, {"q_weight": 1028}, {"inv_freq": 4098},
 ])
 def test_bad_rope(lib, call, rope):
     assert call(lib, rope=rope) == swa.SWA_ERR_INVALID_ARG and swa.swa_last_error()

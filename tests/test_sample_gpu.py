@@ -365,3 +365,28 @@ def test_rows_that_outgrow_their_first_chunk():
     many = xs.repeat(40, 1, 1)
     s = _settings(40 * n, 19, "all")
     _check(many, s, np.random.default_rng(4).random((40 * n, 1)).astype(np.float32), what="one CTA per row")
+
+
+@pytest.mark.parametrize("n", [2, 30, 70, 160])
+def test_lists_of_every_length(n):
+    """min-p alone at lines that leave from one to many thousands of columns
+    listed: given up after the first chunk, cut by the row's own maximum, sorted
+    in each way; rows whose large logits lie in the first chunk only (which
+    promises more than there are) or behind it only."""
+    V = 150001
+    x = _logits("normal", (n, 1, V), seed=23).clone()
+    rng = np.random.default_rng(n)
+    for b in range(n):
+        if b % 5 == 1:
+            x[b, 0, 4000:] = -20.0
+        elif b % 5 == 2:
+            x[b, 0, :140000] = -20.0
+        elif b % 5 == 3:
+            x[b, 0, rng.integers(0, V, 4)] = 16.0
+    s = _settings(n, 29, "m")
+    s["min_p"] = (10.0 ** rng.uniform(-4, -0.1, n)).astype(np.float32)
+    s["temperature"] = np.full(n, 1.0, np.float32)
+    u = rng.random((n, 1)).astype(np.float32)
+    _check(x, s, u, what="min-p")
+    s["top_k"] = rng.choice([0, 100, 255, 256, 257], n).astype(np.int32)
+    _check(x, s, u, what="min-p and top-k")
