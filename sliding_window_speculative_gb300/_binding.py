@@ -638,17 +638,16 @@ class PreparedCall:
 
 _MARSHAL = {"swa_verify_attn": _marshal_verify, "swa_verify_attn_noalloc": _marshal_noalloc,
             "swa_verify_attn_paged": _marshal_paged, "swa_append_verify_attn": _marshal_append,
-           "swa_qk_norm_rope": _marshal_rope_rows,
-           "swa_qk_norm_rope_append": _marshal_rope_append,
-           "swa_sample_accept": _marshal_sample, "swa_sink_verify_attn": _marshal_sink}
+            "swa_sink_verify_attn": _marshal_sink, "swa_qk_norm_rope": _marshal_rope_rows,
+            "swa_qk_norm_rope_append": _marshal_rope_append, "swa_sample_accept": _marshal_sample}
 
 
 def prepare(fn, *args, **kwargs):
     """Validate and marshal a call of swa_verify_attn, swa_verify_attn_noalloc,
     swa_verify_attn_paged, swa_append_verify_attn, swa_sink_verify_attn,
     swa_qk_norm_rope, swa_qk_norm_rope_append or swa_sample_accept once, with
-    the same arguments the function takes, and return a PreparedCall that issues it (on the
-    device that is current then: the tensors').
+    the same arguments the function takes, and return a PreparedCall that
+    issues it (on the device that is current then: the tensors').
 
     The per-call host cost is then one C call: no tensor checks, no struct
     building, no stream lookup (the stream is the one given, or torch's

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) swa_rope_kerne
     while (cur.work < n_work) {
         const int tok = token_of(cur);
         const int b = tok / q_len, i = tok - b * q_len;
-        const int pos = R.q_pos[b] + i;
+        const long long pos = (long long)R.q_pos[b] + i;
         bool kv_live = true;            // the token's key and value rows are stored
         long long kv_step = D, row = 0;  // elements between heads' rows; the first one's
         if (R.to_cache) {
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) swa_rope_kerne
             kv_live = pos >= 0 && pos < P.L && pos < P.seq_lens[b];
             if (kv_live) {
                 bool bad = false;
-                row = cache_row(P, b, 0, pos, &bad) * D;
+                row = cache_row(P, b, 0, (int)pos, &bad) * D;
                 kv_live = !bad;
             }
             kv_step = (long long)(P.block_table != nullptr ? P.page_size : P.L) * D;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) swa_rope_kerne
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
                     const int n = (e < 2 ? pair0 : pair1) + 2 * (e & 1) + o;
-                    rope_cos_sin((uint32_t)((turn_s[n] * (uint64_t)(int64_t)pos) >> 32), c[o], s[o]);
+                    rope_cos_sin((uint32_t)((turn_s[n] * (uint64_t)pos) >> 32), c[o], s[o]);
                 }
                 cs[e] = f2_pack(c[0], c[1]);
                 sn[e] = f2_pack(s[0], s[1]);

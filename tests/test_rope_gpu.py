@@ -96,7 +96,7 @@ def test_norms_are_optional(q_norm, k_norm, packed):
         assert torch.equal(k, c["k"])
 
 
-@pytest.mark.parametrize("pos", [0, 1, 65535, 1 << 20, (1 << 24) + 1, (1 << 31) - 9])
+@pytest.mark.parametrize("pos", [0, 1, 65535, 1 << 20, (1 << 24) + 1, (1 << 31) - 9, (1 << 31) - 1])
 def test_far_positions(pos):
     """The angle keeps its fraction of a turn at any position: 2^-53 of the
     fp64 angle (the definition's own rounding) is the only added slack."""
