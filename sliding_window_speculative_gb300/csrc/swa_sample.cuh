@@ -63,7 +63,8 @@ constexpr int kSampBins = 2 * kSampHalf;
 constexpr int kSampVpt = 8;                // 16-byte vectors of the first chunk per thread
 constexpr int kSampBlocks = kSampBins / 32;  // of 32 bins
 constexpr int kSampList = kSampBins / 2;   // columns the list holds
-constexpr int kSampSmall = 1024;           // rows up to here are always taken by list
+constexpr int kSampSort = 1024;            // longer lists are counted instead
+constexpr int kSampSmall = kSampSort;      // rows up to here are always taken by list
 constexpr int kSampKeys = 512;             // maxima the top-k bound is taken from
 constexpr int kSampListK = kSampKeys / 2;  // largest top-k taken by list
 constexpr int kSampMaxCluster = 8;
@@ -573,6 +574,13 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
             n += sh.list_n[r];
             fits = fits && sh.list_n[r] <= kPart;
         }
+        // (long lists cost more to sort than the histogram does; top-k's are cut
+        // to k first, one CTA's by the row's own line.  Rows of 262144 with 2000
+        // to 4000 columns on min-p's line, us, sorted / counted: 8 rows 57 / 23,
+        // 64 rows 98 / 41; with 600 to 2300 listed by 2 CTAs each 128 rows
+        // 58 / 68, by 4 each 64 rows 62 / 54)
+        const bool by_line = mp > 0.f && !has_p, by_count = k < (long long)n;
+        if (C > 1 && !by_count && n > kSampSort) fits = false;
         if (fits) {
             if (rank != 0) return;
             if constexpr (C > 1) {
@@ -599,7 +607,6 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
             auto value_of = [&](uint32_t key) {
                 return __uint_as_float((key & 0x8000u ? key & 0x7fffu : 0xffffu - key) << 16);
             };
-            const bool by_line = mp > 0.f && !has_p, by_count = k < (long long)n;
             if (n > 160 && (by_line || by_count)) {
                 // fewer to sort: those on min-p's line of the row's own maximum
                 float low = R.cut;
@@ -663,110 +670,113 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 __syncthreads();
                 n = sh.listed;
             }
-            if (n <= NT / 4) {
-                // every entry's place is the number of larger ones: four
-                // threads count for one
-                const uint32_t who = tid >> 2;
-                const uint64_t e = who < n ? sh.list[who] : 0;
-                uint32_t place = 0;
+            if (C > 1 || n <= kSampSort) {
+                if (n <= NT / 4) {
+                    // every entry's place is the number of larger ones: four
+                    // threads count for one
+                    const uint32_t who = tid >> 2;
+                    const uint64_t e = who < n ? sh.list[who] : 0;
+                    uint32_t place = 0;
 #pragma unroll 4
-                for (uint32_t i = tid & 3; i < n; i += 4) place += sh.list[i] > e;
-                place += __shfl_xor_sync(0xffffffffu, place, 1);
-                place += __shfl_xor_sync(0xffffffffu, place, 2);
-                __syncthreads();
-                if (who < n && (tid & 3) == 0) sh.list[place] = e;
-            } else if (n <= NT) {
-                const uint64_t e = (uint32_t)tid < n ? sh.list[tid] : 0;
-                uint32_t place = 0;
-                if ((uint32_t)(tid & ~31) < n)
+                    for (uint32_t i = tid & 3; i < n; i += 4) place += sh.list[i] > e;
+                    place += __shfl_xor_sync(0xffffffffu, place, 1);
+                    place += __shfl_xor_sync(0xffffffffu, place, 2);
+                    __syncthreads();
+                    if (who < n && (tid & 3) == 0) sh.list[place] = e;
+                } else if (n <= NT) {
+                    const uint64_t e = (uint32_t)tid < n ? sh.list[tid] : 0;
+                    uint32_t place = 0;
+                    if ((uint32_t)(tid & ~31) < n)
 #pragma unroll 4
-                    for (uint32_t i = 0; i < n; ++i) place += sh.list[i] > e;
-                __syncthreads();
-                if ((uint32_t)tid < n) sh.list[place] = e;
-            } else {
-                // many equal values: a bitonic network over the list
-                uint32_t size = NT;
-                while (size < n) size *= 2;
-                for (uint32_t i = n + tid; i < size; i += NT) sh.list[i] = 0;
-                __syncthreads();
-                for (uint32_t span = 2; span <= size; span *= 2)
-                    for (uint32_t d = span / 2; d > 0; d /= 2) {
-                        for (uint32_t i = tid; i < size / 2; i += NT) {
-                            const uint32_t x = 2 * i - (i & (d - 1)), y = x + d;
-                            const uint64_t p = sh.list[x], q = sh.list[y];
-                            if ((p < q) == ((x & span) == 0)) {
-                                sh.list[x] = q;
-                                sh.list[y] = p;
+                        for (uint32_t i = 0; i < n; ++i) place += sh.list[i] > e;
+                    __syncthreads();
+                    if ((uint32_t)tid < n) sh.list[place] = e;
+                } else {
+                    // many equal values: a bitonic network over the list
+                    uint32_t size = NT;
+                    while (size < n) size *= 2;
+                    for (uint32_t i = n + tid; i < size; i += NT) sh.list[i] = 0;
+                    __syncthreads();
+                    for (uint32_t span = 2; span <= size; span *= 2)
+                        for (uint32_t d = span / 2; d > 0; d /= 2) {
+                            for (uint32_t i = tid; i < size / 2; i += NT) {
+                                const uint32_t x = 2 * i - (i & (d - 1)), y = x + d;
+                                const uint64_t p = sh.list[x], q = sh.list[y];
+                                if ((p < q) == ((x & span) == 0)) {
+                                    sh.list[x] = q;
+                                    sh.list[y] = p;
+                                }
                             }
+                            __syncthreads();
                         }
-                        __syncthreads();
-                    }
-            }
-            __syncthreads();
-            // ---- in order: weights in units of 2^-50, running sums; eight
-            // consecutive places per thread where there are many
-            const uint32_t kept = k < (long long)n ? (uint32_t)k : n;
-            const int per = kept <= NT ? 1 : kSampList / NT;
-            const float top = value_of((uint32_t)(sh.list[0] >> 32));
-            const float cut = fmaxf(R.cut, cut_of(top));  // (the row's own, now)
-            const uint64_t ymax = falling_of(top);
-            auto weight_at = [&](uint32_t i) -> uint64_t {
-                const float x = i < kept ? value_of((uint32_t)(sh.list[i] >> 32)) : -INF;
-                return x >= cut ? samp_weight(falling_of(x) - ymax, sh.table) >> 12 : 0;
-            };
-            uint64_t sum = 0;
-            for (int i = 0; i < per; ++i) sum += weight_at(tid * per + i);
-            uint64_t pre = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t x = __shfl_up_sync(0xffffffffu, pre, o);
-                if (lane >= o) pre += x;
-            }
-            if (lane == 31) sh.wmass[warp][0] = pre;
-            if (tid == 0) sh.cut64 = ~0ull;
-            __syncthreads();
-            pre -= sum;
-            uint64_t S = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) pre += sh.wmass[w][0];
-                S += sh.wmass[w][0];
-            }
-            if (has_p || mp > 0.f) {
-                const uint64_t mp_w = (uint64_t)scale_down((u128)1 << 51, 0.5f * mp, true);
-                uint64_t X = tp > 0.f && has_p ? (uint64_t)scale_down(S, tp, true) : has_p ? 1 : S;
-                if (X == 0) X = 1;
-                uint64_t m = pre;
-                for (int i = 0; i < per; ++i) {
-                    const uint64_t w = weight_at(tid * per + i);
-                    // where the running weight reaches p's share, and the last
-                    // column on min-p's line
-                    if (m < X && X <= m + w) atomicMin((unsigned long long *)&sh.cut64, m + w);
-                    if (w >= mp_w && w != 0 && weight_at(tid * per + i + 1) < mp_w)
-                        atomicMin((unsigned long long *)&sh.cut64, m + w);
-                    m += w;
                 }
                 __syncthreads();
-                if (sh.cut64 < S) S = sh.cut64;
-            }
-            const uint64_t target = (uint64_t)scale_down(S, u, false);
-            if (pre <= target && target < pre + sum) {
-                uint64_t m = pre;
-                for (int i = 0; i < per; ++i) {
-                    const uint64_t w = weight_at(tid * per + i);
-                    if (m <= target && target < m + w) {
-                        // ln(w / S), by the rest's share where w is most of S
-                        const float sf = __ull2float_rn(S);
-                        finish(0xffffffffu - (uint32_t)sh.list[tid * per + i],
-                               2 * w > S ? log1pf(-(__ull2float_rn(S - w) / sf))
-                                         : logf(__ull2float_rn(w) / sf));
-                    }
-                    m += w;
+                // ---- in order: weights in units of 2^-50, running sums; eight
+                // consecutive places per thread where there are many
+                const uint32_t kept = k < (long long)n ? (uint32_t)k : n;
+                const int per = kept <= NT ? 1 : kSampList / NT;
+                const float top = value_of((uint32_t)(sh.list[0] >> 32));
+                const float cut = fmaxf(R.cut, cut_of(top));  // (the row's own, now)
+                const uint64_t ymax = falling_of(top);
+                auto weight_at = [&](uint32_t i) -> uint64_t {
+                    const float x = i < kept ? value_of((uint32_t)(sh.list[i] >> 32)) : -INF;
+                    return x >= cut ? samp_weight(falling_of(x) - ymax, sh.table) >> 12 : 0;
+                };
+                uint64_t sum = 0;
+                for (int i = 0; i < per; ++i) sum += weight_at(tid * per + i);
+                uint64_t pre = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint64_t x = __shfl_up_sync(0xffffffffu, pre, o);
+                    if (lane >= o) pre += x;
                 }
+                if (lane == 31) sh.wmass[warp][0] = pre;
+                if (tid == 0) sh.cut64 = ~0ull;
+                __syncthreads();
+                pre -= sum;
+                uint64_t S = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) pre += sh.wmass[w][0];
+                    S += sh.wmass[w][0];
+                }
+                if (has_p || mp > 0.f) {
+                    const uint64_t mp_w = (uint64_t)scale_down((u128)1 << 51, 0.5f * mp, true);
+                    uint64_t X = tp > 0.f && has_p ? (uint64_t)scale_down(S, tp, true) : has_p ? 1 : S;
+                    if (X == 0) X = 1;
+                    uint64_t m = pre;
+                    for (int i = 0; i < per; ++i) {
+                        const uint64_t w = weight_at(tid * per + i);
+                        // where the running weight reaches p's share, and the last
+                        // column on min-p's line
+                        if (m < X && X <= m + w) atomicMin((unsigned long long *)&sh.cut64, m + w);
+                        if (w >= mp_w && w != 0 && weight_at(tid * per + i + 1) < mp_w)
+                            atomicMin((unsigned long long *)&sh.cut64, m + w);
+                        m += w;
+                    }
+                    __syncthreads();
+                    if (sh.cut64 < S) S = sh.cut64;
+                }
+                const uint64_t target = (uint64_t)scale_down(S, u, false);
+                if (pre <= target && target < pre + sum) {
+                    uint64_t m = pre;
+                    for (int i = 0; i < per; ++i) {
+                        const uint64_t w = weight_at(tid * per + i);
+                        if (m <= target && target < m + w) {
+                            // ln(w / S), by the rest's share where w is most of S
+                            const float sf = __ull2float_rn(S);
+                            finish(0xffffffffu - (uint32_t)sh.list[tid * per + i],
+                                   2 * w > S ? log1pf(-(__ull2float_rn(S - w) / sf))
+                                             : logf(__ull2float_rn(w) / sf));
+                        }
+                        m += w;
+                    }
+                }
+                return;
             }
-            return;
         }
         // too many: count them (the first CTA's list gives way to its histogram)
+        __syncthreads();
         for (int i = tid; i < kSampBins / 4; i += NT)
             reinterpret_cast<uint4 *>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
@@ -1040,7 +1050,6 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
 
     // ---- its place: the r-th column, in column order, of the bin's value
     uint32_t value = (uint32_t)samp_bin_mk(R, bin) | (bin >= kSampHalf ? 0x8000u : 0u);
-    bool zero = false;  // the value is 0: of either sign
     uint32_t before = 0, here;
     if (samp_shared_bin(bin)) {
         // the two bins of many values, in order one after the other: the value
@@ -1085,7 +1094,6 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
             if (q < rank) before += sh.refine[17][q];
         here = sh.refine[17][rank];
         value = key & 0x8000u ? key & 0x7fffu : 0xffffu - key;
-        zero = value == 0;
     } else {
 #pragma unroll
         for (int q = 0; q < C; ++q)
@@ -1095,10 +1103,10 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     cluster_arrive();  // no CTA leaves while its shared memory is read
     if (r >= before && r < before + here) {
         r -= before;
-        // vectors in column order, eight of a thread's per step
+        // vectors in column order, eight of a thread's per step (compared as
+        // numbers: 0 equals -0)
         const uint32_t both = value * 0x10001u;
         const __nv_bfloat162 want = *reinterpret_cast<const __nv_bfloat162 *>(&both);
-        (void)zero;  // (0 equals -0 as a number)
         constexpr int U = 8;
         for (int g = g0 + tid, step = 0; g - tid < g1; g += U * NT, ++step) {
             uint32_t hit[U];  // bit 2 e (2 e + 1): the lower (upper) half of word e
