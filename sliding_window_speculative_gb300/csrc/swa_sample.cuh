@@ -1103,29 +1103,43 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     cluster_arrive();  // no CTA leaves while its shared memory is read
     if (r >= before && r < before + here) {
         r -= before;
-        // vectors in column order, eight of a thread's per step (compared as
-        // numbers: 0 equals -0)
+        // vectors in column order (compared as numbers: 0 equals -0), eight of
+        // a thread's per step; from whichever end the column is nearer to,
+        // counted in columns of the value
         const uint32_t both = value * 0x10001u;
         const __nv_bfloat162 want = *reinterpret_cast<const __nv_bfloat162 *>(&both);
         constexpr int U = 8;
-        for (int g = g0 + tid, step = 0; g - tid < g1; g += U * NT, ++step) {
-            uint32_t hit[U];  // bit 2 e (2 e + 1): the lower (upper) half of word e
-            {
-                uint4 w[U];
+        const int steps = (g1 - g0 + U * NT - 1) / (U * NT);
+        const bool back = r >= here - here / 2;
+        if (back) r = here - 1 - r;
+        uint4 w[U];
+        auto fetch = [&](int i) {
+            const int first = g0 + (back ? steps - 1 - i : i) * (U * NT), g = first + tid;
+            if (first >= in0 && first + U * NT <= min(g1, in1)) {
+#pragma unroll
+                for (int v = 0; v < U; ++v) w[v] = __ldg(vp + g + v * NT);
+            } else {
 #pragma unroll
                 for (int v = 0; v < U; ++v) w[v] = load(g + v * NT);
+            }
+            return g;
+        };
+        int next = fetch(0);
+        for (int step = 0; step < steps; ++step) {
+            const int g = next;
+            uint32_t hit[U];  // bit 2 e (2 e + 1): the lower (upper) half of word e
 #pragma unroll
-                for (int v = 0; v < U; ++v) {
-                    const uint32_t h[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
-                    hit[v] = 0;
+            for (int v = 0; v < U; ++v) {
+                const uint32_t h[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+                hit[v] = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t m =
-                            __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&h[e]), want);
-                        hit[v] |= ((m & 1u) | ((m >> 15) & 2u)) << (2 * e);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t m =
+                        __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&h[e]), want);
+                    hit[v] |= ((m & 1u) | ((m >> 15) & 2u)) << (2 * e);
                 }
             }
+            if (step + 1 < steps) next = fetch(step + 1);
             auto block_sum = [&](uint32_t n, uint32_t *f, uint32_t &first) {
                 n = __reduce_add_sync(0xffffffffu, n);
                 if (lane == 0) f[warp] = n;
@@ -1147,6 +1161,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 r -= total;
                 continue;
             }
+            if (back) r = total - 1 - r;
             // in this step: its vectors one after the other
             bool done = false;
 #pragma unroll
