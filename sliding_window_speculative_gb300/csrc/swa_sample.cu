@@ -43,7 +43,10 @@ cudaError_t launch_rows(const swa::SampleParams &A, long long rows, int sms, cud
     // on GB300, rows of 262144, us, unfiltered / top-k 50: 64 rows 4 CTAs of
     // 256 threads 30.6 / 18.5, of 512 32.8 / 18.5, 8 of 256 32.8; 128 rows 2 of
     // 512 47.1 / 22.6, 2 of 256 43.7 / 26.0, 1 of 256 - / 32.9; 512 rows 1 of
-    // 256 135 / 67, 1 of 512 133 / 69, 2 of 512 140 / 86.  8 rows, 8 CTAs:
+    // 256 135 / 67, 1 of 512 142 / 69, 2 of 512 145 / 86, 2 of 256 142 / 76; three
+    // CTAs of 256 to an SM, the others following, 124 / 97 where four take
+    // 128 / 79 between events (requests of mixed settings 99-109 and 107-119),
+    // but 64 rows 34.0 where four take 27.5.  8 rows, 8 CTAs:
     // the first chunk held in registers 12.5, read again 16.3.
     const long long nvec = ((long long)A.V + 14) / 8;
     int c = 1;

@@ -30,11 +30,11 @@
 // distributed shared memory) and tell each other the blocks' sums.  From these
 // every CTA finds the cut-offs and the draw for itself, looking into a block
 // only where one falls, and the CTA that holds the r-th column of the chosen
-// value finds it in a second look at its part.  One shared memory increment
-// per column bounds this way, 3.4 cycles per 32 of them with random bank
-// conflicts (on average half a row is read again besides): 512 rows of 262,144
-// unfiltered take 135 us (2.0 TB/s), 64 rows 28 us; the blocks' weights are a
-// fifth of that.
+// value finds it in a second look at its part, from the nearer end.  One shared
+// memory increment per column bounds this way, 3.4 to 4.5 cycles per 32 of them
+// with random bank conflicts (on average a quarter of a row is read again
+// besides): 512 rows of 262,144 unfiltered take 124 us (2.2 TB/s), 64 rows 27.5;
+// the blocks' weights are a fifth of that.
 //
 // Weights and masses are integers, so sums do not depend on any order and
 // comparisons are exact: w = 2^-((max - x) log2(e) / T) in units of 2^-62 (the
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
     const uint64_t mp_w = (uint64_t)scale_down((u128)1 << 63, 0.5f * mp, true);
     {
         constexpr int kMine = kSampBlocks / C / kWarps;  // blocks of this warp
-        static_assert(kMine % 2 == 0 && kMine * kWarps * C == kSampBlocks, "whole pairs of blocks");
+        static_assert(kMine * kWarps * C == kSampBlocks, "whole warps of blocks");
         auto block_of = [&](int i) { return rank * (kSampBlocks / C) + warp + i * kWarps; };
         auto tell = [&](int blk, uint32_t c, uint32_t c_mp, u128 m) {
             if (lane < C) {
@@ -890,15 +890,23 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
             uint32_t c[kMine];
 #pragma unroll
             for (int i = 0; i < kMine; ++i) c[i] = bin_count(block_of(i) * 32 + lane);
+            constexpr int n = kMine < 4 ? kMine : 4;
+            static_assert(kMine % n == 0, "whole groups of blocks");
 #pragma unroll
-            for (int i = 0; i < kMine; i += 2) {
-                if (__any_sync(0xffffffffu, (c[i] | c[i + 1]) != 0)) {
-                    const int blk[2] = {block_of(i), block_of(i + 1)};
-                    uint32_t pair[2] = {c[i], c[i + 1]};
-                    weigh(blk, pair);
+            for (int i = 0; i < kMine; i += n) {
+                int blk[n];
+                uint32_t some[n], any = 0;
+#pragma unroll
+                for (int v = 0; v < n; ++v) {
+                    blk[v] = block_of(i + v);
+                    some[v] = c[i + v];
+                    any |= some[v];
+                }
+                if (__any_sync(0xffffffffu, any != 0)) {
+                    weigh(blk, some);
                 } else {
-                    tell(block_of(i), 0, 0, 0);
-                    tell(block_of(i + 1), 0, 0, 0);
+#pragma unroll
+                    for (int v = 0; v < n; ++v) tell(blk[v], 0, 0, 0);
                 }
             }
         } else {
