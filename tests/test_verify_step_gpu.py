@@ -169,3 +169,40 @@ def test_a_captured_step_replays_on_new_inputs():
             for b in range(B):      # (the captured layer's warm-up wrote the first block too)
                 n = int(pos[b]) + Q
                 assert torch.equal(layer.rows(mine, b, n), plain.rows(ref, b, n))
+
+
+def test_largest_batch():
+    """65,535 sequences, the most an entry point takes: every one's results are
+    those of a batch of three that repeats."""
+    import sliding_window_speculative_gb300 as swa
+    g = torch.Generator().manual_seed(31)
+    B, n, D, L, V = 65535, 3, 64, 16, 37
+    rep = lambda t: t.repeat((B // n,) + (1,) * (t.dim() - 1)).cuda()  # noqa: E731
+    rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16)  # noqa: E731
+    x = rnd(n, 2, 4, D)
+    pos, lens = torch.tensor([0, 5, 13], dtype=torch.int32), torch.tensor([2, 7, 15], dtype=torch.int32)
+    f = (100.0 ** (-torch.arange(D // 2, dtype=torch.float64) / 32)).float().cuda()
+    k, v = rnd(n, 1, L, D), rnd(n, 1, L, D)
+
+    def step(x, k, v, pos, lens):
+        q = swa.swa_qk_norm_rope_append(x[:, :, :2], x[:, :, 2:3], x[:, :, 3:], None, None, 1e-6, f,
+                                        k, v, lens, pos)
+        return (q, k, v) + swa.swa_sink_verify_attn(q, k, v, lens, pos, 4, 2, D ** -0.5)
+
+    small = step(x.cuda(), k.cuda(), v.cuda(), pos.cuda(), lens.cuda())
+    large = step(*(rep(t) for t in (x, k, v, pos, lens)))
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(large, small)):
+        want = b.repeat((B // n,) + (1,) * (b.dim() - 1))
+        if i < 3:
+            assert torch.equal(a, want)
+        else:  # another plan may serve the larger batch: bf16's half step, twice
+            err = (a.double() - want.double()).abs()
+            assert (err <= 2.0 ** -7 * want.double().abs() + 2.0 ** -12).all(), i
+    logits, u = rnd(n, 2, V), torch.rand((n, 2), generator=g)
+    draft, T = torch.tensor([[1], [2], [3]], dtype=torch.int32), torch.tensor([0.7, 1.0, 0.0])
+    small = swa.swa_sample_accept(logits.cuda(), u.cuda(), T.cuda(), draft=draft.cuda())
+    large = swa.swa_sample_accept(rep(logits), rep(u), rep(T), draft=rep(draft))
+    torch.cuda.synchronize()
+    for a, b in zip(large, small):
+        assert torch.equal(a, b.repeat((B // n,) + (1,) * (b.dim() - 1)))
