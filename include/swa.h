@@ -90,8 +90,9 @@ typedef struct {
  * Workspace: when the chosen split count needs split partials in global
  * memory, they go to the workspace set with swa_set_workspace() for the
  * current device, or else to a library-owned buffer grown on demand with
- * cudaMalloc (never while `stream` is capturing: then SWA_ERR_WORKSPACE; an
- * outgrown buffer stays allocated, so that captured calls keep theirs).
+ * cudaMalloc (never while `stream` is capturing: then SWA_ERR_WORKSPACE).
+ * An outgrown buffer is freed first, unless a captured call was given it:
+ * then it stays allocated for the graph's replays.
  * All calls on one device share that buffer, so calls that may run at the
  * same time on different streams race on it; order them on one stream or
  * give each its own device.
@@ -253,10 +254,10 @@ size_t swa_workspace_bytes(const swa_dims *dims, int32_t window);
  * library-owned buffer.  The memory must stay valid until replaced. */
 swa_status swa_set_workspace(void *dev_ptr, size_t bytes);
 
-/* Release the library-owned workspace of the current device, outgrown buffers
- * too (synchronises the device through cudaFree).  Graphs that captured calls
- * with split partials must not be replayed afterwards; the same holds for
- * swa_set_workspace. */
+/* Release the library-owned workspace of the current device, buffers kept for
+ * captured calls too (synchronises the device through cudaFree).  Graphs that
+ * captured calls with split partials must not be replayed afterwards; the
+ * same holds for swa_set_workspace. */
 swa_status swa_release_workspace(void);
 
 /* What the library would launch for these dims on a GPU with `num_sms`

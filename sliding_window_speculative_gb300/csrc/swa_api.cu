@@ -15,6 +15,7 @@
 #include "swa_host.h"
 #include "swa_simt_launch.cuh"
 #include "swa_tc_host.h"
+#include "swa_workspace.h"
 
 // Fault word of each device that loads the library; kernels receive its
 // address and OR bits into it when a bounded wait gives up.  The word after
@@ -330,69 +331,34 @@ Plan make_plan(const swa_dims *d, int32_t window, int num_sms, bool pairs_ok) {
 
 // ------------------------------------------------------------- workspace
 
-// A library-owned buffer that was outgrown stays allocated (a captured graph
-// may replay calls that use it) until the workspace is released or replaced;
-// each is over a quarter larger than the one before, so a few slots hold any
-// number of bytes.
-constexpr int kMaxRetired = 256;
-
-struct Workspace {
-    void *ptr = nullptr;
-    size_t bytes = 0;
-    bool owned = false;
-    void *retired[kMaxRetired] = {};
-    int n_retired = 0;
-};
 std::mutex g_ws_mutex;
-Workspace g_ws[kMaxDevices];
+swa::Workspace g_ws[kMaxDevices];
 
-// Frees the library-owned buffers of a device, outgrown ones too.
-swa_status free_owned(Workspace &w) {
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; i < w.n_retired; ++i) {
-        const cudaError_t f = cudaFree(w.retired[i]);
-        if (e == cudaSuccess) e = f;
-    }
-    w.n_retired = 0;
-    if (w.owned && w.ptr) {
-        const cudaError_t f = cudaFree(w.ptr);
-        if (e == cudaSuccess) e = f;
-        w.ptr = nullptr;
-        w.bytes = 0;
-        w.owned = false;
-    }
+swa_status free_owned(swa::Workspace &w) {
+    const cudaError_t e = swa::workspace_free(w);
     return e == cudaSuccess ? SWA_OK : cuda_fail(e, "cudaFree(workspace)");
 }
 
 swa_status ensure_workspace(int dev, size_t need, cudaStream_t stream, void **out) {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace &w = g_ws[dev];
-    if (w.bytes >= need) {
-        *out = w.ptr;
-        return SWA_OK;
+    swa::Workspace &w = g_ws[dev];
+    if (w.bytes < need) {
+        if (!w.owned && w.ptr != nullptr)
+            return fail(SWA_ERR_WORKSPACE,
+                        "workspace set by the caller holds %zu bytes, %zu needed", w.bytes, need);
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+        if (cap != cudaStreamCaptureStatusNone)
+            return fail(SWA_ERR_WORKSPACE,
+                        "stream is capturing and the workspace (%zu bytes) is below the %zu "
+                        "needed; run one call outside capture first or set a workspace",
+                        w.bytes, need);
+        e = swa::workspace_grow(w, need);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
+    } else if (w.owned && !w.captured) {
+        w.captured = swa::stream_capturing(stream);
     }
-    if (!w.owned && w.ptr != nullptr)
-        return fail(SWA_ERR_WORKSPACE, "workspace set by the caller holds %zu bytes, %zu needed",
-                    w.bytes, need);
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(stream, &cap);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-    if (cap != cudaStreamCaptureStatusNone)
-        return fail(SWA_ERR_WORKSPACE,
-                    "stream is capturing and the workspace (%zu bytes) is below the %zu needed; "
-                    "run one call outside capture first or set a workspace",
-                    w.bytes, need);
-    if (w.n_retired == kMaxRetired)
-        return fail(SWA_ERR_WORKSPACE, "the workspace was outgrown %d times; release it", kMaxRetired);
-    size_t grow = need + need / 4;
-    if (w.ptr != nullptr && grow < w.bytes + w.bytes / 4) grow = w.bytes + w.bytes / 4;
-    void *ptr = nullptr;
-    e = cudaMalloc(&ptr, grow);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
-    if (w.ptr != nullptr) w.retired[w.n_retired++] = w.ptr;
-    w.ptr = ptr;
-    w.bytes = grow;
-    w.owned = true;
     *out = w.ptr;
     return SWA_OK;
 }
@@ -718,12 +684,12 @@ swa_status swa_set_workspace(void *dev_ptr, size_t bytes) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     if (dev >= kMaxDevices) return fail(SWA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace &w = g_ws[dev];
+    swa::Workspace &w = g_ws[dev];
     const swa_status st = free_owned(w);
     if (st != SWA_OK) return st;
     w.ptr = dev_ptr;
     w.bytes = bytes;
-    w.owned = false;
+    w.owned = w.captured = false;
     return SWA_OK;
 }
 
