@@ -370,7 +370,8 @@ swa_status swa_get_debug_options(swa_debug_options *opt);
  * (8 bytes per row and 4 per sequence, zero between calls): the first call
  * with a larger batch * q_len allocates and zeroes it, which is refused
  * with SWA_ERR_WORKSPACE while the stream is capturing (make one call of
- * the largest size before capture).  Calls that overlap on one device race
+ * the largest size before capture); what a captured call was given stays
+ * allocated for its replays.  Calls that overlap on one device race
  * on that scratch; order them (one stream, or events). */
 swa_status swa_greedy_accept(const void *logits, const int32_t *keep_ids, const int32_t *draft,
                              int32_t *argmax_out, int32_t *accepted, int32_t batch,

@@ -840,7 +840,7 @@ bool swa::launch_fault_due() {
 namespace {
 
 struct AcceptScratch {
-    void *ptr = nullptr;
+    swa::Workspace w;
     size_t rows = 0, seqs = 0;  // capacity: best slots, arrival counters
 };
 std::mutex g_acc_mutex;
@@ -848,7 +848,7 @@ AcceptScratch g_acc[kMaxDevices];
 
 // Zero-filled scratch of >= rows 64-bit slots and >= seqs counters; every
 // call leaves it zero again.  Grown (and zeroed on `stream`) outside stream
-// capture only.
+// capture only; what a captured call was given stays for its replays.
 swa_status ensure_accept_scratch(int dev, size_t rows, size_t seqs, cudaStream_t stream,
                                  unsigned long long **best, uint32_t **done) {
     std::lock_guard<std::mutex> lock(g_acc_mutex);
@@ -862,26 +862,23 @@ swa_status ensure_accept_scratch(int dev, size_t rows, size_t seqs, cudaStream_t
                         "stream is capturing and the acceptance scratch (%zu rows, %zu sequences) "
                         "is below the %zu rows, %zu sequences needed; run one call outside capture "
                         "first", a.rows, a.seqs, rows, seqs);
-        if (a.ptr) {
-            e = cudaFree(a.ptr);
-            a.ptr = nullptr;
-            a.rows = a.seqs = 0;
-            if (e != cudaSuccess) return cuda_fail(e, "cudaFree(acceptance scratch)");
-        }
-        const size_t nr = rows + rows / 4, ns = seqs + seqs / 4;
-        const size_t bytes = nr * 8 + ns * 4;
-        e = cudaMalloc(&a.ptr, bytes);
+        e = swa::workspace_grow(a.w, rows * 8 + seqs * 4);
         if (e != cudaSuccess) {
-            a.ptr = nullptr;
+            if (a.w.ptr == nullptr) a.rows = a.seqs = 0;
             return cuda_fail(e, "cudaMalloc(acceptance scratch)");
         }
-        e = cudaMemsetAsync(a.ptr, 0, bytes, stream);
+        a.rows = a.seqs = 0;
+        e = cudaMemsetAsync(a.w.ptr, 0, a.w.bytes, stream);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(acceptance scratch)");
-        a.rows = nr;
-        a.seqs = ns;
+        const size_t nr = rows + rows / 4, ns = seqs + seqs / 4;
+        const bool padded = nr * 8 + ns * 4 <= a.w.bytes;
+        a.rows = padded ? nr : rows;
+        a.seqs = padded ? ns : seqs;
+    } else if (!a.w.captured) {
+        a.w.captured = swa::stream_capturing(stream);
     }
-    *best = static_cast<unsigned long long *>(a.ptr);
-    *done = reinterpret_cast<uint32_t *>(static_cast<unsigned long long *>(a.ptr) + a.rows);
+    *best = static_cast<unsigned long long *>(a.w.ptr);
+    *done = reinterpret_cast<uint32_t *>(static_cast<unsigned long long *>(a.w.ptr) + a.rows);
     return SWA_OK;
 }
 

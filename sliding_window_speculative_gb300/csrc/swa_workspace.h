@@ -1,6 +1,7 @@
 // Device memory of one purpose on one device that grows with the calls using
-// it: the attention's split partials.  Plain host code on the CUDA
-// runtime's C interface (tests run it against a counting stand-in).
+// it: the attention's split partials, the greedy acceptance's scratch.  Plain
+// host code on the CUDA runtime's C interface (tests run it against a counting
+// stand-in).
 //
 // A buffer that a captured call was given has to outlive the graph, which may
 // be replayed at any time, so it is kept when a larger call outgrows it.  Any
