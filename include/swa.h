@@ -202,7 +202,8 @@ swa_status swa_sink_verify_attn(const void *q, const void *k_new, const void *v_
  *       (a, b) = (n, n + rot_dim / 2), or (2n, 2n + 1) if interleaved;
  *       dims from rot_dim on are not rotated (rot_dim 0: none are)
  * in fp32 (the angle modulo a turn exactly, at any position), rounded to bf16
- * once.  Value rows are copied bit by bit. */
+ * once; a pair whose inv_freq is infinite or NaN becomes NaN.  Value rows are
+ * copied bit by bit. */
 typedef struct {
     int64_t q_row, k_row, v_row; /* elements from one token's rows to the next in q, k and v
                                     (at least heads * D, a multiple of 8): views of one fused

@@ -16,7 +16,7 @@
 // token alone, so cosine and sine are computed once and used for all heads.
 //
 // What bounds it is the one read and one write of the rows: 512 x 64 tokens of
-// 12 heads (403 MB) take 71.4 us, 83% of the measured copy bandwidth, with the
+// 12 heads (403 MB) take 72.5 us, 82% of the measured copy bandwidth, with the
 // next batch's loads in flight while one is worked on, whole 32-byte sectors
 // per thread pair and paired fp32 arithmetic (85.0 us without the three).  A
 // block of 8 rows takes 3.5 us, a launch and one memory latency.
@@ -48,7 +48,7 @@ struct RopeParams {
 };
 
 // f / 2 pi as a fraction of a turn in units of 2^-64, modulo a turn:
-// f = m 2^e with a 24-bit m, and K = round(2^64 / 2 pi).
+// f = m 2^e with a 24-bit m (f finite), and K = round(2^64 / 2 pi).
 __device__ __forceinline__ uint64_t rope_turns(float f) {
     constexpr uint64_t K = 2935890503282001226ull;
     const uint32_t u = __float_as_uint(f);
@@ -64,6 +64,11 @@ __device__ __forceinline__ uint64_t rope_turns(float f) {
     else
         t = e > -128 ? hi >> (-64 - e) : 0;
     return (u >> 31) ? 0 - t : t;
+}
+
+// An infinite or NaN frequency has no angle: its pairs become NaN.
+__device__ __forceinline__ bool rope_finite(float f) {
+    return (__float_as_uint(f) & 0x7f800000u) != 0x7f800000u;
 }
 
 // Cosine and sine of t 2^-32 turns: the nearest quarter turn q and the rest r
@@ -101,10 +106,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) swa_rope_kerne
     constexpr int U = 3;               // steps whose loads are in flight together
     __shared__ __align__(16) float w_s[2][D];
     __shared__ uint64_t turn_s[D / 2];
+    __shared__ volatile int odd_s;  // some frequency is not finite
     const int tid = threadIdx.x, lane = tid & 31;
     const int l = lane % LPR, slot = lane / LPR;
     const int heads = R.Hq + 2 * R.Hkv;
     const int q_len = R.cache.q_len;
+    const float kNan = __int_as_float(0x7fffffff);
     grid_dep_wait();
     grid_dep_trigger();
     const bool turns = l < R.rot / 16;  // this lane's dims are rotated
@@ -151,7 +158,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) swa_rope_kerne
         w_s[0][i] = R.q_weight != nullptr ? R.q_weight[i] : 0.f;
         w_s[1][i] = R.k_weight != nullptr ? R.k_weight[i] : 0.f;
     }
-    for (int i = tid; i < R.rot / 2; i += kRopeThreads) turn_s[i] = rope_turns(R.inv_freq[i]);
+    bool odd = false;
+    for (int i = tid; i < R.rot / 2; i += kRopeThreads) {
+        const float f = R.inv_freq[i];
+        turn_s[i] = rope_turns(f);
+        odd = odd || !rope_finite(f);
+    }
+    odd = __syncthreads_or(odd);
+    if (tid == 0) odd_s = odd;
     __syncthreads();
     while (cur.work < n_work) {
         const int tok = token_of(cur);
@@ -187,6 +201,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) swa_rope_kerne
                 }
                 cs[e] = f2_pack(c[0], c[1]);
                 sn[e] = f2_pack(s[0], s[1]);
+            }
+            // (looked up for every token: held in a register 72.9 us)
+            if (odd_s) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int n = (e < 2 ? pair0 : pair1) + 2 * (e & 1);
+                    const uint64_t none = f2_pack(rope_finite(R.inv_freq[n]) ? 0.f : kNan,
+                                                  rope_finite(R.inv_freq[n + 1]) ? 0.f : kNan);
+                    cs[e] = f2_add(cs[e], none);
+                    sn[e] = f2_add(sn[e], none);
+                }
             }
         }
         for (bool same = true; same;) {
