@@ -152,6 +152,27 @@ def _stream_handle(stream, device):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(shape, dtype, device, stream):
+    """A fresh output of a call on `stream` (None: torch's current stream).
+
+    It is allocated on that stream and noted as used on the current one.
+    From the current stream's memory it could be the block of a tensor that
+    was freed while the current stream still reads it, and freed itself it
+    would go to the next tensor while the call writes it."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = _stream_handle(stream, device)
+            stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                      else torch.cuda.default_stream(device))
+        here = torch.cuda.current_stream(device)
+        if stream.cuda_stream != here.cuda_stream:
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(here)
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _marshal_paged(q, k_pages, v_pages, block_table, seq_lens, q_pos, window, scale,
                    out=None, lse=None, num_splits=0, stream=None):
     B, q_len, Hq, D = q.shape
@@ -166,10 +187,10 @@ def _marshal_paged(q, k_pages, v_pages, block_table, seq_lens, q_pos, window, sc
     ps = _dev_tensor(seq_lens, "seq_lens", torch.int32, 1)
     pp = _dev_tensor(q_pos, "q_pos", torch.int32, 1)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     po = _dev_tensor(out, "out", torch.bfloat16, 4)
     if lse is None:
-        lse = torch.empty((B, q_len, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, q_len, Hq), torch.float32, q.device, stream)
     pl = _dev_tensor(lse, "lse", torch.float32, 3)
     num_pages, Hkv, page_size = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
     max_blocks = block_table.shape[1]
@@ -264,7 +285,7 @@ def _marshal_rope(q, k, v, q_weight, k_weight, eps, inv_freq, q_pos, interleaved
     dev = _one_device(q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq,
                       q_pos=q_pos)
     shapes = ((B, q_len, Hq, D), (B, q_len, Hkv, D), (B, q_len, Hkv, D))
-    outs = [torch.empty(s, dtype=torch.bfloat16, device=dev) if t is None else t
+    outs = [_new(s, torch.bfloat16, dev, stream) if t is None else t
             for t, s in zip(outs, shapes)]
     po = []
     for t, s, name in zip(outs, shapes, ("q_out", "k_out", "v_out")):
@@ -367,10 +388,10 @@ def _marshal_append(q, k_new, v_new, k_cache, v_cache, seq_lens, q_pos, window, 
     ps = _dev_tensor(seq_lens, "seq_lens", torch.int32, 1)
     pp = _dev_tensor(q_pos, "q_pos", torch.int32, 1)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     po = _dev_tensor(out, "out", torch.bfloat16, 4)
     if lse is None:
-        lse = torch.empty((B, q_len, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, q_len, Hq), torch.float32, q.device, stream)
     pl = _dev_tensor(lse, "lse", torch.float32, 3)
     paged = None
     if block_table is not None:
@@ -428,9 +449,9 @@ def _marshal_sink(q, k_cache, v_cache, seq_lens, q_pos, window, num_sinks, scale
         raise ValueError("seq_lens and q_pos need one entry per sequence")
     paged, max_len = _paged_of(k_cache, block_table, B)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((B, q_len, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, q_len, Hq), torch.float32, q.device, stream)
     dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new,
                       seq_lens=seq_lens, q_pos=q_pos, block_table=block_table, out=out, lse=lse)
     po = _dev_tensor(out, "out", torch.bfloat16, 4)
@@ -503,12 +524,12 @@ def _marshal_verify(q, k_cache, v_cache, seq_lens, q_pos, window, scale, out=Non
     if seq_lens.numel() != B or q_pos.numel() != B:
         raise ValueError("seq_lens and q_pos need one entry per sequence")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     po = _dev_tensor(out, "out", torch.bfloat16, 4)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if lse is None and want_lse:
-        lse = torch.empty((B, q_len, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, q_len, Hq), torch.float32, q.device, stream)
     pl = None
     if lse is not None:
         pl = _dev_tensor(lse, "lse", torch.float32, 3)
@@ -577,11 +598,11 @@ def _marshal_sample(logits, uniforms, temperature, top_k=None, top_p=None, min_p
     if q_len > 1 and draft is None:
         raise ValueError("draft must be [B, q_len - 1]")
     if tokens is None:
-        tokens = torch.empty((B, q_len), dtype=i32, device=dev)
+        tokens = _new((B, q_len), i32, dev, stream)
     if accepted is None:
-        accepted = torch.empty((B,), dtype=i32, device=dev)
+        accepted = _new((B,), i32, dev, stream)
     if logprobs is None and want_logprobs:
-        logprobs = torch.empty((B, q_len), dtype=f32, device=dev)
+        logprobs = _new((B, q_len), f32, dev, stream)
     if temperature is None:
         raise ValueError("temperature must be [B]")
     settings = SwaSampling(ptr(temperature, "temperature", f32, B), ptr(top_k, "top_k", i32, B),
@@ -682,9 +703,9 @@ def swa_greedy_accept(logits, draft=None, keep_ids=None, argmax=None, accepted=N
         if keep_ids.numel() != V:
             raise ValueError("keep_ids needs one token id per logit column")
     if argmax is None:
-        argmax = torch.empty((B, q_len), dtype=torch.int32, device=logits.device)
+        argmax = _new((B, q_len), torch.int32, logits.device, stream)
     if accepted is None:
-        accepted = torch.empty((B,), dtype=torch.int32, device=logits.device)
+        accepted = _new((B,), torch.int32, logits.device, stream)
     pa = _dev_tensor(argmax, "argmax", torch.int32, 2)
     pc = _dev_tensor(accepted, "accepted", torch.int32, 1)
     if tuple(argmax.shape) != (B, q_len) or accepted.numel() != B:
