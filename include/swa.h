@@ -401,12 +401,14 @@ swa_status swa_greedy_accept(const void *logits, const int32_t *keep_ids, const 
  *   T <= 0 or NaN is greedy: the first candidate, logprob 0.  A row without
  *   candidates gives column 0, logprob 0.
  * Weights are computed to 2^-39 relative or 2^-50 of the largest, whichever is
- * more, and summed exactly, so a call gives the same results every time; in a
- * batch of another size a row may be taken another way, its shares then agree
- * to 2^-37 of S, but for the last case here.  Columns more than 50 T below M
- * are left out (together under 2^-41 of S up to 2^31 columns), and of many
- * candidates those of vanishing magnitude (below 2^-28 of the row's largest) may
- * weigh like 0, within 2^-22 of their weight. */
+ * more, and summed exactly; the cut-offs and the draw compare these.  So a call
+ * gives the same results every time; in a batch of another size a row may be
+ * taken another way, its shares then agree to 2^-37 of S, but for the two cases
+ * here.  Columns more than 50 T below M are left out (together under 2^-41 of S
+ * up to 2^31 columns).  Of many candidates those nearer to 0 than 2^-22 T may
+ * weigh like 0, or like the largest where that is one of them: within 2^-22 of
+ * their weight.  A draw that falls on one of these reads the row 18 more times,
+ * to find its place in the order. */
 typedef struct {
     const float *temperature; /* fp32 [batch] device                           */
     const int32_t *top_k;     /* int32 [batch] device or NULL: no top-k        */

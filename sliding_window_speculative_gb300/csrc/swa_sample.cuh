@@ -42,13 +42,18 @@
 // quartic; relative error below 2^-39), masses as 128-bit sums of count * w.
 //
 // Bins: for each sign 4096 values downwards from a top magnitude, i.e. 32
-// octaves.  The top of the positive values is a few octaves above the first
-// chunk's largest, and a row that exceeds it is counted again; that of the
-// negative ones is the lowest value that can weigh anything.  What is smaller
-// still shares the last bin and weighs like 0 (within 2^-22 of its weight:
-// kept columns lie within 50 T of the maximum), and its order is resolved by
-// value when the draw lands in it.  The first bin of each sign takes what does
-// not count: NaN, and everything below the line.
+// octaves.  The top of the positive values is four octaves above the larger of
+// the first chunk's largest and T, and a row that exceeds it is counted again;
+// that of the negative ones is the lowest value that can weigh anything.  What
+// is smaller still shares the last bin and weighs like 0 or, where that is one
+// of them, like the maximum.  A column that is kept lies within 50 T of the
+// maximum, so a shared one lies within 2^-22 T of 0 (positive: 2^-28 of at most
+// 50 T; negative: 2^-32 of at most 200 T, or the row is counted again) and its
+// weight is off by 2^-22.  Its order is resolved by value when the draw lands
+// in it, by a bisection of 16 passes over the row and two to place it, a
+// cluster barrier each: rows whose every logit is that near to 0 (a temperature
+// far above them, a row of zeros) pay these 18 passes.  The first bin of each
+// sign takes what does not count: NaN, and everything below the line.
 #pragma once
 
 #include <cooperative_groups.h>
