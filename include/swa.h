@@ -84,6 +84,11 @@ typedef struct {
  * sequence's own slab, and rows without a visible key get out = 0,
  * lse = -inf.
  *
+ * Weights of 0 are multiplied too: a V element that is NaN or infinite, at a
+ * position that one row of a block sees, may make that dim NaN in the block's
+ * other rows.  (Positions that no row sees may hold anything, and so may K
+ * where a row does not look.)
+ *
  * Ownership: every pointer stays owned by the caller; nothing is retained
  * after the call except through the workspace described below.
  *
@@ -182,8 +187,8 @@ swa_status swa_append_verify_attn(const void *q, const void *k_new, const void *
  * num_sinks positions: a ring's block table lists pages of their own for them.
  * num_sinks 0..128 (0: the windowed call itself); SWA_ERR_INVALID_ARG below,
  * SWA_ERR_UNSUPPORTED above.  swa_workspace_bytes bounds the workspace as for
- * the windowed call; swa_plan describes it too, but for its kernel 4: these
- * calls take kernel 3 instead. */
+ * the windowed call; swa_plan describes it too, but for its kernel 4 (see
+ * there). */
 swa_status swa_sink_verify_attn(const void *q, const void *k_new, const void *v_new, void *k_cache,
                                 void *v_cache, const swa_paged *paged, const int32_t *seq_lens,
                                 const int32_t *q_pos, int32_t window, int32_t num_sinks,
@@ -268,7 +273,9 @@ typedef struct {
                               (tcgen05) kernel, 3 = rows-major tensor-core kernel, 4 = the
                               rows-major kernel on CTA pairs (clusters of two CTAs, 2 x 128
                               packed rows per item; swa_verify_attn only: a paged, fused-
-                              append or sink call with these dims takes kernel 3 instead) */
+                              append or sink call with these dims takes kernel 3 instead, or
+                              kernel 2 where its items are no more than the SMs; its splits
+                              and grid are then others too) */
     int32_t num_splits;    /* chunks per (sequence, KV head)                    */
     int32_t chunk_keys;    /* keys per chunk                                    */
     int32_t row_tiles;     /* work items along the packed rows R = q_len * G    */

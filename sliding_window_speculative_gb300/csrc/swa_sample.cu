@@ -40,14 +40,21 @@ cudaError_t launch(const swa::SampleParams &A, long long rows, cudaStream_t s) {
 cudaError_t launch_rows(const swa::SampleParams &A, long long rows, int sms, cudaStream_t s) {
     // One CTA per row, four to an SM; clusters share a row while SMs would be
     // left without two CTAs and each still has two vectors per thread.  Measured
-    // on GB300, rows of 262144, us, unfiltered / top-k 50: 64 rows 4 CTAs of
-    // 256 threads 30.6 / 18.5, of 512 32.8 / 18.5, 8 of 256 32.8; 128 rows 2 of
-    // 512 47.1 / 22.6, 2 of 256 43.7 / 26.0, 1 of 256 - / 32.9; 512 rows 1 of
-    // 256 135 / 67, 1 of 512 142 / 69, 2 of 512 145 / 86, 2 of 256 142 / 76; three
-    // CTAs of 256 to an SM, the others following, 124 / 97 where four take
-    // 128 / 79 between events (requests of mixed settings 99-109 and 107-119),
-    // but 64 rows 34.0 where four take 27.5.  8 rows, 8 CTAs:
-    // the first chunk held in registers 12.5, read again 16.3.
+    // on GB300, calls behind one another in a replayed graph, rows of 262144,
+    // us, unfiltered / top-k 50:
+    //   8 rows    8 CTAs of 512 threads, first chunk held in registers 16.3 / 8.7,
+    //             read again 17.6 / 9.4, 8 of 256 17.7 / 11.9, 4 of 512 20.7 / 12.3
+    //   64 rows   4 of 256 27.6 / 18.3, 4 of 512 30.6 / 17.7, 2 of 512 29.4 / 18.1,
+    //             8 of 256 32.3 / 18.8
+    //   128 rows  2 of 512 44.4 / 23.7, 2 of 256 43.7 / 27.0, 4 of 256 41.9 / 24.3,
+    //             1 of 256 53.1 / 38.8
+    //   512 rows  1 of 256 120.6 / 63.1, 1 of 512 122.9 / 64.6, 2 of 256
+    //             124.7 / 69.3, 2 of 512 135.2 / 79.5; at most three CTAs of 256 to
+    //             an SM 145.5 / 90.5
+    // and shorter rows: 48 of 12001 2 of 512 18.6 / 8.5, 1 of 256 19.7 / 7.2, 4 of
+    // 256 18.7 / 9.0; 100 of 12001 2 of 512 22.5 / 10.4, 1 of 256 20.1 / 7.2; 100
+    // of 50257 2 of 512 26.8 / 12.3, 2 of 256 25.6 / 13.5, 1 of 256 29.3 / 15.6;
+    // 30 of 32000 4 of 256 18.3 / 8.7, 8 of 512 20.3 / 10.9, 2 of 512 19.2 / 8.6.
     const long long nvec = ((long long)A.V + 14) / 8;
     int c = 1;
     while (c < swa::kSampMaxCluster && rows * c * 2 <= 2LL * sms && nvec > 1024LL * c) c *= 2;

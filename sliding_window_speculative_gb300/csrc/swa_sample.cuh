@@ -20,9 +20,9 @@
 // short enough to be sorted whole, the columns that reach it go to a list in
 // the first CTA's shared memory, which sorts them and finishes the row by
 // itself.  Almost every 16-byte vector of the row is dismissed by one packed
-// maximum: 512 rows of 262,144 under top-k 50 take 67 us (4.0 TB/s; the first
+// maximum: 512 rows of 262,144 under top-k 50 take 63 us (4.3 TB/s; the first
 // chunk's and the list's latencies and the fourth row of some SMs are the
-// rest), 8 rows 10.8 us, all latency (two cluster barriers, the list).
+// rest), 8 rows 8.7 us, all latency (two cluster barriers, the list).
 //
 // Histogram: else (or when the list overflows) every CTA counts its columns by
 // value into its own histogram; the CTAs weigh and sum the histograms over the
@@ -33,8 +33,10 @@
 // value finds it in a second look at its part, from the nearer end.  One shared
 // memory increment per column bounds this way, 3.4 to 4.5 cycles per 32 of them
 // with random bank conflicts (on average a quarter of a row is read again
-// besides): 512 rows of 262,144 unfiltered take 124 us (2.2 TB/s), 64 rows 27.5;
-// the blocks' weights are a fifth of that.
+// besides): 512 rows of 262,144 unfiltered take 121 us (2.2 TB/s), 64 rows 27.6,
+// 8 rows 16.3, and 3.4, 1.7 and 1.8 us more under top-p 0.9; the blocks' weights
+// are a fifth of that.  The 64 registers that four rows on an SM leave (128 for
+// eight CTAs that hold a chunk) cost each instance 108 to 148 bytes of spills.
 //
 // Weights and masses are integers, so sums do not depend on any order and
 // comparisons are exact: w = 2^-((max - x) log2(e) / T) in units of 2^-62 (the
@@ -71,7 +73,10 @@ constexpr int kSampList = kSampBins / 2;   // columns the list holds
 constexpr int kSampSort = 1024;            // longer lists are counted instead
 constexpr int kSampSmall = kSampSort;      // rows up to here are always taken by list
 constexpr int kSampKeys = 512;             // maxima the top-k bound is taken from
-constexpr int kSampListK = kSampKeys / 2;  // largest top-k taken by list
+// Largest top-k taken by list.  Measured on rows of 262144, us, top-k 256 listed /
+// 257 counted: 8 rows 13.6 / 17.5, 64 rows 27.4 / 29.1, 512 rows 134 / 129; 48 rows
+// of 12001 13.5 / 19.8, 512 rows of 4000 24.7 / 31.6.
+constexpr int kSampListK = kSampKeys / 2;
 constexpr int kSampMaxCluster = 8;
 constexpr int kSampRoom = 4 << 7;          // four octaves above the first chunk's largest
 constexpr float kSampCut = 50.f;           // columns 50 T below the maximum weigh under 2^-72
@@ -613,6 +618,10 @@ __global__ void __launch_bounds__(NT, HOLD ? 1 : 1024 / NT) swa_sample_kernel(co
                 return __uint_as_float((key & 0x8000u ? key & 0x7fffu : 0xffffu - key) << 16);
             };
             if (n > 160 && (by_line || by_count)) {
+                // (from 1 / 161 / 513 on, rows of 262144, us: 8 rows top-k 50
+                // 10.1 / 8.8 / 8.8, 64 rows top-k 50 18.3 / 18.2 / 21.6, 512 rows
+                // min-p 0.3 55.5 / 55.2 / 70.8; 48 rows of 12001 top-k 10
+                // 10.0 / 8.2 / 8.2)
                 // fewer to sort: those on min-p's line of the row's own maximum
                 float low = R.cut;
                 if (by_line) {
