@@ -173,6 +173,13 @@ def _new(shape, dtype, device, stream):
     return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _holds(n, **tensors):
+    """Refuses tensors of fewer than n elements: the kernels would run past them."""
+    for name, t in tensors.items():
+        if t.numel() < n:
+            raise ValueError(f"{name} needs {n} elements (got {tuple(t.shape)})")
+
+
 def _marshal_paged(q, k_pages, v_pages, block_table, seq_lens, q_pos, window, scale,
                    out=None, lse=None, num_splits=0, stream=None):
     B, q_len, Hq, D = q.shape
@@ -192,6 +199,9 @@ def _marshal_paged(q, k_pages, v_pages, block_table, seq_lens, q_pos, window, sc
     if lse is None:
         lse = _new((B, q_len, Hq), torch.float32, q.device, stream)
     pl = _dev_tensor(lse, "lse", torch.float32, 3)
+    _holds(B, seq_lens=seq_lens, q_pos=q_pos)
+    _holds(q.numel(), out=out)
+    _holds(B * q_len * Hq, lse=lse)
     num_pages, Hkv, page_size = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
     max_blocks = block_table.shape[1]
     paged = SwaPaged(pt, max_blocks, page_size, num_pages)
@@ -402,7 +412,12 @@ def _marshal_append(q, k_new, v_new, k_cache, v_cache, seq_lens, q_pos, window, 
         paged = SwaPaged(pt, block_table.shape[1], page_size, num_pages)
         max_len = block_table.shape[1] * page_size
     else:
+        if k_cache.shape[0] < B:
+            raise ValueError("the caches need one slab per sequence")
         max_len = k_cache.shape[2]
+    _holds(B, seq_lens=seq_lens, q_pos=q_pos)
+    _holds(q.numel(), out=out)
+    _holds(B * q_len * Hq, lse=lse)
     dims = make_dims(B, q_len, Hq, Hkv, D, max_len, num_splits)
     handle = _stream_handle(stream, q.device)
     args = (pq, pkn, pvn, pk, pv, ctypes.byref(paged) if paged is not None else None, ps, pp,
