@@ -355,7 +355,7 @@ swa_status ensure_workspace(int dev, size_t need, cudaStream_t stream, void **ou
                         "needed; run one call outside capture first or set a workspace",
                         w.bytes, need);
         e = swa::workspace_grow(w, need);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
+        if (e != cudaSuccess) return cuda_fail(e, "growing the workspace");
     } else if (w.owned && !w.captured) {
         w.captured = swa::stream_capturing(stream);
     }
@@ -865,7 +865,7 @@ swa_status ensure_accept_scratch(int dev, size_t rows, size_t seqs, cudaStream_t
         e = swa::workspace_grow(a.w, rows * 8 + seqs * 4);
         if (e != cudaSuccess) {
             if (a.w.ptr == nullptr) a.rows = a.seqs = 0;
-            return cuda_fail(e, "cudaMalloc(acceptance scratch)");
+            return cuda_fail(e, "growing the acceptance scratch");
         }
         a.rows = a.seqs = 0;
         e = cudaMemsetAsync(a.w.ptr, 0, a.w.bytes, stream);

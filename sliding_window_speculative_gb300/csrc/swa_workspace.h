@@ -64,7 +64,8 @@ inline cudaError_t workspace_free(Workspace &w) {
 
 // A buffer of at least `need` bytes (more than it has), outside stream capture
 // and not the caller's: a quarter more than needed, or exactly that where the
-// quarter does not fit.  On an error a kept buffer stays the current one.
+// quarter does not fit.  On an error a captured buffer, or one that could not be
+// freed (another stream captures), stays the current one.
 inline cudaError_t workspace_grow(Workspace &w, size_t need) {
     Workspace::Kept *node = nullptr;
     if (w.ptr != nullptr && w.captured) {
@@ -72,10 +73,13 @@ inline cudaError_t workspace_grow(Workspace &w, size_t need) {
         if (node == nullptr) return cudaErrorMemoryAllocation;
     } else if (w.ptr != nullptr) {
         const cudaError_t e = cudaFree(w.ptr);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return e;
+        }
         w.ptr = nullptr;
         w.bytes = 0;
         w.owned = false;
-        if (e != cudaSuccess) return e;
     }
     size_t bytes = need + need / 4;
     void *ptr = nullptr;

@@ -15,7 +15,7 @@ PROGRAM = r"""
 
 static size_t room, held, frees;
 static std::map<void *, size_t> live;
-static bool capturing, unanswered;
+static bool capturing, unanswered, unfreeable;
 static size_t next_ptr = 4096;
 
 extern "C" {
@@ -28,6 +28,7 @@ cudaError_t cudaMalloc(void **p, size_t n) {
     return cudaSuccess;
 }
 cudaError_t cudaFree(void *p) {
+    if (unfreeable) return cudaErrorStreamCaptureUnsupported;
     if (live.find(p) == live.end()) return cudaErrorInvalidValue;
     held -= live[p];
     live.erase(p);
@@ -80,6 +81,18 @@ int main() {
         CHECK(swa::workspace_grow(w, 1400) == cudaSuccess && w.bytes == 1400);
         CHECK(live.count(graph) == 1 && live.count(eager) == 0 && held == 1900);
         CHECK(swa::workspace_free(w) == cudaSuccess && held == 0 && w.kept == nullptr);
+    }
+    {   // a buffer that cannot be freed now stays in use
+        Workspace w;
+        room = 2000;
+        CHECK(swa::workspace_grow(w, 400) == cudaSuccess);
+        void *before = w.ptr;
+        unfreeable = true;
+        CHECK(swa::workspace_grow(w, 800) == cudaErrorStreamCaptureUnsupported);
+        unfreeable = false;
+        CHECK(w.ptr == before && w.bytes == 500 && w.owned && held == 500);
+        CHECK(swa::workspace_grow(w, 800) == cudaSuccess && held == 1000);
+        CHECK(swa::workspace_free(w) == cudaSuccess && held == 0);
     }
     {   // any number of captured buffers
         Workspace w;
