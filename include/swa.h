@@ -248,6 +248,70 @@ swa_status swa_qk_norm_rope_append(const void *q, const void *k, const void *v,
                                    const int32_t *q_pos, void *q_out, const swa_dims *dims,
                                    swa_stream_t stream);
 
+/* An 8-bit KV cache: rows of e4m3 elements (1 sign, 4 exponent, 3 fraction bits,
+ * largest 448, no infinities), each row with one power of two.  Half the bytes
+ * of the bf16 cache per key and (sequence, KV head); a row's values are
+ * bf16 numbers, so reading them back rounds nothing.  The pages' reduced cache
+ * is the smaller KV length; they name no 8-bit one.
+ *
+ * A row x of D elements is written as
+ *   e    = the smallest integer in [-50, 50] with |x_d| <= 448 * 2^e for every
+ *          finite x_d
+ *   x8_d = x_d * 2^-e rounded to e4m3 (to nearest, ties to even), at most 448 in
+ *          size; NaN where x_d is infinite or NaN
+ * and stands for x8_d * 2^e.  The rounding is within 2^-4 of the value, or 2^-10
+ * * 2^e where that is more. */
+typedef struct {
+    void *k, *v;           /* e4m3 [B, Hkv, max_len, D], or page pools [num_pages, Hkv,
+                              page_size, D]; device, 16-byte aligned                   */
+    int8_t *k_exp, *v_exp; /* int8 [B, Hkv, max_len], or [num_pages, Hkv, page_size]: the
+                              rows' exponents e                                        */
+} swa_q8_cache;
+
+/* Writes a block's K and V rows into an 8-bit cache.
+ *   k_new, v_new  bf16, token t = b * q_len + i at k_new + t * k_row: [Hkv, D],
+ *                 16-byte aligned; k_row, v_row elements from one token to the
+ *                 next (at least Hkv * D, a multiple of 8): views of one fused
+ *                 projection are taken as they are
+ *   cache, paged  see swa_q8_cache; paged as for swa_verify_attn_paged, or NULL
+ *   seq_lens, q_pos  int32 [B] device
+ *   dims          batch, q_len, num_kv_heads, head_dim and max_len
+ * Row i of sequence b goes to position q_pos[b] + i where that lies in
+ * [0, min(seq_lens[b], max_len)); other rows are dropped and no other byte of
+ * the cache changes.  k_new / v_new must not overlap the cache.  Asynchronous on
+ * `stream`, no workspace, no state; errors as for swa_verify_attn. */
+swa_status swa_q8_append(const void *k_new, const void *v_new, int64_t k_row, int64_t v_row,
+                         const swa_q8_cache *cache, const swa_paged *paged,
+                         const int32_t *seq_lens, const int32_t *q_pos, const swa_dims *dims,
+                         swa_stream_t stream);
+
+/* Reads n positions per sequence of an 8-bit cache back as bf16.
+ *   start         int32 [B] device: the first position of each sequence
+ *   k_out, v_out  bf16 [B, Hkv, n, D] device, 16-byte aligned, written: row r
+ *                 holds position start[b] + r (exactly: no rounding), or zeros
+ *                 where that lies outside [0, min(seq_lens[b], max_len)): a
+ *                 contiguous cache of n rows, as swa_verify_attn takes it
+ *   dims          batch, num_kv_heads, head_dim and max_len
+ * Asynchronous on `stream`, no workspace, no state; errors as for
+ * swa_verify_attn. */
+swa_status swa_q8_read(const swa_q8_cache *cache, const swa_paged *paged, const int32_t *seq_lens,
+                       const int32_t *start, int32_t n, void *k_out, void *v_out,
+                       const swa_dims *dims, swa_stream_t stream);
+
+/* swa_verify_attn (paged == NULL) or swa_verify_attn_paged over an 8-bit cache:
+ * the same definition with the values that the rows stand for.  Arguments,
+ * preconditions, limits, the workspace rules and errors are those of these
+ * calls; the workspace is bounded by swa_q8_workspace_bytes. */
+swa_status swa_q8_verify_attn(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
+                              const int32_t *seq_lens, const int32_t *q_pos, int32_t window,
+                              float scale, void *out, float *lse, const swa_dims *dims,
+                              swa_stream_t stream);
+
+/* Upper bound, in bytes, of the workspace a swa_q8_verify_attn call with these
+ * dims and window may need on any device (pure host arithmetic; 0 if the
+ * arguments are invalid). */
+size_t swa_q8_workspace_bytes(const swa_dims *dims, int32_t window);
+
 /* Upper bound, in bytes, of the split-partial workspace any call with these
  * dims and window may need on any device (pure host arithmetic; 0 if the
  * arguments are invalid).  Layout: fp32 acc [B, Hkv, splits, R, D] followed
@@ -443,6 +507,43 @@ swa_status swa_sample_accept(const void *logits, const int32_t *keep_ids, const 
                              const float *uniforms, const swa_sampling *sampling, int32_t *tokens,
                              float *logprobs, int32_t *accepted, int32_t batch, int32_t q_len,
                              int32_t vocab, swa_stream_t stream);
+
+/* Log probabilities of given tokens, with the distribution's entropy and its
+ * likeliest tokens: what a server reports about the tokens of a verify step
+ * (its drafts, or the tokens swa_sample_accept drew), or about a prompt's.  The
+ * pages report none.
+ *
+ * Per row, with x_j its logits (a NaN counts as -inf) and T the temperature of
+ * its sequence (no temperature, T <= 0 or NaN: 1):
+ *   p_j     = exp(x_j / T) / sum_k exp(x_k / T)
+ *   order   the columns by falling x_j, equal ones by rising column
+ *   logprob = ln p_t of the given token's column t, rank its place in the order
+ *             (from 1 on); a token that is no column's, or negative: -inf and
+ *             rank 0
+ *   entropy = -sum_j p_j ln p_j
+ *   top     the first top_n columns of the order: their tokens and ln p_j
+ * A row whose largest logit is +inf has p = 1 / n on its n columns of +inf and
+ * 0 elsewhere; a row without a logit above -inf has logprobs -inf, entropy 0.
+ *
+ *   logits     bf16 [batch, q_len, vocab]  device, 2-byte aligned
+ *   keep_ids   int32 [vocab]  device or NULL: column j is token keep_ids[j]
+ *              (of several columns of a token the first counts)
+ *   tokens     int32 [batch, q_len]  device
+ *   temperature  fp32 [batch]  device or NULL
+ *   logprobs   fp32 [batch, q_len]  device, written
+ *   ranks      int32 [batch, q_len]  device or NULL, written
+ *   entropy    fp32 [batch, q_len]  device or NULL, written
+ *   top_tokens int32, top_logprobs fp32 [batch, q_len, top_n]  device, written
+ *              (not read when top_n is 0)
+ *   batch 1..65535, q_len 1..512, vocab >= 1, top_n 0..32 and at most vocab.
+ * Sums run in fp32.  Asynchronous on `stream`; no workspace and no state, so
+ * calls on several streams may overlap and be captured.  SWA_ERR_INVALID_ARG on
+ * bad arguments before any CUDA call. */
+swa_status swa_token_logprobs(const void *logits, const int32_t *keep_ids, const int32_t *tokens,
+                              const float *temperature, int32_t top_n, float *logprobs,
+                              int32_t *ranks, float *entropy, int32_t *top_tokens,
+                              float *top_logprobs, int32_t batch, int32_t q_len, int32_t vocab,
+                              swa_stream_t stream);
 
 /* Bytes of the fixed device scratch used by swa_verify_attn_noalloc. */
 #define SWA_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)

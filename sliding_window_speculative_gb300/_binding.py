@@ -52,6 +52,12 @@ class SwaSampling(ctypes.Structure):
                 ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
 
 
+class SwaQ8Cache(ctypes.Structure):
+    """swa_q8_cache of include/swa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p)]
+
+
 class SwaDebugOptions(ctypes.Structure):
     """swa_debug_options of include/swa.h (test and sweep controls)."""
     _fields_ = [("force_kernel", ctypes.c_int32), ("pdl", ctypes.c_int32),
@@ -127,6 +133,18 @@ def load_library(path=LIB_PATH):
     lib.swa_sample_accept.argtypes = [vp, vp, vp, vp, ctypes.POINTER(SwaSampling), vp, vp, vp,
                                       i32, i32, i32, vp]
     lib.swa_sample_accept.restype = ctypes.c_int
+    pd, pp, pc = ctypes.POINTER(SwaDims), ctypes.POINTER(SwaPaged), ctypes.POINTER(SwaQ8Cache)
+    i64 = ctypes.c_int64
+    lib.swa_q8_append.argtypes = [vp, vp, i64, i64, pc, pp, vp, vp, pd, vp]
+    lib.swa_q8_append.restype = ctypes.c_int
+    lib.swa_q8_read.argtypes = [pc, pp, vp, vp, i32, vp, vp, pd, vp]
+    lib.swa_q8_read.restype = ctypes.c_int
+    lib.swa_q8_verify_attn.argtypes = [vp, pc, pp, vp, vp, i32, ctypes.c_float, vp, vp, pd, vp]
+    lib.swa_q8_verify_attn.restype = ctypes.c_int
+    lib.swa_q8_workspace_bytes.argtypes = [pd, i32]
+    lib.swa_q8_workspace_bytes.restype = sz
+    lib.swa_token_logprobs.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp]
+    lib.swa_token_logprobs.restype = ctypes.c_int
     lib.swa_set_debug_options.argtypes = [ctypes.POINTER(SwaDebugOptions)]
     lib.swa_set_debug_options.restype = ctypes.c_int
     lib.swa_get_debug_options.argtypes = [ctypes.POINTER(SwaDebugOptions)]
@@ -649,6 +667,204 @@ def swa_sample_accept(logits, uniforms, temperature, top_k=None, top_p=None, min
                                                      accepted, stream, want_logprobs))
 
 
+def _q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, B, Hkv=None, D=None):
+    """(SwaQ8Cache, SwaPaged or None, logical length) of an 8-bit cache."""
+    e4m3 = torch.float8_e4m3fn
+    pk = _dev_tensor(k_cache, "k_cache", e4m3, 4)
+    pv = _dev_tensor(v_cache, "v_cache", e4m3, 4)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if (Hkv is not None and k_cache.shape[1] != Hkv) or (D is not None and k_cache.shape[3] != D):
+        raise ValueError("the caches' heads or head_dim do not match the rows")
+    exps = []
+    for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+        exps.append(_dev_tensor(t, name, torch.int8, 3))
+        if t.shape != k_cache.shape[:3]:
+            raise ValueError(f"{name} must be {tuple(k_cache.shape[:3])} (got {tuple(t.shape)})")
+    _one_device(k_cache=k_cache, v_cache=v_cache, k_exp=k_exp, v_exp=v_exp, block_table=block_table)
+    paged, max_len = _paged_of(k_cache, block_table, B)
+    return SwaQ8Cache(pk, pv, *exps), paged, max_len
+
+
+def _per_sequence(B, **tensors):
+    """Pointers of int32 [B] tensors."""
+    for name, t in tensors.items():
+        _dev_tensor(t, name, torch.int32, 1)
+        if t.numel() != B:
+            raise ValueError(f"{name} needs one entry per sequence")
+    return [t.data_ptr() for t in tensors.values()]
+
+
+def _marshal_q8_append(k_new, v_new, k_cache, v_cache, k_exp, v_exp, seq_lens, q_pos,
+                       block_table=None, stream=None):
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+        raise ValueError("k_new and v_new must be [B, q_len, Hkv, D]")
+    B, q_len, Hkv, D = k_new.shape
+    pk, rk = _head_rows(k_new, "k_new", (B, q_len, Hkv, D))
+    pv, rv = _head_rows(v_new, "v_new", (B, q_len, Hkv, D))
+    cache, paged, max_len = _q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, B, Hkv, D)
+    ps, pp = _per_sequence(B, seq_lens=seq_lens, q_pos=q_pos)
+    dev = _one_device(k_new=k_new, v_new=v_new, k_cache=k_cache, seq_lens=seq_lens, q_pos=q_pos)
+    dims = make_dims(B, q_len, Hkv, Hkv, D, max_len)
+    args = (pk, pv, rk, rv, ctypes.byref(cache), ctypes.byref(paged) if paged is not None else None,
+            ps, pp, ctypes.byref(dims), _stream_handle(stream, dev))
+    keep = (k_new, v_new, k_cache, v_cache, k_exp, v_exp, seq_lens, q_pos, block_table, cache,
+            paged, dims)
+    return "swa_q8_append", args, keep, (k_cache, v_cache, k_exp, v_exp)
+
+
+def swa_q8_append(k_new, v_new, k_cache, v_cache, k_exp, v_exp, seq_lens, q_pos, block_table=None,
+                  stream=None):
+    """A block's K/V rows quantised into an 8-bit cache (C entry point
+    swa_q8_append).
+
+    k_new, v_new bf16 [B, q_len, Hkv, D], contiguous or views of one fused
+    projection; k_cache, v_cache float8_e4m3fn [B, Hkv, max_len, D] with
+    k_exp, v_exp int8 [B, Hkv, max_len] (the rows' power-of-two scales), or
+    with block_table int32 [B, max_blocks] the pools [num_pages, Hkv,
+    page_size, D] and [num_pages, Hkv, page_size].  The caches are modified
+    in place and returned.  Enqueued on `stream` (default: torch's current
+    stream); does not synchronise.
+    """
+    return _issue_on(k_cache.device, *_marshal_q8_append(
+        k_new, v_new, k_cache, v_cache, k_exp, v_exp, seq_lens, q_pos, block_table, stream))
+
+
+def _marshal_q8_read(k_cache, v_cache, k_exp, v_exp, seq_lens, start, n, block_table=None,
+                     k_out=None, v_out=None, stream=None):
+    if not isinstance(seq_lens, torch.Tensor):
+        raise TypeError("seq_lens must be a torch.Tensor")
+    B, n = seq_lens.numel(), int(n)
+    cache, paged, max_len = _q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, B)
+    ps, pb = _per_sequence(B, seq_lens=seq_lens, start=start)
+    if n < 1:
+        raise ValueError(f"n must be at least 1 (got {n})")
+    Hkv, D = k_cache.shape[1], k_cache.shape[3]
+    dev = _one_device(k_cache=k_cache, seq_lens=seq_lens, start=start, k_out=k_out, v_out=v_out)
+    outs = [_new((B, Hkv, n, D), torch.bfloat16, dev, stream) if t is None else t
+            for t in (k_out, v_out)]
+    po = []
+    for t, name in zip(outs, ("k_out", "v_out")):
+        po.append(_dev_tensor(t, name, torch.bfloat16, 4))
+        if tuple(t.shape) != (B, Hkv, n, D):
+            raise ValueError(f"{name} must be {(B, Hkv, n, D)} (got {tuple(t.shape)})")
+    dims = make_dims(B, 1, Hkv, Hkv, D, max_len)
+    args = (ctypes.byref(cache), ctypes.byref(paged) if paged is not None else None, ps, pb, n, *po,
+            ctypes.byref(dims), _stream_handle(stream, dev))
+    keep = (k_cache, v_cache, k_exp, v_exp, seq_lens, start, block_table, outs, cache, paged, dims)
+    return "swa_q8_read", args, keep, tuple(outs)
+
+
+def swa_q8_read(k_cache, v_cache, k_exp, v_exp, seq_lens, start, n, block_table=None, k_out=None,
+                v_out=None, stream=None):
+    """n positions per sequence of an 8-bit cache as bf16 (C entry point
+    swa_q8_read): positions start[b] + r, r < n, zeros outside
+    [0, min(seq_lens[b], max_len)).  Returns (k_out, v_out) bf16
+    [B, Hkv, n, D], allocated if not given: a contiguous cache of n rows as
+    swa_verify_attn takes it.
+    """
+    return _issue_on(k_cache.device, *_marshal_q8_read(
+        k_cache, v_cache, k_exp, v_exp, seq_lens, start, n, block_table, k_out, v_out, stream))
+
+
+def _marshal_q8_verify(q, k_cache, v_cache, k_exp, v_exp, seq_lens, q_pos, window, scale,
+                       block_table=None, out=None, lse=None, num_splits=0, stream=None,
+                       want_lse=True):
+    pq = _dev_tensor(q, "q", torch.bfloat16, 4)
+    B, q_len, Hq, D = q.shape
+    cache, paged, max_len = _q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, B, D=D)
+    ps, pp = _per_sequence(B, seq_lens=seq_lens, q_pos=q_pos)
+    dev = _one_device(q=q, k_cache=k_cache, seq_lens=seq_lens, q_pos=q_pos, out=out, lse=lse)
+    if out is None:
+        out = _new(q.shape, q.dtype, dev, stream)
+    if lse is None and want_lse:
+        lse = _new((B, q_len, Hq), torch.float32, dev, stream)
+    po = _dev_tensor(out, "out", torch.bfloat16, 4)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    pl = None if lse is None else _dev_tensor(lse, "lse", torch.float32, 3)
+    if lse is not None and tuple(lse.shape) != (B, q_len, Hq):
+        raise ValueError("lse must be [B, q_len, Hq]")
+    dims = make_dims(B, q_len, Hq, k_cache.shape[1], D, max_len, num_splits)
+    args = (pq, ctypes.byref(cache), ctypes.byref(paged) if paged is not None else None, ps, pp,
+            int(window), float(scale), po, pl, ctypes.byref(dims), _stream_handle(stream, dev))
+    keep = (q, k_cache, v_cache, k_exp, v_exp, seq_lens, q_pos, block_table, out, lse, cache, paged,
+            dims)
+    return "swa_q8_verify_attn", args, keep, (out, lse)
+
+
+def swa_q8_verify_attn(q, k_cache, v_cache, k_exp, v_exp, seq_lens, q_pos, window, scale,
+                       block_table=None, out=None, lse=None, num_splits=0, stream=None,
+                       want_lse=True):
+    """Windowed verify attention over an 8-bit cache (C entry point
+    swa_q8_verify_attn): the cache as for swa_q8_append, everything else as
+    for swa_verify_attn (with block_table: swa_verify_attn_paged).  Returns
+    (out, lse).
+    """
+    return _issue_on(q.device, *_marshal_q8_verify(
+        q, k_cache, v_cache, k_exp, v_exp, seq_lens, q_pos, window, scale, block_table, out, lse,
+        num_splits, stream, want_lse))
+
+
+def swa_q8_workspace_bytes(dims, window):
+    return load_library().swa_q8_workspace_bytes(ctypes.byref(dims), int(window))
+
+
+def _marshal_logprobs(logits, tokens, top_n=0, temperature=None, keep_ids=None, logprobs=None,
+                      ranks=None, entropy=None, top_tokens=None, top_logprobs=None, stream=None):
+    pl = _dev_tensor(logits, "logits", torch.bfloat16, 3)
+    B, q_len, V = logits.shape
+    n = int(top_n)
+    if not 0 <= n <= min(32, V):
+        raise ValueError(f"top_n must be in [0, {min(32, V)}] (got {n})")
+    dev = _one_device(logits=logits, tokens=tokens, temperature=temperature, keep_ids=keep_ids,
+                      logprobs=logprobs, ranks=ranks, entropy=entropy, top_tokens=top_tokens,
+                      top_logprobs=top_logprobs)
+
+    def ptr(t, name, dtype, *shape):
+        if t is None:
+            return None
+        p = _dev_tensor(t, name, dtype, len(shape))
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)} (got {tuple(t.shape)})")
+        return p
+
+    f32, i32 = torch.float32, torch.int32
+    if tokens is None:
+        raise ValueError("tokens must be [B, q_len]")
+    outs = [(logprobs, "logprobs", f32, (B, q_len)), (ranks, "ranks", i32, (B, q_len)),
+            (entropy, "entropy", f32, (B, q_len))]
+    if n > 0:
+        outs += [(top_tokens, "top_tokens", i32, (B, q_len, n)),
+                 (top_logprobs, "top_logprobs", f32, (B, q_len, n))]
+    elif top_tokens is not None or top_logprobs is not None:
+        raise ValueError("top_tokens and top_logprobs need top_n > 0")
+    res = [_new(shape, dt, dev, stream) if t is None else t for t, _, dt, shape in outs]
+    po = [ptr(t, name, dt, *shape) for t, (_, name, dt, shape) in zip(res, outs)]
+    args = (pl, ptr(keep_ids, "keep_ids", i32, V), ptr(tokens, "tokens", i32, B, q_len),
+            ptr(temperature, "temperature", f32, B), n, *(po + [None, None])[:5], B, q_len, V,
+            _stream_handle(stream, dev))
+    keep = (logits, tokens, temperature, keep_ids, res)
+    return "swa_token_logprobs", args, keep, tuple((res + [None, None])[:5])
+
+
+def swa_token_logprobs(logits, tokens, top_n=0, temperature=None, keep_ids=None, logprobs=None,
+                       ranks=None, entropy=None, top_tokens=None, top_logprobs=None, stream=None):
+    """Log probabilities of given tokens through the C entry point
+    swa_token_logprobs.
+
+    logits bf16 [B, q_len, V]; tokens int32 [B, q_len]; temperature fp32 [B]
+    or None; keep_ids int32 [V] or None.  Returns (logprobs fp32, ranks
+    int32, entropy fp32, each [B, q_len], top_tokens int32, top_logprobs
+    fp32 [B, q_len, top_n], None when top_n is 0), allocated if not given.
+    Enqueued on `stream` (default: torch's current stream); does not
+    synchronise.
+    """
+    return _issue_on(logits.device, *_marshal_logprobs(
+        logits, tokens, top_n, temperature, keep_ids, logprobs, ranks, entropy, top_tokens,
+        top_logprobs, stream))
+
+
 class PreparedCall:
     """One call validated and marshalled once (see prepare()).
 
@@ -675,14 +891,17 @@ class PreparedCall:
 _MARSHAL = {"swa_verify_attn": _marshal_verify, "swa_verify_attn_noalloc": _marshal_noalloc,
             "swa_verify_attn_paged": _marshal_paged, "swa_append_verify_attn": _marshal_append,
             "swa_sink_verify_attn": _marshal_sink, "swa_qk_norm_rope": _marshal_rope_rows,
-            "swa_qk_norm_rope_append": _marshal_rope_append, "swa_sample_accept": _marshal_sample}
+            "swa_qk_norm_rope_append": _marshal_rope_append, "swa_sample_accept": _marshal_sample,
+            "swa_q8_append": _marshal_q8_append, "swa_q8_read": _marshal_q8_read,
+            "swa_q8_verify_attn": _marshal_q8_verify, "swa_token_logprobs": _marshal_logprobs}
 
 
 def prepare(fn, *args, **kwargs):
     """Validate and marshal a call of swa_verify_attn, swa_verify_attn_noalloc,
     swa_verify_attn_paged, swa_append_verify_attn, swa_sink_verify_attn,
-    swa_qk_norm_rope, swa_qk_norm_rope_append or swa_sample_accept once, with
-    the same arguments the function takes, and return a PreparedCall that
+    swa_qk_norm_rope, swa_qk_norm_rope_append, swa_sample_accept,
+    swa_q8_append, swa_q8_read, swa_q8_verify_attn or swa_token_logprobs once,
+    with the same arguments the function takes, and return a PreparedCall that
     issues it (on the device that is current then: the tensors').
 
     The per-call host cost is then one C call: no tensor checks, no struct

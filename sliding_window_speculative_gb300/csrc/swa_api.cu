@@ -509,12 +509,14 @@ swa_status noalloc_scratch(int dev, void **ptr) {
 // first write the new rows into the cache (swa_append_verify_attn).  With
 // `noalloc` the split partials go to the fixed scratch array above
 // (swa_verify_attn_noalloc) and nothing is ever allocated.  The first `sinks`
-// positions stay visible behind the window (swa_sink_verify_attn).
+// positions stay visible behind the window (swa_sink_verify_attn).  `parts`
+// (non-NULL) holds the split partials instead of the workspace.
 swa_status verify_impl(const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *seq_lens, const int32_t *q_pos, int32_t window, float scale,
                        void *out, float *lse, const swa_dims *dims, swa_stream_t stream,
                        const swa_paged *paged, const void *k_new = nullptr,
-                       const void *v_new = nullptr, bool noalloc = false, int32_t sinks = 0) {
+                       const void *v_new = nullptr, bool noalloc = false, int32_t sinks = 0,
+                       void *parts = nullptr) {
     swa_status st = validate_dims(dims, window);
     if (st != SWA_OK) return st;
     if (!q || !k_cache || !v_cache || !seq_lens || !q_pos || !out)
@@ -581,7 +583,9 @@ swa_status verify_impl(const void *q, const void *k_cache, const void *v_cache,
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (pl.splits > 1) {
         void *ws = nullptr;
-        if (noalloc) {
+        if (parts != nullptr) {
+            ws = parts;
+        } else if (noalloc) {
             if (pl.workspace > (long long)SWA_NOALLOC_SCRATCH_BYTES)
                 return fail(SWA_ERR_WORKSPACE,
                             "this call's %d-way split needs %lld bytes of scratch, above the fixed "
@@ -823,6 +827,26 @@ int swa::api_device_sms(int dev) { return device_sms(dev); }
 
 swa_status swa::api_check_paged(const swa_paged *paged, const swa_dims *dims) {
     return check_paged(paged, dims);
+}
+
+swa_status swa::api_check_dims(const swa_dims *dims, int32_t window) {
+    return validate_dims(dims, window);
+}
+
+swa_status swa::api_workspace(int dev, size_t need, cudaStream_t stream, void **out) {
+    return ensure_workspace(dev, need, stream, out);
+}
+
+size_t swa::api_plan_bytes(const swa_dims *dims, int32_t window, int dev) {
+    return (size_t)make_plan(dims, window, device_sms(dev), true).workspace;
+}
+
+swa_status swa::api_verify_rows(const void *q, const void *k, const void *v,
+                                const int32_t *seq_lens, const int32_t *q_pos, int32_t window,
+                                float scale, void *out, float *lse, const swa_dims *dims,
+                                void *parts, swa_stream_t stream) {
+    return verify_impl(q, k, v, seq_lens, q_pos, window, scale, out, lse, dims, stream, nullptr,
+                       nullptr, nullptr, /*noalloc=*/false, /*sinks=*/0, parts);
 }
 
 bool swa::pdl_enabled() { return g_opt_pdl.load(std::memory_order_relaxed) != 0; }

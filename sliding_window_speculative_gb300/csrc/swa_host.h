@@ -23,6 +23,17 @@ int api_device_sms(int dev);
 // Host checks of a paged cache description against dims.
 swa_status api_check_paged(const swa_paged *paged, const swa_dims *dims);
 
+// The checks of an attention call's dims and window.
+swa_status api_check_dims(const swa_dims *dims, int32_t window);
+// The device's workspace of at least `need` bytes (see swa_verify_attn).
+swa_status api_workspace(int dev, size_t need, cudaStream_t stream, void **out);
+// Bytes of split partials a plain contiguous call of these dims takes, and that
+// call with the partials in `parts`.
+size_t api_plan_bytes(const swa_dims *dims, int32_t window, int dev);
+swa_status api_verify_rows(const void *q, const void *k, const void *v, const int32_t *seq_lens,
+                           const int32_t *q_pos, int32_t window, float scale, void *out, float *lse,
+                           const swa_dims *dims, void *parts, swa_stream_t stream);
+
 inline bool aligned_to(const void *p, uintptr_t n) {
     return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }

@@ -1,0 +1,235 @@
+// Entry points of the 8-bit KV cache: argument checks, launches, and the
+// attention over it.
+#include <cuda_runtime.h>
+
+#include "../../include/swa.h"
+#include "swa_host.h"
+#include "swa_q8.cuh"
+#include "swa_tc_host.h"
+
+namespace {
+
+using swa::aligned_to;
+using swa::api_fail;
+
+swa_status check_dims(const swa_dims *d, bool rows) {
+    if (d == nullptr) return api_fail(SWA_ERR_INVALID_ARG, "dims is NULL");
+    if (d->batch < 1 || d->batch > 65535)
+        return api_fail(SWA_ERR_INVALID_ARG, "batch %d outside [1, 65535]", d->batch);
+    if (rows && (d->q_len < 1 || d->q_len > swa::kMaxBlockLen))
+        return api_fail(SWA_ERR_INVALID_ARG, "q_len %d outside [1, %d]", d->q_len,
+                        swa::kMaxBlockLen);
+    if (d->num_kv_heads < 1 || d->num_kv_heads > 65535)
+        return api_fail(SWA_ERR_INVALID_ARG, "num_kv_heads %d outside [1, 65535]",
+                        d->num_kv_heads);
+    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
+        return api_fail(SWA_ERR_UNSUPPORTED, "head_dim %d not in {64, 128, 256}", d->head_dim);
+    if (d->max_len < 1) return api_fail(SWA_ERR_INVALID_ARG, "max_len %d < 1", d->max_len);
+    return SWA_OK;
+}
+
+swa_status check_cache(const swa_q8_cache *c, const swa_paged *paged, const swa_dims *d) {
+    if (c == nullptr || !c->k || !c->v || !c->k_exp || !c->v_exp)
+        return api_fail(SWA_ERR_INVALID_ARG, "the cache or one of its pointers is NULL");
+    if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16))
+        return api_fail(SWA_ERR_INVALID_ARG, "the K and V caches must be 16-byte aligned");
+    return paged != nullptr ? swa::api_check_paged(paged, d) : SWA_OK;
+}
+
+// The fields that a cache row's place depends on.
+void set_cache(swa::AttnParams &P, const swa_paged *paged, const swa_dims *d,
+               const int32_t *seq_lens, uint32_t *fault) {
+    P.fault = fault;
+    P.B = d->batch;
+    P.Hkv = d->num_kv_heads;
+    P.L = d->max_len;
+    P.seq_lens = seq_lens;
+    if (paged != nullptr) {
+        P.block_table = paged->block_table;
+        P.page_size = paged->page_size;
+        P.max_blocks = paged->max_blocks;
+        P.num_pages = paged->num_pages;
+    }
+}
+
+unsigned blocks_for(long long rows, int rows_per_block, int sms) {
+    const long long n = (rows + rows_per_block - 1) / rows_per_block, cap = 16LL * sms;
+    return (unsigned)(n < cap ? n : cap);
+}
+
+cudaError_t launch_append(const swa::Q8AppendParams &A, int D, int sms, cudaStream_t s) {
+    const dim3 grid(blocks_for(2 * A.rows, swa::kQ8Threads * 8 / D, sms)), block(swa::kQ8Threads);
+    switch (D) {
+        case 64: return swa::launch_kernel(swa::swa_q8_append_kernel<64>, grid, block, 0, s, A);
+        case 128: return swa::launch_kernel(swa::swa_q8_append_kernel<128>, grid, block, 0, s, A);
+        default: return swa::launch_kernel(swa::swa_q8_append_kernel<256>, grid, block, 0, s, A);
+    }
+}
+
+cudaError_t launch_read(const swa::Q8ReadParams &A, int D, int sms, cudaStream_t s) {
+    const dim3 grid(blocks_for(2 * A.rows, swa::kQ8Threads * 16 / D, sms)), block(swa::kQ8Threads);
+    switch (D) {
+        case 64: return swa::launch_kernel(swa::swa_q8_read_kernel<64>, grid, block, 0, s, A);
+        case 128: return swa::launch_kernel(swa::swa_q8_read_kernel<128>, grid, block, 0, s, A);
+        default: return swa::launch_kernel(swa::swa_q8_read_kernel<256>, grid, block, 0, s, A);
+    }
+}
+
+// The bf16 rows of every sequence's windows, [B, Hkv, span, D] for K and for V,
+// the lengths and positions counted from the first of them, and the split
+// partials of the attention over them.
+struct RowsLayout {
+    int span;
+    size_t v, shifted, parts;
+};
+
+RowsLayout rows_layout(const swa_dims *d, int32_t window) {
+    RowsLayout l;
+    const long long span = (long long)window + d->q_len - 1;
+    l.span = (int)(span < d->max_len ? span : d->max_len);
+    const size_t bytes = (size_t)d->batch * d->num_kv_heads * l.span * d->head_dim * 2;
+    l.v = bytes;
+    l.shifted = 2 * bytes;
+    l.parts = l.shifted + ((size_t)d->batch * 8 + 15) / 16 * 16;
+    return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+swa_status swa_q8_append(const void *k_new, const void *v_new, int64_t k_row, int64_t v_row,
+                         const swa_q8_cache *cache, const swa_paged *paged,
+                         const int32_t *seq_lens, const int32_t *q_pos, const swa_dims *dims,
+                         swa_stream_t stream) {
+    swa_status st = check_dims(dims, true);
+    if (st != SWA_OK) return st;
+    if (!k_new || !v_new || !seq_lens || !q_pos)
+        return api_fail(SWA_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned_to(k_new, 16) || !aligned_to(v_new, 16))
+        return api_fail(SWA_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
+    if (!aligned_to(seq_lens, 4) || !aligned_to(q_pos, 4))
+        return api_fail(SWA_ERR_INVALID_ARG, "seq_lens and q_pos must be 4-byte aligned");
+    st = check_cache(cache, paged, dims);
+    if (st != SWA_OK) return st;
+    const int64_t need = (int64_t)dims->num_kv_heads * dims->head_dim;
+    for (int64_t row : {k_row, v_row})
+        if (row < need || row % 8 != 0 || row > ((int64_t)1 << 36))
+            return api_fail(SWA_ERR_INVALID_ARG, "token stride %lld elements is not a multiple of 8 "
+                            "of at least %lld", (long long)row, (long long)need);
+    int dev = 0;
+    uint32_t *fault = nullptr;
+    st = swa::api_device(&dev, &fault);
+    if (st != SWA_OK) return st;
+    swa::Q8AppendParams A{};
+    A.src[0] = static_cast<const __nv_bfloat16 *>(k_new);
+    A.src[1] = static_cast<const __nv_bfloat16 *>(v_new);
+    A.row[0] = k_row;
+    A.row[1] = v_row;
+    A.dst[0] = static_cast<uint8_t *>(cache->k);
+    A.dst[1] = static_cast<uint8_t *>(cache->v);
+    A.exp[0] = cache->k_exp;
+    A.exp[1] = cache->v_exp;
+    set_cache(A.cache, paged, dims, seq_lens, fault);
+    A.cache.q_pos = q_pos;
+    A.cache.q_len = dims->q_len;
+    A.rows = (long long)dims->batch * dims->q_len * dims->num_kv_heads;
+    const cudaError_t e = launch_append(A, dims->head_dim, swa::api_device_sms(dev),
+                                        reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return swa::api_cuda_fail(e, "8-bit append kernel launch");
+    return swa::api_ok();
+}
+
+swa_status swa_q8_read(const swa_q8_cache *cache, const swa_paged *paged, const int32_t *seq_lens,
+                       const int32_t *start, int32_t n, void *k_out, void *v_out,
+                       const swa_dims *dims, swa_stream_t stream) {
+    swa_status st = check_dims(dims, false);
+    if (st != SWA_OK) return st;
+    if (n < 1) return api_fail(SWA_ERR_INVALID_ARG, "n %d < 1", n);
+    if (!seq_lens || !start || !k_out || !v_out)
+        return api_fail(SWA_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16))
+        return api_fail(SWA_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+    if (!aligned_to(seq_lens, 4) || !aligned_to(start, 4))
+        return api_fail(SWA_ERR_INVALID_ARG, "seq_lens and start must be 4-byte aligned");
+    st = check_cache(cache, paged, dims);
+    if (st != SWA_OK) return st;
+    int dev = 0;
+    uint32_t *fault = nullptr;
+    st = swa::api_device(&dev, &fault);
+    if (st != SWA_OK) return st;
+    swa::Q8ReadParams A{};
+    A.src[0] = static_cast<const uint8_t *>(cache->k);
+    A.src[1] = static_cast<const uint8_t *>(cache->v);
+    A.exp[0] = cache->k_exp;
+    A.exp[1] = cache->v_exp;
+    A.dst[0] = static_cast<__nv_bfloat16 *>(k_out);
+    A.dst[1] = static_cast<__nv_bfloat16 *>(v_out);
+    set_cache(A.cache, paged, dims, seq_lens, fault);
+    A.start = start;
+    A.n = n;
+    A.rows = (long long)dims->batch * dims->num_kv_heads * n;
+    const cudaError_t e = launch_read(A, dims->head_dim, swa::api_device_sms(dev),
+                                      reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return swa::api_cuda_fail(e, "8-bit read kernel launch");
+    return swa::api_ok();
+}
+
+size_t swa_q8_workspace_bytes(const swa_dims *dims, int32_t window) {
+    if (swa::api_check_dims(dims, window) != SWA_OK) return 0;
+    const RowsLayout l = rows_layout(dims, window);
+    swa_dims d = *dims;
+    d.max_len = l.span;
+    return l.parts + swa_workspace_bytes(&d, window);
+}
+
+swa_status swa_q8_verify_attn(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
+                              const int32_t *seq_lens, const int32_t *q_pos, int32_t window,
+                              float scale, void *out, float *lse, const swa_dims *dims,
+                              swa_stream_t stream) {
+    swa_status st = swa::api_check_dims(dims, window);
+    if (st != SWA_OK) return st;
+    if (!q || !seq_lens || !q_pos || !out)
+        return api_fail(SWA_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned_to(q, 16) || !aligned_to(out, 16))
+        return api_fail(SWA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+    if (!aligned_to(seq_lens, 4) || !aligned_to(q_pos, 4) || !aligned_to(lse, 4))
+        return api_fail(SWA_ERR_INVALID_ARG, "seq_lens, q_pos and lse must be 4-byte aligned");
+    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f)
+        return api_fail(SWA_ERR_INVALID_ARG, "scale must be finite");
+    st = check_cache(cache, paged, dims);
+    if (st != SWA_OK) return st;
+    int dev = 0;
+    uint32_t *fault = nullptr;
+    st = swa::api_device(&dev, &fault);
+    if (st != SWA_OK) return st;
+
+    const RowsLayout l = rows_layout(dims, window);
+    swa_dims rd = *dims;
+    rd.max_len = l.span;
+    const size_t parts = swa::api_plan_bytes(&rd, window, dev);
+    void *ws = nullptr;
+    st = swa::api_workspace(dev, l.parts + parts, reinterpret_cast<cudaStream_t>(stream), &ws);
+    if (st != SWA_OK) return st;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    swa::Q8ReadParams A{};
+    A.src[0] = static_cast<const uint8_t *>(cache->k);
+    A.src[1] = static_cast<const uint8_t *>(cache->v);
+    A.exp[0] = cache->k_exp;
+    A.exp[1] = cache->v_exp;
+    A.dst[0] = reinterpret_cast<__nv_bfloat16 *>(w);
+    A.dst[1] = reinterpret_cast<__nv_bfloat16 *>(w + l.v);
+    set_cache(A.cache, paged, dims, seq_lens, fault);
+    A.cache.q_pos = q_pos;
+    A.cache.window = window;
+    A.shifted = reinterpret_cast<int32_t *>(w + l.shifted);
+    A.n = l.span;
+    A.rows = (long long)dims->batch * dims->num_kv_heads * l.span;
+    const cudaError_t e = launch_read(A, dims->head_dim, swa::api_device_sms(dev),
+                                      reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return swa::api_cuda_fail(e, "8-bit window kernel launch");
+    return swa::api_verify_rows(q, w, w + l.v, A.shifted, A.shifted + dims->batch, window, scale,
+                                out, lse, &rd, w + l.parts, stream);
+}
+
+}  // extern "C"
