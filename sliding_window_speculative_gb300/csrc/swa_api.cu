@@ -418,11 +418,7 @@ swa_status launch_plan(const Plan &pl, const swa_dims *dims, const swa::AttnPara
         if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
     }
     if (pl.splits > 1) {
-        switch (dims->head_dim) {
-            case 64: e = launch_merge<64>(P, s); break;
-            case 128: e = launch_merge<128>(P, s); break;
-            default: e = launch_merge<256>(P, s); break;
-        }
+        e = swa::api_merge(P, dims->head_dim, s);
         if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
     }
     return SWA_OK;
@@ -848,6 +844,31 @@ swa_status swa::api_verify_rows(const void *q, const void *k, const void *v,
     return verify_impl(q, k, v, seq_lens, q_pos, window, scale, out, lse, dims, stream, nullptr,
                        nullptr, nullptr, /*noalloc=*/false, /*sinks=*/0, parts);
 }
+
+bool swa::api_tc_plan(const swa_dims *dims, int32_t window, int dev, TcPlan *t) {
+    const Plan p = make_plan_with(dims, window, device_sms(dev), 2, false);
+    if (p.kernel != 2) return false;
+    *t = TcPlan{p.rows_per_tile, p.q_rows_per_tile, p.row_tiles, p.tc_n, p.splits, p.chunk,
+                (int)p.grid, p.sms, p.items, p.workspace};
+    return true;
+}
+
+cudaError_t swa::api_merge(const AttnParams &P, int head_dim, cudaStream_t s) {
+    switch (head_dim) {
+        case 64: return launch_merge<64>(P, s);
+        case 128: return launch_merge<128>(P, s);
+        default: return launch_merge<256>(P, s);
+    }
+}
+
+int swa::api_forced_kernel() { return forced_kernel(); }
+
+long long swa::api_wait_limit() {
+    const long long wl = g_opt_wait_limit.load(std::memory_order_relaxed);
+    return wl > 0 ? wl : kWaitLimitCycles;
+}
+
+int swa::api_withhold_fill() { return g_opt_withhold.load(std::memory_order_relaxed); }
 
 bool swa::pdl_enabled() { return g_opt_pdl.load(std::memory_order_relaxed) != 0; }
 

@@ -5,6 +5,7 @@
 #include "../../include/swa.h"
 #include "swa_host.h"
 #include "swa_q8.cuh"
+#include "swa_q8_host.h"
 #include "swa_tc_host.h"
 
 namespace {
@@ -94,6 +95,73 @@ RowsLayout rows_layout(const swa_dims *d, int32_t window) {
     return l;
 }
 
+// Whether a call runs on the fp8 tensor cores straight from the cache: the
+// shapes the key-major kernel takes, unless another kernel is forced.
+bool direct(const swa_dims *d, const swa_paged *paged, int32_t window, int dev, swa::TcPlan *plan) {
+    const int force = swa::api_forced_kernel();
+    if (force != 0 && force != 2) return false;
+    (void)paged;
+    return swa::api_tc_plan(d, window, dev, plan);
+}
+
+swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
+                         const int32_t *seq_lens, const int32_t *q_pos, int32_t window,
+                         float scale, void *out, float *lse, const swa_dims *d,
+                         const swa::TcPlan &pl, int dev, uint32_t *fault, cudaStream_t s) {
+    swa::Q8TcLaunch L{};
+    swa::AttnParams &P = L.T.a;
+    set_cache(P, paged, d, seq_lens, fault);
+    P.q = static_cast<const __nv_bfloat16 *>(q);
+    P.q_pos = q_pos;
+    P.out = static_cast<__nv_bfloat16 *>(out);
+    P.lse = lse;
+    P.q_len = d->q_len;
+    P.Hq = d->num_q_heads;
+    P.G = d->num_q_heads / d->num_kv_heads;
+    P.window = window;
+    P.R = P.q_len * P.G;
+    P.splits = pl.splits;
+    P.chunk = pl.chunk;
+    P.row_tiles = pl.row_tiles;
+    P.rows_per_tile = pl.rows_per_tile;
+    P.qk_scale = scale * swa::kLog2e;
+    P.wait_limit = swa::api_wait_limit();
+    P.withhold_fill = swa::api_withhold_fill();
+    if (pl.splits > 1) {
+        void *ws = nullptr;
+        const swa_status st = swa::api_workspace(dev, (size_t)pl.workspace, s, &ws);
+        if (st != SWA_OK) return st;
+        P.part_acc = static_cast<float *>(ws);
+        P.part_ml = P.part_acc + (size_t)P.B * P.Hkv * P.splits * P.R * d->head_dim;
+    }
+    L.T.rows_per_tile = pl.rows_per_tile;
+    L.T.q_rows_per_tile = pl.q_rows_per_tile;
+    L.T.items = (int)pl.items;
+    L.T.items_per_cta = (int)(pl.items / pl.grid);
+    L.T.items_extra = (int)(pl.items % pl.grid);
+    L.T.early_max = pl.grid * 2 >= pl.sms ? 1 : 8;
+    L.k_exp = cache->k_exp;
+    L.v_exp = cache->v_exp;
+    L.k = cache->k;
+    L.v = cache->v;
+    L.head_dim = d->head_dim;
+    L.n = pl.n;
+    L.grid = pl.grid;
+    L.cache_rows = paged != nullptr
+                       ? (long long)paged->num_pages * d->num_kv_heads * paged->page_size
+                       : (long long)d->batch * d->num_kv_heads * d->max_len;
+    char msg[256] = "";
+    cudaError_t e = swa::q8_tc_launch(L, s, msg, sizeof msg);
+    if (e != cudaSuccess)
+        return msg[0] ? api_fail(SWA_ERR_CUDA, "%s", msg)
+                      : swa::api_cuda_fail(e, "8-bit attention kernel launch");
+    if (pl.splits > 1) {
+        e = swa::api_merge(P, d->head_dim, s);
+        if (e != cudaSuccess) return swa::api_cuda_fail(e, "merge kernel launch");
+    }
+    return swa::api_ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -180,7 +248,9 @@ size_t swa_q8_workspace_bytes(const swa_dims *dims, int32_t window) {
     const RowsLayout l = rows_layout(dims, window);
     swa_dims d = *dims;
     d.max_len = l.span;
-    return l.parts + swa_workspace_bytes(&d, window);
+    const size_t rows = l.parts + swa_workspace_bytes(&d, window);
+    const size_t split = swa_workspace_bytes(dims, window);
+    return rows > split ? rows : split;
 }
 
 swa_status swa_q8_verify_attn(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
@@ -203,6 +273,11 @@ swa_status swa_q8_verify_attn(const void *q, const swa_q8_cache *cache, const sw
     uint32_t *fault = nullptr;
     st = swa::api_device(&dev, &fault);
     if (st != SWA_OK) return st;
+
+    swa::TcPlan plan;
+    if (direct(dims, paged, window, dev, &plan))
+        return attend_direct(q, cache, paged, seq_lens, q_pos, window, scale, out, lse, dims, plan,
+                             dev, fault, reinterpret_cast<cudaStream_t>(stream));
 
     const RowsLayout l = rows_layout(dims, window);
     swa_dims rd = *dims;

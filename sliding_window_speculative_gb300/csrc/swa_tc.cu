@@ -84,6 +84,8 @@ void conf_info(TcConfInfo *c) {
 
 }  // namespace
 
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode() { return load_encode() ? g_encode : nullptr; }
+
 bool tc_conf(int D, int N, TcConfInfo *c) {
     if (D == 256) {
         switch (N) {

@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <stddef.h>
 
 #include <atomic>
@@ -108,6 +109,9 @@ cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, dim3 block, size_t
     if (launch_fault_due()) return cudaErrorLaunchOutOfResources;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+
+// The driver's cuTensorMapEncodeTiled, or NULL.
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode();
 
 // Constants of the (head_dim, padded rows) configuration; false if none.
 bool tc_conf(int D, int N, TcConfInfo *c);
