@@ -13,22 +13,23 @@
 namespace swa {
 namespace {
 
-// Ring slots and Q / P / O buffers per (head_dim, padded rows), within one CTA's
-// 227 KB of shared memory and an SM's 512 TMEM columns.
+// Numbers per weight, ring slots and Q / P / O buffers per (head_dim, padded
+// rows), within one CTA's 227 KB of shared memory and an SM's 512 TMEM columns.
 template <int D, int N>
 struct Q8Conf {
-    static constexpr int NT = D == 256 ? (N == 16 ? 6 : N == 32 ? 5 : 4) : 8;
-    static constexpr int QB = D == 256 && N == 64 ? 1 : 2;
+    static constexpr int NP = D == 256 && N == 64 ? 2 : 3;
+    static constexpr int NT = D == 256 ? (N == 64 ? 3 : 5) : (N == 64 ? 7 : 8);
+    static constexpr int QB = D == 256 && N >= 32 ? 1 : 2;
     static constexpr int PB = 2;
-    static constexpr int OB = D == 256 && N == 64 ? 1 : 2;
-    using C = Q8Cfg<D, N, NT, QB, PB, OB>;
+    static constexpr int OB = N == 64 ? 1 : 2;
+    using C = Q8Cfg<D, N, NP, NT, QB, PB, OB>;
 };
 
 template <int D, int N>
 cudaError_t launch(const Q8TcParams &A, const TcMaps &maps, int grid, cudaStream_t stream) {
     using Cf = Q8Conf<D, N>;
     using C = typename Cf::C;
-    auto kern = swa_q8_tc_kernel<D, N, Cf::NT, Cf::QB, Cf::PB, Cf::OB>;
+    auto kern = swa_q8_tc_kernel<D, N, Cf::NP, Cf::NT, Cf::QB, Cf::PB, Cf::OB>;
     static std::atomic<bool> attr_done[kMaxDevices];
     const cudaError_t e = raise_smem_limit(kern, C::SMEM_BYTES, attr_done);
     if (e != cudaSuccess) return e;

@@ -4,18 +4,21 @@
 // The structure is that of the bf16 key-major kernel: persistent CTAs, keys as
 // the MMA's M dimension, K and V tiles of 128 keys by TMA into a ring,
 //
-//   S^T[128 keys x 2N] = K8_tile[128 x D] . [Q_hi; Q_lo][2N x D]^T
-//   O^T[D x 2N]       += V8_tile^T[D x 128] . [P_hi; P_lo][2N x 128]^T
+//   S^T[128 keys x 2N]  = K8_tile[128 x D] . [Q_hi; Q_lo][2N x D]^T
+//   O^T[D x NP N]      += V8_tile^T[D x 128] . [P_0; ..; P_NP-1][NP N x 128]^T
 //
-// What is not 8-bit by nature is carried in two e4m3 numbers of four
-// significant bits each:
+// What is not 8-bit by nature is carried in e4m3 numbers of four significant
+// bits each:
 //   q = 2^eq (q_hi + q_lo / 16), eq per query row.  A bf16 number has eight
 //     significant bits, so this is exact down to 2^-14 of the row's largest
 //     element and off by at most 2^-22 of it below.
-//   P = p_hi + p_lo / 56: within 2^-9 of P, or within 2^-21 of the row's largest
-//     P where that is more.  (56 is the largest 2^i m, m odd and at most 7,
-//     that keeps the rest of a P up to 256 within 448; a P is first an fp16
-//     number, whose rest times 7 is still exact.)
+//   P = P_0 + (P_1 + P_2 / 16) / 56, three numbers where tensor memory has room
+//     for their sums: that holds an fp16 number's eleven bits, so that P is
+//     within 2^-11, or within 2^-21 of the row's largest P where that is more.
+//     Two numbers: within 2^-9.  (56 is the largest 2^i m, m odd and at most 7,
+//     that keeps what P_0 leaves of a P up to 256 within 448; times 7 that is
+//     still exact in fp16.)  An M = 128 MMA takes 45 cycles with 32 columns, 49
+//     with 64, 57 with 96, 65 with 128 (measured), so the third costs little.
 // Products of e4m3 numbers are exact and summed in fp32 (measured: within 2^-21
 // of the summed magnitudes).
 //
@@ -26,10 +29,20 @@
 // u: weights are resolved relative to what they contribute to the result, so a
 // heavy key of small values does not push the others below the format's range.
 //
-// Warp roles (384 threads): 0 TMA producer, 1 TMEM owner and MMA issuer, 2..9
-// softmax (two warpgroups that split the rows), 10..11 the operands that are not
-// copied as they are: query rows split into their two numbers, and the keys'
-// exponents with the query rows' scales (a ring of tables, a few tiles ahead).
+// Warp roles (512 threads; the registers of the first and last warpgroup that
+// they do not need go to the softmax):
+//   warp 0       TMA producer
+//   warp 1       TMEM owner, issuer of the scores' MMAs
+//   warp 2       issuer of the MMAs into O (one warp for both spent 1.7k cycles a
+//                tile on their conditions beside 2.1k on the MMAs)
+//   warp 3       the keys' factors: a ring of tables, a few tiles ahead
+//   warps 4..11  softmax, two warpgroups that split the packed rows
+//   warps 12..15 query rows split into their two numbers, one item ahead, and
+//                the epilogue of the item before: O is double-buffered, so the
+//                softmax goes on with the next item meanwhile
+//
+// Every wait is bounded; one that gives up sets the fault word and a flag that
+// ends all other waits of the CTA, whose roles then run through their loops.
 #pragma once
 
 #include "swa_q8.cuh"
@@ -37,72 +50,84 @@
 
 namespace swa {
 
-constexpr int kQ8TcThreads = 384;
-constexpr int kQ8Tabs = 4;          // tables of key and row scales
-// The reference maximum of a row sits this far below the largest u of the tile
-// that set it: P = 2^5.2 there, and a later tile may exceed it by 2^2.8 before
-// the references are raised (P at most 2^8).  A lower one would cost the small
-// weights' resolution (2^-10 / 56 / 2^5.2 = 2^-21 of the largest).
-constexpr float kQ8RefBelow = 5.2f;
-constexpr float kQ8RaiseAt = 8.f;
-constexpr float kQ8PLo = 56.f;      // P_lo's scale
-constexpr float kQ8QLo = 16.f;      // Q_lo's
+constexpr int kQ8TcThreads = 512;
+constexpr int kQ8Tabs = 4;          // tables of key factors
+constexpr float kQ8QLo = 16.f;      // scale of Q_lo
+constexpr float kQ8P1 = 56.f;       // scale of P_1, and of P_2 beside it
+constexpr float kQ8P2 = 16.f;
+constexpr float kQ8RaiseAt = 8.f;   // P stays at most 2^8
+
+// Output (and query) row of an item's packed row r: draft row r / G of head
+// r % G.  (An item starts on a draft row; r < 64 and G <= 64, where the product
+// with the rounded-up 2^16 / G is exact.)
+__device__ __forceinline__ size_t q8_row(const AttnParams &P, const TcItem &it, uint32_t inv_g,
+                                         int r) {
+    const int i = (int)((uint32_t)r * inv_g >> 16), gg = r - i * P.G;
+    return ((size_t)it.b * P.q_len + it.i0 + i) * P.Hq + (size_t)it.h * P.G + gg;
+}
+__device__ __forceinline__ uint32_t q8_inv_g(const AttnParams &P) {
+    return 65536u / (uint32_t)P.G + 1u;
+}
 
 struct Q8TcParams {
     TcParams T;
     const int8_t *k_exp, *v_exp;
 };
 
-// A tile's table: per key the factor of its scores (log2 units) and v's
-// exponent, per packed row its query scale.
-template <int N>
-struct Q8Tab {
-    float2 key[kTcTileKeys];
-    float row[N];
-};
-
-template <int D, int N, int NT, int QB, int PB, int OB>
+template <int D, int N, int NP, int NT, int QB, int PB, int OB>
 struct Q8Cfg {
+    // The reference maximum of a row sits this far (log2) below the largest u of
+    // the tile that set it, so a later tile may exceed that by 2^(8 - BELOW)
+    // before the references are raised.  A lower one would cost the small
+    // weights' resolution: half a smallest step of the last number, 2^-10 / 56
+    // (/ 16), is to be within 2^-21 of the largest weight.
+    static constexpr float BELOW = NP == 3 ? 2.f : 5.2f;
     static constexpr int SLABS = D / 128;
     static constexpr int ATOM_BYTES = SLABS * 1024;  // 8 keys x D
     static constexpr int TILE_BYTES = (kTcTileKeys / 8) * ATOM_BYTES;
     static constexpr int Q_SLAB = 2 * N * 128;       // N hi + N lo rows of 128 elements
     static constexpr int Q_BUF = SLABS * Q_SLAB;
-    // P: blocks of 32 columns, [block][key][32 bytes] with 32-byte swizzle;
-    // columns: N hi, then N lo
+    // P: blocks of 32 columns, [block][key][32 bytes] with 32-byte swizzle; the
+    // N columns of P_0, then of P_1, ...
     static constexpr int P_BLOCK = kTcTileKeys * 32;
-    static constexpr int P_BUF = (2 * N / 32) * P_BLOCK;
+    static constexpr int P_BUF = ((NP * N + 31) / 32) * P_BLOCK;
     static constexpr int RING_OFF = 0;
     static constexpr int Q_OFF = RING_OFF + NT * TILE_BYTES;
-    static constexpr int P_OFF = Q_OFF + QB * Q_BUF;
-    static constexpr int TAB_OFF = P_OFF + PB * P_BUF;               // Q8Tab<N> [kQ8Tabs]
-    static constexpr int RED_OFF = TAB_OFF + kQ8Tabs * (int)sizeof(Q8Tab<N>);  // float [2][4][N]
-    static constexpr int LINV_OFF = RED_OFF + 2 * 4 * N * 4;         // float [N]
-    static constexpr int ALPHA_OFF = LINV_OFF + N * 4;               // float [N]
-    static constexpr int ROW_OFF = ALPHA_OFF + N * 4;                // uint32 [N] output rows
-    static constexpr int META_OFF = ROW_OFF + N * 4;                 // TcItem [kTcMetaItems]
+    static constexpr int RAW_OFF = Q_OFF + QB * Q_BUF;  // bf16 [N][D]: the next item's queries
+    static constexpr int P_OFF = RAW_OFF + N * D * 2;
+    static constexpr int TAB_OFF = P_OFF + PB * P_BUF;               // float2 [kQ8Tabs][128]
+    static constexpr int RED_OFF = TAB_OFF + kQ8Tabs * kTcTileKeys * 8;  // float [2][4][N]
+    static constexpr int QSC_OFF = RED_OFF + 2 * 4 * N * 4;          // float [2][N] query scales
+    // float [4][5][N]: per item, a row's sums over each warp's keys, its reference
+    static constexpr int SUM_OFF = QSC_OFF + 2 * N * 4;
+    static constexpr int LINV_OFF = SUM_OFF + 4 * 5 * N * 4;         // float [2][N]
+    static constexpr int ALPHA_OFF = LINV_OFF + 2 * N * 4;           // float [N]
+    static constexpr int ROW_OFF = ALPHA_OFF + N * 4;                // uint32 [2][N] output rows
+    static constexpr int META_OFF = ROW_OFF + 2 * N * 4;             // TcItem [kTcMetaItems]
     static constexpr int FTAB_OFF = META_OFF + kTcMetaItems * (int)sizeof(TcItem);
     static constexpr int BAR_OFF = (FTAB_OFF + kFillTab * 4 + 7) / 8 * 8;
     static constexpr int B_FULL = 0, B_EMPTY = NT, B_QFULL = 2 * NT, B_QEMPTY = B_QFULL + QB,
                          B_SFULL = B_QEMPTY + QB, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
-                         B_PVDONE = B_PFULL + PB, B_OFREE = B_PVDONE + PB, B_DRAIN = B_OFREE + 2,
-                         B_TFULL = B_DRAIN + 1, B_TEMPTY = B_TFULL + kQ8Tabs,
-                         NBARS = B_TEMPTY + kQ8Tabs;
-    static constexpr int B_MIX = 0;  // (the producer's fused appends: none here)
-    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+                         B_PVDONE = B_PFULL + PB, B_OFULL = B_PVDONE + PB, B_OFREE = B_OFULL + OB,
+                         B_LFULL = B_OFREE + OB, B_DRAIN = B_LFULL + 4, B_TFULL = B_DRAIN + 2,
+                         B_TEMPTY = B_TFULL + kQ8Tabs, NBARS = B_TEMPTY + kQ8Tabs;
+    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // tmem base, failed
     static constexpr int END = MISC_OFF + 16;
     static constexpr int SMEM_BYTES = END + 1024;
-    static constexpr int O_COLS = (D / 128) * 2 * N;  // one O^T buffer: hi and lo halves
+    static constexpr int O_HALF = NP * N;             // O^T columns of 128 dims
+    static constexpr int O_COLS = (D / 128) * O_HALF;
     static constexpr int S_COLS = 2 * N;              // one S^T buffer: hi and lo halves
     static constexpr int O_COL = 2 * S_COLS;
     static constexpr int TMEM_USED = O_COL + OB * O_COLS;
     static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
+    // registers per thread: the launch's 128, shifted to the softmax
+    static constexpr int SOFT_REGS = N == 64 ? 168 : 160, OTHER_REGS = 256 - SOFT_REGS;
     static_assert(N == 16 || N == 32 || N == 64, "rows per tile");
     static_assert(NT >= 2 && NT <= 16, "ring slots");
     static_assert(TMEM_USED <= 512, "TMEM");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
     static_assert(Q_OFF % 1024 == 0 && P_OFF % 1024 == 0, "operand alignment");
-    static_assert(RED_OFF % 16 == 0 && META_OFF % 8 == 0, "alignment");
+    static_assert(RED_OFF % 16 == 0 && QSC_OFF % 16 == 0 && META_OFF % 8 == 0, "alignment");
 };
 
 namespace tc {
@@ -137,153 +162,460 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
 // 2^e for any int8 e, kept finite and normal.
 __device__ __forceinline__ float q8_pow2(int e) { return pow2f(e < -126 ? -126 : e); }
 
-// Two floats in [0, 448] as fp16, then as e4m3 hi and lo = e4m3((fp16 - hi) 56):
-// bytes of the first in the low halves.
-__device__ __forceinline__ void split_p(float p0, float p1, uint16_t &hi, uint16_t &lo) {
-    const __half2 p = __floats2half2_rn(p0, p1);
+// The e4m3 pair nearest to an fp16 pair (at most 448), the fp16 pair becoming
+// what is left times `scale`: exact if that has at most 11 bits.
+__device__ __forceinline__ uint16_t take_e4m3(__half2 &p, float scale) {
+    uint16_t c;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
-        : "=h"(hi)
+        : "=h"(c)
         : "r"(*reinterpret_cast<const uint32_t *>(&p)));
-    const uint32_t hb = e4m3x2_to_f16x2(hi);
-    const __half2 r = __hmul2(__hsub2(p, *reinterpret_cast<const __half2 *>(&hb)),
-                              __floats2half2_rn(kQ8PLo, kQ8PLo));
+    const uint32_t b = e4m3x2_to_f16x2(c);
+    p = __hmul2(__hsub2(p, *reinterpret_cast<const __half2 *>(&b)), __floats2half2_rn(scale, scale));
+    return c;
+}
+__device__ __forceinline__ uint16_t last_e4m3(__half2 p) {
+    uint16_t c;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
-        : "=h"(lo)
-        : "r"(*reinterpret_cast<const uint32_t *>(&r)));
+        : "=h"(c)
+        : "r"(*reinterpret_cast<const uint32_t *>(&p)));
+    return c;
 }
 
-// Warps 10 and 11: the query rows of every item as two e4m3 numbers each, and
-// per tile the table of key and row scales.  Warp w of the two takes rows w,
-// w + 2, ..., (RP at a time), the lane i keeping the scale of its i-th row, and
-// keys 64 w ...
-template <class C, int D, int N, int QB>
-__device__ __forceinline__ void q8_operands(const Q8TcParams &A, const TcItem *meta, uint8_t *qs,
-                                            Q8Tab<N> *tabs, uint64_t *bars, int w) {
-    using namespace tc;
-    const TcParams &T = A.T;
-    const AttnParams &P = T.a;
-    constexpr int LPR = D / 8, RP = 32 / LPR;  // lanes per row, rows per pass
-    constexpr int U = 4;                       // passes in flight
-    const int lane = (int)(threadIdx.x & 31);
-    const int sub = lane / LPR, l = lane % LPR;
-    uint32_t g = 0, k = 0;
-    const int n_items = cta_items(T);
-    for (int j = 0; j < n_items; ++j) {
-        const TcItem it = tc_decode<false>(T, cta_item(T, j), j, meta);
-        if (it.n_tiles == 0) continue;
-        const uint32_t qb = k % QB, quse = k / QB;
-        ++k;
-        uint8_t *q = qs + qb * C::Q_BUF;
-        float scale = 1.f;  // of row w + 2 * lane
-        bool waited = false;
-        const int mine = (it.rows - w + 1) / 2;  // rows w, w + 2, ... of this warp
-        for (int i0 = 0; i0 < mine; i0 += RP * U) {
-            uint4 x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = w + 2 * (i0 + u * RP + sub);
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (r < it.rows) {
-                    const int rg = it.row0 + r, i = rg / P.G, gg = rg - i * P.G;
-                    const size_t row = ((size_t)it.b * P.q_len + i) * P.Hq + (size_t)it.h * P.G + gg;
-                    x[u] = __ldg(reinterpret_cast<const uint4 *>(P.q + row * D) + l);
-                }
-            }
-            if (!waited) {
-                // the buffer's previous rows are done with
-                if (!mbar_wait_bounded(&bars[C::B_QEMPTY + qb], (quse & 1) ^ 1, P.fault,
-                                       kFaultCopyTimeout, P.wait_limit))
-                    return;
-                waited = true;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t b[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                float f[8], a = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[2 * e] = bf16lo(b[e]);
-                    f[2 * e + 1] = bf16hi(b[e]);
-                    a = fmaxf(a, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
-                }
-#pragma unroll
-                for (int off = LPR / 2; off >= 1; off >>= 1)
-                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-                // the smallest exponent that holds the row, as for the cache
-                const uint32_t ab = __float_as_uint(a);
-                int e = (int)(ab >> 23) - 135 + ((ab & 0x7fffffu) > 0x600000u ? 1 : 0);
-                e = e < -126 ? -126 : (e > 126 ? 126 : e);
-                const float sc = pow2f(-e);
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const float y0 = f[2 * p] * sc, y1 = f[2 * p + 1] * sc;
-                    const uint16_t h = e4m3x2(y0, y1);
-                    const uint32_t hb = e4m3x2_to_f16x2(h);
-                    const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hb));
-                    const uint16_t r = e4m3x2((y0 - hf.x) * kQ8QLo, (y1 - hf.y) * kQ8QLo);
-                    if (p & 1) {
-                        hi[p >> 1] |= (uint32_t)h << 16;
-                        lo[p >> 1] |= (uint32_t)r << 16;
-                    } else {
-                        hi[p >> 1] = h;
-                        lo[p >> 1] = r;
-                    }
-                }
-                const int i = i0 + u * RP + sub, r = w + 2 * i;
-#pragma unroll
-                for (int s = 0; s < RP; ++s) {
-                    const float v = __shfl_sync(0xffffffffu, pow2f(e), s * LPR);
-                    if (lane == i0 + u * RP + s) scale = v;
-                }
-                if (r < it.rows) {
-                    // 8 bytes at element 8 l: 16-byte chunk (l / 2) % 8 of slab l / 16
-                    const uint32_t ch = (uint32_t)(l >> 1) & 7;
-                    const uint32_t at = (uint32_t)(l >> 4) * C::Q_SLAB + (uint32_t)(l & 1) * 8;
-                    // (N is a multiple of 8: both rows have the same swizzle phase)
-                    const uint32_t sw = (ch ^ (uint32_t)(r & 7)) << 4;
-                    *reinterpret_cast<uint2 *>(q + at + r * 128 + sw) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2 *>(q + at + (N + r) * 128 + sw) =
-                        make_uint2(lo[0], lo[1]);
-                }
-            }
-        }
-        if (!waited &&
-            !mbar_wait_bounded(&bars[C::B_QEMPTY + qb], (quse & 1) ^ 1, P.fault, kFaultCopyTimeout,
-                               P.wait_limit))
-            return;
-        fence_proxy_async_smem();
-        mbar_arrive(&bars[C::B_QFULL + qb]);
+// The largest of the warp's values, in every lane (a NaN is ignored).
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
 
-        for (int t = 0; t < it.n_tiles; ++t, ++g) {
-            float2 key[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int jk = it.t0 + kTcTileKeys * t + 64 * w + 32 * c + lane;
-                int ke = 0, ve = 0;
-                if (jk >= it.cr.c_lo && jk < it.cr.c_hi) {
-                    const long long row = cache_row(P, it.b, it.h, jk);
-                    ke = A.k_exp[row];
-                    ve = A.v_exp[row];
-                }
-                key[c] = make_float2(P.qk_scale * q8_pow2(ke), (float)ve);
-            }
-            const uint32_t slot = g % kQ8Tabs;
-            if (!mbar_wait_bounded(&bars[C::B_TEMPTY + slot], ((g / kQ8Tabs) & 1) ^ 1, P.fault,
-                                   kFaultCopyTimeout, P.wait_limit))
-                return;
-            tabs[slot].key[64 * w + lane] = key[0];
-            tabs[slot].key[64 * w + 32 + lane] = key[1];
-            if (lane < N / 2) tabs[slot].row[w + 2 * lane] = scale;
-            mbar_arrive(&bars[C::B_TFULL + slot]);
+// The kernel's hot code has to stay in the instruction cache beside that of 15
+// other warps (with everything inlined it was 187 KB, and warps waited 26% of
+// their time for instructions): what is rare, or run by several roles, is a
+// function of its own.
+__device__ __noinline__ void q8_wait_on(uint64_t *bar, uint32_t parity, const AttnParams *P,
+                                        volatile uint32_t *failed) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*failed) return;
+        if (clock64() - t0 > P->wait_limit) {
+            atomicOr(P->fault, kFaultCopyTimeout);
+            *failed = 1;
+            return;
         }
     }
 }
 
-template <int D, int N, int NT, int QB, int PB, int OB>
+// Waits for phase `parity` of `bar`, or until some wait of the CTA gave up.
+__device__ __forceinline__ void q8_wait(uint64_t *bar, uint32_t parity, const AttnParams &P,
+                                        volatile uint32_t *failed) {
+    if (!mbar_try_wait(bar, parity)) q8_wait_on(bar, parity, &P, failed);
+}
+
+// The warp's arrival once all its lanes are here (32 arrivals on one barrier would
+// be served one after another).
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// The same without a call, for the softmax: its registers are its rows.
+__device__ __forceinline__ void q8_wait_here(uint64_t *bar, uint32_t parity, const AttnParams &P,
+                                             volatile uint32_t *failed) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint32_t t0 = (uint32_t)(clock64() >> 10);
+    while (!mbar_try_wait(bar, parity)) {
+        if (*failed) return;
+        if ((uint32_t)(clock64() >> 10) - t0 > (uint32_t)(P.wait_limit >> 10)) {
+            atomicOr(P.fault, kFaultCopyTimeout);
+            *failed = 1;
+            return;
+        }
+    }
+}
+
+// The j-th item of this CTA: the first kTcMetaItems from shared memory.
+__device__ __noinline__ void q8_decode(const TcParams *T, int j, TcItem *it) {
+    *it = tc_decode_global<false>(*T, cta_item(*T, j));
+}
+__device__ __forceinline__ TcItem q8_item(const TcParams &T, int j, const TcItem *meta) {
+    if (j < kTcMetaItems) return meta[j];
+    TcItem it;
+    q8_decode(&T, j, &it);
+    return it;
+}
+
+// One lane's copies of a K or V tile: `whole` atoms of consecutive cache rows
+// from row y on, and `partial` one more.
+template <class C>
+__device__ __noinline__ void q8_copy(const CUtensorMap *m4, const CUtensorMap *m1, int y, int whole,
+                                     bool partial, uint8_t *dst, uint64_t *bar, uint64_t policy) {
+    atom_run<C::ATOM_BYTES>(m4, m1, y, whole, partial, dst, bar, policy);
+}
+
+// Fills 0 .. early_fills - 1 of the CTA's first item, one from each of the first
+// warps' lane 0, ahead of the producer (a contiguous cache; see swa_tc.cuh).
+template <class C, int NT>
+__device__ __forceinline__ void q8_early_fills(const TcParams &T, const TcMaps &M,
+                                               volatile uint32_t *ftab, uint8_t *ring,
+                                               uint64_t *bars, int warp) {
+    const AttnParams &P = T.a;
+    if (P.block_table != nullptr || warp >= NT || cta_items(T) < 1) return;
+    TcItem it;
+    q8_decode(&T, 0, &it);
+    if (warp >= early_fills<NT, false>(T, it)) return;
+    const int p = it.t0 + kTcTileKeys * (warp >> 1), kv = warp & 1;
+    const int n = min(kTcTileKeys, it.cr.c_hi - p);
+    ftab[warp] = ((uint32_t)warp << 8) | (uint32_t)warp;  // fill w -> slot w, use parity 0
+    mbar_arrive_expect_tx(&bars[C::B_FULL + warp], (uint32_t)((n + 7) >> 3) * C::ATOM_BYTES);
+    if (P.withhold_fill == warp && blockIdx.x == 0) return;
+    q8_copy<C>(kv ? M.v_atoms : M.k_atoms, kv ? &M.v_atom : &M.k_atom,
+               (int)(((long long)it.b * P.Hkv + it.h) * P.L + p), n >> 3, (n & 7) != 0,
+               ring + warp * C::TILE_BYTES, &bars[C::B_FULL + warp],
+               P.row_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first());
+}
+
+// The TMA producer (warp 0): every item's K and V tiles into the first free ring
+// slots, as the bf16 kernels' (swa_tc.cuh), with a paged tile's page ids read
+// once for K and V and a tile ahead.  A contiguous cache takes lane 0 alone.
+// Waits for every copy it issued before returning.
+template <class C, int NT>
+__device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, const TcItem *meta,
+                                            volatile uint32_t *ftab, uint8_t *ring, uint64_t *bars,
+                                            volatile uint32_t *failed) {
+    using namespace tc;
+    const AttnParams &P = T.a;
+    const int lane = (int)(threadIdx.x & 31);
+    const bool paged = P.block_table != nullptr;
+    if (!paged && lane != 0) return;
+    const uint64_t policy = P.row_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+    const int ps = paged ? P.page_size : 8, pa = ps >> 3;  // rows, atoms per page
+    uint32_t uses[NT];  // fills handed to each slot so far
+    const int n_items = cta_items(T);
+    const int n_early = n_items > 0 ? early_fills<NT, false>(T, meta[0]) : 0;
+#pragma unroll
+    for (int s = 0; s < NT; ++s) uses[s] = s < n_early ? 1 : 0;  // fill s went to slot s
+    uint32_t f = (uint32_t)n_early;
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; j < n_items && ok; ++j) {
+        const TcItem it = q8_item(T, j, meta);
+        int page = 0;  // of this lane's run of the tile
+#pragma unroll 1
+        for (int t = paged ? -1 : 0; t < it.n_tiles && ok; ++t) {
+            // the next tile's page ids are on their way while this one's slots are
+            // waited for
+            int next = 0;
+            if (paged && t + 1 < it.n_tiles) {
+                const int p = it.t0 + kTcTileKeys * (t + 1);
+                const int k0 = p / ps, first = (ps - (p - k0 * ps)) >> 3;
+                const int a = lane == 0 ? 0 : first + (lane - 1) * pa;
+                if (8 * a < min(kTcTileKeys, it.cr.c_hi - p))
+                    next = __ldg(P.block_table + (long long)it.b * P.max_blocks + k0 + lane);
+            }
+            if (t < 0) {
+                page = next;
+                continue;
+            }
+            // this lane's run of atoms: all of the tile, or (paged) a page's
+            const int p = it.t0 + kTcTileKeys * t;
+            const int n = min(kTcTileKeys, it.cr.c_hi - p);
+            const int natoms = (n + 7) >> 3;
+            int a = 0, run = natoms, y;
+            if (paged) {
+                const int in = p % ps, first = (ps - in) >> 3;
+                a = lane == 0 ? 0 : first + (lane - 1) * pa;
+                run = min(lane == 0 ? first : pa, natoms - a);
+                y = (checked_page(P, page, nullptr) * P.Hkv + it.h) * ps + (lane == 0 ? in : 0);
+            } else {
+                y = (int)(((long long)it.b * P.Hkv + it.h) * P.L + p);
+            }
+            const int whole = min(max((n >> 3) - a, 0), run);
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                if (j == 0 && 2 * t + kv < n_early) continue;  // issued ahead of the loop
+                int slot = -1;
+                if (lane == 0) {
+                    uint32_t par = 0;
+                    const long long w0 = clock64();
+                    for (int spin = 0;; ++spin) {
+#pragma unroll
+                        for (int s = 0; s < NT; ++s)
+                            if (slot < 0 && (uses[s] == 0 ||
+                                             mbar_test(&bars[C::B_EMPTY + s], (uses[s] - 1) & 1))) {
+                                slot = s;
+                                par = uses[s] & 1;
+                                ++uses[s];
+                            }
+                        if (slot >= 0 || *failed) break;
+                        if (clock64() - w0 > P.wait_limit) {
+                            atomicOr(P.fault, kFaultCopyTimeout);
+                            *failed = 1;
+                            break;
+                        }
+                        if (spin > 8) __nanosleep(32);
+                    }
+                    if (slot >= 0) {
+                        ftab[f % kFillTab] = (f << 8) | (par << 4) | (uint32_t)slot;
+                        mbar_arrive_expect_tx(&bars[C::B_FULL + slot],
+                                              (uint32_t)natoms * C::ATOM_BYTES);
+                    }
+                }
+                if (paged) slot = __shfl_sync(0xffffffffu, slot, 0);
+                ok = slot >= 0;
+                if (!ok) break;
+                // (tests of the bounded waits: this fill's copies are never issued)
+                if (run > 0 && !(P.withhold_fill == (int)f && blockIdx.x == 0))
+                    q8_copy<C>(kv ? M.v_atoms : M.k_atoms, kv ? &M.v_atom : &M.k_atom, y, whole,
+                               run > whole, ring + slot * C::TILE_BYTES + a * C::ATOM_BYTES,
+                               &bars[C::B_FULL + slot], policy);
+                ++f;
+            }
+            page = next;
+        }
+    }
+    if (lane != 0) return;
+    // every copy this CTA issued has landed before it exits
+#pragma unroll
+    for (int s = 0; s < NT; ++s)
+        if (uses[s] > 0)
+            mbar_wait_bounded(&bars[C::B_FULL + s], (uses[s] - 1) & 1, P.fault, kFaultCopyTimeout,
+                              P.wait_limit);
+}
+
+// Warp 3: per tile and key the factor of its scores (k's scale, in log2 units) and
+// v's exponent.  A lane takes four keys of a tile (of one page, if paged: tiles
+// then start on an 8-key boundary); the exponents of the next three tiles are on
+// their way while a tile waits for its slot.
+template <class C>
+__device__ __forceinline__ void q8_tables(const Q8TcParams &A, const TcItem *meta, float2 *tabs,
+                                          uint64_t *bars, volatile uint32_t *failed) {
+    const TcParams &T = A.T;
+    const AttnParams &P = T.a;
+    constexpr int AHEAD = 3;
+    const int lane = (int)(threadIdx.x & 31);
+    const int n_items = cta_items(T);
+    uint32_t g = 0;  // tiles asked for
+    int8_t e[AHEAD + 1][8];
+    auto publish = [&](uint32_t f, const int8_t(&x)[8]) {
+        const uint32_t slot = f % kQ8Tabs;
+        q8_wait(&bars[C::B_TEMPTY + slot], ((f / kQ8Tabs) & 1) ^ 1, P, failed);
+        float4 *tab = reinterpret_cast<float4 *>(tabs + slot * kTcTileKeys + 4 * lane);
+#pragma unroll
+        for (int c = 0; c < 4; c += 2)
+            tab[c / 2] = make_float4(P.qk_scale * q8_pow2(x[c]), (float)x[4 + c],
+                                     P.qk_scale * q8_pow2(x[c + 1]), (float)x[5 + c]);
+        warp_arrive(&bars[C::B_TFULL + slot]);
+    };
+    // (past the last item AHEAD steps more publish what is still held)
+#pragma unroll 1
+    for (int j = 0; j <= n_items; ++j) {
+        TcItem it;
+        it.n_tiles = AHEAD;
+        if (j < n_items) it = q8_item(T, j, meta);
+#pragma unroll 1
+        for (int t = 0; t < it.n_tiles; ++t, ++g) {
+#pragma unroll
+            for (int a = AHEAD; a > 0; --a)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) e[a][c] = e[a - 1][c];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) e[0][c] = 0;
+            if (j < n_items) {
+                const int jk = it.t0 + kTcTileKeys * t + 4 * lane;
+                if (jk + 3 >= it.cr.c_lo && jk < it.cr.c_hi) {
+                    const long long row = cache_row(P, it.b, it.h, jk);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (jk + c >= it.cr.c_lo && jk + c < it.cr.c_hi) {
+                            e[0][c] = A.k_exp[row + c];
+                            e[0][4 + c] = A.v_exp[row + c];
+                        }
+                }
+            }
+            if (g >= AHEAD) publish(g - AHEAD, e[AHEAD]);
+        }
+    }
+}
+
+// Warps 12..15, first job: an item's query rows as two e4m3 numbers each, and
+// their scales.  Warp w of the four takes rows w, w + 4, ..., RP at a time.  The
+// rows come through a buffer of their own, an item ahead of their use
+// (q8_fetch_queries): a plain load takes microseconds while the tiles' copies
+// keep the memory busy.  A thread splits what it copied itself.
+template <int D>
+__device__ __forceinline__ void q8_fetch_queries(const AttnParams &P, const TcItem &it, uint8_t *raw,
+                                                 int w, uint32_t inv_g) {
+    constexpr int LPR = D / 8, RP = 32 / LPR;  // lanes per row, rows per pass
+    const int lane = (int)(threadIdx.x & 31);
+    const int l = lane % LPR;
+#pragma unroll 1
+    for (int r = w + 4 * (lane / LPR); r < it.rows; r += 4 * RP)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         smem_u32(raw + r * (D * 2) + l * 16)),
+                     "l"(P.q + q8_row(P, it, inv_g, r) * D + l * 8)
+                     : "memory");
+}
+
+template <class C, int D, int N, int QB>
+__device__ __forceinline__ void q8_queries(const AttnParams &P, const TcItem &it, uint32_t k,
+                                           const uint8_t *raw, uint8_t *qs, float *qsc,
+                                           uint64_t *bars, volatile uint32_t *failed, int w) {
+    constexpr int LPR = D / 8, RP = 32 / LPR;
+    const int lane = (int)(threadIdx.x & 31);
+    const int sub = lane / LPR, l = lane % LPR;
+    const uint32_t qb = k % QB;
+    uint8_t *q = qs + qb * C::Q_BUF;
+    // 8 bytes at element 8 l: 16-byte chunk (l / 2) % 8 of slab l / 16
+    const uint32_t at = (uint32_t)(l >> 4) * C::Q_SLAB + (uint32_t)(l & 1) * 8;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // the buffer's previous rows are done with
+    q8_wait(&bars[C::B_QEMPTY + qb], ((k / QB) & 1) ^ 1, P, failed);
+#pragma unroll 2
+    for (int r0 = w; r0 < it.rows; r0 += 4 * RP) {
+        const int r = r0 + 4 * sub;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < it.rows) x = *reinterpret_cast<const uint4 *>(raw + r * (D * 2) + l * 16);
+        const uint32_t b[4] = {x.x, x.y, x.z, x.w};
+        float a = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a = tc::fmax3(a, fabsf(bf16lo(b[e])), fabsf(bf16hi(b[e])));
+        if constexpr (LPR == 32) {
+            a = warp_max(a);
+        } else {
+#pragma unroll
+            for (int off = LPR / 2; off >= 1; off >>= 1)
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        }
+        // the smallest exponent that holds the row, as for the cache
+        const uint32_t ab = __float_as_uint(a);
+        int e = (int)(ab >> 23) - 135 + ((ab & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = e < -126 ? -126 : (e > 126 ? 126 : e);
+        const float sc = pow2f(-e);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            // (exact in fp16 from 2^-17 on: eight bits above its 2^-24)
+            __half2 y = __floats2half2_rn(bf16lo(b[p]) * sc, bf16hi(b[p]) * sc);
+            const uint32_t h = take_e4m3(y, kQ8QLo), t = last_e4m3(y);
+            hi[p >> 1] = p & 1 ? hi[p >> 1] | (h << 16) : h;
+            lo[p >> 1] = p & 1 ? lo[p >> 1] | (t << 16) : t;
+        }
+        if (r < it.rows) {
+            // (N is a multiple of 8: both rows have the same swizzle phase)
+            const uint32_t sw = (((uint32_t)(l >> 1) & 7) ^ (uint32_t)(r & 7)) << 4;
+            *reinterpret_cast<uint2 *>(q + at + r * 128 + sw) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(q + at + (N + r) * 128 + sw) = make_uint2(lo[0], lo[1]);
+            if (l == 0) qsc[(k & 1) * N + r] = pow2f(e);
+        }
+    }
+    fence_proxy_async_smem();
+    warp_arrive(&bars[C::B_QFULL + qb]);
+}
+
+// Warps 12..15, second job: the k-th item's O through 1 / l to the output (or to
+// the split partials), and the rows of an item without keys.
+template <class C, int D, int N, int NP, int OB>
+__device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &it, uint32_t k,
+                                            uint32_t tmem, const float *sums, float *linv,
+                                            uint32_t *rowidx, uint64_t *bars,
+                                            volatile uint32_t *failed, uint32_t inv_g) {
+    using namespace tc;
+    constexpr int MH = D / 128;
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    const int t = (int)threadIdx.x - (kQ8TcThreads - 128);  // 0..127
+    const int lane = t & 31, quad = t >> 5;
+    const size_t bh = (size_t)it.b * P.Hkv + it.h;
+    const size_t prow0 = (bh * P.splits + it.split) * P.R + it.row0;
+    if (it.n_tiles == 0) {
+        for (int idx = t; idx < it.rows * D; idx += 128) {
+            const int r = idx / D, d = idx % D;
+            if (P.splits == 1) {
+                const size_t orow = q8_row(P, it, inv_g, r);
+                P.out[orow * D + d] = __float2bfloat16_rn(0.f);
+                if (d == 0 && P.lse != nullptr) P.lse[orow] = NEG_INF;
+            } else {
+                P.part_acc[(prow0 + r) * D + d] = 0.f;
+                if (d == 0) {
+                    P.part_ml[(prow0 + r) * 2] = NEG_INF;
+                    P.part_ml[(prow0 + r) * 2 + 1] = 0.f;
+                }
+            }
+        }
+        return;
+    }
+    // (below 2^31 by the plan's size checks)
+    uint32_t *rows = rowidx + (k & 1) * N;
+    float *li = linv + (k & 1) * N;
+    const uint32_t ob = k % OB;
+    const uint32_t orow = t < it.rows ? (uint32_t)q8_row(P, it, inv_g, t) : 0u;
+    q8_wait(&bars[C::B_LFULL + (k & 3)], (k >> 2) & 1, P, failed);
+    if (t < it.rows) {
+        const float *sum = sums + (k & 3) * 5 * N + t;
+        const float l = (sum[0] + sum[N]) + (sum[2 * N] + sum[3 * N]);
+        const float m = sum[4 * N];
+        const bool any = !(l <= 0.f);  // (a NaN stays one)
+        rows[t] = orow;
+        li[t] = any ? __frcp_rn(l) : 0.f;
+        if (P.splits > 1) {
+            P.part_ml[(prow0 + t) * 2] = any ? m : NEG_INF;
+            P.part_ml[(prow0 + t) * 2 + 1] = l;
+        } else if (P.lse != nullptr) {
+            P.lse[orow] = any ? (m + __log2f(l)) * kLn2 : NEG_INF;
+        }
+    }
+    asm volatile("bar.sync 5, 128;" ::: "memory");
+    q8_wait(&bars[C::B_OFULL + ob], (k / OB) & 1, P, failed);
+    fence_after_sync();
+    const uint32_t o0 = tmem + ((uint32_t)(quad * 32) << 16) + C::O_COL + ob * C::O_COLS;
+    const uint64_t s1 = f2_pack(1.f / kQ8P1, 1.f / kQ8P1), s2 = f2_pack(1.f / kQ8P2, 1.f / kQ8P2);
+    // neighbouring lanes hold neighbouring dims: each pair swaps halves of two
+    // rows, so that a lane stores two dims of one row
+    const bool odd = lane & 1;
+    __nv_bfloat16 *out = P.out + (t & ~1);
+#pragma unroll 1
+    for (int c0 = 0; c0 < N; c0 += 16) {
+        if (c0 >= it.rows) break;
+#pragma unroll
+        for (int mh = 0; mh < MH; ++mh) {
+            uint32_t o[NP][16];
+#pragma unroll
+            for (int p = 0; p < NP; ++p) tmem_load<16>(o0 + mh * C::O_HALF + p * N + c0, o[p]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                auto pair = [&](int p) {
+                    return f2_pack(__uint_as_float(o[p][e]), __uint_as_float(o[p][e + 1]));
+                };
+                uint64_t x2 = pair(1);
+                if constexpr (NP == 3) x2 = f2_fma(pair(2), s2, x2);
+                x2 = f2_fma(x2, s1, pair(0));
+                float a, b;
+                if (P.splits == 1) {
+                    const float2 l2 = *reinterpret_cast<const float2 *>(li + c0 + e);
+                    f2_unpack(f2_mul(x2, f2_pack(l2.x, l2.y)), a, b);
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                    const int r = c0 + e + (odd ? 1 : 0);
+                    const uint32_t w = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                    if (r < it.rows)
+                        *reinterpret_cast<uint32_t *>(out + (size_t)rows[r] * D + mh * 128) = w;
+                } else {
+                    f2_unpack(x2, a, b);
+                    float *acc = P.part_acc + (prow0 + c0 + e) * D + mh * 128 + t;
+                    if (c0 + e < it.rows) acc[0] = a;
+                    if (c0 + e + 1 < it.rows) acc[D] = b;
+                }
+            }
+        }
+    }
+    // O and the item's sums may be overwritten
+    fence_before_sync();
+    warp_arrive(&bars[C::B_OFREE + ob]);
+}
+
+template <int D, int N, int NP, int NT, int QB, int PB, int OB>
 __global__ void __launch_bounds__(kQ8TcThreads, 1)
     swa_q8_tc_kernel(const __grid_constant__ Q8TcParams A, const __grid_constant__ TcMaps M) {
-    using C = Q8Cfg<D, N, NT, QB, PB, OB>;
+    using C = Q8Cfg<D, N, NP, NT, QB, PB, OB>;
     using namespace tc;
     constexpr int MH = D / 128;
     const float NEG_INF = -__int_as_float(0x7f800000);
@@ -295,9 +627,12 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                                               ~static_cast<uintptr_t>(1023));
     uint8_t *ring = sm + C::RING_OFF;
     uint8_t *qs = sm + C::Q_OFF;
+    uint8_t *raw = sm + C::RAW_OFF;
     uint8_t *ps = sm + C::P_OFF;
-    Q8Tab<N> *tabs = reinterpret_cast<Q8Tab<N> *>(sm + C::TAB_OFF);
+    float2 *tabs = reinterpret_cast<float2 *>(sm + C::TAB_OFF);
     float *red = reinterpret_cast<float *>(sm + C::RED_OFF);
+    float *qsc = reinterpret_cast<float *>(sm + C::QSC_OFF);
+    float *sums = reinterpret_cast<float *>(sm + C::SUM_OFF);
     float *linv = reinterpret_cast<float *>(sm + C::LINV_OFF);
     float *alpha_sm = reinterpret_cast<float *>(sm + C::ALPHA_OFF);
     uint32_t *rowidx = reinterpret_cast<uint32_t *>(sm + C::ROW_OFF);
@@ -305,6 +640,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
     volatile uint32_t *ftab = reinterpret_cast<volatile uint32_t *>(sm + C::FTAB_OFF);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::BAR_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC_OFF);
+    volatile uint32_t *failed = tmem_slot + 1;
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
@@ -318,28 +654,33 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
         prefetch_tmap(mp);
     }
     if (tid == 0) {
+        *failed = 0;
         for (int i = 0; i < NT; ++i) {
             mbar_init(&bars[C::B_FULL + i], 1);
             mbar_init(&bars[C::B_EMPTY + i], 1);
         }
         for (int i = 0; i < QB; ++i) {
-            mbar_init(&bars[C::B_QFULL + i], 64);
+            mbar_init(&bars[C::B_QFULL + i], 4);
             mbar_init(&bars[C::B_QEMPTY + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[C::B_SFULL + i], 1);
-            mbar_init(&bars[C::B_SFREE + i], 256);
-            mbar_init(&bars[C::B_OFREE + i], 256);
+            mbar_init(&bars[C::B_SFREE + i], 8);
         }
         for (int i = 0; i < PB; ++i) {
-            mbar_init(&bars[C::B_PFULL + i], 256);
+            mbar_init(&bars[C::B_PFULL + i], 8);
             mbar_init(&bars[C::B_PVDONE + i], 1);
         }
-        for (int i = 0; i < kQ8Tabs; ++i) {
-            mbar_init(&bars[C::B_TFULL + i], 64);
-            mbar_init(&bars[C::B_TEMPTY + i], 256);
+        for (int i = 0; i < OB; ++i) {
+            mbar_init(&bars[C::B_OFULL + i], 1);
+            mbar_init(&bars[C::B_OFREE + i], 4);
         }
-        mbar_init(&bars[C::B_DRAIN], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bars[C::B_LFULL + i], 8);
+        for (int i = 0; i < kQ8Tabs; ++i) {
+            mbar_init(&bars[C::B_TFULL + i], 1);
+            mbar_init(&bars[C::B_TEMPTY + i], 8);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(&bars[C::B_DRAIN + i], 1);
         fence_barrier_init();
     }
     // query rows past an item's stay what they are here: zero, or another
@@ -347,6 +688,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
     // references either)
     for (int i = tid; i < QB * C::Q_BUF / 16; i += kQ8TcThreads)
         reinterpret_cast<uint4 *>(qs)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < 2 * N; i += kQ8TcThreads) qsc[i] = 0.f;
     fence_proxy_async_smem();
     for (int i = tid; i < kFillTab; i += kQ8TcThreads) ftab[i] = 0xffffffffu;
     if (warp == 1) {
@@ -356,94 +698,112 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
     __syncthreads();
     grid_dep_wait();
     grid_dep_trigger();
-    if (lane == 0) issue_early_fills<C, NT, false, false, false>(T, M, ftab, ring, qs, bars, warp);
+    if (lane == 0) q8_early_fills<C, NT>(T, M, ftab, ring, bars, warp);
     for (int j = tid; j < kTcMetaItems; j += kQ8TcThreads)
-        if (j < cta_items(T)) meta[j] = tc_decode_global<false>(T, cta_item(T, j));
+        if (j < cta_items(T)) q8_decode(&T, j, &meta[j]);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    const int n_items = cta_items(T);
 
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+    }
     if (warp == 0) {
         // ======================================================= producer
-        tile_producer<C, NT, QB, false, false, false>(T, M, meta, ftab, ring, qs, bars, true);
-    } else if (warp == 1) {
+        q8_producer<C, NT>(T, M, meta, ftab, ring, bars, failed);
+    } else if (warp <= 2) {
         // ============================================================ MMA
-        // The event loop of the bf16 key-major kernel: S of the next tile and
-        // PV of the oldest tile whose P is ready, each as soon as its operands
-        // have landed.
+        // Warp 1 issues S = K8 Q^T of every tile, warp 2 O += V8^T P^T, each as
+        // soon as its operands have landed.  A step's conditions are one barrier
+        // per lane, tested by one instruction.
+        const bool pv = warp == 2;
         const bool leader = lane == 0;
         constexpr uint32_t ID_QK = idesc_e4m3_f32(128, 2 * N, 0, 0);
-        constexpr uint32_t ID_PV = idesc_e4m3_f32(128, 2 * N, 1, 1);
-        const uint32_t ring_a = smem_u32(ring);
-        const uint32_t qs_a = smem_u32(qs);
-        const uint32_t ps_a = smem_u32(ps);
-        struct Cursor {
-            int j, t, n_tiles;
-            int last_keys;  // keys of the item's last tile
-            int head;       // key rows before the chunk in its first tile (paged cache)
-            uint32_t k, g;
-            bool valid;
-            int slot;       // this cursor's fill: slot, parity (-1: not yet looked up)
-            uint32_t par;
-        };
-        auto lookup = [&](Cursor &c, uint32_t fill) -> bool {
-            if (c.slot >= 0) return true;
-            const uint32_t e = ftab[fill % kFillTab];
-            if ((e >> 8) != (fill & 0xffffffu)) return false;
-            c.slot = (int)(e & 15u);
-            c.par = (e >> 4) & 1u;
-            return true;
-        };
-        const int n_items = cta_items(T);
-        auto seek = [&](Cursor &c) {
-            for (; c.j < n_items; ++c.j) {
-                const TcItem it = tc_decode<false>(T, cta_item(T, c.j), c.j, meta);
-                if (it.n_tiles > 0) {
-                    c.n_tiles = it.n_tiles;
-                    c.last_keys = it.cr.c_hi - it.t0 - kTcTileKeys * (it.n_tiles - 1);
-                    c.head = it.cr.c_lo - it.t0;
-                    c.t = 0;
-                    c.valid = true;
-                    return;
+        constexpr uint32_t ID_PV = idesc_e4m3_f32(128, NP * N, 1, 1);
+        const uint64_t ring_d = smem_desc_sw128(smem_u32(ring), 16, C::ATOM_BYTES);
+        const uint64_t q_d = smem_desc_sw128(smem_u32(qs), 16, 1024);
+        const uint64_t p_d = smem_desc_sw32(smem_u32(ps), C::P_BLOCK, 256);
+        // lane 0: the tile's fill; 1: the S or P buffer; 2: an item's first tile,
+        // the queries or the O buffer
+        auto ready = [&](uint32_t fill, int b1, uint32_t par1, int b2, uint32_t par2,
+                         bool first) -> int {
+            uint32_t e = 0xffffffffu;
+            int idle = 0;
+            long long since = 0;
+            uint64_t *bar = &bars[lane == 1 ? b1 : b2];
+            const uint32_t par = lane == 1 ? par1 : par2;
+            bool done = lane > 2 || (lane == 2 && !first);
+            for (;;) {
+                if (lane == 0) {
+                    e = ftab[fill % kFillTab];
+                    if ((e >> 8) == (fill & 0xffffffu))
+                        done = mbar_test(&bars[C::B_FULL + (e & 15u)], (e >> 4) & 1u);
+                } else if (!done) {
+                    done = mbar_test(bar, par);
+                }
+                if (__all_sync(0xffffffffu, done)) break;
+                if ((++idle & 63) == 0) {
+                    const long long now = clock64();
+                    if (idle == 64) since = now;
+                    const bool over = now - since > P.wait_limit;
+                    if (over && lane == 0) {
+                        atomicOr(P.fault, kFaultCopyTimeout);
+                        *failed = 1;
+                    }
+                    if (__any_sync(0xffffffffu, over || *failed)) return -1;
                 }
             }
-            c.valid = false;
+            return (int)(__shfl_sync(0xffffffffu, e, 0) & 15u);
         };
-        auto advance = [&](Cursor &c) {
-            ++c.g;
-            c.slot = -1;
-            if (++c.t < c.n_tiles) return;
-            ++c.k;
-            ++c.j;
-            seek(c);
-        };
-        Cursor qc{0, 0, 0, 0, 0, 0u, 0u, false, -1, 0u};
-        seek(qc);
-        Cursor pc = qc;
-        long long idle_since = clock64();
-        while (pc.valid) {
-            bool progressed = false;
-            // ---- PV of tile pc.g (its S was issued before)
-            if (pc.g < qc.g || !qc.valid) {
-                const uint32_t pb = pc.g % PB;
-                bool ready = mbar_test(&bars[C::B_PFULL + pb], (pc.g / PB) & 1);
-                if (ready && pc.t == 0)
-                    ready = mbar_test(&bars[C::B_OFREE + pc.k % OB], ((pc.k / OB) & 1) ^ 1);
-                ready = ready && lookup(pc, 2 * pc.g + 1) &&
-                        mbar_test(&bars[C::B_FULL + pc.slot], pc.par);
-                const uint32_t vslot = (uint32_t)pc.slot;
-                if (ready) {
+        uint32_t g = 0, k = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int j = 0; j < n_items && ok; ++j) {
+            const TcItem it = q8_item(T, j, meta);
+            if (it.n_tiles == 0) continue;
+#pragma unroll 1
+            for (int t = 0; t < it.n_tiles; ++t, ++g) {
+                const bool first = t == 0, last = t == it.n_tiles - 1;
+                if (!pv) {
+                    const uint32_t sb = g & 1, qb = k % QB;
+                    const int slot = ready(2 * g, C::B_SFREE + sb, ((g >> 1) & 1) ^ 1,
+                                           C::B_QFULL + qb, (k / QB) & 1, first);
+                    ok = slot >= 0;
+                    if (!ok) break;
+                    fence_after_sync();
+                    if (leader) {
+                        const uint64_t qbase = q_d + (uint64_t)(qb * (C::Q_BUF >> 4));
+                        const uint64_t abase = ring_d + (uint64_t)(slot * (C::TILE_BYTES >> 4));
+                        const uint32_t d = tmem + sb * C::S_COLS;
+#pragma unroll
+                        for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_e4m3_ss(d, abase + (uint64_t)(s * 64 + kk * 2),
+                                            qbase + (uint64_t)(s * (C::Q_SLAB >> 4) + kk * 2), ID_QK,
+                                            (s | kk) != 0);
+                        mma_commit(&bars[C::B_SFULL + sb]);
+                        mma_commit(&bars[C::B_EMPTY + slot]);
+                        if (last) mma_commit(&bars[C::B_QEMPTY + qb]);
+                    }
+                } else {
+                    const uint32_t pb = g % PB, ob = k % OB;
+                    const int slot = ready(2 * g + 1, C::B_PFULL + pb, (g / PB) & 1,
+                                           C::B_OFREE + ob, ((k / OB) & 1) ^ 1, first);
+                    ok = slot >= 0;
+                    if (!ok) break;
                     fence_after_sync();
                     // only the 32-key steps that hold valid keys are multiplied; the
                     // rows of the last step past the chunk's end, and those before
                     // the chunk in a paged cache's first tile, are zeroed first, so
                     // that 0 * (whatever the slot holds there) cannot reach O
-                    const int nv = pc.t == pc.n_tiles - 1 ? pc.last_keys : kTcTileKeys;
+                    const int nv = last ? it.cr.c_hi - it.t0 - kTcTileKeys * t : kTcTileKeys;
                     const int steps = (nv + 31) >> 5;
-                    uint8_t *vt = ring + vslot * C::TILE_BYTES;
-                    const int z = pc.t == 0 ? pc.head : 0;
+                    const int z = first ? it.cr.c_lo - it.t0 : 0;
                     if ((nv & 31) || z > 0) {
+                        uint8_t *vt = ring + slot * C::TILE_BYTES;
                         zero_v_rows<C>(vt, nv, 32 * steps, lane);
                         zero_v_rows<C>(vt, 0, z, lane);
                         fence_proxy_async_smem();
@@ -451,167 +811,123 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                     }
                     if (leader) {
                         // A = V^T, MN-major: a slab holds 128 dims, 8-key groups one
-                        // atom apart; B = [P_hi; P_lo], MN-major, 2N columns
-                        const uint64_t bbase =
-                            smem_desc_sw32(ps_a + pb * C::P_BUF, C::P_BLOCK, 256);
-                        const uint64_t abase = smem_desc_sw128(ring_a + vslot * C::TILE_BYTES, 16,
-                                                               C::ATOM_BYTES);
-                        const uint32_t ob = pc.k % OB;
-                        const uint32_t acc0 = pc.t > 0 ? 1u : 0u;
+                        // atom apart; B = the parts of P, MN-major
+                        const uint64_t bbase = p_d + (uint64_t)(pb * (C::P_BUF >> 4));
+                        const uint64_t abase = ring_d + (uint64_t)(slot * (C::TILE_BYTES >> 4));
+                        const uint32_t d = tmem + C::O_COL + ob * C::O_COLS;
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4) {
                             if (k4 >= steps) break;
 #pragma unroll
                             for (int mh = 0; mh < MH; ++mh)
-                                mma_e4m3_ss(tmem + C::O_COL + ob * C::O_COLS + mh * 2 * N,
+                                mma_e4m3_ss(d + mh * C::O_HALF,
                                             abase + (uint64_t)((mh * 1024 + k4 * 4 * C::ATOM_BYTES) >> 4),
                                             bbase + (uint64_t)(k4 * 1024 >> 4), ID_PV,
-                                            (acc0 | (uint32_t)k4) != 0);
+                                            k4 > 0 || !first);
                         }
-                        mma_commit(&bars[C::B_EMPTY + vslot]);
                         mma_commit(&bars[C::B_PVDONE + pb]);
+                        mma_commit(&bars[C::B_EMPTY + slot]);
+                        if (last) mma_commit(&bars[C::B_OFULL + ob]);
                     }
-                    __syncwarp();
-                    advance(pc);
-                    progressed = true;
                 }
+                __syncwarp();
             }
-            // ---- S of tile qc.g, at most one tile ahead of the PV cursor
-            if (qc.valid && qc.g <= pc.g + 1) {
-                const uint32_t sb = qc.g & 1;
-                const bool ready = mbar_test(&bars[C::B_SFREE + sb], ((qc.g >> 1) & 1) ^ 1) &&
-                                   mbar_test(&bars[C::B_QFULL + qc.k % QB], (qc.k / QB) & 1) &&
-                                   lookup(qc, 2 * qc.g) &&
-                                   mbar_test(&bars[C::B_FULL + qc.slot], qc.par);
-                const uint32_t kslot = (uint32_t)qc.slot;
-                if (ready) {
-                    fence_after_sync();
-                    if (leader) {
-                        const uint64_t qbase =
-                            smem_desc_sw128(qs_a + (qc.k % QB) * C::Q_BUF, 16, 1024);
-                        const uint64_t abase =
-                            smem_desc_sw128(ring_a + kslot * C::TILE_BYTES, 16, C::ATOM_BYTES);
-#pragma unroll
-                        for (int s = 0; s < C::SLABS; ++s)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_e4m3_ss(tmem + sb * C::S_COLS,
-                                            abase + (uint64_t)(s * 64 + kk * 2),
-                                            qbase + (uint64_t)(s * (C::Q_SLAB >> 4) + kk * 2), ID_QK,
-                                            (s | kk) != 0);
-                        mma_commit(&bars[C::B_EMPTY + kslot]);
-                        mma_commit(&bars[C::B_SFULL + sb]);
-                        if (qc.t == qc.n_tiles - 1) mma_commit(&bars[C::B_QEMPTY + qc.k % QB]);
-                    }
-                    __syncwarp();
-                    advance(qc);
-                    progressed = true;
-                }
-            }
-            if (progressed) {
-                idle_since = clock64();
-            } else if (clock64() - idle_since > P.wait_limit) {
-                atomicOr(P.fault, kFaultCopyTimeout);
-                break;
-            }
+            ++k;
         }
         // all issued MMAs complete before TMEM is released
         if (leader) {
-            mma_commit(&bars[C::B_DRAIN]);
-            mbar_wait_bounded(&bars[C::B_DRAIN], 0, P.fault, kFaultCopyTimeout, P.wait_limit);
+            mma_commit(&bars[C::B_DRAIN + (pv ? 1 : 0)]);
+            mbar_wait_bounded(&bars[C::B_DRAIN + (pv ? 1 : 0)], 0, P.fault, kFaultCopyTimeout,
+                              P.wait_limit);
         }
         __syncwarp();
-    } else if (warp < 10) {
+    } else if (warp < 4) {
+        // ===================================================== key factors
+        q8_tables<C>(A, meta, tabs, bars, failed);
+    } else if (warp < 12) {
         // ===================================================== softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFT_REGS));
         constexpr int HN = N / 2;                // rows per softmax warpgroup
-        constexpr int OW = HN >= 16 ? 16 : 8;    // TMEM columns per O or S load
-        constexpr int NCH = HN / OW;
-        const int wg = (warp - 2) >> 2;          // softmax warpgroup
-        const int sw = (warp - 2) & 3;           // warp within the group
-        const int quad = warp & 3;               // TMEM lane quadrant of this warp
-        const int lk = quad * 32 + lane;         // TMEM lane: key of S^T, dim row of O^T
-        const int gtid = sw * 32 + lane;         // 0..127 within the group
+        constexpr int OW = HN >= 16 ? 16 : 8;    // TMEM columns per load
+        const int wg = (warp - 4) >> 2;          // softmax warpgroup
+        const int sw = warp & 3;                 // warp within the group: TMEM lane quadrant
+        const int lk = sw * 32 + lane;           // TMEM lane: key of S^T, dim row of O^T
         const int r0 = wg * HN;                  // first packed row of this group
-        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
         const uint32_t flip = (uint32_t)(lk >> 2) & 1;  // 32-byte swizzle phase of key lk
         uint32_t g = 0, k = 0;
-        bool ok = true;
-        const int n_items = cta_items(T);
-        for (int j = 0; j < n_items && ok; ++j) {
-            const TcItem it = tc_decode<false>(T, cta_item(T, j), j, meta);
-            const size_t bh = (size_t)it.b * P.Hkv + it.h;
-            const int my_rows = min(HN, it.rows - r0);  // rows of this group in the item
-            if (it.n_tiles == 0) {
-                // no key in this chunk: empty result for every row
-                for (int idx = gtid; idx < my_rows * D; idx += 128) {
-                    const int r = it.row0 + r0 + idx / D, d = idx % D;
-                    const int i = r / P.G, gg = r - i * P.G;
-                    const size_t orow =
-                        ((size_t)it.b * P.q_len + i) * P.Hq + (size_t)it.h * P.G + gg;
-                    if (P.splits == 1) {
-                        P.out[orow * D + d] = __float2bfloat16_rn(0.f);
-                        if (d == 0 && P.lse != nullptr) P.lse[orow] = NEG_INF;
-                    } else {
-                        const size_t prow = (bh * P.splits + it.split) * P.R + r;
-                        P.part_acc[prow * D + d] = 0.f;
-                        if (d == 0) {
-                            P.part_ml[prow * 2] = NEG_INF;
-                            P.part_ml[prow * 2 + 1] = 0.f;
-                        }
-                    }
-                }
-                continue;
-            }
-            const uint32_t ob = k % OB;
-            const uint32_t ocol0 = tl + C::O_COL + ob * C::O_COLS;  // this lane's O^T row
+        for (int j = 0; j < n_items; ++j) {
+            TcItem it;
+            if (j < kTcMetaItems) it = meta[j];
+            else it = tc_decode_global<false>(T, cta_item(T, j));
+            if (it.n_tiles == 0) continue;
+            const uint32_t ocol0 = tl + C::O_COL + (k % OB) * C::O_COLS + r0;  // this lane's O^T row
+            const float *rs = qsc + (k & 1) * N + r0;
             float mref[HN], lrow[HN];
 #pragma unroll
-            for (int r = 0; r < HN; ++r) {
-                mref[r] = kNoRef;
-                lrow[r] = 0.f;
-            }
+            for (int r = 0; r < HN; ++r) lrow[r] = 0.f;
 
             const int qp_i0 = it.cr.qp + it.i0;  // position of the item's first draft row
+            // first keys of the tiles that every row sees whole
+            const int i_last = (it.rows - 1) / P.G;
+            const int inner_lo =
+                (int)max((long long)qp_i0 + i_last - P.window + 1, (long long)it.cr.c_lo);
+            const int inner_hi = min(qp_i0, it.cr.c_hi - 1) - (kTcTileKeys - 1);
             for (int t = 0; t < it.n_tiles; ++t, ++g) {
                 const uint32_t sb = g & 1, slot = g % kQ8Tabs;
                 const int j0 = it.t0 + kTcTileKeys * t;
-                const int jk = j0 + lk;
-                // packed rows [ra, rb) of this group whose window holds key jk
-                int ra = 0, rb = 0;
-                if (jk >= it.cr.c_lo && jk < it.cr.c_hi) {
-                    const long long lo_i = (long long)jk - qp_i0;
-                    const long long hi_i = (long long)jk + P.window - qp_i0;
-                    const long long a = lo_i < 0 ? 0 : lo_i * P.G;
-                    long long bnd = hi_i < 0 ? 0 : hi_i * P.G;
-                    if (bnd > it.rows) bnd = it.rows;
-                    ra = (int)(a < it.rows ? a : it.rows) - r0;
-                    rb = (int)bnd - r0;
+                // packed rows [ra, rb) of this group whose window holds the key:
+                // all of them in a tile between the item's last window start and
+                // its first row's position
+                int ra = 0, rb = HN;
+                if (j0 < inner_lo || j0 > inner_hi) {
+                    const int jk = j0 + lk;
+                    ra = rb = 0;
+                    if (jk >= it.cr.c_lo && jk < it.cr.c_hi) {
+                        // (jk < q_pos + q_len: the first difference is below 512)
+                        const int lo_i = jk - qp_i0;
+                        const long long hi_i = (long long)lo_i + P.window;
+                        ra = min(max(lo_i, 0) * P.G, (int)it.rows) - r0;
+                        rb = (hi_i >= it.rows ? (int)it.rows : min(max((int)hi_i, 0) * P.G, (int)it.rows)) - r0;
+                    }
                 }
-                bool got = mbar_wait_bounded(&bars[C::B_TFULL + slot], (g / kQ8Tabs) & 1, P.fault,
-                                             kFaultCopyTimeout, P.wait_limit);
-                const float2 key = tabs[slot].key[lk];
-                got = got && mbar_wait_bounded(&bars[C::B_SFULL + sb], (g >> 1) & 1, P.fault,
-                                               kFaultCopyTimeout, P.wait_limit);
+                // one barrier per lane, tested by one instruction: the tile's table and
+                // scores, the P buffer's previous PV, an item's query scales
+                const uint32_t pb = g % PB;
+                {
+                    uint64_t *bar = &bars[lane == 0   ? C::B_TFULL + slot
+                                          : lane == 1 ? C::B_SFULL + sb
+                                          : lane == 2 ? C::B_PVDONE + pb
+                                                      : C::B_QFULL + k % QB];
+                    const uint32_t par = (lane == 0   ? g / kQ8Tabs
+                                          : lane == 1 ? g >> 1
+                                          : lane == 2 ? g / PB + 1
+                                                      : k / QB) & 1;
+                    if (lane < (t == 0 ? 4 : 3) && (lane != 2 || g >= (uint32_t)PB))
+                        q8_wait_here(bar, par, P, failed);
+                    __syncwarp();
+                }
+                const float2 key = tabs[slot * kTcTileKeys + lk];
                 fence_after_sync();
                 // u = (S_hi + S_lo / 16) * row scale * key factor + e_v
                 float v[HN];
                 {
                     const uint64_t lo2 = f2_pack(1.f / kQ8QLo, 1.f / kQ8QLo);
                     const uint64_t ks2 = f2_pack(key.x, key.x), ve2 = f2_pack(key.y, key.y);
-                    const bool all = ra <= 0 && rb >= HN;
                     uint32_t hi[HN], lo[HN];
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c) {
-                        tmem_load<OW>(tl + sb * C::S_COLS + r0 + c * OW, hi + c * OW);
-                        tmem_load<OW>(tl + sb * C::S_COLS + N + r0 + c * OW, lo + c * OW);
+                    for (int c = 0; c < HN; c += OW) {
+                        tmem_load<OW>(tl + sb * C::S_COLS + r0 + c, hi + c);
+                        tmem_load<OW>(tl + sb * C::S_COLS + N + r0 + c, lo + c);
                     }
                     tmem_wait_ld();
                     fence_before_sync();
-                    mbar_arrive(&bars[C::B_SFREE + sb]);
+                    __syncwarp();
+                    if (lane < 2) mbar_arrive(&bars[lane == 0 ? C::B_SFREE + sb : C::B_TEMPTY + slot]);
 #pragma unroll
                     for (int r4 = 0; r4 < HN; r4 += 4) {
-                        const float4 rs = *reinterpret_cast<const float4 *>(&tabs[slot].row[r0 + r4]);
-                        const uint64_t rs2[2] = {f2_pack(rs.x, rs.y), f2_pack(rs.z, rs.w)};
+                        const float4 s4 = *reinterpret_cast<const float4 *>(rs + r4);
+                        const uint64_t rs2[2] = {f2_pack(s4.x, s4.y), f2_pack(s4.z, s4.w)};
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
                             const int r = r4 + 2 * p;
@@ -622,34 +938,31 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                             f2_unpack(f2_fma(f2_mul(s2, rs2[p]), ks2, ve2), v[r], v[r + 1]);
                         }
                     }
-                    mbar_arrive(&bars[C::B_TEMPTY + slot]);
-                    if (!all) {
+                    if (ra > 0 || rb < HN) {
 #pragma unroll
                         for (int r = 0; r < HN; ++r)
                             if (r < ra || r >= rb) v[r] = NEG_INF;
                     }
                 }
 
-                bool flag = false;
+                bool raise = t == 0;  // an item's first tile sets the references
+                if (t > 0) {
+                    bool flag = false;
 #pragma unroll
-                for (int r = 0; r < HN; ++r) flag |= v[r] > mref[r] + kQ8RaiseAt;
-                const bool raise = group_any(wg, flag || !got);
+                    for (int r = 0; r < HN; ++r) flag |= v[r] > mref[r] + kQ8RaiseAt;
+                    raise = group_any(wg, flag);
+                }
                 if (raise) {
-                    ok = !group_any(wg, !got);
-                    if (!ok) break;
-                    // exact tile maximum per row; raise the references
+                    // exact tile maximum per row
                     float *rd = red + (g & 1) * 4 * N + r0;
-                    constexpr int CW = HN >= 32 ? 32 : HN;
+                    float mine = NEG_INF;
 #pragma unroll
-                    for (int c = 0; c < HN / CW; ++c) {
-                        float tmp[CW];
-#pragma unroll
-                        for (int e = 0; e < CW; ++e) tmp[e] = v[c * CW + e];
-                        const float m = lane_reduce<CW, true>(tmp);
-                        if (lane < CW) rd[sw * N + c * CW + lane] = m;
+                    for (int r = 0; r < HN; ++r) {
+                        const float m = warp_max(v[r]);
+                        if (lane == r) mine = m;
                     }
+                    if (lane < HN) rd[sw * N + lane] = mine;
                     group_sync(wg);
-                    const bool rescale = t > 0;
                     float my_alpha = 1.f;
 #pragma unroll
                     for (int r4 = 0; r4 < HN; r4 += 4) {
@@ -657,63 +970,54 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                         const float4 a1 = *reinterpret_cast<const float4 *>(rd + N + r4);
                         const float4 a2 = *reinterpret_cast<const float4 *>(rd + 2 * N + r4);
                         const float4 a3 = *reinterpret_cast<const float4 *>(rd + 3 * N + r4);
-                        const float tm[4] = {fmaxf(fmaxf(a0.x, a1.x), fmaxf(a2.x, a3.x)),
-                                             fmaxf(fmaxf(a0.y, a1.y), fmaxf(a2.y, a3.y)),
-                                             fmaxf(fmaxf(a0.z, a1.z), fmaxf(a2.z, a3.z)),
-                                             fmaxf(fmaxf(a0.w, a1.w), fmaxf(a2.w, a3.w))};
+                        const float tm[4] = {fmaxf(fmax3(a0.x, a1.x, a2.x), a3.x),
+                                             fmaxf(fmax3(a0.y, a1.y, a2.y), a3.y),
+                                             fmaxf(fmax3(a0.z, a1.z, a2.z), a3.z),
+                                             fmaxf(fmax3(a0.w, a1.w, a2.w), a3.w)};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int r = r4 + e;
-                            const float mo = mref[r];
-                            const float mn = fmaxf(mo, tm[e] - kQ8RefBelow);
-                            if (rescale) {
-                                const float al = mn == mo ? 1.f : fast_exp2(mo - mn);
-                                if (gtid == r) my_alpha = al;
+                            if (t == 0) {
+                                mref[r] = fmaxf(kNoRef, tm[e] - C::BELOW);
+                            } else {
+                                const float mo = mref[r];
+                                mref[r] = fmaxf(mo, tm[e] - C::BELOW);
+                                const float al = fast_exp2(mo - mref[r]);
+                                if (lane == r) my_alpha = al;
                                 lrow[r] *= al;
                             }
-                            mref[r] = mn;
                         }
                     }
-                    if (rescale) {
-                        if (gtid < HN) alpha_sm[r0 + gtid] = my_alpha;
+                    if (t > 0) {
                         // every PV of this item so far has completed before O is scaled
-                        const uint32_t gp = g - 1;
-                        ok = !group_any(wg, !mbar_wait_bounded(&bars[C::B_PVDONE + gp % PB],
-                                                               (gp / PB) & 1, P.fault,
-                                                               kFaultCopyTimeout, P.wait_limit));
-                        if (!ok) break;
-                        fence_after_sync();  // (the vote also published alpha_sm)
+                        // (each warp its own lanes, the factors from its lanes)
+                        q8_wait_here(&bars[C::B_PVDONE + (g - 1) % PB], ((g - 1) / PB) & 1, P, failed);
+                        fence_after_sync();
+                        if (sw == 0 && lane < HN) alpha_sm[r0 + lane] = my_alpha;
+                        group_sync(wg);
 #pragma unroll 1
-                        for (int mh = 0; mh < 2 * MH; ++mh) {  // hi and lo halves of each
-#pragma unroll 1
+                        for (int c = 0; c < MH * NP; ++c) {
+                            const uint32_t ocol = ocol0 + c * N;
+#pragma unroll
                             for (int c0 = 0; c0 < HN; c0 += OW) {
                                 uint32_t o[OW];
-                                const uint32_t ocol = ocol0 + mh * N + r0 + c0;
-                                tmem_load<OW>(ocol, o);
+                                tmem_load<OW>(ocol + c0, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < OW; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) *
                                                            alpha_sm[r0 + c0 + e]);
-                                tmem_store<OW>(ocol, o);
+                                tmem_store<OW>(ocol + c0, o);
                             }
                         }
                         tmem_wait_st();
                     }
                 }
-                // P buffer free: its previous PV has completed
-                const uint32_t pb = g % PB;
-                if (g >= (uint32_t)PB) {
-                    const uint32_t gp = g - PB;
-                    ok = !group_any(wg, !mbar_wait_bounded(&bars[C::B_PVDONE + pb], (gp / PB) & 1,
-                                                           P.fault, kFaultCopyTimeout,
-                                                           P.wait_limit));
-                    if (!ok) break;
-                }
-                // P = 2^(u - ref) as two e4m3 numbers; the row sum adds P 2^-e_v
-                const float ive = pow2f(-(int)key.y < -126 ? -126 : (int)-key.y > 127 ? 127 : (int)-key.y);
+                // P = 2^(u - ref) in e4m3 numbers; the row sum adds P 2^-e_v
+                const int ve = (int)key.y;
+                const float ive = pow2f(ve > 126 ? -126 : (ve < -127 ? 127 : -ve));
                 const uint64_t iv2 = f2_pack(ive, ive);
-                uint32_t ph[HN / 4], pl[HN / 4];
+                uint32_t pk[NP][HN / 4];
 #pragma unroll
                 for (int r = 0; r < HN; r += 2) {
                     float d0, d1;
@@ -721,129 +1025,81 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                     const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
                     f2_unpack(f2_fma(f2_pack(p0, p1), iv2, f2_pack(lrow[r], lrow[r + 1])), lrow[r],
                               lrow[r + 1]);
-                    uint16_t h, l;
-                    split_p(p0, p1, h, l);
-                    if (r & 2) {
-                        ph[r / 4] |= (uint32_t)h << 16;
-                        pl[r / 4] |= (uint32_t)l << 16;
-                    } else {
-                        ph[r / 4] = h;
-                        pl[r / 4] = l;
-                    }
-                }
-                // columns r0 .. of hi and N + r0 .. of lo, key lk's 32-byte rows
-                uint8_t *pt = ps + pb * C::P_BUF + lk * 32;
-                if constexpr (HN == 8) {
-                    *reinterpret_cast<uint2 *>(pt + (flip << 4) + wg * 8) = make_uint2(ph[0], ph[1]);
-                    *reinterpret_cast<uint2 *>(pt + ((flip ^ 1) << 4) + wg * 8) =
-                        make_uint2(pl[0], pl[1]);
-                } else if constexpr (HN == 16) {
-                    const uint32_t ch = ((uint32_t)wg ^ flip) << 4;
-                    *reinterpret_cast<uint4 *>(pt + ch) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                    *reinterpret_cast<uint4 *>(pt + C::P_BLOCK + ch) =
-                        make_uint4(pl[0], pl[1], pl[2], pl[3]);
-                } else {
+                    __half2 p = __floats2half2_rn(p0, p1);
+                    uint32_t c[NP];
+                    c[0] = take_e4m3(p, kQ8P1);
+                    if constexpr (NP == 3) c[1] = take_e4m3(p, kQ8P2);
+                    c[NP - 1] = last_e4m3(p);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t ch = ((uint32_t)c ^ flip) << 4;
-                        *reinterpret_cast<uint4 *>(pt + wg * C::P_BLOCK + ch) =
-                            make_uint4(ph[4 * c], ph[4 * c + 1], ph[4 * c + 2], ph[4 * c + 3]);
-                        *reinterpret_cast<uint4 *>(pt + (2 + wg) * C::P_BLOCK + ch) =
-                            make_uint4(pl[4 * c], pl[4 * c + 1], pl[4 * c + 2], pl[4 * c + 3]);
+                    for (int i = 0; i < NP; ++i)
+                        pk[i][r / 4] = r & 2 ? pk[i][r / 4] | (c[i] << 16) : c[i];
+                }
+                // columns i N + r0 .. of part i, in key lk's 32-byte rows
+                uint8_t *pt = ps + pb * C::P_BUF + lk * 32;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    if constexpr (HN == 8) {
+                        *reinterpret_cast<uint2 *>(pt + (i >> 1) * C::P_BLOCK +
+                                                   (((uint32_t)(i & 1) ^ flip) << 4) + wg * 8) =
+                            make_uint2(pk[i][0], pk[i][1]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < HN / 16; ++c) {
+                            const int col = i * N + wg * HN + 16 * c;
+                            *reinterpret_cast<uint4 *>(
+                                pt + (col >> 5) * C::P_BLOCK +
+                                (((uint32_t)(col >> 4) & 1u) ^ flip) * 16) =
+                                make_uint4(pk[i][4 * c], pk[i][4 * c + 1], pk[i][4 * c + 2],
+                                           pk[i][4 * c + 3]);
+                        }
                     }
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&bars[C::B_PFULL + pb]);
+                warp_arrive(&bars[C::B_PFULL + pb]);
             }
-            if (!ok) break;
 
-            // -------------------------------------------------- epilogue
-            // row sums (they do not depend on the last PV): lanes, then the
-            // group's four warps
-            float *rl = red + (g & 1) * 4 * N + r0;
-            {
-                constexpr int CW = HN >= 32 ? 32 : HN;
-#pragma unroll
-                for (int c = 0; c < HN / CW; ++c) {
-                    float tmp[CW];
-#pragma unroll
-                    for (int e = 0; e < CW; ++e) tmp[e] = lrow[c * CW + e];
-                    const float s = lane_reduce<CW, false>(tmp);
-                    if (lane < CW) rl[sw * N + c * CW + lane] = s;
-                }
-            }
-            group_sync(wg);
-            if (gtid < my_rows) {
-                const int r = gtid;
-                const float l = (rl[r] + rl[N + r]) + (rl[2 * N + r] + rl[3 * N + r]);
+            // the warp's row sums and the references, for the epilogue
+            constexpr int CW = HN >= 32 ? 32 : HN;
+            const float l = lane_reduce<CW, false>(lrow);
+            float *sum = sums + (k & 3) * 5 * N + r0 + lane;
+            if (lane < HN) sum[sw * N] = l;
+            if (sw == 0) {
                 float m = NEG_INF;
 #pragma unroll
                 for (int q = 0; q < HN; ++q)
-                    if (q == r) m = mref[q];
-                const bool any = !(l <= 0.f);  // (a NaN stays one)
-                linv[r0 + r] = any ? __frcp_rn(l) : 0.f;
-                const int rg = it.row0 + r0 + r;
-                if (P.splits == 1) {
-                    const int i = rg / P.G, gg = rg - i * P.G;
-                    const uint32_t orow =
-                        (uint32_t)(((size_t)it.b * P.q_len + i) * P.Hq + (size_t)it.h * P.G + gg);
-                    rowidx[r0 + r] = orow;
-                    if (P.lse != nullptr) P.lse[orow] = any ? (m + __log2f(l)) * kLn2 : NEG_INF;
-                } else {
-                    const size_t prow = (bh * P.splits + it.split) * P.R + rg;
-                    P.part_ml[prow * 2] = any ? m : NEG_INF;
-                    P.part_ml[prow * 2 + 1] = l;
-                }
+                    if (q == lane) m = mref[q];
+                if (lane < HN) sum[4 * N] = m;
             }
-            const uint32_t gl = g - 1;  // the item's last tile
-            ok = !group_any(wg, !mbar_wait_bounded(&bars[C::B_PVDONE + gl % PB], (gl / PB) & 1,
-                                                   P.fault, kFaultCopyTimeout, P.wait_limit));
-            if (!ok) break;
-            fence_after_sync();  // (the vote also published linv and rowidx)
-            const size_t prow0 = (bh * P.splits + it.split) * P.R + it.row0 + r0;
-#pragma unroll
-            for (int mh = 0; mh < MH; ++mh) {
-                const int d = mh * 128 + lk;
-#pragma unroll
-                for (int c0 = 0; c0 < HN; c0 += OW) {
-                    uint32_t o[OW], ol[OW];
-                    tmem_load<OW>(ocol0 + mh * 2 * N + r0 + c0, o);
-                    tmem_load<OW>(ocol0 + mh * 2 * N + N + r0 + c0, ol);
-                    tmem_wait_ld();
-                    if (mh == MH - 1 && c0 == HN - OW) {
-                        fence_before_sync();
-                        mbar_arrive(&bars[C::B_OFREE + ob]);  // O buffer may be reused
-                    }
-                    float x[OW];
-#pragma unroll
-                    for (int e = 0; e < OW; ++e)
-                        x[e] = fmaf(__uint_as_float(ol[e]), 1.f / kQ8PLo, __uint_as_float(o[e]));
-                    if (P.splits == 1) {
-                        // neighbouring lanes hold neighbouring dims: each pair swaps
-                        // halves of two rows, so a lane stores two dims of one row
-#pragma unroll
-                        for (int e = 0; e < OW; e += 2) {
-                            const float a = x[e] * linv[r0 + c0 + e], b = x[e + 1] * linv[r0 + c0 + e + 1];
-                            const bool odd = lane & 1;
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                            const int r = c0 + e + (odd ? 1 : 0);
-                            const uint32_t w = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
-                            if (r < my_rows)
-                                *reinterpret_cast<uint32_t *>(P.out + (size_t)rowidx[r0 + r] * D +
-                                                              (d & ~1)) = w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < OW; ++e)
-                            if (c0 + e < my_rows) P.part_acc[(prow0 + c0 + e) * D + d] = x[e];
-                    }
-                }
-            }
+            warp_arrive(&bars[C::B_LFULL + (k & 3)]);
             ++k;
         }
     } else {
-        // ============================================== the other operands
-        q8_operands<C, D, N, QB>(A, meta, qs, tabs, bars, warp - 10);
+        // ====================================== query rows and epilogues
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+        const uint32_t inv_g = q8_inv_g(P);
+        const int w = warp - 12;
+        uint32_t kq = 0, k = 0;  // items with keys whose queries are split, finished
+        int jq = 0;
+        TcItem next;             // the item whose queries are on their way
+        auto fetch = [&]() {
+            for (next.n_tiles = 0; jq < n_items && next.n_tiles == 0; ++jq) next = q8_item(T, jq, meta);
+            if (next.n_tiles > 0) q8_fetch_queries<D>(P, next, raw, w, inv_g);
+        };
+        fetch();
+        // queries one item ahead of the epilogues
+#pragma unroll 1
+        for (int j = -1; j < n_items; ++j) {
+            TcItem it;
+            it.n_tiles = 1;
+            if (j >= 0) it = q8_item(T, j, meta);
+            if (it.n_tiles > 0 && next.n_tiles > 0) {
+                q8_queries<C, D, N, QB>(P, next, kq++, raw, qs, qsc, bars, failed, w);
+                fetch();
+            }
+            if (j < 0) continue;
+            q8_epilogue<C, D, N, NP, OB>(P, it, k, tmem, sums, linv, rowidx, bars, failed, inv_g);
+            if (it.n_tiles > 0) ++k;
+        }
     }
 
     // ---------------------------------------------------------- teardown
