@@ -9,6 +9,36 @@
 using swa::aligned_to;
 using swa::api_fail;
 
+namespace {
+
+template <int NT>
+cudaError_t launch(const swa::LogpParams &A, long long rows, int c, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(rows * c));
+    cfg.blockDim = dim3(NT);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = swa::pdl_enabled() ? 2 : 1;
+    if (swa::launch_fault_due()) return cudaErrorLaunchOutOfResources;
+    return cudaLaunchKernelEx(&cfg, swa::swa_logprobs_kernel<NT>, A, c);
+}
+
+cudaError_t launch_rows(const swa::LogpParams &A, long long rows, int sms, cudaStream_t s) {
+    const long long nvec = ((long long)A.V + 14) / 8;
+    int c = 1;
+    while (c < swa::kLogpMaxCluster && rows * c * 2 <= 2LL * sms && nvec > 1024LL * c) c *= 2;
+    return c >= 8 ? launch<512>(A, rows, c, s) : launch<256>(A, rows, c, s);
+}
+
+}  // namespace
+
 extern "C" swa_status swa_token_logprobs(const void *logits, const int32_t *keep_ids,
                                          const int32_t *tokens, const float *temperature,
                                          int32_t top_n, float *logprobs, int32_t *ranks,
@@ -49,9 +79,8 @@ extern "C" swa_status swa_token_logprobs(const void *logits, const int32_t *keep
     A.q_len = q_len;
     A.V = vocab;
     A.top = top_n;
-    const cudaError_t e =
-        swa::launch_kernel(swa::swa_logprobs_kernel, dim3((unsigned)(batch * q_len)),
-                           dim3(swa::kLogpThreads), 0, reinterpret_cast<cudaStream_t>(stream), A);
+    const cudaError_t e = launch_rows(A, (long long)batch * q_len, swa::api_device_sms(dev),
+                                      reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return swa::api_cuda_fail(e, "log probability kernel launch");
     return swa::api_ok();
 }

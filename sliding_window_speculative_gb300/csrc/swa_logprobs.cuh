@@ -1,12 +1,36 @@
 // Log probabilities of given tokens, entropies and the likeliest tokens.
+//
+// One pass over a row of logits keeps, with M the largest logit so far,
+//   s = sum 2^(c (x - M)),   w = sum 2^(c (x - M)) (x - M),   c = log2(e) / T,
+// so that ln p_j = ln2 (c (x_j - M) - log2 s) and the entropy is
+// ln2 (log2 s - c w / s); counts what comes before the given token in the order;
+// and stores the largest logit of every block of 256 columns.
+//
+// The top n columns of the order lie in the n blocks that come first by falling
+// largest logit, equal ones by rising place: a column in another block has n
+// blocks before its own, each with a column before it in the order.  So
+// whatever the logits are, n blocks are read a second time (from L2), and of
+// their columns those at least as large as the last block's largest are ranked
+// by counting.
+//
+// What bounds it is the one read of the logits: 5.6 instructions and one
+// exponential per logit, pairs in packed arithmetic.  A cluster of CTAs shares a
+// row where there are few rows.
 #pragma once
 
-#include "swa_common.cuh"
+#include <cooperative_groups.h>
+
+#include "swa_tc_ptx.cuh"
 
 namespace swa {
 
-constexpr int kLogpThreads = 256;
 constexpr int kLogpMaxTop = 32;
+constexpr int kLogpMaxCluster = 8;
+constexpr int kLogpBlocks = 2048;   // blocks per CTA at most; longer rows have larger ones
+constexpr int kLogpPerBlock = 32;   // candidates taken of one block at most
+
+// Smaller logits count as -2^100 in the sums: a difference of two is then finite.
+constexpr float kLogpLow = -1.2676506e30f;
 
 struct LogpParams {
     const uint16_t *logits;
@@ -17,110 +41,465 @@ struct LogpParams {
     int q_len, V, top;
 };
 
-// A logit as the order takes it: NaN is -inf, -0 is 0.
-__device__ __forceinline__ float logp_value(uint16_t b) {
-    const float x = __uint_as_float((uint32_t)b << 16);
-    return x == x ? x + 0.f : -__int_as_float(0x7f800000);
+struct LogpStats {
+    float m, s, w;
+    int before;
+};
+
+struct LogpShared {
+    uint32_t block[kLogpBlocks];  // a block's largest logit as a rising key
+    unsigned long long cand[kLogpMaxTop * kLogpPerBlock];
+    uint32_t best[16 * kLogpMaxTop];  // per warp its first blocks
+    uint32_t pick[kLogpMaxTop];       // the first blocks of the row, in order
+    LogpStats warp[16];
+    LogpStats cta;                    // read by the cluster's first CTA
+    int col, infs, n_cand;
+};
+
+// Rising with the value; -0 counts as 0.
+__device__ __forceinline__ uint32_t logp_key16(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f) >> 16;
+    return b & 0x8000u ? (~b & 0xffffu) : (b | 0x8000u);
+}
+__device__ __forceinline__ float logp_of_key16(uint32_t k) {
+    return __uint_as_float((k & 0x8000u ? k & 0x7fffu : ~k & 0xffffu) << 16);
 }
 
-// Rising with the value, and with a falling column.
-__device__ __forceinline__ unsigned long long logp_key(float x, int col) {
-    const uint32_t u = __float_as_uint(x);
-    return ((unsigned long long)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32) | (uint32_t)~col;
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));  // (a NaN is ignored)
+    return r;
+}
+// 1 in each half where a > b
+__device__ __forceinline__ uint32_t bf16x2_gt(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float logp_warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-// One row per CTA.
-__global__ void __launch_bounds__(kLogpThreads) swa_logprobs_kernel(const LogpParams A) {
+// The running sums moved from reference m to n >= m.
+__device__ __forceinline__ void logp_move(float c, float m, float n, float &s, float &w) {
+    const float d = m - n, a = fast_exp2(d * c);
+    w = a * fmaf(d, s, w);
+    s *= a;
+}
+
+// A row's columns in vectors of 8 at 16-byte addresses: column of element e of
+// vector v is 8 v + e - shift.  Elements outside the row are -inf.
+struct LogpRow {
+    const uint16_t *x;  // the row
+    int V, shift;
+    __device__ __forceinline__ uint4 load(long long v) const {
+        const long long c0 = 8 * v - shift;
+        if (c0 >= 0 && c0 + 8 <= V) return __ldcs(reinterpret_cast<const uint4 *>(x + c0));
+        uint32_t r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const long long c = c0 + 2 * e;
+            const uint32_t lo = c >= 0 && c < V ? x[c] : 0xff80u;
+            const uint32_t hi = c + 1 >= 0 && c + 1 < V ? x[c + 1] : 0xff80u;
+            r[e] = lo | (hi << 16);
+        }
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    }
+};
+
+// C CTAs of NT threads (a cluster) per row.
+template <int NT>
+__global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(const LogpParams A, const int C) {
+    namespace cg = cooperative_groups;
+    using namespace tc;
+    constexpr int NW = NT / 32, U = 4;
     const float INF = __int_as_float(0x7f800000);
-    __shared__ float red[3][kLogpThreads];
-    __shared__ unsigned long long best[kLogpThreads];
-    __shared__ int col_sm, count[kLogpThreads];
+    constexpr uint32_t kNegInf2 = 0xff80ff80u, kLow2 = 0xf180f180u;  // -2^100
+    __shared__ LogpShared S;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int rank = C > 1 ? (int)cluster.block_rank() : 0;
     grid_dep_wait();
     grid_dep_trigger();
-    const long long row = blockIdx.x;
-    const int t = threadIdx.x;
-    const uint16_t *x = A.logits + row * A.V;
+    const long long row = blockIdx.x / C;
+    LogpRow R;
+    R.x = A.logits + row * A.V;
+    R.V = A.V;
+    R.shift = (int)((reinterpret_cast<uintptr_t>(R.x) >> 1) & 7);
+    const long long nvec = ((long long)R.shift + A.V + 7) / 8;
+    const long long units = (nvec + 31) / 32;        // of 32 vectors
+    const long long u0 = units * rank / C, u1 = units * (rank + 1) / C;
+    int bshift = 0;                                  // blocks of 2^bshift units
+    while ((((units + C - 1) / C) >> bshift) + 2 > kLogpBlocks) ++bshift;
+    const long long b0 = u0 >> bshift;               // this CTA's first block
+
     float T = A.temperature ? A.temperature[row / A.q_len] : 1.f;
     T = T > 0.f ? fminf(T, 3.0e38f) : 1.f;
-    // the given token's column
+    const float inv_t = fminf(1.f / T, 3.0e38f), c = fminf(kLog2e / T, 3.0e38f);
+
+    // the given token's column and logit
     const int tok = A.tokens[row];
-    if (t == 0) col_sm = A.keep || tok < 0 || tok >= A.V ? 0x7fffffff : tok;
+    int col = A.keep || tok < 0 || tok >= A.V ? -1 : tok;
+    if (t == 0) {
+        S.col = 0x7fffffff;
+        S.infs = S.n_cand = 0;
+    }
+    for (int i = t; i < kLogpBlocks; i += NT) S.block[i] = 0;
     __syncthreads();
-    if (A.keep && tok >= 0)
-        for (int j = t; j < A.V; j += kLogpThreads)
-            if (A.keep[j] == tok) atomicMin(&col_sm, j);
-    __syncthreads();
-    const int col = col_sm < A.V ? col_sm : -1;
-    const float xt = col >= 0 ? logp_value(x[col]) : 0.f;
-    float m = -INF;
+    if (A.keep && tok >= 0) {
+        const int j0 = (int)((long long)A.V * rank / C), j1 = (int)((long long)A.V * (rank + 1) / C);
+        for (int j = j0 + t; j < j1; j += NT)
+            if (A.keep[j] == tok) atomicMin(&S.col, j);
+        if (C > 1) cluster.sync();
+        else __syncthreads();
+        int first = 0x7fffffff;
+        for (int r = 0; r < C; ++r)
+            first = min(first, C > 1 ? *cluster.map_shared_rank(&S.col, r) : S.col);
+        if (first < A.V) col = first;
+    }
+    // a column before the token's counts if its logit is at least the token's:
+    // above the next number below that; behind it if it is larger
+    float xt = 0.f;
+    uint32_t thr_before = 0x7f807f80u, thr_behind = 0x7f807f80u;
+    long long tv = 0;
+    int tpos = 0;
+    if (col >= 0) {
+        uint32_t b = R.x[col];
+        if ((b & 0x7fffu) > 0x7f80u) b = 0xff80u;   // NaN
+        if (b == 0x8000u) b = 0;
+        xt = __uint_as_float(b << 16);
+        const uint32_t below = b == 0 ? 0x8001u : (b & 0x8000u ? b + 1 : b - 1);
+        // (a token of -inf: the columns before it all come before it, counted below)
+        if (b != 0xff80u) thr_before = below | (below << 16);
+        thr_behind = b | (b << 16);
+        tv = ((long long)col + R.shift) >> 3;
+        tpos = (col + R.shift) & 7;
+    }
+
+    // ---------------------------------------------------------------- the pass
+    float m = kLogpLow;
+    uint64_t s2 = 0, w2 = 0;   // pairs of partial sums
     int before = 0;
-    for (int j = t; j < A.V; j += kLogpThreads) {
-        const float v = logp_value(x[j]);
-        m = fmaxf(m, v);
-        before += col >= 0 && (v > xt || (v == xt && j < col));
-    }
-    red[0][t] = m;
-    count[t] = before;
-    __syncthreads();
-    for (int n = kLogpThreads / 2; n > 0; n >>= 1) {
-        if (t < n) {
-            red[0][t] = fmaxf(red[0][t], red[0][t + n]);
-            count[t] += count[t + n];
+    const uint64_t c2 = f2_pack(c, c);
+    for (long long u = u0 + warp; u < u1; u += NW * U) {
+        uint4 x[U];
+        uint32_t count = 0;  // bf16 pairs, at most 4 U in each half
+        float mu[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const long long v = (u + NW * k) * 32 + lane;
+            x[k] = u + NW * k < u1 && v < nvec ? R.load(v)
+                                               : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
         }
-        __syncthreads();
-    }
-    m = red[0][0];
-    float s = 0.f, u = 0.f;
-    for (int j = t; j < A.V; j += kLogpThreads) {
-        const float v = logp_value(x[j]);
-        const float y = v == m ? 0.f : (v - m) / T;  // (both may be infinite)
-        const float e = expf(y);
-        s += e;
-        if (e > 0.f) u += e * y;
-    }
-    red[1][t] = s;
-    red[2][t] = u;
-    __syncthreads();
-    for (int n = kLogpThreads / 2; n > 0; n >>= 1) {
-        if (t < n) {
-            red[1][t] += red[1][t + n];
-            red[2][t] += red[2][t + n];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const long long v = (u + NW * k) * 32 + lane;
+            uint32_t *y = reinterpret_cast<uint32_t *>(&x[k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = bf16x2_max(y[e], kNegInf2);  // NaN is -inf
+            const uint32_t a = bf16x2_max(bf16x2_max(y[0], y[1]), bf16x2_max(y[2], y[3]));
+            mu[k] = logp_warp_max(fmaxf(bf16lo(a), bf16hi(a)));
+            const uint32_t thr = v < tv ? thr_before : thr_behind;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) count = bf16x2_add(count, bf16x2_gt(y[e], thr));
+            if (v == tv && col >= 0) {
+                const bool none = thr_before == 0x7f807f80u;
+                for (int e = 0; e < tpos; ++e) {
+                    const float z = e & 1 ? bf16hi(y[e >> 1]) : bf16lo(y[e >> 1]);
+                    before += none ? -(z > xt) : (z == xt);
+                }
+            }
         }
-        __syncthreads();
+        before += (int)bf16lo(count) + (int)bf16hi(count);
+        float n = m;
+#pragma unroll
+        for (int k = 0; k < U; ++k) n = fmaxf(n, mu[k]);
+        if (A.top > 0 && lane < U && u + NW * lane < u1) {
+            float mine = mu[0];
+#pragma unroll
+            for (int k = 1; k < U; ++k)
+                if (lane == k) mine = mu[k];
+            atomicMax(&S.block[((u + NW * lane) >> bshift) - b0], logp_key16(mine));
+        }
+        if (n > m) {  // (the warp's)
+            float sa, sb, wa, wb;
+            f2_unpack(s2, sa, sb);
+            f2_unpack(w2, wa, wb);
+            logp_move(c, m, n, sa, wa);
+            logp_move(c, m, n, sb, wb);
+            s2 = f2_pack(sa, sb);
+            w2 = f2_pack(wa, wb);
+            m = n;
+        }
+        const uint64_t m2 = f2_pack(m, m);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const uint32_t *y = reinterpret_cast<const uint32_t *>(&x[k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t z = bf16x2_max(y[e], kLow2);
+                const uint64_t d2 = f2_sub(f2_pack(bf16lo(z), bf16hi(z)), m2);
+                float a, b;
+                f2_unpack(f2_mul(d2, c2), a, b);
+                const uint64_t e2 = f2_pack(fast_exp2(a), fast_exp2(b));
+                s2 = f2_add(s2, e2);
+                w2 = f2_fma(e2, d2, w2);
+            }
+        }
     }
-    s = red[1][0];
-    u = red[2][0];
-    const float ls = logf(s);
-    const bool none = m == -INF;
-    auto logprob = [&](float v) {
-        return none ? -INF : (v == m ? 0.f : (v - m) / T) - ls;
+    // ---------------------------------------------- sums of the warp, CTA, row
+    float s, w;
+    {
+        float sb, wb;
+        f2_unpack(s2, s, sb);
+        f2_unpack(w2, w, wb);
+        s += sb;
+        w += wb;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, off);
+        w += __shfl_xor_sync(0xffffffffu, w, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    if (lane == 0) S.warp[warp] = LogpStats{m, s, w, before};
+    __syncthreads();
+    auto join = [&](LogpStats &a, const LogpStats &b) {
+        const float n = fmaxf(a.m, b.m);
+        float bs = b.s, bw = b.w;
+        logp_move(c, a.m, n, a.s, a.w);
+        logp_move(c, b.m, n, bs, bw);
+        a = LogpStats{n, a.s + bs, a.w + bw, a.before + b.before};
     };
     if (t == 0) {
+        LogpStats a = S.warp[0];
+        for (int i = 1; i < NW; ++i) join(a, S.warp[i]);
+        S.cta = a;
+    }
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+    LogpStats a = C > 1 ? *cluster.map_shared_rank(&S.cta, 0) : S.cta;
+    for (int r = 1; r < C; ++r) join(a, *cluster.map_shared_rank(&S.cta, r));
+    if (a.m == INF) {
+        // the columns of +inf share the row
+        int n = 0;
+        for (long long v = u0 * 32 + t; v < min(u1 * 32, nvec); v += NT) {
+            const uint4 x = R.load(v);
+            const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+            for (int e = 0; e < 4; ++e) n += (bf16lo(y[e]) == INF) + (bf16hi(y[e]) == INF);
+        }
+        if (n) atomicAdd(&S.infs, n);
+        if (C > 1) cluster.sync();
+        else __syncthreads();
+        n = 0;
+        for (int r = 0; r < C; ++r) n += C > 1 ? *cluster.map_shared_rank(&S.infs, r) : S.infs;
+        a.s = (float)n;
+        a.w = 0.f;
+    }
+    bool none = false;
+    if (a.m < INF && (a.m <= kLogpLow || T > 1.0e25f)) {
+        // no logit above what the sums tell apart, or a temperature at which even
+        // -2^100 has weight: the row again, from its own largest logit and
+        // without those of -inf (every CTA all of it)
+        float n = -INF;
+        for (long long v = t; v < nvec; v += NT) {
+            const uint4 x = R.load(v);
+            const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+            for (int e = 0; e < 4; ++e) n = fmax3(n, bf16lo(y[e]), bf16hi(y[e]));
+        }
+        n = logp_warp_max(n);
+        __syncthreads();
+        if (lane == 0) S.warp[warp].m = n;
+        __syncthreads();
+        for (int i = 0; i < NW; ++i) n = fmaxf(n, S.warp[i].m);
+        none = n == -INF;
+        s = w = 0.f;
+        for (long long v = t; v < nvec && !none; v += NT) {
+            const uint4 x = R.load(v);
+            const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+            for (int e = 0; e < 8; ++e) {
+                const float z = e & 1 ? bf16hi(y[e >> 1]) : bf16lo(y[e >> 1]);
+                if (!(z > -INF)) continue;
+                const float f = fast_exp2((z - n) * c);
+                s += f;
+                w = fmaf(f, z - n, w);
+            }
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, off);
+            w += __shfl_xor_sync(0xffffffffu, w, off);
+        }
+        if (lane == 0) {
+            S.warp[warp].s = s;
+            S.warp[warp].w = w;
+        }
+        __syncthreads();
+        a.m = n;
+        a.s = a.w = 0.f;
+        for (int i = 0; i < NW; ++i) {
+            a.s += S.warp[i].s;
+            a.w += S.warp[i].w;
+        }
+    }
+    const float ls = log2f(a.s);
+    auto logprob = [&](float x) {
+        if (none || x == -INF) return -INF;
+        const float d = x == a.m ? 0.f : x - a.m;
+        return d * inv_t - ls * kLn2;
+    };
+    if (rank == 0 && t == 0) {
         A.logprobs[row] = col >= 0 ? logprob(xt) : -INF;
-        if (A.ranks) A.ranks[row] = col >= 0 ? count[0] + 1 : 0;
-        if (A.entropy) A.entropy[row] = none ? 0.f : ls - u / s;
+        if (A.ranks)
+            A.ranks[row] = col < 0 ? 0 : a.before + 1 + (xt == -INF ? col : 0);
+        if (A.entropy) A.entropy[row] = none ? 0.f : kLn2 * (ls - c * (a.w / a.s));
     }
-    unsigned long long last = ~0ull;
-    for (int k = 0; k < A.top; ++k) {
-        unsigned long long b = 0;
-        for (int j = t; j < A.V; j += kLogpThreads) {
-            const unsigned long long key = logp_key(logp_value(x[j]), j);
-            if (key < last && key > b) b = key;
+
+    // -------------------------------------------------------- the first n columns
+    if (A.top > 0 && rank == 0) {
+        const int top = A.top;
+        // per warp its first blocks: a key holds the logit and, equal logits
+        // falling, the block
+        const long long all = ((units - 1) >> bshift) + 1;
+        constexpr int PER = 8;  // keys per lane and batch
+        uint32_t mine = 0;      // lane i: the warp's i-th block so far
+        for (long long base = 0; base < all; base += (long long)NT * PER) {
+            uint32_t key[PER];
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                const long long b = base + (long long)q * NT + t;
+                key[q] = 0;
+                if (b < all) {
+                    // a block at the border of two CTAs' units is in both
+                    uint32_t k = 0;
+                    for (int r = 0; r < C; ++r) {
+                        const long long lo = (units * r / C) >> bshift;
+                        const long long hi = (units * (r + 1) / C - 1) >> bshift;
+                        if (units * r / C < units * (r + 1) / C && b >= lo && b <= hi)
+                            k = max(k, C > 1 ? *cluster.map_shared_rank(&S.block[b - lo], r)
+                                             : S.block[b - lo]);
+                    }
+                    key[q] = (k << 16) | (0xffffu - (uint32_t)b);
+                }
+            }
+            // the batch's first `top` beside those of the batches before
+            uint32_t old = mine, got = 0;
+            for (int i = 0; i < top; ++i) {
+                uint32_t k = old;
+#pragma unroll
+                for (int q = 0; q < PER; ++q) k = max(k, key[q]);
+                const uint32_t b = __reduce_max_sync(0xffffffffu, k);
+                if (lane == i) got = b;
+                if (old == b) old = 0;
+#pragma unroll
+                for (int q = 0; q < PER; ++q)
+                    if (key[q] == b) key[q] = 0;
+            }
+            mine = got;
+        }
+        if (lane < top) S.best[warp * kLogpMaxTop + lane] = mine;
+        __syncthreads();
+        // the row's first blocks by counting
+        for (int i = t; i < NW * top; i += NT) {
+            const uint32_t k = S.best[(i / top) * kLogpMaxTop + i % top];
+            int r = 0;
+            for (int wv = 0; wv < NW; ++wv)
+                for (int q = 0; q < top; ++q) r += S.best[wv * kLogpMaxTop + q] > k;
+            if (k != 0 && r < top) S.pick[r] = k;
+        }
+        if (t < top && t >= all) S.pick[t] = 0;
+        __syncthreads();
+        // their columns at least as large as the last one's largest
+        const int nb = (int)min((long long)top, all);
+        const float least = nb < top ? -INF : logp_of_key16(S.pick[nb - 1] >> 16);
+        for (int i = warp; i < nb; i += NW) {
+            const long long b = 0xffffu - (S.pick[i] & 0xffffu);
+            const long long v0 = (b << bshift) * 32, v1 = min(((b + 1) << bshift) * 32, nvec);
+            auto key_of = [&](uint32_t y, int e, long long v) -> unsigned long long {
+                const uint32_t z = bf16x2_max(y, kNegInf2);
+                const float f = e & 1 ? bf16hi(z) : bf16lo(z);
+                const long long j = 8 * v + e - R.shift;
+                if (!(f >= least) || j < 0 || j >= A.V) return 0;
+                return ((unsigned long long)logp_key16(f) << 32) | (uint32_t)~(uint32_t)j;
+            };
+            // (a lane's first vector stays in registers: its only one unless rows
+            // are longer than kLogpBlocks blocks of 256)
+            const uint4 x0 = v0 + lane < v1 ? R.load(v0 + lane) : make_uint4(0, 0, 0, 0);
+            int n = 0;
+            for (long long v = v0 + lane; v < v1; v += 32) {
+                const uint4 x = v < v0 + 32 ? x0 : R.load(v);
+                const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) n += key_of(y[e >> 1], e, v) != 0;
+            }
+            const int sum = __reduce_add_sync(0xffffffffu, n);
+            if (sum <= kLogpPerBlock) {
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&S.n_cand, sum);
+                at = __shfl_sync(0xffffffffu, at, 0);
+                int incl = n;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += o;
+                }
+                at += incl - n;
+                for (long long v = v0 + lane; n > 0 && v < v1; v += 32) {
+                    const uint4 x = v < v0 + 32 ? x0 : R.load(v);
+                    const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const unsigned long long k = key_of(y[e >> 1], e, v);
+                        if (k != 0) S.cand[at++] = k;
+                    }
+                }
+            } else {
+                // many equal ones: the block's first `top`, one after another
+                unsigned long long last = ~0ull;
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&S.n_cand, top);
+                at = __shfl_sync(0xffffffffu, at, 0);
+                for (int q = 0; q < top; ++q) {
+                    unsigned long long k = 0;
+                    for (long long v = v0 + lane; v < v1; v += 32) {
+                        const uint4 x = v < v0 + 32 ? x0 : R.load(v);
+                        const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const unsigned long long z = key_of(y[e >> 1], e, v);
+                            if (z < last && z > k) k = z;
+                        }
+                    }
+                    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+                    const uint32_t lo = __reduce_max_sync(
+                        0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+                    last = ((unsigned long long)hi << 32) | lo;
+                    if (lane == 0) S.cand[at + q] = last;
+                }
+            }
         }
         __syncthreads();
-        best[t] = b;
-        __syncthreads();
-        for (int n = kLogpThreads / 2; n > 0; n >>= 1) {
-            if (t < n && best[t + n] > best[t]) best[t] = best[t + n];
-            __syncthreads();
-        }
-        last = best[0];
-        if (t == 0) {
-            const int j = (int)~(uint32_t)last;
-            A.top_tokens[row * A.top + k] = A.keep ? A.keep[j] : j;
-            A.top_logprobs[row * A.top + k] = logprob(logp_value(x[j]));
+        const int n = S.n_cand;
+        for (int i = t; i < n; i += NT) {
+            const unsigned long long k = S.cand[i];
+            int r = 0;
+            for (int q = 0; q < n; ++q) r += S.cand[q] > k;
+            if (r < top) {
+                const int j = (int)~(uint32_t)k;
+                A.top_tokens[row * top + r] = A.keep ? A.keep[j] : j;
+                A.top_logprobs[row * top + r] = logprob(logp_of_key16((uint32_t)(k >> 32)));
+            }
         }
     }
+    // the other CTAs' shared memory is read above
+    if (C > 1) cluster.sync();
 }
 
 }  // namespace swa

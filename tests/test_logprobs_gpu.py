@@ -43,8 +43,8 @@ def check(x, tokens, top=0, T=None, keep=None, rows=None):
         base = (V / 32 + 64) * 2.0 ** -24 + 2.0 ** -20
 
         def near(a, w):
-            if np.isinf(w):
-                return a == w
+            if abs(w) > np.finfo(np.float32).max:     # (what fp32 holds of it)
+                return a == np.copysign(np.inf, w)
             # |y| is at most |log probability|: the largest weight is 1
             return abs(a - w) <= 2.0 ** -22 * (abs(w) + 1) + base
 
@@ -126,6 +126,25 @@ def test_infinities_and_nan():
     check(x, tok, 20)
     check(x, tok, 32, T=[0.25])
     check(x, [[4, 18, 7, 5, 1, 5, 6, 3000, 3000]], 0)
+
+
+def test_rows_of_the_lowest_values():
+    """Masks of the type's lowest value, alone and beside -inf, and rows whose
+    logits are all far below what others are."""
+    V = 1500
+    low = torch.finfo(torch.bfloat16).min
+    x = torch.full((1, 7, V), low)
+    x[0, 1, ::2] = -float("inf")
+    x[0, 2, 700] = -3.0
+    x[0, 3, :] = -1e35
+    x[0, 3, 5] = -2e35
+    x[0, 4, 1:] = -float("inf")
+    x[0, 5, :9] = -2e30
+    x[0, 6, :] = 3e38
+    x[0, 6, 3] = low
+    x = x.to(torch.bfloat16)
+    check(x, [[0, 1, 700, 5, 0, 3, 3]], 20)
+    check(x, [[9, 2, 3, 6, 7, 1400, 4]], 5, T=[0.1])
 
 
 def test_temperatures():
