@@ -20,6 +20,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "swa_tc_ptx.cuh"
 
 namespace swa {
@@ -28,6 +30,7 @@ constexpr int kLogpMaxTop = 32;
 constexpr int kLogpMaxCluster = 8;
 constexpr int kLogpBlocks = 2048;   // blocks per CTA at most; longer rows have larger ones
 constexpr int kLogpPerBlock = 32;   // candidates taken of one block at most
+constexpr int kLogpKeys = 8;        // block keys per thread (2048 of 256 threads)
 
 // Smaller logits count as -2^100 in the sums: a difference of two is then finite.
 constexpr float kLogpLow = -1.2676506e30f;
@@ -47,13 +50,19 @@ struct LogpStats {
 };
 
 struct LogpShared {
-    uint32_t block[kLogpBlocks];  // a block's largest logit as a rising key
-    unsigned long long cand[kLogpMaxTop * kLogpPerBlock];
-    uint32_t best[16 * kLogpMaxTop];  // per warp its first blocks
-    uint32_t pick[kLogpMaxTop];       // the first blocks of the row, in order
+    uint32_t block[kLogpBlocks];      // a block's largest logit as a rising key
+    union {
+        uint32_t lane[512];           // per thread its first block of the CTA
+        unsigned long long cand[kLogpMaxTop * kLogpPerBlock];
+    };
+    uint32_t list[kLogpMaxTop * kLogpKeys];  // the CTA's blocks that may be among the first
+    uint32_t best[kLogpMaxCluster * kLogpMaxTop];
+    uint32_t first[kLogpMaxTop];      // the CTA's first blocks, in order
+    uint32_t pick[kLogpMaxTop];       // the row's
     LogpStats warp[16];
     LogpStats cta;                    // read by the cluster's first CTA
-    int col, infs, n_cand;
+    int col, infs, n_cand, n_list;
+    uint32_t least;
 };
 
 // Rising with the value; -0 counts as 0.
@@ -116,7 +125,7 @@ struct LogpRow {
 
 // C CTAs of NT threads (a cluster) per row.
 template <int NT>
-__global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(const LogpParams A, const int C) {
+__global__ void __launch_bounds__(NT, 1024 / NT) swa_logprobs_kernel(const LogpParams A, const int C) {
     namespace cg = cooperative_groups;
     using namespace tc;
     constexpr int NW = NT / 32, U = 4;
@@ -135,10 +144,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(con
     R.shift = (int)((reinterpret_cast<uintptr_t>(R.x) >> 1) & 7);
     const long long nvec = ((long long)R.shift + A.V + 7) / 8;
     const long long units = (nvec + 31) / 32;        // of 32 vectors
-    const long long u0 = units * rank / C, u1 = units * (rank + 1) / C;
     int bshift = 0;                                  // blocks of 2^bshift units
     while ((((units + C - 1) / C) >> bshift) + 2 > kLogpBlocks) ++bshift;
-    const long long b0 = u0 >> bshift;               // this CTA's first block
+    const long long blocks = ((units - 1) >> bshift) + 1;
+    const long long b0 = blocks * rank / C, b1 = blocks * (rank + 1) / C;  // this CTA's
+    const long long u0 = b0 << bshift, u1 = min(b1 << bshift, units);
 
     float T = A.temperature ? A.temperature[row / A.q_len] : 1.f;
     T = T > 0.f ? fminf(T, 3.0e38f) : 1.f;
@@ -149,9 +159,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(con
     int col = A.keep || tok < 0 || tok >= A.V ? -1 : tok;
     if (t == 0) {
         S.col = 0x7fffffff;
-        S.infs = S.n_cand = 0;
+        S.infs = S.n_cand = S.n_list = 0;
+        S.least = 0;
     }
-    for (int i = t; i < kLogpBlocks; i += NT) S.block[i] = 0;
+    if (A.top > 0)
+        for (int i = t; i < (int)(b1 - b0); i += NT) S.block[i] = 0;
     __syncthreads();
     if (A.keep && tok >= 0) {
         const int j0 = (int)((long long)A.V * rank / C), j1 = (int)((long long)A.V * (rank + 1) / C);
@@ -188,46 +200,39 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(con
     uint64_t s2 = 0, w2 = 0;   // pairs of partial sums
     int before = 0;
     const uint64_t c2 = f2_pack(c, c);
-    for (long long u = u0 + warp; u < u1; u += NW * U) {
-        uint4 x[U];
-        uint32_t count = 0;  // bf16 pairs, at most 4 U in each half
-        float mu[U];
+    // K units u, u + NW, ... whose vectors are in x; `exact`: one of them may hold
+    // the given token's column
+    auto take = [&](auto K, const uint4 *x, long long u, bool exact) {
+        constexpr int N = decltype(K)::value;
+        uint32_t count = 0;  // bf16 pairs, at most 4 N in each half
+        float n = m, mine = -INF;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const long long v = (u + NW * k) * 32 + lane;
-            x[k] = u + NW * k < u1 && v < nvec ? R.load(v)
-                                               : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const long long v = (u + NW * k) * 32 + lane;
-            uint32_t *y = reinterpret_cast<uint32_t *>(&x[k]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = bf16x2_max(y[e], kNegInf2);  // NaN is -inf
-            const uint32_t a = bf16x2_max(bf16x2_max(y[0], y[1]), bf16x2_max(y[2], y[3]));
-            mu[k] = logp_warp_max(fmaxf(bf16lo(a), bf16hi(a)));
-            const uint32_t thr = v < tv ? thr_before : thr_behind;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) count = bf16x2_add(count, bf16x2_gt(y[e], thr));
-            if (v == tv && col >= 0) {
-                const bool none = thr_before == 0x7f807f80u;
-                for (int e = 0; e < tpos; ++e) {
-                    const float z = e & 1 ? bf16hi(y[e >> 1]) : bf16lo(y[e >> 1]);
-                    before += none ? -(z > xt) : (z == xt);
+        for (int k = 0; k < N; ++k) {
+            const uint32_t *y = reinterpret_cast<const uint32_t *>(&x[k]);
+            const uint32_t a = bf16x2_max(
+                bf16x2_max(bf16x2_max(y[0], y[1]), bf16x2_max(y[2], y[3])), kNegInf2);
+            const float mu = logp_warp_max(fmaxf(bf16lo(a), bf16hi(a)));
+            n = fmaxf(n, mu);
+            if (lane == k) mine = mu;
+            uint32_t thr = u + NW * k < (tv >> 5) ? thr_before : thr_behind;
+            if (exact) {
+                const long long v = (u + NW * k) * 32 + lane;
+                thr = v < tv ? thr_before : thr_behind;
+                if (v == tv && col >= 0) {
+                    const bool none = thr_before == 0x7f807f80u;
+                    for (int e = 0; e < tpos; ++e) {
+                        const uint32_t z2 = bf16x2_max(y[e >> 1], kNegInf2);
+                        const float z = e & 1 ? bf16hi(z2) : bf16lo(z2);
+                        before += none ? -(z > xt) : (z == xt);
+                    }
                 }
             }
-        }
-        before += (int)bf16lo(count) + (int)bf16hi(count);
-        float n = m;
 #pragma unroll
-        for (int k = 0; k < U; ++k) n = fmaxf(n, mu[k]);
-        if (A.top > 0 && lane < U && u + NW * lane < u1) {
-            float mine = mu[0];
-#pragma unroll
-            for (int k = 1; k < U; ++k)
-                if (lane == k) mine = mu[k];
-            atomicMax(&S.block[((u + NW * lane) >> bshift) - b0], logp_key16(mine));
+            for (int e = 0; e < 4; ++e) count = bf16x2_add(count, bf16x2_gt(y[e], thr));
         }
+        before += (int)(bf16lo(count) + bf16hi(count));
+        if (A.top > 0 && lane < N)
+            atomicMax(&S.block[(int)(((u + NW * lane) >> bshift) - b0)], logp_key16(mine));
         if (n > m) {  // (the warp's)
             float sa, sb, wa, wb;
             f2_unpack(s2, sa, sb);
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(con
         }
         const uint64_t m2 = f2_pack(m, m);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
+        for (int k = 0; k < N; ++k) {
             const uint32_t *y = reinterpret_cast<const uint32_t *>(&x[k]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -253,6 +258,26 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(con
                 w2 = f2_fma(e2, d2, w2);
             }
         }
+    };
+    // the units that lie wholly inside the row, U at a time, then the others
+    const long long i0 = max(u0, R.shift > 0 ? 1LL : 0LL);
+    const long long i1 = min(u1, ((long long)R.shift + A.V) / 256);
+    const long long groups = i1 > i0 ? (i1 - i0) / (NW * U) : 0;
+    const uint4 *p = reinterpret_cast<const uint4 *>(R.x - R.shift) + (i0 + warp) * 32 + lane;
+    long long u = i0 + warp;
+    for (long long g = 0; g < groups; ++g, u += NW * U, p += NW * U * 32) {
+        uint4 x[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) x[k] = __ldcs(p + NW * 32 * k);
+        const long long at = (tv >> 5) - u;
+        take(std::integral_constant<int, U>{}, x, u, at >= 0 && at < NW * U && at % NW == 0);
+    }
+    for (long long q = warp; q < (u1 - u0) - groups * (NW * U); q += NW) {
+        // (those before i0, then those behind the groups)
+        const long long un = u0 + q < i0 ? u0 + q : u0 + q + groups * (NW * U);
+        const long long v = un * 32 + lane;
+        const uint4 x = v < nvec ? R.load(v) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
+        take(std::integral_constant<int, 1>{}, &x, un, true);
     }
     // ---------------------------------------------- sums of the warp, CTA, row
     float s, w;
@@ -271,6 +296,43 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(con
     }
     if (lane == 0) S.warp[warp] = LogpStats{m, s, w, before};
     __syncthreads();
+    const int top = A.top;
+    if (top > 0) {
+        // This CTA's first blocks.  A key holds a block's logit and, equal logits
+        // falling, its place: all differ.  The top-th largest of the threads' own
+        // largest keys bounds them from below, and at most `top` threads have keys
+        // above it.
+        uint32_t key[kLogpKeys], mine = 0;
+#pragma unroll
+        for (int q = 0; q < kLogpKeys; ++q) {
+            const int b = q * NT + t;
+            key[q] = b < (int)(b1 - b0) ? (S.block[b] << 16) | (0xffffu - (uint32_t)(b0 + b)) : 0u;
+            mine = max(mine, key[q]);
+        }
+        S.lane[t] = mine;
+        __syncthreads();
+        int r = 0;
+        const uint4 *all = reinterpret_cast<const uint4 *>(S.lane);
+        const int used = min(NT, (int)(b1 - b0));  // threads with a block
+        for (int i = 0; i < (used + 3) / 4; ++i) {
+            const uint4 k = all[i];
+            r += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+        }
+        if (mine != 0 && r == top - 1) S.least = mine;
+        __syncthreads();
+        const uint32_t least = S.least;  // 0: fewer than `top` blocks
+#pragma unroll
+        for (int q = 0; q < kLogpKeys; ++q)
+            if (key[q] != 0 && key[q] >= least) S.list[atomicAdd(&S.n_list, 1)] = key[q];
+        if (t < top) S.first[t] = 0;
+        __syncthreads();
+        for (int i = t; i < S.n_list; i += NT) {
+            const uint32_t k = S.list[i];
+            int r2 = 0;
+            for (int q = 0; q < S.n_list; ++q) r2 += S.list[q] > k;
+            if (r2 < top) S.first[r2] = k;
+        }
+    }
     auto join = [&](LogpStats &a, const LogpStats &b) {
         const float n = fmaxf(a.m, b.m);
         float bs = b.s, bw = b.w;
@@ -363,87 +425,60 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(con
     }
 
     // -------------------------------------------------------- the first n columns
-    if (A.top > 0 && rank == 0) {
-        const int top = A.top;
-        // per warp its first blocks: a key holds the logit and, equal logits
-        // falling, the block
-        const long long all = ((units - 1) >> bshift) + 1;
-        constexpr int PER = 8;  // keys per lane and batch
-        uint32_t mine = 0;      // lane i: the warp's i-th block so far
-        for (long long base = 0; base < all; base += (long long)NT * PER) {
-            uint32_t key[PER];
-#pragma unroll
-            for (int q = 0; q < PER; ++q) {
-                const long long b = base + (long long)q * NT + t;
-                key[q] = 0;
-                if (b < all) {
-                    // a block at the border of two CTAs' units is in both
-                    uint32_t k = 0;
-                    for (int r = 0; r < C; ++r) {
-                        const long long lo = (units * r / C) >> bshift;
-                        const long long hi = (units * (r + 1) / C - 1) >> bshift;
-                        if (units * r / C < units * (r + 1) / C && b >= lo && b <= hi)
-                            k = max(k, C > 1 ? *cluster.map_shared_rank(&S.block[b - lo], r)
-                                             : S.block[b - lo]);
-                    }
-                    key[q] = (k << 16) | (0xffffu - (uint32_t)b);
-                }
-            }
-            // the batch's first `top` beside those of the batches before
-            uint32_t old = mine, got = 0;
-            for (int i = 0; i < top; ++i) {
-                uint32_t k = old;
-#pragma unroll
-                for (int q = 0; q < PER; ++q) k = max(k, key[q]);
-                const uint32_t b = __reduce_max_sync(0xffffffffu, k);
-                if (lane == i) got = b;
-                if (old == b) old = 0;
-#pragma unroll
-                for (int q = 0; q < PER; ++q)
-                    if (key[q] == b) key[q] = 0;
-            }
-            mine = got;
-        }
-        if (lane < top) S.best[warp * kLogpMaxTop + lane] = mine;
+    if (top > 0 && rank == 0) {
+        // the row's first blocks among the CTAs' by counting
+        for (int i = t; i < C * top; i += NT)
+            S.best[i] = C > 1 ? *cluster.map_shared_rank(&S.first[i % top], i / top) : S.first[i];
         __syncthreads();
-        // the row's first blocks by counting
-        for (int i = t; i < NW * top; i += NT) {
-            const uint32_t k = S.best[(i / top) * kLogpMaxTop + i % top];
+        for (int i = t; i < C * top; i += NT) {
+            const uint32_t k = S.best[i];
             int r = 0;
-            for (int wv = 0; wv < NW; ++wv)
-                for (int q = 0; q < top; ++q) r += S.best[wv * kLogpMaxTop + q] > k;
+            for (int q = 0; q < C * top; ++q) r += S.best[q] > k;
             if (k != 0 && r < top) S.pick[r] = k;
         }
-        if (t < top && t >= all) S.pick[t] = 0;
         __syncthreads();
-        // their columns at least as large as the last one's largest
-        const int nb = (int)min((long long)top, all);
+        // their columns at least as large as the last one's largest; a lane's first
+        // vector of each of the warp's blocks at once (the only one unless rows are
+        // longer than kLogpBlocks blocks of 256)
+        const int nb = (int)min((long long)top, blocks);
         const float least = nb < top ? -INF : logp_of_key16(S.pick[nb - 1] >> 16);
-        for (int i = warp; i < nb; i += NW) {
-            const long long b = 0xffffu - (S.pick[i] & 0xffffu);
+        constexpr int BW = (kLogpMaxTop + NW - 1) / NW;  // blocks per warp
+        uint4 x0[BW];
+#pragma unroll
+        for (int h = 0; h < BW; ++h) {
+            const int i = warp + NW * h;
+            x0[h] = make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
+            if (i < nb) {
+                const long long v = ((0xffffLL - (S.pick[i] & 0xffffu)) << bshift) * 32 + lane;
+                if (v < nvec) x0[h] = R.load(v);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < BW; ++h) {
+            const int i = warp + NW * h;
+            if (i >= nb) break;
+            const long long b = 0xffffLL - (S.pick[i] & 0xffffu);
             const long long v0 = (b << bshift) * 32, v1 = min(((b + 1) << bshift) * 32, nvec);
-            auto key_of = [&](uint32_t y, int e, long long v) -> unsigned long long {
-                const uint32_t z = bf16x2_max(y, kNegInf2);
+            auto vec = [&](long long v) { return v < v0 + 32 ? x0[h] : R.load(v); };
+            auto key_of = [&](const uint4 &x, int e, long long v) -> unsigned long long {
+                const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+                const uint32_t z = bf16x2_max(y[e >> 1], kNegInf2);
                 const float f = e & 1 ? bf16hi(z) : bf16lo(z);
                 const long long j = 8 * v + e - R.shift;
                 if (!(f >= least) || j < 0 || j >= A.V) return 0;
                 return ((unsigned long long)logp_key16(f) << 32) | (uint32_t)~(uint32_t)j;
             };
-            // (a lane's first vector stays in registers: its only one unless rows
-            // are longer than kLogpBlocks blocks of 256)
-            const uint4 x0 = v0 + lane < v1 ? R.load(v0 + lane) : make_uint4(0, 0, 0, 0);
             int n = 0;
             for (long long v = v0 + lane; v < v1; v += 32) {
-                const uint4 x = v < v0 + 32 ? x0 : R.load(v);
-                const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+                const uint4 x = vec(v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) n += key_of(y[e >> 1], e, v) != 0;
+                for (int e = 0; e < 8; ++e) n += key_of(x, e, v) != 0;
             }
             const int sum = __reduce_add_sync(0xffffffffu, n);
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&S.n_cand, min(sum, kLogpPerBlock));
+            at = __shfl_sync(0xffffffffu, at, 0);
             if (sum <= kLogpPerBlock) {
-                int at = 0;
-                if (lane == 0) at = atomicAdd(&S.n_cand, sum);
-                at = __shfl_sync(0xffffffffu, at, 0);
                 int incl = n;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -452,28 +487,23 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) swa_logprobs_kernel(con
                 }
                 at += incl - n;
                 for (long long v = v0 + lane; n > 0 && v < v1; v += 32) {
-                    const uint4 x = v < v0 + 32 ? x0 : R.load(v);
-                    const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+                    const uint4 x = vec(v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const unsigned long long k = key_of(y[e >> 1], e, v);
+                        const unsigned long long k = key_of(x, e, v);
                         if (k != 0) S.cand[at++] = k;
                     }
                 }
             } else {
-                // many equal ones: the block's first `top`, one after another
+                // many equal ones: the block's first kLogpPerBlock, one after another
                 unsigned long long last = ~0ull;
-                int at = 0;
-                if (lane == 0) at = atomicAdd(&S.n_cand, top);
-                at = __shfl_sync(0xffffffffu, at, 0);
-                for (int q = 0; q < top; ++q) {
+                for (int q = 0; q < kLogpPerBlock; ++q) {
                     unsigned long long k = 0;
                     for (long long v = v0 + lane; v < v1; v += 32) {
-                        const uint4 x = v < v0 + 32 ? x0 : R.load(v);
-                        const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
+                        const uint4 x = vec(v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const unsigned long long z = key_of(y[e >> 1], e, v);
+                            const unsigned long long z = key_of(x, e, v);
                             if (z < last && z > k) k = z;
                         }
                     }
