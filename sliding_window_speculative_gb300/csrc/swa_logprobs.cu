@@ -27,14 +27,31 @@ cudaError_t launch(const swa::LogpParams &A, long long rows, int c, cudaStream_t
     cfg.attrs = attr;
     cfg.numAttrs = swa::pdl_enabled() ? 2 : 1;
     if (swa::launch_fault_due()) return cudaErrorLaunchOutOfResources;
-    return cudaLaunchKernelEx(&cfg, swa::swa_logprobs_kernel<NT>, A, c);
+    return cudaLaunchKernelEx(&cfg, swa::swa_logprobs_kernel<NT>, A,
+                              c == 8 ? 3 : c >> 1);
 }
 
 cudaError_t launch_rows(const swa::LogpParams &A, long long rows, int sms, cudaStream_t s) {
+    // One CTA per row, four to an SM; clusters share a row while that leaves at most
+    // three CTAs to an SM and each CTA eight vectors per thread.  Many rows that are
+    // not long get CTAs of 128 threads: the steps behind the pass are a larger share
+    // of theirs.  Measured on GB300, calls behind one another in a replayed graph, us
+    // (rows x columns, alternatives):
+    //   8 x 262144, 5      8 CTAs of 512 threads 10.0, of 256 10.2, 4 of 512 12.1, 2 of
+    //                      512 14.1
+    //   64 x 262144, 5     4 of 256 13.9, 2 of 512 14.6, 8 of 256 17.2, 1 of 512 21.2
+    //   200 x 262144, 5    4 of 256 34.9, 2 of 256 36.4, 1 of 512 35.0, 1 of 256 43.0
+    //   512 x 262144, 20   1 of 256 65.7, 1 of 512 70.7, 2 of 128 70.9, 2 of 256 75.0
+    //   512 x 50257, 5     1 of 128 19.3, 1 of 256 21.3, 1 of 512 26.7
+    //   240 x 12001, 20    1 of 256 7.7, 1 of 128 9.4, 1 of 512 9.7
+    //   100 x 32000, 5     2 of 256 9.2, 4 of 256 11.3, 1 of 256 10.2
+    //   4000 x 1000, 5     1 of 128 24.3, 1 of 256 43.0
     const long long nvec = ((long long)A.V + 14) / 8;
     int c = 1;
-    while (c < swa::kLogpMaxCluster && rows * c * 2 <= 2LL * sms && nvec > 1024LL * c) c *= 2;
-    return c >= 8 ? launch<512>(A, rows, c, s) : launch<256>(A, rows, c, s);
+    while (c < swa::kLogpMaxCluster && rows * c * 2 <= 3LL * sms && nvec > 2048LL * c) c *= 2;
+    if (c == swa::kLogpMaxCluster) return launch<512>(A, rows, c, s);
+    if (c == 1 && rows > 3LL * sms && nvec <= 8192) return launch<128>(A, rows, c, s);
+    return launch<256>(A, rows, c, s);
 }
 
 }  // namespace

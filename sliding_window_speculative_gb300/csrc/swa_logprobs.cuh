@@ -4,7 +4,8 @@
 //   s = sum 2^(c (x - M)),   w = sum 2^(c (x - M)) (x - M),   c = log2(e) / T,
 // so that ln p_j = ln2 (c (x_j - M) - log2 s) and the entropy is
 // ln2 (log2 s - c w / s); counts what comes before the given token in the order;
-// and stores the largest logit of every block of 256 columns.
+// and stores the largest logit of every block of columns: of a vector of 8 in
+// rows of up to 2048 vectors per CTA, else of a warp's 32 vectors.
 //
 // The top n columns of the order lie in the n blocks that come first by falling
 // largest logit, equal ones by rising place: a column in another block has n
@@ -28,9 +29,9 @@ namespace swa {
 
 constexpr int kLogpMaxTop = 32;
 constexpr int kLogpMaxCluster = 8;
-constexpr int kLogpBlocks = 2048;   // blocks per CTA at most; longer rows have larger ones
+constexpr int kLogpBlocks = 2048;   // blocks per CTA at most
 constexpr int kLogpPerBlock = 32;   // candidates taken of one block at most
-constexpr int kLogpKeys = 8;        // block keys per thread (2048 of 256 threads)
+constexpr int kLogpList = 256;      // blocks ranked by counting at most
 
 // Smaller logits count as -2^100 in the sums: a difference of two is then finite.
 constexpr float kLogpLow = -1.2676506e30f;
@@ -52,17 +53,19 @@ struct LogpStats {
 struct LogpShared {
     uint32_t block[kLogpBlocks];      // a block's largest logit as a rising key
     union {
-        uint32_t lane[512];           // per thread its first block of the CTA
+        struct {
+            uint32_t list[kLogpBlocks - 512];  // the CTA's blocks that may be among the first
+            uint32_t lane[512];                // per thread its first block of the CTA
+        };
         unsigned long long cand[kLogpMaxTop * kLogpPerBlock];
     };
-    uint32_t list[kLogpMaxTop * kLogpKeys];  // the CTA's blocks that may be among the first
     uint32_t best[kLogpMaxCluster * kLogpMaxTop];
     uint32_t first[kLogpMaxTop];      // the CTA's first blocks, in order
     uint32_t pick[kLogpMaxTop];       // the row's
     LogpStats warp[16];
     LogpStats cta;                    // read by the cluster's first CTA
     int col, infs, n_cand, n_list;
-    uint32_t least;
+    uint32_t least, kth[16];
 };
 
 // Rising with the value; -0 counts as 0.
@@ -125,7 +128,8 @@ struct LogpRow {
 
 // C CTAs of NT threads (a cluster) per row.
 template <int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) swa_logprobs_kernel(const LogpParams A, const int C) {
+__global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1024 / NT)
+    swa_logprobs_kernel(const LogpParams A, const int log_c) {
     namespace cg = cooperative_groups;
     using namespace tc;
     constexpr int NW = NT / 32, U = 4;
@@ -134,23 +138,34 @@ __global__ void __launch_bounds__(NT, 1024 / NT) swa_logprobs_kernel(const LogpP
     __shared__ LogpShared S;
     cg::cluster_group cluster = cg::this_cluster();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int rank = C > 1 ? (int)cluster.block_rank() : 0;
+    const int C = 1 << log_c;
+    const int rank = (int)blockIdx.x & (C - 1);
     grid_dep_wait();
     grid_dep_trigger();
-    const long long row = blockIdx.x / C;
+    const long long row = blockIdx.x >> log_c;
     LogpRow R;
     R.x = A.logits + row * A.V;
     R.V = A.V;
     R.shift = (int)((reinterpret_cast<uintptr_t>(R.x) >> 1) & 7);
     const long long nvec = ((long long)R.shift + A.V + 7) / 8;
     const long long units = (nvec + 31) / 32;        // of 32 vectors
-    int bshift = 0;                                  // blocks of 2^bshift units
-    while ((((units + C - 1) / C) >> bshift) + 2 > kLogpBlocks) ++bshift;
-    const long long blocks = ((units - 1) >> bshift) + 1;
-    const long long b0 = blocks * rank / C, b1 = blocks * (rank + 1) / C;  // this CTA's
-    const long long u0 = b0 << bshift, u1 = min(b1 << bshift, units);
+    // blocks of 2^bshift vectors: one, or units and powers of two of them
+    int bshift = 0;
+    if (((units + C - 1) >> log_c) * 32 > kLogpBlocks) {
+        bshift = 5;
+        while ((((units + C - 1) >> log_c) >> (bshift - 5)) + 2 > kLogpBlocks) ++bshift;
+    }
+    const bool fine = bshift == 0;
+    const int ushift = fine ? 0 : bshift - 5;        // a CTA has whole blocks and units
+    const long long groups_of = ((units - 1) >> ushift) + 1;
+    const long long u0 = ((groups_of * rank) >> log_c) << ushift;
+    const long long u1 = min(((groups_of * (rank + 1)) >> log_c) << ushift, units);
+    const long long b0 = (u0 * 32) >> bshift;        // this CTA's first block
+    const int n_blocks =
+        u1 > u0 ? (int)(((min(u1 * 32, nvec) - 1) >> bshift) + 1 - b0) : 0;
+    const long long blocks = ((nvec - 1) >> bshift) + 1;  // the row's
 
-    float T = A.temperature ? A.temperature[row / A.q_len] : 1.f;
+    float T = A.temperature ? A.temperature[(uint32_t)row / (uint32_t)A.q_len] : 1.f;
     T = T > 0.f ? fminf(T, 3.0e38f) : 1.f;
     const float inv_t = fminf(1.f / T, 3.0e38f), c = fminf(kLog2e / T, 3.0e38f);
 
@@ -162,11 +177,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) swa_logprobs_kernel(const LogpP
         S.infs = S.n_cand = S.n_list = 0;
         S.least = 0;
     }
-    if (A.top > 0)
-        for (int i = t; i < (int)(b1 - b0); i += NT) S.block[i] = 0;
+    if (A.top > 0 && !fine)
+        for (int i = t; i < n_blocks; i += NT) S.block[i] = 0;
     __syncthreads();
     if (A.keep && tok >= 0) {
-        const int j0 = (int)((long long)A.V * rank / C), j1 = (int)((long long)A.V * (rank + 1) / C);
+        const int j0 = (int)(((long long)A.V * rank) >> log_c);
+        const int j1 = (int)(((long long)A.V * (rank + 1)) >> log_c);
         for (int j = j0 + t; j < j1; j += NT)
             if (A.keep[j] == tok) atomicMin(&S.col, j);
         if (C > 1) cluster.sync();
@@ -211,9 +227,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) swa_logprobs_kernel(const LogpP
             const uint32_t *y = reinterpret_cast<const uint32_t *>(&x[k]);
             const uint32_t a = bf16x2_max(
                 bf16x2_max(bf16x2_max(y[0], y[1]), bf16x2_max(y[2], y[3])), kNegInf2);
-            const float mu = logp_warp_max(fmaxf(bf16lo(a), bf16hi(a)));
+            const float own = fmaxf(bf16lo(a), bf16hi(a));
+            const float mu = logp_warp_max(own);
             n = fmaxf(n, mu);
             if (lane == k) mine = mu;
+            if (fine && A.top > 0) {
+                const long long b = (u + NW * k) * 32 + lane - b0;
+                if (b < n_blocks) S.block[b] = logp_key16(own);
+            }
             uint32_t thr = u + NW * k < (tv >> 5) ? thr_before : thr_behind;
             if (exact) {
                 const long long v = (u + NW * k) * 32 + lane;
@@ -231,8 +252,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) swa_logprobs_kernel(const LogpP
             for (int e = 0; e < 4; ++e) count = bf16x2_add(count, bf16x2_gt(y[e], thr));
         }
         before += (int)(bf16lo(count) + bf16hi(count));
-        if (A.top > 0 && lane < N)
-            atomicMax(&S.block[(int)(((u + NW * lane) >> bshift) - b0)], logp_key16(mine));
+        if (A.top > 0 && !fine && lane < N)
+            atomicMax(&S.block[(int)(((u + NW * lane) >> (bshift - 5)) - b0)], logp_key16(mine));
         if (n > m) {  // (the warp's)
             float sa, sb, wa, wb;
             f2_unpack(s2, sa, sb);
@@ -299,38 +320,65 @@ __global__ void __launch_bounds__(NT, 1024 / NT) swa_logprobs_kernel(const LogpP
     const int top = A.top;
     if (top > 0) {
         // This CTA's first blocks.  A key holds a block's logit and, equal logits
-        // falling, its place: all differ.  The top-th largest of the threads' own
-        // largest keys bounds them from below, and at most `top` threads have keys
-        // above it.
-        uint32_t key[kLogpKeys], mine = 0;
+        // falling, its place: all differ.  Threads' own largest keys bound the
+        // top-th largest key from below: `per` of them in each warp are at least the
+        // warps' smallest per-th largest.
+        constexpr int PER = kLogpBlocks / NT;
+        uint32_t key[PER], mine = 0;
 #pragma unroll
-        for (int q = 0; q < kLogpKeys; ++q) {
+        for (int q = 0; q < PER; ++q) {
             const int b = q * NT + t;
-            key[q] = b < (int)(b1 - b0) ? (S.block[b] << 16) | (0xffffu - (uint32_t)(b0 + b)) : 0u;
+            key[q] = b < n_blocks ? (S.block[b] << 16) | (0xffffu - (uint32_t)(b0 + b)) : 0u;
             mine = max(mine, key[q]);
         }
-        S.lane[t] = mine;
-        __syncthreads();
-        int r = 0;
-        const uint4 *all = reinterpret_cast<const uint4 *>(S.lane);
-        const int used = min(NT, (int)(b1 - b0));  // threads with a block
-        for (int i = 0; i < (used + 3) / 4; ++i) {
-            const uint4 k = all[i];
-            r += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+        const int per = (top + NW - 1) / NW;
+        uint32_t left = mine, kth = 0;
+        for (int i = 0; i < per; ++i) {
+            kth = __reduce_max_sync(0xffffffffu, left);
+            if (left == kth) left = 0;
         }
-        if (mine != 0 && r == top - 1) S.least = mine;
-        __syncthreads();
-        const uint32_t least = S.least;  // 0: fewer than `top` blocks
-#pragma unroll
-        for (int q = 0; q < kLogpKeys; ++q)
-            if (key[q] != 0 && key[q] >= least) S.list[atomicAdd(&S.n_list, 1)] = key[q];
+        if (lane == 0) S.kth[warp] = kth;
         if (t < top) S.first[t] = 0;
         __syncthreads();
-        for (int i = t; i < S.n_list; i += NT) {
+        uint32_t least = S.kth[0];
+        for (int i = 1; i < NW; ++i) least = min(least, S.kth[i]);
+        int above = 0;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) above += key[q] != 0 && key[q] >= least;
+        int at = above > 0 ? atomicAdd(&S.n_list, above) : 0;
+        __syncthreads();
+        int n_list = S.n_list;
+        if (n_list > kLogpList) {
+            // too loose (large logits crowd in few warps): the top-th largest of all
+            // threads' own largest, which leaves at most top * PER
+            S.lane[t] = mine;
+            __syncthreads();
+            if (t == 0) S.n_list = 0;
+            int r = 0;
+            const uint4 *all = reinterpret_cast<const uint4 *>(S.lane);
+            for (int i = 0; i < NT / 4; ++i) {
+                const uint4 k = all[i];
+                r += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+            }
+            if (mine != 0 && r == top - 1) S.least = mine;
+            __syncthreads();
+            least = S.least;
+            above = 0;
+#pragma unroll
+            for (int q = 0; q < PER; ++q) above += key[q] != 0 && key[q] >= least;
+            at = above > 0 ? atomicAdd(&S.n_list, above) : 0;
+            __syncthreads();
+            n_list = S.n_list;
+        }
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (key[q] != 0 && key[q] >= least) S.list[at++] = key[q];
+        __syncthreads();
+        for (int i = t; i < n_list; i += NT) {
             const uint32_t k = S.list[i];
-            int r2 = 0;
-            for (int q = 0; q < S.n_list; ++q) r2 += S.list[q] > k;
-            if (r2 < top) S.first[r2] = k;
+            int r = 0;
+            for (int q = 0; q < n_list; ++q) r += S.list[q] > k;
+            if (r < top) S.first[r] = k;
         }
     }
     auto join = [&](LogpStats &a, const LogpStats &b) {
@@ -442,68 +490,83 @@ __global__ void __launch_bounds__(NT, 1024 / NT) swa_logprobs_kernel(const LogpP
         // longer than kLogpBlocks blocks of 256)
         const int nb = (int)min((long long)top, blocks);
         const float least = nb < top ? -INF : logp_of_key16(S.pick[nb - 1] >> 16);
+        if (fine) {
+            // a thread per element
+            for (int i = t; i < 8 * nb; i += NT) {
+                const long long j =
+                    8 * (0xffffLL - (S.pick[i >> 3] & 0xffffu)) + (i & 7) - R.shift;
+                if (j < 0 || j >= A.V) continue;
+                uint32_t b = R.x[j];
+                if ((b & 0x7fffu) > 0x7f80u) b = 0xff80u;
+                const float f = __uint_as_float(b << 16);
+                if (f >= least)
+                    S.cand[atomicAdd(&S.n_cand, 1)] =
+                        ((unsigned long long)logp_key16(f) << 32) | (uint32_t)~(uint32_t)j;
+            }
+        }
         constexpr int BW = (kLogpMaxTop + NW - 1) / NW;  // blocks per warp
         uint4 x0[BW];
+        const int nw = fine ? 0 : nb;
 #pragma unroll
         for (int h = 0; h < BW; ++h) {
             const int i = warp + NW * h;
             x0[h] = make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
-            if (i < nb) {
-                const long long v = ((0xffffLL - (S.pick[i] & 0xffffu)) << bshift) * 32 + lane;
+            if (i < nw) {
+                const long long v = ((0xffffLL - (S.pick[i] & 0xffffu)) << bshift) + lane;
                 if (v < nvec) x0[h] = R.load(v);
             }
         }
 #pragma unroll
         for (int h = 0; h < BW; ++h) {
             const int i = warp + NW * h;
-            if (i >= nb) break;
+            if (i >= nw) break;
             const long long b = 0xffffLL - (S.pick[i] & 0xffffu);
-            const long long v0 = (b << bshift) * 32, v1 = min(((b + 1) << bshift) * 32, nvec);
+            const long long v0 = b << bshift, v1 = min((b + 1) << bshift, nvec);
             auto vec = [&](long long v) { return v < v0 + 32 ? x0[h] : R.load(v); };
-            auto key_of = [&](const uint4 &x, int e, long long v) -> unsigned long long {
+            // elements of a vector that are candidates, and the key of one
+            auto mask_of = [&](const uint4 &x, long long v) -> uint32_t {
                 const uint32_t *y = reinterpret_cast<const uint32_t *>(&x);
-                const uint32_t z = bf16x2_max(y[e >> 1], kNegInf2);
-                const float f = e & 1 ? bf16hi(z) : bf16lo(z);
-                const long long j = 8 * v + e - R.shift;
-                if (!(f >= least) || j < 0 || j >= A.V) return 0;
-                return ((unsigned long long)logp_key16(f) << 32) | (uint32_t)~(uint32_t)j;
+                uint32_t m8 = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t z = bf16x2_max(y[e >> 1], kNegInf2);
+                    m8 |= (uint32_t)((e & 1 ? bf16hi(z) : bf16lo(z)) >= least) << e;
+                }
+                if (least == -INF)
+                    for (int e = 0; e < 8; ++e) {
+                        const long long j = 8 * v + e - R.shift;
+                        if (j < 0 || j >= A.V) m8 &= ~(1u << e);
+                    }
+                return m8;
+            };
+            auto key_of = [&](const uint4 &x, int e, long long v) -> unsigned long long {
+                const uint32_t y = e < 4 ? (e < 2 ? x.x : x.y) : (e < 6 ? x.z : x.w);
+                const uint32_t z = bf16x2_max(y, kNegInf2);
+                return ((unsigned long long)logp_key16(e & 1 ? bf16hi(z) : bf16lo(z)) << 32) |
+                       (uint32_t)~(uint32_t)(8 * v + e - R.shift);
             };
             int n = 0;
-            for (long long v = v0 + lane; v < v1; v += 32) {
-                const uint4 x = vec(v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) n += key_of(x, e, v) != 0;
-            }
+            for (long long v = v0 + lane; v < v1; v += 32) n += __popc(mask_of(vec(v), v));
             const int sum = __reduce_add_sync(0xffffffffu, n);
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&S.n_cand, min(sum, kLogpPerBlock));
-            at = __shfl_sync(0xffffffffu, at, 0);
             if (sum <= kLogpPerBlock) {
-                int incl = n;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, incl, off);
-                    if (lane >= off) incl += o;
-                }
-                at += incl - n;
-                for (long long v = v0 + lane; n > 0 && v < v1; v += 32) {
+                if (n == 0) continue;
+                int at = atomicAdd(&S.n_cand, n);
+                for (long long v = v0 + lane; v < v1; v += 32) {
                     const uint4 x = vec(v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const unsigned long long k = key_of(x, e, v);
-                        if (k != 0) S.cand[at++] = k;
-                    }
+                    for (uint32_t m8 = mask_of(x, v); m8 != 0; m8 &= m8 - 1)
+                        S.cand[at++] = key_of(x, __ffs(m8) - 1, v);
                 }
             } else {
                 // many equal ones: the block's first kLogpPerBlock, one after another
                 unsigned long long last = ~0ull;
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&S.n_cand, kLogpPerBlock);
                 for (int q = 0; q < kLogpPerBlock; ++q) {
                     unsigned long long k = 0;
                     for (long long v = v0 + lane; v < v1; v += 32) {
                         const uint4 x = vec(v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const unsigned long long z = key_of(x, e, v);
+                        for (uint32_t m8 = mask_of(x, v); m8 != 0; m8 &= m8 - 1) {
+                            const unsigned long long z = key_of(x, __ffs(m8) - 1, v);
                             if (z < last && z > k) k = z;
                         }
                     }

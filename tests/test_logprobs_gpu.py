@@ -86,6 +86,26 @@ def test_long_rows(V, rows):
     check(x, tok, 20, T=np.linspace(0.3, 1.5, B), rows=sorted(set(some)))
 
 
+@pytest.mark.parametrize("V,top", [(200, 32), (1000, 5), (3001, 20)])
+def test_many_short_rows(V, top):
+    x = logits(30, 40, V, seed=4)
+    tok = np.random.default_rng(1).integers(0, V, (30, 40))
+    check(x, tok, top, rows=[(0, 0), (7, 39), (15, 20), (29, 39), (29, 0)])
+
+
+def test_large_logits_crowded():
+    """The largest logits next to one another, so that one warp's columns hold all
+    of the first tokens, in rows of either block size."""
+    for V in (16000, 120000):
+        x = logits(1, 4, V, seed=12)
+        x[0, 0, 4096:4352] = 30.0
+        x[0, 1, 2048:2304] = torch.arange(256).float().add(20).to(torch.bfloat16)
+        for k in range(40):
+            x[0, 2, 8192 * (k % 14) // 14 * 8 % V] = 25.0
+        x[0, 3] = torch.sort(x[0, 3].float()).values.to(torch.bfloat16)
+        check(x, [[4100, 2303, 5, V - 1]], 32)
+
+
 def test_equal_logits_go_by_column():
     V = 5000
     for x in (torch.zeros((1, 2, V)), torch.full((1, 2, V), -3.0)):
