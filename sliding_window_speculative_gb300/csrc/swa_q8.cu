@@ -53,27 +53,55 @@ void set_cache(swa::AttnParams &P, const swa_paged *paged, const swa_dims *d,
     }
 }
 
-unsigned blocks_for(long long rows, int rows_per_block, int sms) {
-    const long long n = (rows + rows_per_block - 1) / rows_per_block, cap = 16LL * sms;
-    return (unsigned)(n < cap ? n : cap);
-}
-
-cudaError_t launch_append(const swa::Q8AppendParams &A, int D, int sms, cudaStream_t s) {
-    const dim3 grid(blocks_for(2 * A.rows, swa::kQ8Threads * 8 / D, sms)), block(swa::kQ8Threads);
-    switch (D) {
-        case 64: return swa::launch_kernel(swa::swa_q8_append_kernel<64>, grid, block, 0, s, A);
-        case 128: return swa::launch_kernel(swa::swa_q8_append_kernel<128>, grid, block, 0, s, A);
-        default: return swa::launch_kernel(swa::swa_q8_append_kernel<256>, grid, block, 0, s, A);
+// CTAs of U rows per group of lanes: chunks of `rows` rows for each of `units`.
+struct Shape {
+    int unroll, chunks;
+    dim3 grid;
+};
+Shape shape_of(long long units, long long rows, int D, int sms) {
+    Shape f;
+    for (f.unroll = 4;; f.unroll = 1) {
+        const int per = swa::kQ8Threads * 8 / D * f.unroll;
+        f.chunks = (int)((rows + per - 1) / per);
+        const long long ctas = units * f.chunks;
+        f.grid = dim3((unsigned)(ctas < 0x7fffffffLL ? ctas : 0x7fffffffLL));
+        // four rows at once once that still gives every SM a few CTAs
+        if (f.unroll == 1 || ctas >= 8LL * sms) return f;
     }
 }
 
-cudaError_t launch_read(const swa::Q8ReadParams &A, int D, int sms, cudaStream_t s) {
-    const dim3 grid(blocks_for(2 * A.rows, swa::kQ8Threads * 16 / D, sms)), block(swa::kQ8Threads);
-    switch (D) {
-        case 64: return swa::launch_kernel(swa::swa_q8_read_kernel<64>, grid, block, 0, s, A);
-        case 128: return swa::launch_kernel(swa::swa_q8_read_kernel<128>, grid, block, 0, s, A);
-        default: return swa::launch_kernel(swa::swa_q8_read_kernel<256>, grid, block, 0, s, A);
-    }
+template <int D, int U>
+cudaError_t append_as(const swa::Q8AppendParams &A, const Shape &f, cudaStream_t s) {
+    return swa::launch_kernel(swa::swa_q8_append_kernel<D, U>, f.grid, dim3(swa::kQ8Threads), 0, s,
+                              A);
+}
+template <int D, int U>
+cudaError_t read_as(const swa::Q8ReadParams &A, const Shape &f, cudaStream_t s) {
+    return swa::launch_kernel(swa::swa_q8_read_kernel<D, U>, f.grid, dim3(swa::kQ8Threads), 0, s, A);
+}
+
+cudaError_t launch_append(swa::Q8AppendParams &A, int D, int sms, cudaStream_t s) {
+    const Shape f = shape_of(2LL * A.cache.B, (long long)A.cache.q_len * A.cache.Hkv, D, sms);
+    A.chunks = f.chunks;
+    if (f.unroll == 1)
+        return D == 64    ? append_as<64, 1>(A, f, s)
+               : D == 128 ? append_as<128, 1>(A, f, s)
+                          : append_as<256, 1>(A, f, s);
+    return D == 64    ? append_as<64, 4>(A, f, s)
+           : D == 128 ? append_as<128, 4>(A, f, s)
+                      : append_as<256, 4>(A, f, s);
+}
+
+cudaError_t launch_read(swa::Q8ReadParams &A, int D, int sms, cudaStream_t s) {
+    const Shape f = shape_of(2LL * A.cache.B * A.cache.Hkv, A.n, D, sms);
+    A.chunks = f.chunks;
+    if (f.unroll == 1)
+        return D == 64    ? read_as<64, 1>(A, f, s)
+               : D == 128 ? read_as<128, 1>(A, f, s)
+                          : read_as<256, 1>(A, f, s);
+    return D == 64    ? read_as<64, 4>(A, f, s)
+           : D == 128 ? read_as<128, 4>(A, f, s)
+                      : read_as<256, 4>(A, f, s);
 }
 
 // The bf16 rows of every sequence's windows, [B, Hkv, span, D] for K and for V,
@@ -201,7 +229,6 @@ swa_status swa_q8_append(const void *k_new, const void *v_new, int64_t k_row, in
     set_cache(A.cache, paged, dims, seq_lens, fault);
     A.cache.q_pos = q_pos;
     A.cache.q_len = dims->q_len;
-    A.rows = (long long)dims->batch * dims->q_len * dims->num_kv_heads;
     const cudaError_t e = launch_append(A, dims->head_dim, swa::api_device_sms(dev),
                                         reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return swa::api_cuda_fail(e, "8-bit append kernel launch");
@@ -236,7 +263,6 @@ swa_status swa_q8_read(const swa_q8_cache *cache, const swa_paged *paged, const 
     set_cache(A.cache, paged, dims, seq_lens, fault);
     A.start = start;
     A.n = n;
-    A.rows = (long long)dims->batch * dims->num_kv_heads * n;
     const cudaError_t e = launch_read(A, dims->head_dim, swa::api_device_sms(dev),
                                       reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return swa::api_cuda_fail(e, "8-bit read kernel launch");
@@ -299,7 +325,6 @@ swa_status swa_q8_verify_attn(const void *q, const swa_q8_cache *cache, const sw
     A.cache.window = window;
     A.shifted = reinterpret_cast<int32_t *>(w + l.shifted);
     A.n = l.span;
-    A.rows = (long long)dims->batch * dims->num_kv_heads * l.span;
     const cudaError_t e = launch_read(A, dims->head_dim, swa::api_device_sms(dev),
                                       reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return swa::api_cuda_fail(e, "8-bit window kernel launch");

@@ -41,69 +41,99 @@ struct Q8AppendParams {
     uint8_t *dst[2];
     int8_t *exp[2];
     AttnParams cache;  // seq_lens, q_pos, q_len, Hkv, L, the block table
-    long long rows;    // batch * q_len * Hkv
+    int chunks;        // of one sequence's q_len * Hkv rows
 };
 
+// What bounds both kernels is the one read and one write of the rows.  A CTA takes
+// U rows per group of lanes from one sequence (and one of K and V), all loads in
+// flight at once; the sequence is found by one division per CTA.
+// Measured, 512 sequences of 64 tokens and 2 heads of 256 written into pages and read
+// back (202 MB): 58 us with one row at a time and its indices from 64-bit divisions.
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The largest 16-bit half over the LPR lanes of a row.  All lanes of the warp call
+// it where LPR is 32; otherwise those of whole rows.
+template <int LPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    v = max(v & 0xffffu, v >> 16);
+    if constexpr (LPR == 32) return __reduce_max_sync(0xffffffffu, v);
+    const uint32_t mask = (LPR == 16 ? 0xffffu : 0xffu) << ((threadIdx.x & 31) / LPR * LPR);
+#pragma unroll
+    for (int off = LPR / 2; off >= 1; off >>= 1) v = max(v, __shfl_xor_sync(mask, v, off));
+    return v;
+}
+
 // One row per D / 8 lanes, 8 elements each.
-template <int D>
+template <int D, int U>
 __global__ void __launch_bounds__(kQ8Threads) swa_q8_append_kernel(const Q8AppendParams A) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes per row, rows per warp
+    constexpr int LPR = D / 8, GROUPS = kQ8Threads / LPR;
     grid_dep_wait();
     grid_dep_trigger();
     const AttnParams &P = A.cache;
-    const int l = threadIdx.x % LPR, sub = (threadIdx.x % 32) / LPR;
-    const long long warp = (long long)blockIdx.x * (kQ8Threads / 32) + threadIdx.x / 32;
-    const long long step = (long long)gridDim.x * (kQ8Threads / 32) * RPW;
-    // (the trip count is the warp's: lanes past the last row take part in the
-    // shuffles with zeros)
-    for (long long r0 = warp * RPW; r0 < 2 * A.rows; r0 += step) {
-        const long long r = r0 + sub;
-        const bool there = r < 2 * A.rows;
-        const int kv = r >= A.rows;
-        const long long rr = there ? r - (kv ? A.rows : 0) : 0;
-        const long long tok = rr / P.Hkv;
-        const int h = (int)(rr - tok * P.Hkv);
-        const int b = (int)(tok / P.q_len), i = (int)(tok - (long long)b * P.q_len);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (there)
-            w = __ldg(reinterpret_cast<const uint4 *>(A.src[kv] + tok * A.row[kv] +
-                                                      (long long)h * D + l * 8));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        float x[8], a = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = bf16lo(u[e]);
-            x[2 * e + 1] = bf16hi(u[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (!(fabsf(x[e]) < __int_as_float(0x7f800000))) x[e] = __int_as_float(0x7fffffff);
-            a = fmaxf(a, fabsf(x[e]));  // (a NaN is ignored)
-        }
-#pragma unroll
-        for (int off = LPR / 2; off >= 1; off >>= 1)
-            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-        // a = 1.f 2^k: 448 = 1.75 2^8 holds it at e = k - 8 up to 1.75, else k - 7
-        const uint32_t ab = __float_as_uint(a);
-        int e = (int)(ab >> 23) - 127 - 8 + ((ab & 0x7fffffu) > 0x600000u ? 1 : 0);
-        e = e < kQ8MinExp ? kQ8MinExp : (e > kQ8MaxExp ? kQ8MaxExp : e);
-        const float sc = pow2f(-e);
-        uint32_t y[2];
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-            y[p] = (uint32_t)e4m3x2(x[4 * p] * sc, x[4 * p + 1] * sc) |
-                   ((uint32_t)e4m3x2(x[4 * p + 2] * sc, x[4 * p + 3] * sc) << 16);
-        const long long pos = (long long)P.q_pos[b] + i;
+    const int l = threadIdx.x % LPR;
+    const int n = P.q_len * P.Hkv;  // rows of a sequence: token, then head
+    for (long long c = blockIdx.x; c < 2LL * P.B * A.chunks; c += gridDim.x) {
+        // (K's and V's rows of a token are neighbours in a fused projection)
+        const int kv = (int)(c & 1);
+        const int b = (int)((c >> 1) / A.chunks);
+        const int r0 = (int)((c >> 1) - (long long)b * A.chunks) * (GROUPS * U) + threadIdx.x / LPR;
+        const long long q_pos = P.q_pos[b];
         long long end = P.seq_lens[b];
         if constexpr (kDebugChecks)
-            if (there && l == 0 && (end < 0 || end > P.L)) debug_oob(P.fault);
+            if (threadIdx.x == 0 && (end < 0 || end > P.L)) debug_oob(P.fault);
         if (end > P.L) end = P.L;
-        if (!there || pos < 0 || pos >= end) continue;
-        bool bad = false;
-        const long long row = cache_row(P, b, h, (int)pos, &bad);
-        if (bad) continue;
-        *reinterpret_cast<uint2 *>(A.dst[kv] + row * D + l * 8) = make_uint2(y[0], y[1]);
-        if (l == 0) A.exp[kv][row] = (int8_t)e;
+        uint4 w[U];
+        long long to[U];  // cache rows, -1: none
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int r = r0 + GROUPS * j, tok = r / P.Hkv, h = r - tok * P.Hkv;
+            w[j] = make_uint4(0, 0, 0, 0);
+            if (r < n)
+                w[j] = __ldcs(reinterpret_cast<const uint4 *>(
+                    A.src[kv] + ((long long)b * P.q_len + tok) * A.row[kv] + (long long)h * D +
+                    l * 8));
+            to[j] = -1;
+            const long long pos = q_pos + tok;
+            if (r < n && pos >= 0 && pos < end) {
+                bool bad = false;
+                const long long row = cache_row(P, b, h, (int)pos, &bad);
+                if (!bad) to[j] = row;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+            // the largest magnitude: a bf16's bits without the sign rise with it
+            uint32_t a = row_max<LPR>(max_u16x2(max_u16x2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu),
+                                                max_u16x2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu)));
+            if (a >= 0x7f80u) {
+                // infinities or NaN: NaN all, the largest of the others
+                uint32_t fin = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t v = (u[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+                    if (v >= 0x7f80u) u[e >> 1] |= 0x7fffu << (16 * (e & 1));
+                    else fin = max(fin, v);
+                }
+                a = row_max<LPR>(fin);
+            }
+            // a = 1.f 2^k: 448 = 1.75 2^8 holds it at e = k - 8 up to 1.75, else k - 7
+            int e = (int)(a >> 7) - 127 - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
+            e = e < kQ8MinExp ? kQ8MinExp : (e > kQ8MaxExp ? kQ8MaxExp : e);
+            const float sc = pow2f(-e);
+            uint32_t y[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                y[p] = (uint32_t)e4m3x2(bf16lo(u[2 * p]) * sc, bf16hi(u[2 * p]) * sc) |
+                       ((uint32_t)e4m3x2(bf16lo(u[2 * p + 1]) * sc, bf16hi(u[2 * p + 1]) * sc) << 16);
+            if (to[j] < 0) continue;
+            *reinterpret_cast<uint2 *>(A.dst[kv] + to[j] * D + l * 8) = make_uint2(y[0], y[1]);
+            if (l == 0) A.exp[kv][to[j]] = (int8_t)e;
+        }
     }
 }
 
@@ -114,8 +144,7 @@ struct Q8ReadParams {
     AttnParams cache;       // seq_lens, Hkv, L, the block table
     const int32_t *start;   // first position of each sequence; NULL: that of its window
     int32_t *shifted;       // (start NULL) [2][B]: lengths and q_pos counted from there
-    int n;
-    long long rows;         // batch * Hkv * n
+    int n, chunks;          // positions per sequence; chunks of them
 };
 
 // First position of a sequence's windows, in [0, L].
@@ -124,15 +153,14 @@ __device__ __forceinline__ int q8_window_start(const AttnParams &P, int b) {
     return (int)(lo < 0 ? 0 : (lo > P.L ? P.L : lo));
 }
 
-// One row per D / 16 lanes, 16 elements each.
-template <int D>
+// One row per D / 8 lanes, 8 elements each.
+template <int D, int U>
 __global__ void __launch_bounds__(kQ8Threads) swa_q8_read_kernel(const Q8ReadParams A) {
-    constexpr int LPR = D / 16;
+    constexpr int LPR = D / 8, GROUPS = kQ8Threads / LPR;
     grid_dep_wait();
     grid_dep_trigger();
     const AttnParams &P = A.cache;
     const int l = threadIdx.x % LPR;
-    const long long step = (long long)gridDim.x * (kQ8Threads / LPR);
     if (A.start == nullptr) {
         for (long long b = (long long)blockIdx.x * kQ8Threads + threadIdx.x; b < P.B;
              b += (long long)gridDim.x * kQ8Threads) {
@@ -142,35 +170,48 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_read_kernel(const Q8ReadPar
             A.shifted[P.B + b] = (int)max((long long)P.q_pos[b] - lo, -(1LL << 31));
         }
     }
-    for (long long r = (long long)blockIdx.x * (kQ8Threads / LPR) + threadIdx.x / LPR;
-         r < 2 * A.rows; r += step) {
-        const int kv = r >= A.rows;
-        const long long rr = r - (kv ? A.rows : 0);
-        const long long unit = rr / A.n;
-        const int i = (int)(rr - unit * A.n);
+    const long long units = (long long)P.B * P.Hkv;
+    for (long long c = blockIdx.x; c < 2 * units * A.chunks; c += gridDim.x) {
+        const long long uk = c / A.chunks;
+        const int i0 = (int)(c - uk * A.chunks) * (GROUPS * U) + threadIdx.x / LPR;
+        const int kv = uk >= units;
+        const long long unit = uk - (kv ? units : 0);
         const int b = (int)(unit / P.Hkv), h = (int)(unit - (long long)b * P.Hkv);
-        const long long pos = (A.start ? (long long)A.start[b] : q8_window_start(P, b)) + i;
+        const long long first = A.start ? (long long)A.start[b] : q8_window_start(P, b);
         long long end = P.seq_lens[b];
         if constexpr (kDebugChecks)
-            if (l == 0 && (end < 0 || end > P.L)) debug_oob(P.fault);
+            if (threadIdx.x == 0 && (end < 0 || end > P.L)) debug_oob(P.fault);
         if (end > P.L) end = P.L;
-        uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (pos >= 0 && pos < end) {
-            const long long row = cache_row(P, b, h, (int)pos);
-            const uint4 w = *reinterpret_cast<const uint4 *>(A.src[kv] + row * D + l * 16);
-            int e = A.exp[kv][row];
-            const float sc = pow2f(e < -126 ? -126 : e);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint2 w[U];
+        int e[U];
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
+        for (int j = 0; j < U; ++j) {
+            const int i = i0 + GROUPS * j;
+            const long long pos = first + i;
+            w[j] = make_uint2(0, 0);
+            e[j] = 0;
+            if (i < A.n && pos >= 0 && pos < end) {
+                const long long row = cache_row(P, b, h, (int)pos);
+                w[j] = __ldcs(reinterpret_cast<const uint2 *>(A.src[kv] + row * D + l * 8));
+                e[j] = A.exp[kv][row];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int i = i0 + GROUPS * j;
+            if (i >= A.n) break;
+            const float sc = pow2f(e[j] < -126 ? -126 : e[j]);
+            const uint32_t u[2] = {w[j].x, w[j].y};
+            uint32_t o[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
                 const uint32_t f = e4m3x2_to_f16x2((uint16_t)(u[p >> 1] >> (16 * (p & 1))));
                 const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&f));
                 o[p] = pack_bf16x2(x.x * sc, x.y * sc);
             }
+            *reinterpret_cast<uint4 *>(A.dst[kv] + (unit * A.n + i) * D + l * 8) =
+                make_uint4(o[0], o[1], o[2], o[3]);
         }
-        uint4 *d = reinterpret_cast<uint4 *>(A.dst[kv] + rr * D + l * 16);
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
