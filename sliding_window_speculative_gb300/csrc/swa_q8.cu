@@ -123,19 +123,88 @@ RowsLayout rows_layout(const swa_dims *d, int32_t window) {
     return l;
 }
 
-// Whether a call runs on the fp8 tensor cores straight from the cache: the
-// shapes the key-major kernel takes, unless another kernel is forced.
-bool direct(const swa_dims *d, const swa_paged *paged, int32_t window, int dev, swa::TcPlan *plan) {
+// The fp8 tensor-core kernel's work of a call: items of `rows` packed rows and
+// `splits` chunks of `chunk` keys per (sequence, KV head).
+struct Plan {
+    int rows, q_rows, row_tiles, n, splits, chunk, grid;
+    long long items;
+    size_t workspace;
+};
+
+constexpr int kTileKeys = 128;
+constexpr int kMaxSplits = 64;
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// False where that kernel does not take the shape.
+bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
+    const int G = d->num_q_heads / d->num_kv_heads, D = d->head_dim;
+    const int R = d->q_len * G;
+    if ((D != 128 && D != 256) || G > 32 ||
+        (long long)d->batch * d->num_kv_heads * d->max_len >= (1LL << 31) ||
+        (long long)d->batch * d->q_len * d->num_q_heads >= (1LL << 31) ||
+        (long long)d->batch * d->num_kv_heads * d->q_len * kMaxSplits >= (1LL << 31))
+        return false;
+    Plan p;
+    auto rows_of = [&](int r) {
+        p.rows = r >= R ? R : (r < G ? G : r / G * G);
+        p.q_rows = p.rows / G;
+        p.row_tiles = ceil_div(d->q_len, p.q_rows);
+    };
+    rows_of(32);
+    long long span = (long long)window + d->q_len - 1;
+    if (span > d->max_len) span = d->max_len;
+    long long item = (long long)window + p.q_rows - 1;  // keys of an item without a split
+    if (item > span) item = span;
+    const long long units = (long long)d->batch * d->num_kv_heads * p.row_tiles;
+    long long chunk = span;
+    if (d->num_splits > 0) {
+        const int n = d->num_splits < kMaxSplits ? d->num_splits : kMaxSplits;
+        chunk = (span + n - 1) / n;
+    } else if (units < sms && item > 3 * kTileKeys) {
+        // as many items as the SMs' pipelines (two each) take at once, whole tiles
+        // each; up to three tiles a split costs more (partials, a merge) than it wins
+        long long n = 2LL * sms / units;
+        if (n > (item + kTileKeys - 1) / kTileKeys) n = (item + kTileKeys - 1) / kTileKeys;
+        chunk = (item + n - 1) / n;
+        chunk = (chunk + kTileKeys - 1) / kTileKeys * kTileKeys;
+        if ((span + chunk - 1) / chunk > kMaxSplits) chunk = (span + kMaxSplits - 1) / kMaxSplits;
+    }
+    p.chunk = (int)chunk;
+    p.splits = ceil_div(span, chunk);
+    if (d->num_splits == 0) {
+        // fewer rows per item while many SMs would stay idle
+        const long long per_unit = (long long)d->batch * d->num_kv_heads * p.splits;
+        for (int r : {8, 16}) {
+            const int rows = r < G ? G : r / G * G;
+            if (rows >= p.rows) break;
+            const long long n = per_unit * ceil_div(d->q_len, rows / G);
+            if (r == 8 ? n * 16 <= sms : n * 5 <= 3LL * sms) {
+                rows_of(r);
+                break;
+            }
+        }
+    }
+    p.n = p.rows <= 16 ? 16 : 32;
+    p.items = (long long)p.splits * d->batch * d->num_kv_heads * p.row_tiles;
+    p.grid = (int)(p.items < sms ? p.items : sms);
+    p.workspace = p.splits > 1 ? (size_t)d->batch * d->num_kv_heads * p.splits * R * (D + 2) * 4 : 0;
+    *out = p;
+    return true;
+}
+
+// Whether a call runs on the fp8 tensor cores straight from the cache, unless a
+// kernel is forced (2: that one; others: bf16 rows and that kernel over them).
+bool direct(const swa_dims *d, int32_t window, int sms, Plan *plan) {
     const int force = swa::api_forced_kernel();
     if (force != 0 && force != 2) return false;
-    (void)paged;
-    return swa::api_tc_plan(d, window, dev, plan);
+    return plan_direct(d, window, sms, plan);
 }
 
 swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
                          const int32_t *seq_lens, const int32_t *q_pos, int32_t window,
                          float scale, void *out, float *lse, const swa_dims *d,
-                         const swa::TcPlan &pl, int dev, uint32_t *fault, cudaStream_t s) {
+                         const Plan &pl, int dev, uint32_t *fault, cudaStream_t s) {
     swa::Q8TcLaunch L{};
     swa::AttnParams &P = L.T.a;
     set_cache(P, paged, d, seq_lens, fault);
@@ -151,23 +220,22 @@ swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_pag
     P.splits = pl.splits;
     P.chunk = pl.chunk;
     P.row_tiles = pl.row_tiles;
-    P.rows_per_tile = pl.rows_per_tile;
+    P.rows_per_tile = pl.rows;
     P.qk_scale = scale * swa::kLog2e;
     P.wait_limit = swa::api_wait_limit();
     P.withhold_fill = swa::api_withhold_fill();
     if (pl.splits > 1) {
         void *ws = nullptr;
-        const swa_status st = swa::api_workspace(dev, (size_t)pl.workspace, s, &ws);
+        const swa_status st = swa::api_workspace(dev, pl.workspace, s, &ws);
         if (st != SWA_OK) return st;
         P.part_acc = static_cast<float *>(ws);
         P.part_ml = P.part_acc + (size_t)P.B * P.Hkv * P.splits * P.R * d->head_dim;
     }
-    L.T.rows_per_tile = pl.rows_per_tile;
-    L.T.q_rows_per_tile = pl.q_rows_per_tile;
+    L.T.rows_per_tile = pl.rows;
+    L.T.q_rows_per_tile = pl.q_rows;
     L.T.items = (int)pl.items;
     L.T.items_per_cta = (int)(pl.items / pl.grid);
     L.T.items_extra = (int)(pl.items % pl.grid);
-    L.T.early_max = pl.grid * 2 >= pl.sms ? 1 : 8;
     L.k_exp = cache->k_exp;
     L.v_exp = cache->v_exp;
     L.k = cache->k;
@@ -300,8 +368,8 @@ swa_status swa_q8_verify_attn(const void *q, const swa_q8_cache *cache, const sw
     st = swa::api_device(&dev, &fault);
     if (st != SWA_OK) return st;
 
-    swa::TcPlan plan;
-    if (direct(dims, paged, window, dev, &plan))
+    Plan plan;
+    if (direct(dims, window, swa::api_device_sms(dev), &plan))
         return attend_direct(q, cache, paged, seq_lens, q_pos, window, scale, out, lse, dims, plan,
                              dev, fault, reinterpret_cast<cudaStream_t>(stream));
 

@@ -55,11 +55,12 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t max_u16x2_half(uint32_t v) { return max(v & 0xffffu, v >> 16); }
 // The largest 16-bit half over the LPR lanes of a row.  All lanes of the warp call
 // it where LPR is 32; otherwise those of whole rows.
 template <int LPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
-    v = max(v & 0xffffu, v >> 16);
+    v = max_u16x2_half(v);
     if constexpr (LPR == 32) return __reduce_max_sync(0xffffffffu, v);
     const uint32_t mask = (LPR == 16 ? 0xffffu : 0xffu) << ((threadIdx.x & 31) / LPR * LPR);
 #pragma unroll

@@ -13,23 +13,14 @@
 namespace swa {
 namespace {
 
-// Numbers per weight, ring slots and Q / P / O buffers per (head_dim, padded
-// rows), within one CTA's 227 KB of shared memory and an SM's 512 TMEM columns.
-template <int D, int N>
-struct Q8Conf {
-    static constexpr int NP = D == 256 && N == 64 ? 2 : 3;
-    static constexpr int NT = D == 256 ? (N == 64 ? 3 : 5) : (N == 64 ? 7 : 8);
-    static constexpr int QB = D == 256 && N >= 32 ? 1 : 2;
-    static constexpr int PB = 2;
-    static constexpr int OB = N == 64 ? 1 : 2;
-    using C = Q8Cfg<D, N, NP, NT, QB, PB, OB>;
-};
+// K (and V) tiles per pipeline, within one CTA's 227 KB of shared memory.
+template <int D>
+constexpr int kRing = D == 256 ? 1 : 2;
 
 template <int D, int N>
 cudaError_t launch(const Q8TcParams &A, const TcMaps &maps, int grid, cudaStream_t stream) {
-    using Cf = Q8Conf<D, N>;
-    using C = typename Cf::C;
-    auto kern = swa_q8_tc_kernel<D, N, Cf::NP, Cf::NT, Cf::QB, Cf::PB, Cf::OB>;
+    using C = Q8Cfg<D, N, kRing<D>>;
+    auto kern = swa_q8_tc_kernel<D, N, kRing<D>>;
     static std::atomic<bool> attr_done[kMaxDevices];
     const cudaError_t e = raise_smem_limit(kern, C::SMEM_BYTES, attr_done);
     if (e != cudaSuccess) return e;
@@ -41,7 +32,6 @@ cudaError_t launch_n(const Q8TcParams &A, const TcMaps &maps, int n, int grid, c
     switch (n) {
         case 16: return launch<D, 16>(A, maps, grid, s);
         case 32: return launch<D, 32>(A, maps, grid, s);
-        case 64: return launch<D, 64>(A, maps, grid, s);
         default: return cudaErrorInvalidConfiguration;
     }
 }
