@@ -126,7 +126,7 @@ RowsLayout rows_layout(const swa_dims *d, int32_t window) {
 // The fp8 tensor-core kernel's work of a call: items of `rows` packed rows and
 // `splits` chunks of `chunk` keys per (sequence, KV head).
 struct Plan {
-    int rows, q_rows, row_tiles, n, splits, chunk, grid;
+    int rows, q_rows, row_tiles, n, splits, chunk, grid, early;
     long long items;
     size_t workspace;
 };
@@ -162,9 +162,9 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
         const int n = d->num_splits < kMaxSplits ? d->num_splits : kMaxSplits;
         chunk = (span + n - 1) / n;
     } else if (units < sms && item > 3 * kTileKeys) {
-        // as many items as the SMs' pipelines (two each) take at once, whole tiles
-        // each; up to three tiles a split costs more (partials, a merge) than it wins
-        long long n = 2LL * sms / units;
+        // as many items as SMs, whole tiles each; up to three tiles a split costs more
+        // (partials, a merge) than it wins
+        long long n = sms / units;
         if (n > (item + kTileKeys - 1) / kTileKeys) n = (item + kTileKeys - 1) / kTileKeys;
         chunk = (item + n - 1) / n;
         chunk = (chunk + kTileKeys - 1) / kTileKeys * kTileKeys;
@@ -188,6 +188,8 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     p.n = p.rows <= 16 ? 16 : 32;
     p.items = (long long)p.splits * d->batch * d->num_kv_heads * p.row_tiles;
     p.grid = (int)(p.items < sms ? p.items : sms);
+    // (once every SM loads at once the first K tile should land first)
+    p.early = p.grid * 2 >= sms ? 1 : 8;
     p.workspace = p.splits > 1 ? (size_t)d->batch * d->num_kv_heads * p.splits * R * (D + 2) * 4 : 0;
     *out = p;
     return true;
@@ -236,6 +238,7 @@ swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_pag
     L.T.items = (int)pl.items;
     L.T.items_per_cta = (int)(pl.items / pl.grid);
     L.T.items_extra = (int)(pl.items % pl.grid);
+    L.T.early_max = pl.early;
     L.k_exp = cache->k_exp;
     L.v_exp = cache->v_exp;
     L.k = cache->k;

@@ -13,14 +13,19 @@
 namespace swa {
 namespace {
 
-// K (and V) tiles per pipeline, within one CTA's 227 KB of shared memory.
-template <int D>
-constexpr int kRing = D == 256 ? 1 : 2;
+// Ring slots and query buffers per (head_dim, padded rows), within one CTA's 227 KB
+// of shared memory.
+template <int D, int N>
+struct Q8Conf {
+    static constexpr int NT = D == 256 ? 5 : 10;
+    static constexpr int QB = D == 256 && N == 32 ? 1 : 2;
+};
 
 template <int D, int N>
 cudaError_t launch(const Q8TcParams &A, const TcMaps &maps, int grid, cudaStream_t stream) {
-    using C = Q8Cfg<D, N, kRing<D>>;
-    auto kern = swa_q8_tc_kernel<D, N, kRing<D>>;
+    using Cf = Q8Conf<D, N>;
+    using C = Q8Cfg<D, N, Cf::NT, Cf::QB>;
+    auto kern = swa_q8_tc_kernel<D, N, Cf::NT, Cf::QB>;
     static std::atomic<bool> attr_done[kMaxDevices];
     const cudaError_t e = raise_smem_limit(kern, C::SMEM_BYTES, attr_done);
     if (e != cudaSuccess) return e;

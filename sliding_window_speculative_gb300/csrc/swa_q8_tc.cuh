@@ -1,8 +1,8 @@
 // Windowed verify attention over the 8-bit cache on the fp8 tensor cores
 // (tcgen05 kind::f8f6f4), the e4m3 rows fed to them as they lie in the cache.
 //
-// As in the bf16 key-major kernel keys are the MMA's M dimension; per tile of 128
-// keys
+// The structure is that of the bf16 key-major kernel: persistent CTAs, keys as
+// the MMA's M dimension, K and V tiles of 128 keys by TMA into a ring,
 //
 //   S^T[128 keys x 2N] = K8_tile[128 x D] . [Q_hi; Q_lo][2N x D]^T
 //   O^T[D x 3N]       += V8_tile^T[D x 128] . [P_0; P_1; P_2][3N x 128]^T
@@ -28,16 +28,23 @@
 // u: weights are resolved relative to what they contribute to the result, so a
 // heavy key of small values does not push the others below the format's range.
 //
-// A CTA runs two pipelines, each taking every other of the CTA's items on its own
-// from the first copy to the output, so that what one waits for (a tile, the
-// tensor core, its own epilogue) is the other's time.  Per pipeline:
-//   loader     one warp: K and V tiles by TMA
-//   issuer     one warp: the MMAs
-//   softmax    four warps, a thread per key, all N rows of the item each: query rows
-//              into their two numbers, softmax, epilogue
-// (384 threads.)  Measured, 512 sequences of 8 rows, windows 188 / 1024: one
-// pipeline whose rows were split between two warpgroups took 52 / 125-131 us; waits
-// on one another and instruction fetches were most of it.
+// What bounds it beside the cache's bytes is the instruction caches: sixteen warps
+// of five roles run different code, and a warp that runs straight through code that
+// the nearest cache (some hundred instructions for four warps) does not hold waits
+// for every line of it.  Unrolled, the kernel issued an instruction in 30% of its
+// cycles and a single MMA took 100 cycles to issue; so the loops over rows stay
+// rolled, eight rows a turn.
+//
+// Warp roles (512 threads; the registers of the first and last warpgroup that
+// they do not need go to the softmax):
+//   warp 0       TMA producer
+//   warp 1       TMEM owner, issuer of the scores' MMAs
+//   warp 2       issuer of the MMAs into O
+//   warp 3       the keys' factors: a ring of tables, a few tiles ahead
+//   warps 4..11  softmax, two warpgroups that split the packed rows
+//   warps 12..15 query rows split into their two numbers, one item ahead, and
+//                the epilogue of the item before: O is double-buffered, so the
+//                softmax goes on with the next item meanwhile
 //
 // Every wait is bounded; one that gives up sets the fault word and a flag that
 // ends all other waits of the CTA, whose roles then run through their loops.
@@ -48,13 +55,13 @@
 
 namespace swa {
 
-constexpr int kQ8TcThreads = 384;
-constexpr int kQ8Meta = 16;         // items per CTA decoded once into shared memory
+constexpr int kQ8TcThreads = 512;
+constexpr int kQ8Tabs = 4;          // tables of key factors
 constexpr float kQ8QLo = 16.f;      // scale of Q_lo
 constexpr float kQ8P1 = 56.f;       // scale of P_1, and of P_2 beside it
 constexpr float kQ8P2 = 16.f;
 // The reference maximum of a row sits this far (log2) below the largest u of the
-// tile that set it, and P stays at most 2^8: a later tile may exceed that u by 2^6
+// tiles that set it, and P stays at most 2^8: a later tile may exceed that u by 2^6
 // before the references are raised.  A lower one would cost the small weights'
 // resolution: half a smallest step of P_2, 2^-10 / 56 / 16, is to be within 2^-21 of
 // the largest weight.
@@ -66,7 +73,7 @@ struct Q8TcParams {
     const int8_t *k_exp, *v_exp;
 };
 
-template <int D, int N, int NK>
+template <int D, int N, int NT, int QB>
 struct Q8Cfg {
     static constexpr int SLABS = D / 128;
     static constexpr int ATOM_BYTES = SLABS * 1024;  // 8 keys x D
@@ -77,38 +84,46 @@ struct Q8Cfg {
     // N columns of P_0, then of P_1 and P_2
     static constexpr int P_BLOCK = kTcTileKeys * 32;
     static constexpr int P_BUF = ((3 * N + 31) / 32) * P_BLOCK;
-    // one pipeline's part
-    static constexpr int K_OFF = 0;                   // NK tiles
-    static constexpr int V_OFF = K_OFF + NK * TILE_BYTES;
-    static constexpr int Q_OFF = V_OFF + NK * TILE_BYTES;
-    static constexpr int RAW_OFF = Q_OFF + Q_BUF;     // bf16 [N][D]: the next item's queries
+    static constexpr int RING_OFF = 0;
+    static constexpr int Q_OFF = RING_OFF + NT * TILE_BYTES;
+    static constexpr int RAW_OFF = Q_OFF + QB * Q_BUF;  // bf16 [N][D]: the next item's queries
     static constexpr int P_OFF = RAW_OFF + N * D * 2;
-    static constexpr int RED_OFF = P_OFF + P_BUF;     // float [4][N]: per warp maxima, sums
-    static constexpr int REF_OFF = RED_OFF + 4 * N * 4;   // float [N] references
-    static constexpr int QSC_OFF = REF_OFF + N * 4;       // float [2][N] query scales
-    static constexpr int ALPHA_OFF = QSC_OFF + 2 * N * 4; // float [N]: rescale factors, 1 / l
-    static constexpr int ROW_OFF = ALPHA_OFF + N * 4;     // uint32 [N] output rows
-    static constexpr int PIPE = (ROW_OFF + N * 4 + 1023) / 1024 * 1024;
-    // the CTA's
-    static constexpr int META_OFF = 2 * PIPE;         // TcItem [kQ8Meta]
-    static constexpr int BAR_OFF = (META_OFF + kQ8Meta * (int)sizeof(TcItem) + 7) / 8 * 8;
-    // per pipeline
-    static constexpr int B_KFULL = 0, B_KEMPTY = NK, B_VFULL = 2 * NK, B_VEMPTY = 3 * NK,
-                         B_QFULL = 4 * NK, B_SFULL = B_QFULL + 1, B_SFREE = B_SFULL + 1,
-                         B_PFULL = B_SFREE + 1, B_PVDONE = B_PFULL + 1, B_DRAIN = B_PVDONE + 1,
-                         NBARS = B_DRAIN + 1;
-    static constexpr int MISC_OFF = BAR_OFF + 2 * NBARS * 8;  // tmem base, failed
-    static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
+    static constexpr int TAB_OFF = P_OFF + 2 * P_BUF;                // float2 [kQ8Tabs][128]
+    static constexpr int RED_OFF = TAB_OFF + kQ8Tabs * kTcTileKeys * 8;  // float [4][N]
+    static constexpr int REF_OFF = RED_OFF + 4 * N * 4;              // float [N] references
+    static constexpr int ALPHA_OFF = REF_OFF + N * 4;                // float [N]
+    static constexpr int QSC_OFF = ALPHA_OFF + N * 4;                // float [2][N] query scales
+    // float [4][5][N]: per item, a row's sums over each warp's keys, its reference
+    static constexpr int SUM_OFF = QSC_OFF + 2 * N * 4;
+    static constexpr int LINV_OFF = SUM_OFF + 4 * 5 * N * 4;         // float [2][N]
+    static constexpr int ROW_OFF = LINV_OFF + 2 * N * 4;             // uint32 [2][N] output rows
+    static constexpr int META_OFF = ROW_OFF + 2 * N * 4;             // TcItem [kTcMetaItems]
+    static constexpr int FTAB_OFF = META_OFF + kTcMetaItems * (int)sizeof(TcItem);
+    static constexpr int BAR_OFF = (FTAB_OFF + kFillTab * 4 + 7) / 8 * 8;
+    static constexpr int B_FULL = 0, B_EMPTY = NT, B_QFULL = 2 * NT, B_QEMPTY = B_QFULL + QB,
+                         B_SFULL = B_QEMPTY + QB, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
+                         B_PVDONE = B_PFULL + 2, B_OFULL = B_PVDONE + 2, B_OFREE = B_OFULL + 2,
+                         B_LFULL = B_OFREE + 2, B_DRAIN = B_LFULL + 4, B_TFULL = B_DRAIN + 2,
+                         B_TEMPTY = B_TFULL + kQ8Tabs, NBARS = B_TEMPTY + kQ8Tabs;
+    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // tmem base, failed
+    static constexpr int END = MISC_OFF + 16;
+    static constexpr int SMEM_BYTES = END + 1024;
     static constexpr int O_HALF = 3 * N;              // O^T columns of 128 dims
-    static constexpr int O_COL = 2 * N;               // behind the S^T buffer
-    static constexpr int PIPE_COLS = O_COL + (D / 128) * O_HALF;
-    static constexpr int TMEM_COLS = 2 * PIPE_COLS <= 128   ? 128
-                                     : 2 * PIPE_COLS <= 256 ? 256
-                                                            : 512;
+    static constexpr int O_COLS = (D / 128) * O_HALF;
+    static constexpr int S_COLS = 2 * N;              // one tile's S^T: hi and lo halves
+    static constexpr int O_COL = 2 * S_COLS;
+    static constexpr int TMEM_USED = O_COL + 2 * O_COLS;
+    static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
+    // registers per thread: the launch's 128, shifted to the softmax
+    static constexpr int SOFT_REGS = 160, OTHER_REGS = 256 - SOFT_REGS;
     static_assert(N == 16 || N == 32, "rows per item");
-    static_assert(2 * PIPE_COLS <= 512, "TMEM");
+    // (K tiles are multiplied up to four ahead of the oldest V tile: their fills
+    // entries are behind it in the table, their slots refilled)
+    static_assert(NT >= 2 && NT + 5 <= kFillTab, "ring slots");
+    static_assert(TMEM_USED <= 512, "TMEM");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-    static_assert(Q_OFF % 1024 == 0 && P_OFF % 1024 == 0 && RED_OFF % 16 == 0, "alignment");
+    static_assert(Q_OFF % 1024 == 0 && P_OFF % 1024 == 0, "operand alignment");
+    static_assert(RED_OFF % 16 == 0 && META_OFF % 8 == 0, "alignment");
 };
 
 // Output (and query) row of an item's packed row r: draft row r / G of head
@@ -139,14 +154,25 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn, in
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, K = 32, single issuing thread.
-__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[smem] * B[smem]^T, K = 32, issued by the lane whose `lead` is set.
+// (All lanes come here: the operands are then uniform registers without a move for
+// each.)
+__device__ __forceinline__ void mma_e4m3_ss(bool lead, uint32_t d_tmem, uint64_t a_desc,
+                                            uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_by(bool lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar)), "r"((uint32_t)lead)
         : "memory");
 }
 
@@ -181,11 +207,60 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// The hot code has to stay in the instruction caches beside that of 11 other warps
-// (with everything inlined an earlier form was 187 KB, and warps waited 26% of
-// their time for instructions): what is rare is a function of its own.
+// The kernel's hot code has to stay in the instruction caches beside that of 15
+// other warps (with everything inlined it was 187 KB, and warps waited 26% of
+// their time for instructions): what is rare, or run by several roles, is a
+// function of its own.
+__device__ __noinline__ void q8_wait_on(uint64_t *bar, uint32_t parity, const AttnParams *P,
+                                        volatile uint32_t *failed) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*failed) return;
+        if (clock64() - t0 > P->wait_limit) {
+            atomicOr(P->fault, kFaultCopyTimeout);
+            *failed = 1;
+            return;
+        }
+    }
+}
+
+// Waits for phase `parity` of `bar`, or until some wait of the CTA gave up.
+__device__ __forceinline__ void q8_wait(uint64_t *bar, uint32_t parity, const AttnParams &P,
+                                        volatile uint32_t *failed) {
+    if (!mbar_try_wait(bar, parity)) q8_wait_on(bar, parity, &P, failed);
+}
+
+// The same without a call, for the softmax: its registers are its rows.
+__device__ __forceinline__ void q8_wait_here(uint64_t *bar, uint32_t parity, const AttnParams &P,
+                                             volatile uint32_t *failed) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint32_t t0 = (uint32_t)(clock64() >> 10);
+    while (!mbar_try_wait(bar, parity)) {
+        if (*failed) return;
+        if ((uint32_t)(clock64() >> 10) - t0 > (uint32_t)(P.wait_limit >> 10)) {
+            atomicOr(P.fault, kFaultCopyTimeout);
+            *failed = 1;
+            return;
+        }
+    }
+}
+
+// The warp's arrival once all its lanes are here (32 arrivals on one barrier would
+// be served one after another).
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// The j-th item of this CTA: the first kTcMetaItems from shared memory.
 __device__ __noinline__ void q8_decode(const TcParams *T, int j, TcItem *it) {
     *it = tc_decode_global<false>(*T, cta_item(*T, j));
+}
+__device__ __forceinline__ TcItem q8_item(const TcParams &T, int j, const TcItem *meta) {
+    if (j < kTcMetaItems) return meta[j];
+    TcItem it;
+    q8_decode(&T, j, &it);
+    return it;
 }
 
 // One lane's copies of a K or V tile: `whole` atoms of consecutive cache rows
@@ -196,305 +271,233 @@ __device__ __noinline__ void q8_copy(const CUtensorMap *m4, const CUtensorMap *m
     atom_run<C::ATOM_BYTES>(m4, m1, y, whole, partial, dst, bar, policy);
 }
 
-// The warp's arrival once all its lanes are here (32 arrivals on one barrier would
-// be served one after another).
-__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-// Lane 0 waits for phase `parity` of `bar`, or until some wait of the CTA gave up;
-// the warp goes on together.
-__device__ __forceinline__ void q8_wait(uint64_t *bar, uint32_t parity, const AttnParams &P,
-                                        volatile uint32_t *failed) {
-    if ((threadIdx.x & 31) == 0 && !mbar_try_wait(bar, parity)) {
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar, parity) && *failed == 0) {
-            if (clock64() - t0 > P.wait_limit) {
-                atomicOr(P.fault, kFaultCopyTimeout);
-                *failed = 1;
-            }
-        }
-    }
-    __syncwarp();
-}
-
-// A polling loop's patience: false once it ran `limit` cycles without progress, or
-// another wait gave up.
-struct Q8Patience {
-    long long since = 0;
-    int idle = 0;
-    __device__ __forceinline__ bool more(const AttnParams &P, volatile uint32_t *failed) {
-        if ((++idle & 63) != 0) return true;
-        const long long now = clock64();
-        if (idle == 64) since = now;
-        if (now - since > P.wait_limit) {
-            atomicOr(P.fault, kFaultCopyTimeout);
-            *failed = 1;
-        }
-        return __any_sync(0xffffffffu, *failed != 0) == 0;
-    }
-};
-
-// A walk over the tiles of a pipeline's items: every second of the CTA's.
-struct Q8Cursor {
-    int j, t;
-    uint32_t g;   // tiles so far
+// Fills 0 .. early_fills - 1 of the CTA's first item, one from each of the first
+// warps' lane 0, ahead of the producer (a contiguous cache; see swa_tc.cuh).
+template <class C, int NT>
+__device__ __forceinline__ void q8_early_fills(const TcParams &T, const TcMaps &M,
+                                               volatile uint32_t *ftab, uint8_t *ring,
+                                               uint64_t *bars, int warp) {
+    const AttnParams &P = T.a;
+    if (P.block_table != nullptr || warp >= NT || cta_items(T) < 1) return;
     TcItem it;
-    bool valid;
-    __device__ __forceinline__ void seek(const TcParams &T, const TcItem *meta, int n_items) {
-        t = 0;
-        for (valid = false; j < n_items; j += 2) {
-            if (j < kQ8Meta && meta != nullptr) it = meta[j];
-            else q8_decode(&T, j, &it);
-            if (it.n_tiles > 0) {
-                valid = true;
-                return;
-            }
-        }
-    }
-    __device__ __forceinline__ void next(const TcParams &T, const TcItem *meta, int n_items) {
-        ++g;
-        if (++t < it.n_tiles) return;
-        j += 2;
-        seek(T, meta, n_items);
-    }
-};
+    q8_decode(&T, 0, &it);
+    if (warp >= early_fills<NT, false>(T, it)) return;
+    const int t = warp >> 1, kv = warp & 1;  // K, V, K, V, ...
+    const int p = it.t0 + kTcTileKeys * t;
+    const int n = min(kTcTileKeys, it.cr.c_hi - p);
+    ftab[warp] = ((uint32_t)warp << 8) | (uint32_t)warp;  // fill w -> slot w, use parity 0
+    mbar_arrive_expect_tx(&bars[C::B_FULL + warp], (uint32_t)((n + 7) >> 3) * C::ATOM_BYTES);
+    if (P.withhold_fill == warp && blockIdx.x == 0) return;
+    q8_copy<C>(kv ? M.v_atoms : M.k_atoms, kv ? &M.v_atom : &M.k_atom,
+               (int)(((long long)it.b * P.Hkv + it.h) * P.L + p), n >> 3, (n & 7) != 0,
+               ring + warp * C::TILE_BYTES, &bars[C::B_FULL + warp],
+               P.row_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first());
+}
 
-// Loader of pipeline p: K and V tiles into their rings, each as soon as its slot is
-// free.  A contiguous cache's tile is copied by lane 0; a paged one's runs of pages
-// by a lane each, the page ids read a tile ahead.  begin() issues the first tiles,
-// before the CTA's items are decoded for all roles; run() the rest, and waits for
-// every copy.
-template <class C, int NK>
-struct Q8Loader {
-    const TcParams &T;
-    const TcMaps &M;
-    uint8_t *pipe;
-    uint64_t *bars;
-    volatile uint32_t *failed;
-    Q8Cursor c[2];  // K, V
-    int page[2];
-    int n_items, lane, p;
-
-    __device__ __forceinline__ int first_atom(const TcItem &it, int t) const {
-        const int ps = T.a.page_size, at = it.t0 + kTcTileKeys * t;
-        return lane == 0 ? 0 : ((ps - at % ps) >> 3) + (lane - 1) * (ps >> 3);
-    }
-    __device__ __forceinline__ void prefetch(int kv) {
-        const AttnParams &P = T.a;
-        if (P.block_table == nullptr || !c[kv].valid) return;
-        const TcItem &it = c[kv].it;
-        const int at = it.t0 + kTcTileKeys * c[kv].t;
-        if (8 * first_atom(it, c[kv].t) < min(kTcTileKeys, it.cr.c_hi - at))
-            page[kv] = __ldg(P.block_table + (long long)it.b * P.max_blocks + at / P.page_size + lane);
-    }
-    __device__ __noinline__ void fill(int kv, const TcItem *meta) {
-        using namespace tc;
-        const AttnParams &P = T.a;
-        const TcItem &it = c[kv].it;
-        const int at = it.t0 + kTcTileKeys * c[kv].t;
-        const int n = min(kTcTileKeys, it.cr.c_hi - at), natoms = (n + 7) >> 3;
-        const uint32_t slot = c[kv].g % NK;
-        uint64_t *bar = &bars[(kv ? C::B_VFULL : C::B_KFULL) + slot];
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)natoms * C::ATOM_BYTES);
-        __syncwarp();
-        int a = 0, run = lane == 0 ? natoms : 0, y;
-        if (P.block_table != nullptr) {
-            const int ps = P.page_size, in = at % ps;
-            a = first_atom(it, c[kv].t);
-            run = min(lane == 0 ? (ps - in) >> 3 : ps >> 3, natoms - a);
-            y = (checked_page(P, page[kv], nullptr) * P.Hkv + it.h) * ps + (lane == 0 ? in : 0);
-        } else {
-            y = (int)(((long long)it.b * P.Hkv + it.h) * P.L + at);
-        }
-        // (tests of the bounded waits: this fill's copies are never issued)
-        const bool withhold =
-            P.withhold_fill == (int)(2 * c[kv].g) + kv && blockIdx.x == 0 && p == 0;
-        if (run > 0 && !withhold) {
-            const int whole = min(max((n >> 3) - a, 0), run);
-            q8_copy<C>(kv ? M.v_atoms : M.k_atoms, kv ? &M.v_atom : &M.k_atom, y, whole,
-                       run > whole,
-                       pipe + (kv ? C::V_OFF : C::K_OFF) + slot * C::TILE_BYTES + a * C::ATOM_BYTES,
-                       bar, P.row_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first());
-        }
-        c[kv].next(T, meta, n_items);
-        prefetch(kv);
-    }
-    __device__ __forceinline__ void begin() {
-        c[0].j = p;
-        c[0].g = 0;
-        c[0].seek(T, nullptr, n_items);
-        c[1] = c[0];
-        page[0] = page[1] = 0;
-        prefetch(0);
-        page[1] = page[0];
-        if (c[0].valid) {
-            fill(0, nullptr);
-            fill(1, nullptr);
-        }
-    }
-    __device__ __forceinline__ void run(const TcItem *meta) {
-        const AttnParams &P = T.a;
-        Q8Patience patience;
-        while (c[0].valid || c[1].valid) {
-            bool free = false;
-            if (lane < 2 && c[lane].valid)
-                free = mbar_test(&bars[(lane ? C::B_VEMPTY : C::B_KEMPTY) + c[lane].g % NK],
-                                 ((c[lane].g / NK) & 1) ^ 1);
-            const uint32_t f = __ballot_sync(0xffffffffu, free);
-            if (f & 1u) fill(0, meta);
-            if (f & 2u) fill(1, meta);
-            if (f != 0) patience.idle = 0;
-            else if (!patience.more(P, failed)) break;
-            else if (patience.idle > 8) __nanosleep(32);
-        }
-        // every copy issued has landed before the CTA exits
-        if (lane < 2 * NK) {
-            const uint32_t kv = (uint32_t)lane / NK, slot = (uint32_t)lane % NK, g = c[kv].g;
-            if (g > slot)
-                mbar_wait_bounded(&bars[(kv ? C::B_VFULL : C::B_KFULL) + slot],
-                                  ((g - 1 - slot) / NK) & 1, P.fault, kFaultCopyTimeout,
-                                  P.wait_limit);
-        }
-        __syncwarp();
-    }
-};
-
-// Issuer of pipeline p's MMAs: the next tile's scores and the oldest tile's PV, each
-// as soon as its operands are there (one barrier per lane, tested by one
-// instruction).
-template <class C, int D, int N, int NK>
-__device__ __forceinline__ void q8_issue(const TcParams &T, const TcItem *meta, uint8_t *pipe,
-                                         uint64_t *bars, uint32_t tmem, int n_items, int p,
-                                         volatile uint32_t *failed) {
+// The TMA producer (warp 0): every item's K and V tiles in order into the first free
+// ring slots.  Lane s looks after slot s, so that one test finds a free one, and
+// issues the slot's copy (a paged tile's runs of pages go to a lane each, the page
+// ids read a tile ahead).  Waits for every copy it issued before returning.
+template <class C, int NT>
+__device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, const TcItem *meta,
+                                            volatile uint32_t *ftab, uint8_t *ring, uint64_t *bars,
+                                            volatile uint32_t *failed) {
     using namespace tc;
-    constexpr int MH = D / 128;
-    constexpr uint32_t ID_QK = idesc_e4m3_f32(128, 2 * N, 0, 0);
-    constexpr uint32_t ID_PV = idesc_e4m3_f32(128, 3 * N, 1, 1);
     const AttnParams &P = T.a;
     const int lane = (int)(threadIdx.x & 31);
-    const uint64_t k_d = smem_desc_sw128(smem_u32(pipe + C::K_OFF), 16, C::ATOM_BYTES);
-    const uint64_t v_d = smem_desc_sw128(smem_u32(pipe + C::V_OFF), 16, C::ATOM_BYTES);
-    const uint64_t q_d = smem_desc_sw128(smem_u32(pipe + C::Q_OFF), 16, 1024);
-    const uint64_t p_d = smem_desc_sw32(smem_u32(pipe + C::P_OFF), C::P_BLOCK, 256);
-    Q8Cursor s, o;  // the next scores, the next PV
-    s.j = p;
-    s.g = 0;
-    s.seek(T, meta, n_items);
-    o = s;
-    uint32_t k = 0;  // items whose scores have begun
-    Q8Patience patience;
-    while (o.valid) {
-        // 0: the K tile, 1: the S buffer, 2: an item's queries; 3: the V tile, 4: P
-        const int which = lane == 0   ? C::B_KFULL + (int)(s.g % NK)
-                          : lane == 1 ? C::B_SFREE
-                          : lane == 2 ? C::B_QFULL
-                          : lane == 3 ? C::B_VFULL + (int)(o.g % NK)
-                                      : C::B_PFULL;
-        const uint32_t par = lane == 0   ? s.g / NK
-                             : lane == 1 ? s.g + 1
-                             : lane == 2 ? k
-                             : lane == 3 ? o.g / NK
-                                         : o.g;
-        bool there = false;
-        if (lane < 5 && (lane > 2 ? o.g < s.g : s.valid))
-            there = (lane == 2 && s.t > 0) || mbar_test(&bars[which], par & 1);
-        const uint32_t r = __ballot_sync(0xffffffffu, there);
-        if ((r & 7u) == 7u) {
-            const bool last = s.t == s.it.n_tiles - 1;
-            const uint32_t slot = s.g % NK;
-            fence_after_sync();
-            if (lane == 0) {
-                const uint64_t a = k_d + (uint64_t)(slot * (C::TILE_BYTES >> 4));
-#pragma unroll
-                for (int sl = 0; sl < C::SLABS; ++sl)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_e4m3_ss(tmem, a + (uint64_t)(sl * 64 + kk * 2),
-                                    q_d + (uint64_t)(sl * (C::Q_SLAB >> 4) + kk * 2), ID_QK,
-                                    (sl | kk) != 0);
-                mma_commit(&bars[C::B_SFULL]);
-                mma_commit(&bars[C::B_KEMPTY + slot]);
-            }
-            __syncwarp();
-            if (last) ++k;
-            s.next(T, meta, n_items);
-        }
-        if ((r & 24u) == 24u) {
-            const uint32_t slot = o.g % NK;
-            const bool last = o.t == o.it.n_tiles - 1;
-            fence_after_sync();
-            // only the 32-key steps that hold valid keys are multiplied; the rows of
-            // the last step past the chunk's end, and those before the chunk in a
-            // paged cache's first tile, are zeroed first, so that 0 * (whatever the
-            // slot holds there) cannot reach O
-            const int nv = last ? o.it.cr.c_hi - o.it.t0 - kTcTileKeys * o.t : kTcTileKeys;
-            const int steps = (nv + 31) >> 5;
-            const int z = o.t == 0 ? o.it.cr.c_lo - o.it.t0 : 0;
-            if ((nv & 31) || z > 0) {
-                uint8_t *vt = pipe + C::V_OFF + slot * C::TILE_BYTES;
-                zero_v_rows<C>(vt, nv, 32 * steps, lane);
-                zero_v_rows<C>(vt, 0, z, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            if (lane == 0) {
-                // A = V^T, MN-major: a slab holds 128 dims, 8-key groups one atom
-                // apart; B = the parts of P, MN-major
-                const uint64_t a = v_d + (uint64_t)(slot * (C::TILE_BYTES >> 4));
-                const uint32_t acc = o.t > 0 ? 1u : 0u;
-#pragma unroll
-                for (int k4 = 0; k4 < 4; ++k4) {
-                    if (k4 >= steps) break;
-#pragma unroll
-                    for (int mh = 0; mh < MH; ++mh)
-                        mma_e4m3_ss(tmem + C::O_COL + mh * C::O_HALF,
-                                    a + (uint64_t)((mh * 1024 + k4 * 4 * C::ATOM_BYTES) >> 4),
-                                    p_d + (uint64_t)(k4 * 1024 >> 4), ID_PV, k4 > 0 ? 1u : acc);
+    const bool paged = P.block_table != nullptr;
+    const uint64_t policy = P.row_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+    const int ps = paged ? P.page_size : 8, pa = ps >> 3;  // rows, atoms per page
+    const int n_items = cta_items(T);
+    const int n_early = n_items > 0 ? early_fills<NT, false>(T, meta[0]) : 0;
+    uint32_t uses = lane < n_early ? 1 : 0;  // fills handed to this lane's slot so far
+    uint32_t f = (uint32_t)n_early;
+#pragma unroll 1
+    for (int j = 0; j < n_items; ++j) {
+        const TcItem it = q8_item(T, j, meta);
+        const int y0 = paged ? it.h * ps : (int)(((long long)it.b * P.Hkv + it.h) * P.L);
+        int page = 0, next = 0;  // of this lane's run of a tile
+#pragma unroll 1
+        for (int t = paged ? -1 : 0; t < it.n_tiles; ++t) {
+            // this lane's run of atoms: all of the tile, or (paged) a page's
+            const int p = it.t0 + kTcTileKeys * t;
+            const int n = min(kTcTileKeys, it.cr.c_hi - p);
+            const int natoms = (n + 7) >> 3;
+            int a = 0, run = natoms, y = y0 + p;
+            if (paged) {
+                // the next tile's page ids are on their way during this one's fills
+                page = next;
+                if (t + 1 < it.n_tiles) {
+                    const int p1 = p + kTcTileKeys, k0 = p1 / ps;
+                    const int a1 =
+                        lane == 0 ? 0 : ((ps - (p1 - k0 * ps)) >> 3) + (lane - 1) * pa;
+                    if (8 * a1 < min(kTcTileKeys, it.cr.c_hi - p1))
+                        next = __ldg(P.block_table + (long long)it.b * P.max_blocks + k0 + lane);
                 }
-                mma_commit(&bars[C::B_PVDONE]);
-                mma_commit(&bars[C::B_VEMPTY + slot]);
+                if (t < 0) continue;
+                const int in = p % ps, first = (ps - in) >> 3;
+                a = lane == 0 ? 0 : first + (lane - 1) * pa;
+                run = min(lane == 0 ? first : pa, natoms - a);
+                y = checked_page(P, page, nullptr) * P.Hkv * ps + y0 + (lane == 0 ? in : 0);
             }
-            __syncwarp();
-            o.next(T, meta, n_items);
+            const int whole = min(max((n >> 3) - a, 0), run);
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                if (j == 0 && 2 * t + kv < n_early) continue;
+                uint32_t free;
+                int idle = 0;
+                long long since = 0;
+                for (;;) {
+                    free = __ballot_sync(
+                        0xffffffffu,
+                        lane < NT && (uses == 0 ||
+                                      mbar_test(&bars[C::B_EMPTY + lane], (uses - 1) & 1)));
+                    if (free) break;
+                    if ((++idle & 63) == 0) {
+                        const long long now = clock64();
+                        if (idle == 64) since = now;
+                        const bool over = now - since > P.wait_limit;
+                        if (over && lane == 0) {
+                            atomicOr(P.fault, kFaultCopyTimeout);
+                            *failed = 1;
+                        }
+                        if (__any_sync(0xffffffffu, over || *failed)) break;
+                    }
+                }
+                if (!free) goto drain;
+                const int slot = __ffs((int)free) - 1;
+                if (lane == slot) {
+                    ftab[f % kFillTab] = (f << 8) | ((uses & 1) << 4) | (uint32_t)slot;
+                    mbar_arrive_expect_tx(&bars[C::B_FULL + slot], (uint32_t)natoms * C::ATOM_BYTES);
+                    ++uses;
+                }
+                __syncwarp();
+                // (tests of the bounded waits: this fill's copies are never issued)
+                if (run > 0 && (paged || lane == slot) &&
+                    !(P.withhold_fill == (int)f && blockIdx.x == 0)) {
+                    uint8_t *dst = ring + slot * C::TILE_BYTES;
+                    const CUtensorMap *m4 = kv ? M.v_atoms : M.k_atoms;
+                    if (!paged && whole == 16)
+                        tma_load_4d_hint(dst, m4, 0, y, 0, 0, &bars[C::B_FULL + slot], policy);
+                    else
+                        q8_copy<C>(m4, kv ? &M.v_atom : &M.k_atom, y, whole, run > whole,
+                                   dst + a * C::ATOM_BYTES, &bars[C::B_FULL + slot], policy);
+                }
+                ++f;
+            }
         }
-        if ((r & 7u) == 7u || (r & 24u) == 24u) patience.idle = 0;
-        else if (!patience.more(P, failed)) break;
     }
-    // all issued MMAs complete before TMEM is released
-    if (lane == 0 && s.g > 0) {
-        mma_commit(&bars[C::B_DRAIN]);
-        mbar_wait_bounded(&bars[C::B_DRAIN], 0, P.fault, kFaultCopyTimeout, P.wait_limit);
-    }
+drain:
+    // every copy this CTA issued has landed before it exits
+    if (uses > 0)
+        mbar_wait_bounded(&bars[C::B_FULL + lane], (uses - 1) & 1, P.fault, kFaultCopyTimeout,
+                          P.wait_limit);
     __syncwarp();
 }
 
-// Barriers of one pipeline's softmax warps, and a vote of theirs.
-__device__ __forceinline__ void q8_sync(int p) {
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + p) : "memory");
-}
-__device__ __forceinline__ bool q8_any(int p, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, %2, 128, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "r"(3 + p)
-        : "memory");
-    return r != 0;
+// Warp 3: per tile and key the factor of its scores (k's scale, in log2 units) and
+// v's exponent.  A lane takes four keys of a tile (of one page, if paged: tiles
+// then start on an 8-key boundary).  A load takes microseconds beside the tiles'
+// copies, several tiles' time: the exponents of SLOTS tiles are on their way at
+// once, and the page ids of SLOTS more.  (Each slot has registers of its own: to
+// move a value on is to wait for it.)
+template <class C>
+__device__ __forceinline__ void q8_tables(const Q8TcParams &A, const TcItem *meta, float2 *tabs,
+                                          uint64_t *bars, volatile uint32_t *failed) {
+    const TcParams &T = A.T;
+    const AttnParams &P = T.a;
+    constexpr int SLOTS = 3;
+    const int lane = (int)(threadIdx.x & 31);
+    const int n_items = cta_items(T);
+    const bool paged = P.block_table != nullptr;
+    const int8_t *kx = A.k_exp, *vx = A.v_exp;
+    int e[SLOTS][8], page[SLOTS], row[SLOTS];
+    uint32_t masks = 0;  // per slot four bits: this lane's keys that exist
+    // the tiles in order; in a paged cache where this lane's keys are
+    int j = -1, t = 0, blk = 0, in = 0;
+    const int ps = paged ? P.page_size : 8;
+    const int blks = kTcTileKeys / ps, rest = kTcTileKeys % ps;  // pages per tile
+    TcItem it;
+    it.n_tiles = 0;
+    // slot s: where the next tile's exponents are; false past the last
+    auto locate = [&](int s) -> bool {
+        while (t >= it.n_tiles) {
+            if (++j >= n_items) return false;
+            it = q8_item(T, j, meta);
+            t = 0;
+            if (paged) {
+                blk = (it.t0 + 4 * lane) / ps;
+                in = it.t0 + 4 * lane - blk * ps;
+            }
+        }
+        const int jk = it.t0 + kTcTileKeys * t++ + 4 * lane;
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (jk + c >= it.cr.c_lo && jk + c < it.cr.c_hi) m |= 1u << c;
+        masks = (masks & ~(0xfu << (4 * s))) | (m << (4 * s));
+        // (rows are below 2^31, as the tensor maps' are)
+        if (paged) {
+            row[s] = it.h * ps + in;
+            if (m) page[s] = __ldg(P.block_table + (long long)it.b * P.max_blocks + blk);
+            blk += blks;
+            in += rest;
+            if (in >= ps) {
+                in -= ps;
+                ++blk;
+            }
+        } else {
+            row[s] = (int)(((long long)it.b * P.Hkv + it.h) * P.L + jk);
+        }
+        return true;
+    };
+    int located = 0, f = -2 * SLOTS;  // tiles located, published
+#pragma unroll 1
+    for (;;) {
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s, ++f) {
+            if (f >= 0) {
+                if (f >= located) return;
+                const uint32_t slot = f % kQ8Tabs;
+                q8_wait(&bars[C::B_TEMPTY + slot], ((f / kQ8Tabs) & 1) ^ 1, P, failed);
+                float4 *tab = reinterpret_cast<float4 *>(tabs + slot * kTcTileKeys + 4 * lane);
+#pragma unroll
+                for (int c = 0; c < 4; c += 2)
+                    tab[c / 2] =
+                        make_float4(P.qk_scale * q8_pow2(e[s][c]), (float)e[s][4 + c],
+                                    P.qk_scale * q8_pow2(e[s][c + 1]), (float)e[s][5 + c]);
+                warp_arrive(&bars[C::B_TFULL + slot]);
+            }
+            if (f + SLOTS >= 0 && f + SLOTS < located) {
+                long long at = row[s];
+                const uint32_t m = (masks >> (4 * s)) & 0xfu;
+                if (paged && m)
+                    at += (long long)checked_page(P, page[s], nullptr) * P.Hkv * ps;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    e[s][c] = e[s][4 + c] = 0;
+                    if (m >> c & 1) {
+                        e[s][c] = kx[at + c];
+                        e[s][4 + c] = vx[at + c];
+                    }
+                }
+            }
+            if (locate(s)) ++located;
+        }
+    }
 }
 
-// An item's query rows into the raw buffer, an item ahead of their use: a plain
-// load takes microseconds while the tiles' copies keep the memory busy.  Warp w of
-// the four has rows w, w + 4, ..., as q8_queries: a thread splits what it copied.
+// Warps 12..15, first job: an item's query rows as two e4m3 numbers each, and
+// their scales.  Warp w of the four takes rows w, w + 4, ..., RP at a time.  The
+// rows come through a buffer of their own, an item ahead of their use
+// (q8_fetch_queries): a plain load takes microseconds while the tiles' copies
+// keep the memory busy.  A thread splits what it copied itself.
 template <int D>
 __device__ __forceinline__ void q8_fetch_queries(const AttnParams &P, const TcItem &it, uint8_t *raw,
                                                  int w, uint32_t inv_g) {
     constexpr int LPR = D / 8, RP = 32 / LPR;  // lanes per row, rows per pass
-    const int lane = (int)(threadIdx.x & 31), l = lane % LPR;
+    const int lane = (int)(threadIdx.x & 31);
+    const int l = lane % LPR;
 #pragma unroll 1
     for (int r = w + 4 * (lane / LPR); r < it.rows; r += 4 * RP)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
@@ -503,27 +506,30 @@ __device__ __forceinline__ void q8_fetch_queries(const AttnParams &P, const TcIt
                      : "memory");
 }
 
-// The rows from the raw buffer as two e4m3 numbers each, and their scales.
-template <class C, int D, int N>
-__device__ __forceinline__ void q8_queries(int rows, const uint8_t *raw, uint8_t *q, float *qsc,
-                                           uint64_t *bars, int w) {
+template <class C, int D, int N, int QB>
+__device__ __forceinline__ void q8_queries(const AttnParams &P, const TcItem &it, uint32_t k,
+                                           const uint8_t *raw, uint8_t *qs, float *qsc,
+                                           uint64_t *bars, volatile uint32_t *failed, int w) {
     constexpr int LPR = D / 8, RP = 32 / LPR;
     const int lane = (int)(threadIdx.x & 31);
     const int sub = lane / LPR, l = lane % LPR;
+    const uint32_t qb = k % QB;
+    uint8_t *q = qs + qb * C::Q_BUF;
     // 8 bytes at element 8 l: 16-byte chunk (l / 2) % 8 of slab l / 16
     const uint32_t at = (uint32_t)(l >> 4) * C::Q_SLAB + (uint32_t)(l & 1) * 8;
     asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 2
-    for (int r0 = w; r0 < rows; r0 += 4 * RP) {
+    // the buffer's previous rows are done with
+    q8_wait(&bars[C::B_QEMPTY + qb], ((k / QB) & 1) ^ 1, P, failed);
+#pragma unroll 1
+    for (int r0 = w; r0 < it.rows; r0 += 4 * RP) {
         const int r = r0 + 4 * sub;
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows) x = *reinterpret_cast<const uint4 *>(raw + r * (D * 2) + l * 16);
+        if (r < it.rows) x = *reinterpret_cast<const uint4 *>(raw + r * (D * 2) + l * 16);
         const uint32_t b[4] = {x.x, x.y, x.z, x.w};
         // the smallest exponent that holds the row, as for the cache
-        const uint32_t a = __reduce_max_sync(
-            LPR == 32 ? 0xffffffffu : 0xffffu << (16 * sub),
-            max_u16x2_half(max_u16x2(max_u16x2(b[0] & 0x7fff7fffu, b[1] & 0x7fff7fffu),
-                                     max_u16x2(b[2] & 0x7fff7fffu, b[3] & 0x7fff7fffu))));
+        const uint32_t a =
+            row_max<LPR>(max_u16x2(max_u16x2(b[0] & 0x7fff7fffu, b[1] & 0x7fff7fffu),
+                                   max_u16x2(b[2] & 0x7fff7fffu, b[3] & 0x7fff7fffu)));
         int e = (int)(a >> 7) - 135 + ((a & 0x7fu) > 0x60u ? 1 : 0);
         e = e < -126 ? -126 : (e > 126 ? 126 : e);
         const float sc = pow2f(-e);
@@ -536,361 +542,147 @@ __device__ __forceinline__ void q8_queries(int rows, const uint8_t *raw, uint8_t
             hi[p >> 1] = p & 1 ? hi[p >> 1] | (h << 16) : h;
             lo[p >> 1] = p & 1 ? lo[p >> 1] | (t << 16) : t;
         }
-        if (r < rows) {
+        if (r < it.rows) {
             // (N is a multiple of 8: both rows have the same swizzle phase)
             const uint32_t sw = (((uint32_t)(l >> 1) & 7) ^ (uint32_t)(r & 7)) << 4;
             *reinterpret_cast<uint2 *>(q + at + r * 128 + sw) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2 *>(q + at + (N + r) * 128 + sw) = make_uint2(lo[0], lo[1]);
-            if (l == 0) qsc[r] = pow2f(e);
+            if (l == 0) qsc[(k & 1) * N + r] = pow2f(e);
         }
     }
     fence_proxy_async_smem();
-    warp_arrive(&bars[C::B_QFULL]);
+    warp_arrive(&bars[C::B_QFULL + qb]);
 }
 
-// The rows of an item without keys.
-template <int D>
-__device__ __noinline__ void q8_empty_item(const AttnParams *A, const TcItem *item, uint32_t inv_g,
-                                           int t) {
-    const AttnParams &P = *A;
-    const TcItem &it = *item;
-    const float NEG_INF = -__int_as_float(0x7f800000);
-    const size_t prow0 =
-        (((size_t)it.b * P.Hkv + it.h) * P.splits + it.split) * P.R + it.row0;
-    for (int idx = t; idx < it.rows * D; idx += 128) {
-        const int r = idx / D, d = idx % D;
-        if (P.splits == 1) {
-            const size_t orow = q8_row(P, it, inv_g, r);
-            P.out[orow * D + d] = __float2bfloat16_rn(0.f);
-            if (d == 0 && P.lse != nullptr) P.lse[orow] = NEG_INF;
-        } else {
-            P.part_acc[(prow0 + r) * D + d] = 0.f;
-            if (d == 0) {
-                P.part_ml[(prow0 + r) * 2] = NEG_INF;
-                P.part_ml[(prow0 + r) * 2 + 1] = 0.f;
-            }
-        }
-    }
-}
-
-// The softmax warps of pipeline p: queries, softmax and epilogue of its items.
-template <class C, int D, int N>
-__device__ __forceinline__ void q8_softmax(const Q8TcParams &A, const TcItem *meta, uint8_t *pipe,
-                                           uint64_t *bars, uint32_t tmem, int n_items, int p,
-                                           volatile uint32_t *failed) {
+// Warps 12..15, second job: the k-th item's O through 1 / l to the output (or to
+// the split partials), and the rows of an item without keys.
+template <class C, int D, int N, int OB>
+__device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &it, uint32_t k,
+                                            uint32_t tmem, const float *sums, float *linv,
+                                            uint32_t *rowidx, uint64_t *bars,
+                                            volatile uint32_t *failed, uint32_t inv_g) {
     using namespace tc;
     constexpr int MH = D / 128;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    const TcParams &T = A.T;
-    const AttnParams &P = T.a;
-    uint8_t *q = pipe + C::Q_OFF, *raw = pipe + C::RAW_OFF;
-    float *red = reinterpret_cast<float *>(pipe + C::RED_OFF);
-    float *ref = reinterpret_cast<float *>(pipe + C::REF_OFF);
-    float *qsc = reinterpret_cast<float *>(pipe + C::QSC_OFF);
-    float *alpha = reinterpret_cast<float *>(pipe + C::ALPHA_OFF);
-    uint32_t *rowidx = reinterpret_cast<uint32_t *>(pipe + C::ROW_OFF);
-    const int lane = (int)(threadIdx.x & 31), sw = (int)(threadIdx.x >> 5) & 3;
-    const int lk = sw * 32 + lane;  // TMEM lane: key of S^T, dim row of O^T
-    const uint32_t s_col = tmem + ((uint32_t)(sw * 32) << 16), o_col = s_col + C::O_COL;
-    const uint32_t inv_g = q8_inv_g(P);
-    uint8_t *pt = pipe + C::P_OFF + lk * 32;        // key lk's row of P
-    const uint32_t flip = (uint32_t)(lk >> 2) & 1;  // its 32-byte swizzle phase
-
-    auto item = [&](int j) {
-        TcItem it;
-        if (j < kQ8Meta) it = meta[j];
-        else q8_decode(&T, j, &it);
-        return it;
-    };
-    // the exponents of this thread's key in tile t of an item, k's and v's
-    int8_t ke = 0, ve = 0;
-    auto fetch_key = [&](const TcItem &it, int t) {
-        const int jk = it.t0 + kTcTileKeys * t + lk;
-        ke = ve = 0;
-        if (jk >= it.cr.c_lo && jk < it.cr.c_hi) {
-            const long long row = cache_row(P, it.b, it.h, jk);
-            ke = A.k_exp[row];
-            ve = A.v_exp[row];
+    const int t = (int)threadIdx.x - (kQ8TcThreads - 128);  // 0..127
+    const int lane = t & 31, quad = t >> 5;
+    const size_t bh = (size_t)it.b * P.Hkv + it.h;
+    const size_t prow0 = (bh * P.splits + it.split) * P.R + it.row0;
+    if (it.n_tiles == 0) {
+        for (int idx = t; idx < it.rows * D; idx += 128) {
+            const int r = idx / D, d = idx % D;
+            if (P.splits == 1) {
+                const size_t orow = q8_row(P, it, inv_g, r);
+                P.out[orow * D + d] = __float2bfloat16_rn(0.f);
+                if (d == 0 && P.lse != nullptr) P.lse[orow] = NEG_INF;
+            } else {
+                P.part_acc[(prow0 + r) * D + d] = 0.f;
+                if (d == 0) {
+                    P.part_ml[(prow0 + r) * 2] = NEG_INF;
+                    P.part_ml[(prow0 + r) * 2 + 1] = 0.f;
+                }
+            }
         }
-    };
-    // the next item with keys: its queries are on their way, or split already
-    int jn = p;
-    TcItem nx;
-    auto seek = [&]() {
-        for (; jn < n_items; jn += 2) {
-            nx = item(jn);
-            if (nx.n_tiles > 0) return;
-        }
-    };
-    seek();
-    if (jn < n_items) {
-        q8_fetch_queries<D>(P, nx, raw, sw, inv_g);
-        fetch_key(nx, 0);
-        q8_queries<C, D, N>(nx.rows, raw, q, qsc, bars, sw);
+        return;
     }
-    q8_sync(p);  // (the scales; later items' are behind the epilogue's)
-    uint32_t g = 0, k = 0;
-#pragma unroll 1
-    for (int j = p; j < n_items; j += 2) {
-        const TcItem it = item(j);
-        if (it.n_tiles == 0) {
-            q8_empty_item<D>(&P, &it, inv_g, lk);
-            continue;
+    // (below 2^31 by the plan's size checks)
+    uint32_t *rows = rowidx + (k & 1) * N;
+    float *li = linv + (k & 1) * N;
+    const uint32_t ob = k % OB;
+    const uint32_t orow = t < it.rows ? (uint32_t)q8_row(P, it, inv_g, t) : 0u;
+    q8_wait(&bars[C::B_LFULL + (k & 3)], (k >> 2) & 1, P, failed);
+    if (t < it.rows) {
+        const float *sum = sums + (k & 3) * 5 * N + t;
+        const float l = (sum[0] + sum[N]) + (sum[2 * N] + sum[3 * N]);
+        const float m = sum[4 * N];
+        const bool any = !(l <= 0.f);  // (a NaN stays one)
+        rows[t] = orow;
+        li[t] = any ? __frcp_rn(l) : 0.f;
+        if (P.splits > 1) {
+            P.part_ml[(prow0 + t) * 2] = any ? m : NEG_INF;
+            P.part_ml[(prow0 + t) * 2 + 1] = l;
+        } else if (P.lse != nullptr) {
+            P.lse[orow] = any ? (m + __log2f(l)) * kLn2 : NEG_INF;
         }
-        jn = j + 2;
-        seek();
-        if (jn < n_items) q8_fetch_queries<D>(P, nx, raw, sw, inv_g);
-        const float *rs = qsc + (k & 1) * N;
-        float lrow[N];
-#pragma unroll
-        for (int r = 0; r < N; ++r) lrow[r] = 0.f;
-        const int qp_i0 = it.cr.qp + it.i0;  // position of the item's first draft row
-        // first keys of the tiles that every row sees whole
-        const int i_last = (int)((uint32_t)(it.rows - 1) * inv_g >> 16);
-        const int inner_lo =
-            (int)max((long long)qp_i0 + i_last - P.window + 1, (long long)it.cr.c_lo);
-        const int inner_hi = min(qp_i0, it.cr.c_hi - 1) - (kTcTileKeys - 1);
-#pragma unroll 1
-        for (int t = 0; t < it.n_tiles; ++t, ++g) {
-            // this key's factor (log2 units) and v's exponent; the next tile's are
-            // on their way from here on
-            const float kx = P.qk_scale * pow2f(ke < -126 ? -126 : ke), vx = (float)ve;
-            const float ive = pow2f(ve > 126 ? -126 : (ve < -127 ? 127 : -ve));
-            if (t + 1 < it.n_tiles) fetch_key(it, t + 1);
-            else if (jn < n_items) fetch_key(nx, 0);
-            // packed rows [ra, rb) whose window holds the key
-            const int j0 = it.t0 + kTcTileKeys * t;
-            int ra = 0, rb = N;
-            if (j0 < inner_lo || j0 > inner_hi) {
-                const int jk = j0 + lk;
-                ra = rb = 0;
-                if (jk >= it.cr.c_lo && jk < it.cr.c_hi) {
-                    // (jk < q_pos + q_len: the first difference is below 512)
-                    const int lo_i = jk - qp_i0;
-                    const long long hi_i = (long long)lo_i + P.window;
-                    ra = min(max(lo_i, 0) * P.G, (int)it.rows);
-                    rb = hi_i >= it.rows ? (int)it.rows
-                                         : min(max((int)hi_i, 0) * P.G, (int)it.rows);
-                }
-            }
-            q8_wait(&bars[C::B_SFULL], g & 1, P, failed);
-            fence_after_sync();
-            // u = (S_hi + S_lo / 16) * row scale * key factor + e_v
-            float v[N];
-            {
-                const uint64_t lo2 = f2_pack(1.f / kQ8QLo, 1.f / kQ8QLo);
-                const uint64_t ks2 = f2_pack(kx, kx), ve2 = f2_pack(vx, vx);
-#pragma unroll
-                for (int c = 0; c < N; c += 16) {
-                    uint32_t hi[16], lo[16];
-                    tmem_load<16>(s_col + c, hi);
-                    tmem_load<16>(s_col + N + c, lo);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 s4 = *reinterpret_cast<const float4 *>(rs + c + e);
-                        const uint64_t rs2[2] = {f2_pack(s4.x, s4.y), f2_pack(s4.z, s4.w)};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int r = e + 2 * h;
-                            const uint64_t s2 =
-                                f2_fma(f2_pack(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])),
-                                       lo2,
-                                       f2_pack(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
-                            f2_unpack(f2_fma(f2_mul(s2, rs2[h]), ks2, ve2), v[c + r], v[c + r + 1]);
-                        }
-                    }
-                }
-                fence_before_sync();
-                warp_arrive(&bars[C::B_SFREE]);
-                if (ra > 0 || rb < N) {
-#pragma unroll
-                    for (int r = 0; r < N; ++r)
-                        if (r < ra || r >= rb) v[r] = NEG_INF;
-                }
-            }
-            bool raise = t == 0;  // an item's first tile sets the references
-            if (t > 0) {
-                float over = NEG_INF;
-#pragma unroll
-                for (int r = 0; r < N; r += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4 *>(ref + r);
-                    over = fmax3(over, v[r] - m4.x, v[r + 1] - m4.y);
-                    over = fmax3(over, v[r + 2] - m4.z, v[r + 3] - m4.w);
-                }
-                raise = q8_any(p, over > kQ8RaiseAt);
-            }
-            if (raise) {
-                // exact tile maximum per row
-                float mine = NEG_INF;
-#pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    const float m = warp_max(v[r]);
-                    if (lane == r) mine = m;
-                }
-                if (lane < N) red[sw * N + lane] = mine;
-                q8_sync(p);
-                if (lk < N) {
-                    const float tm =
-                        fmaxf(fmax3(red[lk], red[N + lk], red[2 * N + lk]), red[3 * N + lk]);
-                    const float mo = t == 0 ? kNoRef : ref[lk];
-                    const float mn = fmaxf(mo, tm - kQ8RefBelow);
-                    ref[lk] = mn;
-                    alpha[lk] = fast_exp2(mo - mn);
-                }
-                if (t > 0) {
-                    // every PV of this item so far has completed before O is scaled
-                    q8_wait(&bars[C::B_PVDONE], (g - 1) & 1, P, failed);
-                    fence_after_sync();
-                }
-                q8_sync(p);
-                if (t > 0) {
-#pragma unroll
-                    for (int r = 0; r < N; ++r) lrow[r] *= alpha[r];
-#pragma unroll 1
-                    for (int c = 0; c < MH * 3 * N; c += 16) {
-                        uint32_t o[16];
-                        tmem_load<16>(o_col + c, o);
-                        tmem_wait_ld();
-                        const float *a = alpha + c % N;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * a[e]);
-                        tmem_store<16>(o_col + c, o);
-                    }
-                    tmem_wait_st();
-                }
-            }
-            // the P buffer's previous PV has completed
-            if (g > 0) q8_wait(&bars[C::B_PVDONE], (g - 1) & 1, P, failed);
-            // P = 2^(u - ref) in e4m3 numbers; the row sum adds P 2^-e_v
-            const uint64_t iv2 = f2_pack(ive, ive);
-#pragma unroll
-            for (int c = 0; c < N; c += 16) {
-                uint32_t pk[3][4];
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4 *>(ref + c + e);
-                    const uint64_t m2[2] = {f2_pack(m4.x, m4.y), f2_pack(m4.z, m4.w)};
-                    uint32_t w[3][2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = c + e + 2 * h;
-                        float d0, d1;
-                        f2_unpack(f2_sub(f2_pack(v[r], v[r + 1]), m2[h]), d0, d1);
-                        const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
-                        f2_unpack(f2_fma(f2_pack(p0, p1), iv2, f2_pack(lrow[r], lrow[r + 1])),
-                                  lrow[r], lrow[r + 1]);
-                        __half2 x = __floats2half2_rn(p0, p1);
-                        w[0][h] = take_e4m3(x, kQ8P1);
-                        w[1][h] = take_e4m3(x, kQ8P2);
-                        w[2][h] = last_e4m3(x);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) pk[i][e / 4] = w[i][0] | (w[i][1] << 16);
-                }
-                // columns i N + c .. of part i
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const int col = i * N + c;
-                    *reinterpret_cast<uint4 *>(pt + (col >> 5) * C::P_BLOCK +
-                                               (((uint32_t)(col >> 4) & 1u) ^ flip) * 16) =
-                        make_uint4(pk[i][0], pk[i][1], pk[i][2], pk[i][3]);
-                }
-            }
-            fence_proxy_async_smem();
-            warp_arrive(&bars[C::B_PFULL]);
-        }
-
-        // ------------------------------------------------------ epilogue
-        // (the last scores are complete, so the queries' buffer is free)
-        if (jn < n_items) q8_queries<C, D, N>(nx.rows, raw, q, qsc + ((k + 1) & 1) * N, bars, sw);
-        const float l1 = lane_reduce<N, false>(lrow);
-        if (lane < N) red[sw * N + lane] = l1;
-        q8_sync(p);
-        const size_t prow0 =
-            (((size_t)it.b * P.Hkv + it.h) * P.splits + it.split) * P.R + it.row0;
-        if (lk < it.rows) {
-            const float l = (red[lk] + red[N + lk]) + (red[2 * N + lk] + red[3 * N + lk]);
-            const float m = ref[lk];
-            const bool any = !(l <= 0.f);  // (a NaN stays one)
-            const uint32_t orow = (uint32_t)q8_row(P, it, inv_g, lk);
-            alpha[lk] = any ? __frcp_rn(l) : 0.f;
-            rowidx[lk] = orow;  // (below 2^31 by the plan's size checks)
-            if (P.splits > 1) {
-                P.part_ml[(prow0 + lk) * 2] = any ? m : NEG_INF;
-                P.part_ml[(prow0 + lk) * 2 + 1] = l;
-            } else if (P.lse != nullptr) {
-                P.lse[orow] = any ? (m + __log2f(l)) * kLn2 : NEG_INF;
-            }
-        }
-        q8_wait(&bars[C::B_PVDONE], (g - 1) & 1, P, failed);
-        fence_after_sync();
-        q8_sync(p);
-        const uint64_t s1 = f2_pack(1.f / kQ8P1, 1.f / kQ8P1);
-        const uint64_t s2 = f2_pack(1.f / kQ8P2, 1.f / kQ8P2);
-        // neighbouring lanes hold neighbouring dims: each pair swaps halves of two
-        // rows, so that a lane stores two dims of one row
-        const bool odd = lane & 1;
-        __nv_bfloat16 *out = P.out + (lk & ~1);
-#pragma unroll 1
-        for (int c0 = 0; c0 < it.rows; c0 += 16) {
-#pragma unroll 1
-            for (int mh = 0; mh < MH; ++mh) {
-                uint32_t o[3][16];
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    tmem_load<16>(o_col + mh * C::O_HALF + i * N + c0, o[i]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    auto pair = [&](int i) {
-                        return f2_pack(__uint_as_float(o[i][e]), __uint_as_float(o[i][e + 1]));
-                    };
-                    const uint64_t x2 = f2_fma(f2_fma(pair(2), s2, pair(1)), s1, pair(0));
-                    float a, b;
-                    if (P.splits == 1) {
-                        const float2 l2 = *reinterpret_cast<const float2 *>(alpha + c0 + e);
-                        f2_unpack(f2_mul(x2, f2_pack(l2.x, l2.y)), a, b);
-                        const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                        const int r = c0 + e + (odd ? 1 : 0);
-                        const uint32_t w = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
-                        if (r < it.rows)
-                            *reinterpret_cast<uint32_t *>(out + (size_t)rowidx[r] * D + mh * 128) =
-                                w;
-                    } else {
-                        f2_unpack(x2, a, b);
-                        float *acc = P.part_acc + (prow0 + c0 + e) * D + mh * 128 + lk;
-                        if (c0 + e < it.rows) acc[0] = a;
-                        if (c0 + e + 1 < it.rows) acc[D] = b;
-                    }
-                }
-            }
-        }
-        fence_before_sync();  // (O is read before the next item's first P is announced)
-        ++k;
     }
+    asm volatile("bar.sync 5, 128;" ::: "memory");
+    q8_wait(&bars[C::B_OFULL + ob], (k / OB) & 1, P, failed);
+    fence_after_sync();
+    const uint32_t o0 = tmem + ((uint32_t)(quad * 32) << 16) + C::O_COL + ob * C::O_COLS;
+    const uint64_t s1 = f2_pack(1.f / kQ8P1, 1.f / kQ8P1), s2 = f2_pack(1.f / kQ8P2, 1.f / kQ8P2);
+    // neighbouring lanes hold neighbouring dims: each pair swaps halves of two
+    // rows, so that a lane stores two dims of one row
+    const bool odd = lane & 1;
+    __nv_bfloat16 *out = P.out + (t & ~1);
+#pragma unroll 1
+    for (int c = 0; c < MH * (N / 8); ++c) {
+        const int c0 = c / MH * 8, mh = c % MH;
+        if (c0 >= it.rows) break;
+        uint32_t o[3][8];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) tmem_load<8>(o0 + mh * C::O_HALF + p * N + c0, o[p]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            auto pair = [&](int p) {
+                return f2_pack(__uint_as_float(o[p][e]), __uint_as_float(o[p][e + 1]));
+            };
+            const uint64_t x2 = f2_fma(f2_fma(pair(2), s2, pair(1)), s1, pair(0));
+            float a, b;
+            if (P.splits == 1) {
+                const float2 l2 = *reinterpret_cast<const float2 *>(li + c0 + e);
+                f2_unpack(f2_mul(x2, f2_pack(l2.x, l2.y)), a, b);
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                const int r = c0 + e + (odd ? 1 : 0);
+                const uint32_t w = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                if (r < it.rows)
+                    *reinterpret_cast<uint32_t *>(out + (size_t)rows[r] * D + mh * 128) = w;
+            } else {
+                f2_unpack(x2, a, b);
+                float *acc = P.part_acc + (prow0 + c0 + e) * D + mh * 128 + t;
+                if (c0 + e < it.rows) acc[0] = a;
+                if (c0 + e + 1 < it.rows) acc[D] = b;
+            }
+        }
+    }
+    // O and the item's sums may be overwritten
+    fence_before_sync();
+    warp_arrive(&bars[C::B_OFREE + ob]);
 }
 
-template <int D, int N, int NK>
+template <int D, int N, int NT, int QB>
 __global__ void __launch_bounds__(kQ8TcThreads, 1)
     swa_q8_tc_kernel(const __grid_constant__ Q8TcParams A, const __grid_constant__ TcMaps M) {
-    using C = Q8Cfg<D, N, NK>;
+    using C = Q8Cfg<D, N, NT, QB>;
     using namespace tc;
+    constexpr int MH = D / 128, OB = 2;
+    const float NEG_INF = -__int_as_float(0x7f800000);
     const TcParams &T = A.T;
+    const AttnParams &P = T.a;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
+    uint8_t *ring = sm + C::RING_OFF;
+    uint8_t *qs = sm + C::Q_OFF;
+    uint8_t *raw = sm + C::RAW_OFF;
+    uint8_t *ps = sm + C::P_OFF;
+    float2 *tabs = reinterpret_cast<float2 *>(sm + C::TAB_OFF);
+    float *red = reinterpret_cast<float *>(sm + C::RED_OFF);
+    float *refs = reinterpret_cast<float *>(sm + C::REF_OFF);
+    float *alphas = reinterpret_cast<float *>(sm + C::ALPHA_OFF);
+    float *qsc = reinterpret_cast<float *>(sm + C::QSC_OFF);
+    float *sums = reinterpret_cast<float *>(sm + C::SUM_OFF);
+    float *linv = reinterpret_cast<float *>(sm + C::LINV_OFF);
+    uint32_t *rowidx = reinterpret_cast<uint32_t *>(sm + C::ROW_OFF);
     TcItem *meta = reinterpret_cast<TcItem *>(sm + C::META_OFF);
+    volatile uint32_t *ftab = reinterpret_cast<volatile uint32_t *>(sm + C::FTAB_OFF);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::BAR_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC_OFF);
     volatile uint32_t *failed = tmem_slot + 1;
+
     const int tid = threadIdx.x;
-    const int warp = tid >> 5, lane = tid & 31;
-    // the pipeline of this warp: 0 and 3 load, 1 and 2 issue, 4..7 and 8..11 softmax
-    const int p = warp < 4 ? warp >> 1 : (warp - 4) >> 2;
-    uint8_t *pipe = sm + p * C::PIPE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::BAR_OFF) + p * C::NBARS;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     // ---------------------------------------------------------------- setup
     if (warp == 0 && lane < 10) {
@@ -900,22 +692,25 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                                             : &M.v_atom;
         prefetch_tmap(mp);
     }
-    if ((warp == 0 || warp == 3) && lane < C::NBARS) {
-        // arrivals: one (a commit, or a copy's bytes), or one per softmax warp
-        mbar_init(&bars[lane], lane == C::B_QFULL || lane == C::B_SFREE || lane == C::B_PFULL ? 4 : 1);
+    // arrivals on a barrier: one (a commit, a copy's bytes, one warp), or one from
+    // each warp of a role
+    for (int i = tid; i < C::NBARS; i += kQ8TcThreads) {
+        const bool soft = (i >= C::B_SFREE && i < C::B_PVDONE) ||
+                          (i >= C::B_LFULL && i < C::B_DRAIN) || i >= C::B_TEMPTY;
+        const bool four = (i >= C::B_QFULL && i < C::B_QEMPTY) ||
+                          (i >= C::B_OFREE && i < C::B_LFULL);
+        mbar_init(&bars[i], soft ? 8 : four ? 4 : 1);
         fence_barrier_init();
     }
     if (tid == 0) *failed = 0;
-    // query rows past an item's stay what they are here: zero, or another item's
-    // (their columns are never looked at, but should not raise the references
-    // either)
-    if (warp >= 4) {
-        for (int i = tid & 127; i < C::Q_BUF / 16; i += 128)
-            reinterpret_cast<uint4 *>(pipe + C::Q_OFF)[i] = make_uint4(0, 0, 0, 0);
-        float *z = reinterpret_cast<float *>(pipe + C::RED_OFF);
-        for (int i = tid & 127; i < (C::PIPE - C::RED_OFF) / 4; i += 128) z[i] = 0.f;
-        fence_proxy_async_smem();
-    }
+    // query rows past an item's stay what they are here: zero, or another
+    // item's (their columns are never looked at, but should not raise the
+    // references either)
+    for (int i = tid; i < QB * C::Q_BUF / 16; i += kQ8TcThreads)
+        reinterpret_cast<uint4 *>(qs)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < 2 * N; i += kQ8TcThreads) qsc[i] = 0.f;
+    fence_proxy_async_smem();
+    for (int i = tid; i < kFillTab; i += kQ8TcThreads) ftab[i] = 0xffffffffu;
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
@@ -923,28 +718,404 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
     __syncthreads();
     grid_dep_wait();
     grid_dep_trigger();
+    if (lane == 0) q8_early_fills<C, NT>(T, M, ftab, ring, bars, warp);
+    for (int j = tid; j < kTcMetaItems; j += kQ8TcThreads)
+        if (j < cta_items(T)) q8_decode(&T, j, &meta[j]);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int n_items = cta_items(T);
-    if (warp == 0 || warp == 3) {
-        Q8Loader<C, NK> load{T, M, pipe, bars, failed, {}, {}, n_items, lane, p};
-        load.begin();
-        __syncthreads();
-        load.run(meta);
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+    }
+    if (warp == 0) {
+        // ======================================================= producer
+        q8_producer<C, NT>(T, M, meta, ftab, ring, bars, failed);
+    } else if (warp <= 2) {
+        // ============================================================ MMA
+        // Warp 1 issues S = K8 Q^T of every tile, warp 2 O += V8^T P^T, each as
+        // soon as its operands have landed.  A step's conditions are one barrier
+        // per lane, tested by one instruction.
+        const bool pv = warp == 2;
+        const bool leader = lane == 0;
+        constexpr uint32_t ID_QK = idesc_e4m3_f32(128, 2 * N, 0, 0);
+        constexpr uint32_t ID_PV = idesc_e4m3_f32(128, 3 * N, 1, 1);
+        const uint64_t ring_d = smem_desc_sw128(smem_u32(ring), 16, C::ATOM_BYTES);
+        const uint64_t q_d = smem_desc_sw128(smem_u32(qs), 16, 1024);
+        const uint64_t p_d = smem_desc_sw32(smem_u32(ps), C::P_BLOCK, 256);
+        // lane 0: the tile's fill; 1 and 2: barriers b1 and b2 (b < 0: none)
+        auto ready = [&](uint32_t fill, int b1, uint32_t par1, int b2, uint32_t par2) -> int {
+            uint32_t e = 0xffffffffu;
+            int idle = 0;
+            long long since = 0;
+            const int b = lane == 1 ? b1 : b2;
+            const uint32_t par = (lane == 1 ? par1 : par2) & 1;
+            bool done = lane > 2 || (lane > 0 && b < 0);
+            for (;;) {
+                if (lane == 0) {
+                    e = ftab[fill % kFillTab];
+                    if ((e >> 8) == (fill & 0xffffffu))
+                        done = mbar_test(&bars[C::B_FULL + (e & 15u)], (e >> 4) & 1u);
+                } else if (!done) {
+                    done = mbar_test(&bars[b], par);
+                }
+                if (__all_sync(0xffffffffu, done)) break;
+                if ((++idle & 63) == 0) {
+                    const long long now = clock64();
+                    if (idle == 64) since = now;
+                    const bool over = now - since > P.wait_limit;
+                    if (over && lane == 0) {
+                        atomicOr(P.fault, kFaultCopyTimeout);
+                        *failed = 1;
+                    }
+                    if (__any_sync(0xffffffffu, over || *failed)) return -1;
+                }
+            }
+            return (int)(__shfl_sync(0xffffffffu, e, 0) & 15u);
+        };
+        uint32_t g = 0, k = 0;  // tiles, items with keys so far
+        bool ok = true;
+#pragma unroll 1
+        for (int j = 0; j < n_items && ok; ++j) {
+            const TcItem it = q8_item(T, j, meta);
+            const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
+            if (n_tiles == 0) continue;
+            const int left0 = __shfl_sync(0xffffffffu, it.cr.c_hi - it.t0, 0);
+            const int z0 = __shfl_sync(0xffffffffu, it.cr.c_lo - it.t0, 0);
+#pragma unroll 1
+            for (int t = 0; t < n_tiles; ++t, ++g) {
+                const bool first = t == 0, last = t == n_tiles - 1;
+                const uint32_t h = g & 1;
+                if (!pv) {
+                    const uint32_t qb = k % QB;
+                    const int slot = ready(2 * g, C::B_SFREE + (int)h, (g >> 1) + 1,
+                                           first ? C::B_QFULL + (int)qb : -1, k / QB);
+                    ok = slot >= 0;
+                    if (!ok) break;
+                    fence_after_sync();
+                    const uint64_t qbase = q_d + (uint64_t)(qb * (C::Q_BUF >> 4));
+                    const uint64_t abase = ring_d + (uint64_t)(slot * (C::TILE_BYTES >> 4));
+                    const uint32_t d = tmem + h * C::S_COLS;
+#pragma unroll
+                    for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_e4m3_ss(leader, d, abase + (uint64_t)(s * 64 + kk * 2),
+                                        qbase + (uint64_t)(s * (C::Q_SLAB >> 4) + kk * 2), ID_QK,
+                                        (s | kk) != 0);
+                    mma_commit_by(leader, &bars[C::B_SFULL + h]);
+                    mma_commit_by(leader, &bars[C::B_EMPTY + slot]);
+                    if (last) mma_commit_by(leader, &bars[C::B_QEMPTY + qb]);
+                } else {
+                    const uint32_t ob = k % OB;
+                    const int slot = ready(2 * g + 1, C::B_PFULL + (int)h, g >> 1,
+                                           first ? C::B_OFREE + (int)ob : -1, (k / OB) + 1);
+                    ok = slot >= 0;
+                    if (!ok) break;
+                    fence_after_sync();
+                    // only the 32-key steps that hold valid keys are multiplied; the
+                    // rows of the last step past the chunk's end, and those before
+                    // the chunk in a paged cache's first tile, are zeroed first, so
+                    // that 0 * (whatever the slot holds there) cannot reach O
+                    const int nv = last ? left0 - kTcTileKeys * t : kTcTileKeys;
+                    const int steps = (nv + 31) >> 5;
+                    const int z = first ? z0 : 0;
+                    if ((nv & 31) || z > 0) {
+                        uint8_t *vt = ring + slot * C::TILE_BYTES;
+                        zero_v_rows<C>(vt, nv, 32 * steps, lane);
+                        zero_v_rows<C>(vt, 0, z, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    // A = V^T, MN-major: a slab holds 128 dims, 8-key groups one
+                    // atom apart; B = the parts of P, MN-major
+                    const uint64_t bbase = p_d + (uint64_t)(h * (C::P_BUF >> 4));
+                    const uint64_t abase = ring_d + (uint64_t)(slot * (C::TILE_BYTES >> 4));
+                    const uint32_t d = tmem + C::O_COL + ob * C::O_COLS;
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        if (k4 >= steps) break;
+#pragma unroll
+                        for (int mh = 0; mh < MH; ++mh)
+                            mma_e4m3_ss(leader, d + mh * C::O_HALF,
+                                        abase + (uint64_t)((mh * 1024 + k4 * 4 * C::ATOM_BYTES) >> 4),
+                                        bbase + (uint64_t)(k4 * 1024 >> 4), ID_PV,
+                                        k4 > 0 || !first);
+                    }
+                    mma_commit_by(leader, &bars[C::B_PVDONE + h]);
+                    mma_commit_by(leader, &bars[C::B_EMPTY + slot]);
+                    if (last) mma_commit_by(leader, &bars[C::B_OFULL + ob]);
+                }
+                __syncwarp();
+            }
+            ++k;
+        }
+        // all issued MMAs complete before TMEM is released
+        if (leader) {
+            mma_commit(&bars[C::B_DRAIN + (pv ? 1 : 0)]);
+            mbar_wait_bounded(&bars[C::B_DRAIN + (pv ? 1 : 0)], 0, P.fault, kFaultCopyTimeout,
+                              P.wait_limit);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ===================================================== key factors
+        q8_tables<C>(A, meta, tabs, bars, failed);
+    } else if (warp < 12) {
+        // ===================================================== softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFT_REGS));
+        constexpr int HN = N / 2;                // rows per softmax warpgroup
+        const int wg = (warp - 4) >> 2;          // softmax warpgroup
+        const int sw = warp & 3;                 // warp within the group: TMEM lane quadrant
+        const int lk = sw * 32 + lane;           // TMEM lane: key of S^T, dim row of O^T
+        const int r0 = wg * HN;                  // first packed row of this group
+        const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
+        const uint32_t flip = (uint32_t)(lk >> 2) & 1;  // 32-byte swizzle phase of key lk
+        float *rd = red + r0, *ref = refs + r0, *alpha = alphas + r0;
+        constexpr int CH = HN / 8;               // chunks of eight rows
+        // the loops over a thread's rows are rolled: the arrays turn by eight rows a
+        // time instead
+        auto turn = [](float(&x)[HN]) {
+            if constexpr (HN == 16) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = x[e];
+                    x[e] = x[8 + e];
+                    x[8 + e] = y;
+                }
+            }
+        };
+        uint32_t g = 0, k = 0;                   // tiles, items with keys so far
+#pragma unroll 1
+        for (int j = 0; j < n_items; ++j) {
+            const TcItem it = q8_item(T, j, meta);
+            if (it.n_tiles == 0) continue;
+            const float *rs = qsc + (k & 1) * N + r0;
+            float lrow[HN];
+#pragma unroll
+            for (int r = 0; r < HN; ++r) lrow[r] = 0.f;
+            const int qp_i0 = it.cr.qp + it.i0;  // position of the item's first draft row
+            // first keys of the tiles that every row sees whole
+            const int i_last = (it.rows - 1) / P.G;
+            const int inner_lo =
+                (int)max((long long)qp_i0 + i_last - P.window + 1, (long long)it.cr.c_lo);
+            const int inner_hi = min(qp_i0, it.cr.c_hi - 1) - (kTcTileKeys - 1);
+#pragma unroll 1
+            for (int t = 0; t < it.n_tiles; ++t, ++g) {
+                const uint32_t h = g & 1, slot = g % kQ8Tabs;
+                const int j0 = it.t0 + kTcTileKeys * t;
+                // packed rows [ra, rb) of this group whose window holds the key: all
+                // of them in a tile between the item's last window start and its
+                // first row's position
+                int ra = 0, rb = HN;
+                if (j0 < inner_lo || j0 > inner_hi) {
+                    const int jk = j0 + lk;
+                    ra = rb = 0;
+                    if (jk >= it.cr.c_lo && jk < it.cr.c_hi) {
+                        // (jk < q_pos + q_len: the first difference is below 512)
+                        const int lo_i = jk - qp_i0;
+                        const long long hi_i = (long long)lo_i + P.window;
+                        ra = min(max(lo_i, 0) * P.G, (int)it.rows) - r0;
+                        rb = (hi_i >= it.rows ? (int)it.rows
+                                              : min(max((int)hi_i, 0) * P.G, (int)it.rows)) -
+                             r0;
+                    }
+                }
+                // one barrier per lane, tested by one instruction: the tile's table
+                // and scores, an item's query scales
+                {
+                    uint64_t *bar = &bars[lane == 0   ? C::B_TFULL + slot
+                                          : lane == 1 ? C::B_SFULL + h
+                                                      : C::B_QFULL + k % QB];
+                    const uint32_t par =
+                        (lane == 0 ? g / kQ8Tabs : lane == 1 ? g >> 1 : k / QB) & 1;
+                    if (lane < (t == 0 ? 3 : 2)) q8_wait_here(bar, par, P, failed);
+                    __syncwarp();
+                }
+                const float2 key = tabs[slot * kTcTileKeys + lk];
+                fence_after_sync();
+                // u = (S_hi + S_lo / 16) * row scale * key factor + e_v
+                float v[HN], over = NEG_INF;
+                const uint64_t lo2 = f2_pack(1.f / kQ8QLo, 1.f / kQ8QLo);
+                const uint64_t ks2 = f2_pack(key.x, key.x), ve2 = f2_pack(key.y, key.y);
+#pragma unroll 1
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t hi[8], lo[8];
+                    tmem_load<8>(tl + h * C::S_COLS + r0 + 8 * c, hi);
+                    tmem_load<8>(tl + h * C::S_COLS + N + r0 + 8 * c, lo);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int r4 = 0; r4 < 8; r4 += 4) {
+                        const float4 s4 = *reinterpret_cast<const float4 *>(rs + 8 * c + r4);
+                        const uint64_t rs2[2] = {f2_pack(s4.x, s4.y), f2_pack(s4.z, s4.w)};
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const int r = r4 + 2 * p;
+                            const uint64_t s2 =
+                                f2_fma(f2_pack(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])),
+                                       lo2,
+                                       f2_pack(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
+                            f2_unpack(f2_fma(f2_mul(s2, rs2[p]), ks2, ve2), v[r], v[r + 1]);
+                        }
+                    }
+                    if (ra > 0 || rb < HN) {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (8 * c + r < ra || 8 * c + r >= rb) v[r] = NEG_INF;
+                    }
+#pragma unroll
+                    for (int r4 = 0; r4 < 8; r4 += 4) {
+                        const float4 m4 = *reinterpret_cast<const float4 *>(ref + 8 * c + r4);
+                        over = fmax3(over, v[r4] - m4.x, v[r4 + 1] - m4.y);
+                        over = fmax3(over, v[r4 + 2] - m4.z, v[r4 + 3] - m4.w);
+                    }
+                    turn(v);
+                }
+                // the scores and the table are read
+                fence_before_sync();
+                __syncwarp();
+                if (lane < 2)
+                    mbar_arrive(&bars[lane == 0 ? C::B_SFREE + h : C::B_TEMPTY + slot]);
+
+                // an item's first tile sets the references
+                if (t == 0 || group_any(wg, over > kQ8RaiseAt)) {
+                    // exact maximum per row over the tile's keys
+#pragma unroll 1
+                    for (int c = 0; c < CH; ++c) {
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = v[e];
+                        const float m = lane_reduce<8, true>(x);
+                        if (lane < 8) rd[sw * N + 8 * c + lane] = m;
+                        turn(v);
+                    }
+                    group_sync(wg);
+                    if (lk < HN) {
+                        const float tm =
+                            fmaxf(fmax3(rd[lk], rd[N + lk], rd[2 * N + lk]), rd[3 * N + lk]);
+                        const float mo = t == 0 ? kNoRef : ref[lk];
+                        const float mn = fmaxf(mo, tm - kQ8RefBelow);
+                        ref[lk] = mn;
+                        alpha[lk] = fast_exp2(mo - mn);
+                    }
+                    // every PV of this item so far has completed before O is scaled
+                    if (t > 0) {
+                        q8_wait_here(&bars[C::B_PVDONE + (h ^ 1)], ((g - 1) >> 1) & 1, P, failed);
+                        fence_after_sync();
+                    }
+                    group_sync(wg);
+                    if (t > 0) {
+                        const uint32_t o0 = tl + C::O_COL + (k % OB) * C::O_COLS + r0;
+#pragma unroll 1
+                        for (int c = 0; c < CH; ++c) {
+                            const float *al = alpha + 8 * c;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) lrow[e] *= al[e];
+                            turn(lrow);
+#pragma unroll 1
+                            for (int i = 0; i < MH * 3; ++i) {
+                                uint32_t o[8];
+                                tmem_load<8>(o0 + i * N + 8 * c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * al[e]);
+                                tmem_store<8>(o0 + i * N + 8 * c, o);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // the P buffer's previous PV has completed
+                if (lane == 0) q8_wait_here(&bars[C::B_PVDONE + h], ((g >> 1) + 1) & 1, P, failed);
+                __syncwarp();
+                // P = 2^(u - ref) in e4m3 numbers; the row sum adds P 2^-e_v
+                const int ev = (int)key.y;
+                const float ive = pow2f(ev > 126 ? -126 : (ev < -127 ? 127 : -ev));
+                const uint64_t iv2 = f2_pack(ive, ive);
+                uint8_t *pt = ps + h * C::P_BUF + lk * 32;
+#pragma unroll 1
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t pk[3][4];
+#pragma unroll
+                    for (int r4 = 0; r4 < 8; r4 += 4) {
+                        const float4 m4 = *reinterpret_cast<const float4 *>(ref + 8 * c + r4);
+                        const uint64_t m2[2] = {f2_pack(m4.x, m4.y), f2_pack(m4.z, m4.w)};
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int r = r4 + 2 * q;
+                            float d0, d1;
+                            f2_unpack(f2_sub(f2_pack(v[r], v[r + 1]), m2[q]), d0, d1);
+                            const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
+                            f2_unpack(f2_fma(f2_pack(p0, p1), iv2, f2_pack(lrow[r], lrow[r + 1])),
+                                      lrow[r], lrow[r + 1]);
+                            __half2 x = __floats2half2_rn(p0, p1);
+                            pk[0][r / 2] = take_e4m3(x, kQ8P1);
+                            pk[1][r / 2] = take_e4m3(x, kQ8P2);
+                            pk[2][r / 2] = last_e4m3(x);
+                        }
+                    }
+                    // columns i N + r0 + 8 c .. of part i, in key lk's 32-byte rows
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint32_t at =
+                            N == 16 ? (i >> 1) * C::P_BLOCK + (((uint32_t)(i & 1) ^ flip) << 4) + wg * 8
+                                    : i * C::P_BLOCK + (((uint32_t)wg ^ flip) << 4) + 8 * c;
+                        *reinterpret_cast<uint2 *>(pt + at) =
+                            make_uint2(pk[i][0] | (pk[i][1] << 16), pk[i][2] | (pk[i][3] << 16));
+                    }
+                    turn(v);
+                    turn(lrow);
+                }
+                fence_proxy_async_smem();
+                warp_arrive(&bars[C::B_PFULL + h]);
+            }
+
+            // the warp's row sums and the references, for the epilogue
+            const float l = lane_reduce<HN, false>(lrow);
+            float *sum = sums + (k & 3) * 5 * N + r0 + lane;
+            if (lane < HN) {
+                sum[sw * N] = l;
+                if (sw == 0) sum[4 * N] = ref[lane];
+            }
+            warp_arrive(&bars[C::B_LFULL + (k & 3)]);
+            ++k;
+        }
     } else {
-        for (int j = tid - 128; j >= 0 && j < kQ8Meta; j += kQ8TcThreads)
-            if (j < n_items) q8_decode(&T, j, &meta[j]);
-        fence_before_sync();
-        __syncthreads();
-        fence_after_sync();
-        const uint32_t tmem = *tmem_slot + p * C::PIPE_COLS;
-        if (warp < 4) q8_issue<C, D, N, NK>(T, meta, pipe, bars, tmem, n_items, p, failed);
-        else q8_softmax<C, D, N>(A, meta, pipe, bars, tmem, n_items, p, failed);
+        // ====================================== query rows and epilogues
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+        const uint32_t inv_g = q8_inv_g(P);
+        const int w = warp - 12;
+        uint32_t kq = 0, k = 0;  // items with keys whose queries are split, finished
+        int jq = 0;
+        TcItem next;             // the item whose queries are on their way
+        auto fetch = [&]() {
+            for (next.n_tiles = 0; jq < n_items && next.n_tiles == 0; ++jq) next = q8_item(T, jq, meta);
+            if (next.n_tiles > 0) q8_fetch_queries<D>(P, next, raw, w, inv_g);
+        };
+        fetch();
+        // queries one item ahead of the epilogues
+#pragma unroll 1
+        for (int j = -1; j < n_items; ++j) {
+            TcItem it;
+            it.n_tiles = 1;
+            if (j >= 0) it = q8_item(T, j, meta);
+            if (it.n_tiles > 0 && next.n_tiles > 0) {
+                q8_queries<C, D, N, QB>(P, next, kq++, raw, qs, qsc, bars, failed, w);
+                fetch();
+            }
+            if (j < 0) continue;
+            q8_epilogue<C, D, N, OB>(P, it, k, tmem, sums, linv, rowidx, bars, failed, inv_g);
+            if (it.n_tiles > 0) ++k;
+        }
     }
 
     // ---------------------------------------------------------- teardown
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (warp == 1) tmem_dealloc(*tmem_slot, C::TMEM_COLS);
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
 }  // namespace swa
