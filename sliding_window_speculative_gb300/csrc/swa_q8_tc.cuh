@@ -308,6 +308,7 @@ __device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, 
     const bool paged = P.block_table != nullptr;
     const uint64_t policy = P.row_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     const int ps = paged ? P.page_size : 8, pa = ps >> 3;  // rows, atoms per page
+    const int blks = kTcTileKeys / ps, rest = kTcTileKeys % ps;  // pages per tile
     const int n_items = cta_items(T);
     const int n_early = n_items > 0 ? early_fills<NT, false>(T, meta[0]) : 0;
     uint32_t uses = lane < n_early ? 1 : 0;  // fills handed to this lane's slot so far
@@ -317,6 +318,7 @@ __device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, 
         const TcItem it = q8_item(T, j, meta);
         const int y0 = paged ? it.h * ps : (int)(((long long)it.b * P.Hkv + it.h) * P.L);
         int page = 0, next = 0;  // of this lane's run of a tile
+        int blk = it.t0 / ps, in = it.t0 - blk * ps, in1 = in;  // where the next tile begins
 #pragma unroll 1
         for (int t = paged ? -1 : 0; t < it.n_tiles; ++t) {
             // this lane's run of atoms: all of the tile, or (paged) a page's
@@ -327,18 +329,24 @@ __device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, 
             if (paged) {
                 // the next tile's page ids are on their way during this one's fills
                 page = next;
+                const int in0 = in1;
+                in1 = in;
                 if (t + 1 < it.n_tiles) {
-                    const int p1 = p + kTcTileKeys, k0 = p1 / ps;
-                    const int a1 =
-                        lane == 0 ? 0 : ((ps - (p1 - k0 * ps)) >> 3) + (lane - 1) * pa;
-                    if (8 * a1 < min(kTcTileKeys, it.cr.c_hi - p1))
-                        next = __ldg(P.block_table + (long long)it.b * P.max_blocks + k0 + lane);
+                    const int a1 = lane == 0 ? 0 : ((ps - in) >> 3) + (lane - 1) * pa;
+                    if (8 * a1 < min(kTcTileKeys, it.cr.c_hi - p - kTcTileKeys))
+                        next = __ldg(P.block_table + (long long)it.b * P.max_blocks + blk + lane);
+                    blk += blks;
+                    in += rest;
+                    if (in >= ps) {
+                        in -= ps;
+                        ++blk;
+                    }
                 }
                 if (t < 0) continue;
-                const int in = p % ps, first = (ps - in) >> 3;
+                const int first = (ps - in0) >> 3;
                 a = lane == 0 ? 0 : first + (lane - 1) * pa;
                 run = min(lane == 0 ? first : pa, natoms - a);
-                y = checked_page(P, page, nullptr) * P.Hkv * ps + y0 + (lane == 0 ? in : 0);
+                y = checked_page(P, page, nullptr) * P.Hkv * ps + y0 + (lane == 0 ? in0 : 0);
             }
             const int whole = min(max((n >> 3) - a, 0), run);
 #pragma unroll 1
@@ -377,8 +385,10 @@ __device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, 
                     !(P.withhold_fill == (int)f && blockIdx.x == 0)) {
                     uint8_t *dst = ring + slot * C::TILE_BYTES;
                     const CUtensorMap *m4 = kv ? M.v_atoms : M.k_atoms;
-                    if (!paged && whole == 16)
-                        tma_load_4d_hint(dst, m4, 0, y, 0, 0, &bars[C::B_FULL + slot], policy);
+                    // (16, 8, 4 or 2 whole atoms are one copy)
+                    if (run == whole && whole > 1 && (whole & (whole - 1)) == 0)
+                        tma_load_4d_hint(dst + a * C::ATOM_BYTES, m4 + (__clz(whole) - 27), 0, y, 0,
+                                         0, &bars[C::B_FULL + slot], policy);
                     else
                         q8_copy<C>(m4, kv ? &M.v_atom : &M.k_atom, y, whole, run > whole,
                                    dst + a * C::ATOM_BYTES, &bars[C::B_FULL + slot], policy);
@@ -874,6 +884,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
         const uint32_t flip = (uint32_t)(lk >> 2) & 1;  // 32-byte swizzle phase of key lk
         float *rd = red + r0, *ref = refs + r0, *alpha = alphas + r0;
         constexpr int CH = HN / 8;               // chunks of eight rows
+        constexpr uint32_t ALL = (1u << HN) - 1;
         // the loops over a thread's rows are rolled: the arrays turn by eight rows a
         // time instead
         auto turn = [](float(&x)[HN]) {
@@ -905,32 +916,35 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
             for (int t = 0; t < it.n_tiles; ++t, ++g) {
                 const uint32_t h = g & 1, slot = g % kQ8Tabs;
                 const int j0 = it.t0 + kTcTileKeys * t;
-                // packed rows [ra, rb) of this group whose window holds the key: all
-                // of them in a tile between the item's last window start and its
-                // first row's position
-                int ra = 0, rb = HN;
+                // bit r: this group's row r sees the key; all of them in a tile between
+                // the item's last window start and its first row's position
+                uint32_t sees = ALL;
                 if (j0 < inner_lo || j0 > inner_hi) {
                     const int jk = j0 + lk;
-                    ra = rb = 0;
+                    sees = 0;
                     if (jk >= it.cr.c_lo && jk < it.cr.c_hi) {
-                        // (jk < q_pos + q_len: the first difference is below 512)
-                        const int lo_i = jk - qp_i0;
-                        const long long hi_i = (long long)lo_i + P.window;
-                        ra = min(max(lo_i, 0) * P.G, (int)it.rows) - r0;
-                        rb = (hi_i >= it.rows ? (int)it.rows
-                                              : min(max((int)hi_i, 0) * P.G, (int)it.rows)) -
-                             r0;
+                        // the draft rows [lo, lo + window) (jk < q_pos + q_len: lo < 512)
+                        const int lo = jk - qp_i0;
+                        const int ra = max(max(lo, 0) * P.G - r0, 0);
+                        const int rb = (lo >= it.rows - P.window
+                                            ? (int)it.rows
+                                            : min(max(lo + P.window, 0) * P.G, (int)it.rows)) - r0;
+                        if (ra < HN && rb > ra) sees = (ALL << ra) & (ALL >> max(HN - rb, 0));
                     }
                 }
                 // one barrier per lane, tested by one instruction: the tile's table
-                // and scores, an item's query scales
+                // and scores, the previous PV of the tile's P buffer, an item's query
+                // scales
                 {
                     uint64_t *bar = &bars[lane == 0   ? C::B_TFULL + slot
                                           : lane == 1 ? C::B_SFULL + h
+                                          : lane == 2 ? C::B_PVDONE + h
                                                       : C::B_QFULL + k % QB];
-                    const uint32_t par =
-                        (lane == 0 ? g / kQ8Tabs : lane == 1 ? g >> 1 : k / QB) & 1;
-                    if (lane < (t == 0 ? 3 : 2)) q8_wait_here(bar, par, P, failed);
+                    const uint32_t par = (lane == 0   ? g / kQ8Tabs
+                                          : lane == 1 ? g >> 1
+                                          : lane == 2 ? (g >> 1) + 1
+                                                      : k / QB) & 1;
+                    if (lane < (t == 0 ? 4 : 3)) q8_wait_here(bar, par, P, failed);
                     __syncwarp();
                 }
                 const float2 key = tabs[slot * kTcTileKeys + lk];
@@ -959,10 +973,11 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                             f2_unpack(f2_fma(f2_mul(s2, rs2[p]), ks2, ve2), v[r], v[r + 1]);
                         }
                     }
-                    if (ra > 0 || rb < HN) {
+                    if (sees != ALL) {
+                        const uint32_t s8 = sees >> (8 * c);
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
-                            if (8 * c + r < ra || 8 * c + r >= rb) v[r] = NEG_INF;
+                            if (!(s8 & (1u << r))) v[r] = NEG_INF;
                     }
 #pragma unroll
                     for (int r4 = 0; r4 < 8; r4 += 4) {
@@ -1027,9 +1042,6 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                         tmem_wait_st();
                     }
                 }
-                // the P buffer's previous PV has completed
-                if (lane == 0) q8_wait_here(&bars[C::B_PVDONE + h], ((g >> 1) + 1) & 1, P, failed);
-                __syncwarp();
                 // P = 2^(u - ref) in e4m3 numbers; the row sum adds P 2^-e_v
                 const int ev = (int)key.y;
                 const float ive = pow2f(ev > 126 ? -126 : (ev < -127 ? 127 : -ev));
