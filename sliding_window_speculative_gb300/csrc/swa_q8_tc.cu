@@ -13,19 +13,11 @@
 namespace swa {
 namespace {
 
-// Ring slots and query buffers per (head_dim, padded rows), within one CTA's 227 KB
-// of shared memory.
-template <int D, int N>
-struct Q8Conf {
-    static constexpr int NT = D == 256 ? 5 : 10;
-    static constexpr int QB = D == 256 && N == 32 ? 1 : 2;
-};
-
 template <int D, int N>
 cudaError_t launch(const Q8TcParams &A, const TcMaps &maps, int grid, cudaStream_t stream) {
-    using Cf = Q8Conf<D, N>;
-    using C = Q8Cfg<D, N, Cf::NT, Cf::QB>;
-    auto kern = swa_q8_tc_kernel<D, N, Cf::NT, Cf::QB>;
+    constexpr int NT = D == 256 ? 5 : 10;  // ring slots within 227 KB of shared memory
+    using C = Q8Cfg<D, N, NT>;
+    auto kern = swa_q8_tc_kernel<D, N, NT>;
     static std::atomic<bool> attr_done[kMaxDevices];
     const cudaError_t e = raise_smem_limit(kern, C::SMEM_BYTES, attr_done);
     if (e != cudaSuccess) return e;

@@ -73,7 +73,7 @@ struct Q8TcParams {
     const int8_t *k_exp, *v_exp;
 };
 
-template <int D, int N, int NT, int QB>
+template <int D, int N, int NT>
 struct Q8Cfg {
     static constexpr int SLABS = D / 128;
     static constexpr int ATOM_BYTES = SLABS * 1024;  // 8 keys x D
@@ -86,8 +86,7 @@ struct Q8Cfg {
     static constexpr int P_BUF = ((3 * N + 31) / 32) * P_BLOCK;
     static constexpr int RING_OFF = 0;
     static constexpr int Q_OFF = RING_OFF + NT * TILE_BYTES;
-    static constexpr int RAW_OFF = Q_OFF + QB * Q_BUF;  // bf16 [N][D]: the next item's queries
-    static constexpr int P_OFF = RAW_OFF + N * D * 2;
+    static constexpr int P_OFF = Q_OFF + 2 * Q_BUF;
     static constexpr int TAB_OFF = P_OFF + 2 * P_BUF;                // float2 [kQ8Tabs][128]
     static constexpr int RED_OFF = TAB_OFF + kQ8Tabs * kTcTileKeys * 8;  // float [4][N]
     static constexpr int REF_OFF = RED_OFF + 4 * N * 4;              // float [N] references
@@ -100,8 +99,8 @@ struct Q8Cfg {
     static constexpr int META_OFF = ROW_OFF + 2 * N * 4;             // TcItem [kTcMetaItems]
     static constexpr int FTAB_OFF = META_OFF + kTcMetaItems * (int)sizeof(TcItem);
     static constexpr int BAR_OFF = (FTAB_OFF + kFillTab * 4 + 7) / 8 * 8;
-    static constexpr int B_FULL = 0, B_EMPTY = NT, B_QFULL = 2 * NT, B_QEMPTY = B_QFULL + QB,
-                         B_SFULL = B_QEMPTY + QB, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
+    static constexpr int B_FULL = 0, B_EMPTY = NT, B_QFULL = 2 * NT, B_QEMPTY = B_QFULL + 2,
+                         B_SFULL = B_QEMPTY + 2, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
                          B_PVDONE = B_PFULL + 2, B_OFULL = B_PVDONE + 2, B_OFREE = B_OFULL + 2,
                          B_LFULL = B_OFREE + 2, B_DRAIN = B_LFULL + 4, B_TFULL = B_DRAIN + 2,
                          B_TEMPTY = B_TFULL + kQ8Tabs, NBARS = B_TEMPTY + kQ8Tabs;
@@ -498,44 +497,57 @@ __device__ __forceinline__ void q8_tables(const Q8TcParams &A, const TcItem *met
 }
 
 // Warps 12..15, first job: an item's query rows as two e4m3 numbers each, and
-// their scales.  Warp w of the four takes rows w, w + 4, ..., RP at a time.  The
-// rows come through a buffer of their own, an item ahead of their use
-// (q8_fetch_queries): a plain load takes microseconds while the tiles' copies
-// keep the memory busy.  A thread splits what it copied itself.
-template <int D>
-__device__ __forceinline__ void q8_fetch_queries(const AttnParams &P, const TcItem &it, uint8_t *raw,
-                                                 int w, uint32_t inv_g) {
+// their scales.  Warp w of the four takes rows w, w + 4, ..., RP at a time, a lane
+// eight elements.  They are on their way an item ahead (a plain load takes
+// microseconds while the tiles' copies keep the memory busy), to the very sixteen
+// bytes that their two numbers take afterwards: eight at q8_query_at(r, l), eight
+// at row N + r.
+template <class C>
+__device__ __forceinline__ uint32_t q8_query_at(int r, int l) {
+    // elements 8 l ..: 16-byte chunk (l / 2) % 8 of slab l / 16
+    return (uint32_t)(l >> 4) * C::Q_SLAB + r * 128 +
+           ((((uint32_t)(l >> 1) & 7) ^ (uint32_t)(r & 7)) << 4) + (uint32_t)(l & 1) * 8;
+}
+
+// The k-th item with keys, once the buffer's previous rows are done with.
+template <class C, int D, int N>
+__device__ __forceinline__ void q8_fetch_queries(const AttnParams &P, const TcItem &it, uint32_t k,
+                                                 uint8_t *qs, uint64_t *bars,
+                                                 volatile uint32_t *failed, int w,
+                                                 uint32_t inv_g) {
     constexpr int LPR = D / 8, RP = 32 / LPR;  // lanes per row, rows per pass
     const int lane = (int)(threadIdx.x & 31);
     const int l = lane % LPR;
+    uint8_t *q = qs + (k & 1) * C::Q_BUF;
+    q8_wait(&bars[C::B_QEMPTY + (k & 1)], ((k >> 1) & 1) ^ 1, P, failed);
 #pragma unroll 1
-    for (int r = w + 4 * (lane / LPR); r < it.rows; r += 4 * RP)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         smem_u32(raw + r * (D * 2) + l * 16)),
-                     "l"(P.q + q8_row(P, it, inv_g, r) * D + l * 8)
+    for (int r = w + 4 * (lane / LPR); r < it.rows; r += 4 * RP) {
+        const __nv_bfloat16 *src = P.q + q8_row(P, it, inv_g, r) * D + l * 8;
+        const uint32_t dst = smem_u32(q + q8_query_at<C>(r, l));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + N * 128), "l"(src + 4)
                      : "memory");
+    }
 }
 
-template <class C, int D, int N, int QB>
-__device__ __forceinline__ void q8_queries(const AttnParams &P, const TcItem &it, uint32_t k,
-                                           const uint8_t *raw, uint8_t *qs, float *qsc,
-                                           uint64_t *bars, volatile uint32_t *failed, int w) {
+template <class C, int D, int N>
+__device__ __forceinline__ void q8_queries(const TcItem &it, uint32_t k, uint8_t *qs, float *qsc,
+                                           uint64_t *bars, int w) {
     constexpr int LPR = D / 8, RP = 32 / LPR;
     const int lane = (int)(threadIdx.x & 31);
     const int sub = lane / LPR, l = lane % LPR;
-    const uint32_t qb = k % QB;
-    uint8_t *q = qs + qb * C::Q_BUF;
-    // 8 bytes at element 8 l: 16-byte chunk (l / 2) % 8 of slab l / 16
-    const uint32_t at = (uint32_t)(l >> 4) * C::Q_SLAB + (uint32_t)(l & 1) * 8;
+    uint8_t *q = qs + (k & 1) * C::Q_BUF;
     asm volatile("cp.async.wait_all;" ::: "memory");
-    // the buffer's previous rows are done with
-    q8_wait(&bars[C::B_QEMPTY + qb], ((k / QB) & 1) ^ 1, P, failed);
 #pragma unroll 1
     for (int r0 = w; r0 < it.rows; r0 += 4 * RP) {
         const int r = r0 + 4 * sub;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < it.rows) x = *reinterpret_cast<const uint4 *>(raw + r * (D * 2) + l * 16);
-        const uint32_t b[4] = {x.x, x.y, x.z, x.w};
+        // (N is a multiple of 8: both rows have the same swizzle phase)
+        uint2 *at = reinterpret_cast<uint2 *>(q + q8_query_at<C>(r, l));
+        uint32_t b[4] = {0, 0, 0, 0};
+        if (r < it.rows) {
+            const uint2 x = at[0], y = at[N * 16];
+            b[0] = x.x, b[1] = x.y, b[2] = y.x, b[3] = y.y;
+        }
         // the smallest exponent that holds the row, as for the cache
         const uint32_t a =
             row_max<LPR>(max_u16x2(max_u16x2(b[0] & 0x7fff7fffu, b[1] & 0x7fff7fffu),
@@ -553,15 +565,13 @@ __device__ __forceinline__ void q8_queries(const AttnParams &P, const TcItem &it
             lo[p >> 1] = p & 1 ? lo[p >> 1] | (t << 16) : t;
         }
         if (r < it.rows) {
-            // (N is a multiple of 8: both rows have the same swizzle phase)
-            const uint32_t sw = (((uint32_t)(l >> 1) & 7) ^ (uint32_t)(r & 7)) << 4;
-            *reinterpret_cast<uint2 *>(q + at + r * 128 + sw) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2 *>(q + at + (N + r) * 128 + sw) = make_uint2(lo[0], lo[1]);
+            at[0] = make_uint2(hi[0], hi[1]);
+            at[N * 16] = make_uint2(lo[0], lo[1]);
             if (l == 0) qsc[(k & 1) * N + r] = pow2f(e);
         }
     }
     fence_proxy_async_smem();
-    warp_arrive(&bars[C::B_QFULL + qb]);
+    warp_arrive(&bars[C::B_QFULL + (k & 1)]);
 }
 
 // Warps 12..15, second job: the k-th item's O through 1 / l to the output (or to
@@ -660,10 +670,10 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
     warp_arrive(&bars[C::B_OFREE + ob]);
 }
 
-template <int D, int N, int NT, int QB>
+template <int D, int N, int NT>
 __global__ void __launch_bounds__(kQ8TcThreads, 1)
     swa_q8_tc_kernel(const __grid_constant__ Q8TcParams A, const __grid_constant__ TcMaps M) {
-    using C = Q8Cfg<D, N, NT, QB>;
+    using C = Q8Cfg<D, N, NT>;
     using namespace tc;
     constexpr int MH = D / 128, OB = 2;
     const float NEG_INF = -__int_as_float(0x7f800000);
@@ -675,7 +685,6 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                                               ~static_cast<uintptr_t>(1023));
     uint8_t *ring = sm + C::RING_OFF;
     uint8_t *qs = sm + C::Q_OFF;
-    uint8_t *raw = sm + C::RAW_OFF;
     uint8_t *ps = sm + C::P_OFF;
     float2 *tabs = reinterpret_cast<float2 *>(sm + C::TAB_OFF);
     float *red = reinterpret_cast<float *>(sm + C::RED_OFF);
@@ -716,7 +725,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
     // query rows past an item's stay what they are here: zero, or another
     // item's (their columns are never looked at, but should not raise the
     // references either)
-    for (int i = tid; i < QB * C::Q_BUF / 16; i += kQ8TcThreads)
+    for (int i = tid; i < 2 * C::Q_BUF / 16; i += kQ8TcThreads)
         reinterpret_cast<uint4 *>(qs)[i] = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < 2 * N; i += kQ8TcThreads) qsc[i] = 0.f;
     fence_proxy_async_smem();
@@ -799,9 +808,9 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                 const bool first = t == 0, last = t == n_tiles - 1;
                 const uint32_t h = g & 1;
                 if (!pv) {
-                    const uint32_t qb = k % QB;
+                    const uint32_t qb = k & 1;
                     const int slot = ready(2 * g, C::B_SFREE + (int)h, (g >> 1) + 1,
-                                           first ? C::B_QFULL + (int)qb : -1, k / QB);
+                                           first ? C::B_QFULL + (int)qb : -1, k >> 1);
                     ok = slot >= 0;
                     if (!ok) break;
                     fence_after_sync();
@@ -939,11 +948,11 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                     uint64_t *bar = &bars[lane == 0   ? C::B_TFULL + slot
                                           : lane == 1 ? C::B_SFULL + h
                                           : lane == 2 ? C::B_PVDONE + h
-                                                      : C::B_QFULL + k % QB];
+                                                      : C::B_QFULL + (k & 1)];
                     const uint32_t par = (lane == 0   ? g / kQ8Tabs
                                           : lane == 1 ? g >> 1
                                           : lane == 2 ? (g >> 1) + 1
-                                                      : k / QB) & 1;
+                                                      : k >> 1) & 1;
                     if (lane < (t == 0 ? 4 : 3)) q8_wait_here(bar, par, P, failed);
                     __syncwarp();
                 }
@@ -998,10 +1007,12 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                     // exact maximum per row over the tile's keys
 #pragma unroll 1
                     for (int c = 0; c < CH; ++c) {
-                        float x[8];
+                        float m = NEG_INF;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = v[e];
-                        const float m = lane_reduce<8, true>(x);
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = warp_max(v[e]);
+                            if (lane == e) m = x;
+                        }
                         if (lane < 8) rd[sw * N + 8 * c + lane] = m;
                         turn(v);
                     }
@@ -1099,12 +1110,13 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
         const uint32_t inv_g = q8_inv_g(P);
         const int w = warp - 12;
-        uint32_t kq = 0, k = 0;  // items with keys whose queries are split, finished
+        uint32_t kq = 0, k = 0;  // items with keys whose queries are fetched, finished
         int jq = 0;
         TcItem next;             // the item whose queries are on their way
         auto fetch = [&]() {
             for (next.n_tiles = 0; jq < n_items && next.n_tiles == 0; ++jq) next = q8_item(T, jq, meta);
-            if (next.n_tiles > 0) q8_fetch_queries<D>(P, next, raw, w, inv_g);
+            if (next.n_tiles > 0)
+                q8_fetch_queries<C, D, N>(P, next, kq++, qs, bars, failed, w, inv_g);
         };
         fetch();
         // queries one item ahead of the epilogues
@@ -1114,7 +1126,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
             it.n_tiles = 1;
             if (j >= 0) it = q8_item(T, j, meta);
             if (it.n_tiles > 0 && next.n_tiles > 0) {
-                q8_queries<C, D, N, QB>(P, next, kq++, raw, qs, qsc, bars, failed, w);
+                q8_queries<C, D, N>(next, kq - 1, qs, qsc, bars, w);
                 fetch();
             }
             if (j < 0) continue;
