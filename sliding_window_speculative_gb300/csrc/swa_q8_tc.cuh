@@ -538,7 +538,7 @@ __device__ __forceinline__ void q8_queries(const TcItem &it, uint32_t k, uint8_t
     const int sub = lane / LPR, l = lane % LPR;
     uint8_t *q = qs + (k & 1) * C::Q_BUF;
     asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
+#pragma unroll 2
     for (int r0 = w; r0 < it.rows; r0 += 4 * RP) {
         const int r = r0 + 4 * sub;
         // (N is a multiple of 8: both rows have the same swizzle phase)
@@ -585,7 +585,7 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
     constexpr int MH = D / 128;
     const float NEG_INF = -__int_as_float(0x7f800000);
     const int t = (int)threadIdx.x - (kQ8TcThreads - 128);  // 0..127
-    const int lane = t & 31, quad = t >> 5;
+    const int quad = t >> 5;
     const size_t bh = (size_t)it.b * P.Hkv + it.h;
     const size_t prow0 = (bh * P.splits + it.split) * P.R + it.row0;
     if (it.n_tiles == 0) {
@@ -630,38 +630,38 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
     fence_after_sync();
     const uint32_t o0 = tmem + ((uint32_t)(quad * 32) << 16) + C::O_COL + ob * C::O_COLS;
     const uint64_t s1 = f2_pack(1.f / kQ8P1, 1.f / kQ8P1), s2 = f2_pack(1.f / kQ8P2, 1.f / kQ8P2);
-    // neighbouring lanes hold neighbouring dims: each pair swaps halves of two
-    // rows, so that a lane stores two dims of one row
-    const bool odd = lane & 1;
-    __nv_bfloat16 *out = P.out + (t & ~1);
+    // (a warp stores 64 bytes of a row at a time: whole sectors)
+    __nv_bfloat16 *out = P.out + t;
 #pragma unroll 1
-    for (int c = 0; c < MH * (N / 8); ++c) {
-        const int c0 = c / MH * 8, mh = c % MH;
-        if (c0 >= it.rows) break;
-        uint32_t o[3][8];
+    for (int c = 0; c < it.rows; c += 8) {
+        uint32_t o[MH][3][8];
 #pragma unroll
-        for (int p = 0; p < 3; ++p) tmem_load<8>(o0 + mh * C::O_HALF + p * N + c0, o[p]);
+        for (int mh = 0; mh < MH; ++mh)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) tmem_load<8>(o0 + mh * C::O_HALF + p * N + c, o[mh][p]);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-            auto pair = [&](int p) {
-                return f2_pack(__uint_as_float(o[p][e]), __uint_as_float(o[p][e + 1]));
-            };
-            const uint64_t x2 = f2_fma(f2_fma(pair(2), s2, pair(1)), s1, pair(0));
-            float a, b;
-            if (P.splits == 1) {
-                const float2 l2 = *reinterpret_cast<const float2 *>(li + c0 + e);
-                f2_unpack(f2_mul(x2, f2_pack(l2.x, l2.y)), a, b);
-                const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                const int r = c0 + e + (odd ? 1 : 0);
-                const uint32_t w = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
-                if (r < it.rows)
-                    *reinterpret_cast<uint32_t *>(out + (size_t)rows[r] * D + mh * 128) = w;
-            } else {
-                f2_unpack(x2, a, b);
-                float *acc = P.part_acc + (prow0 + c0 + e) * D + mh * 128 + t;
-                if (c0 + e < it.rows) acc[0] = a;
-                if (c0 + e + 1 < it.rows) acc[D] = b;
+            const uint2 row = *reinterpret_cast<const uint2 *>(rows + c + e);
+            const float2 l2 = *reinterpret_cast<const float2 *>(li + c + e);
+            const bool one = c + e < it.rows, two = c + e + 1 < it.rows;
+#pragma unroll
+            for (int mh = 0; mh < MH; ++mh) {
+                auto part = [&](int p) {
+                    return f2_pack(__uint_as_float(o[mh][p][e]), __uint_as_float(o[mh][p][e + 1]));
+                };
+                const uint64_t x2 = f2_fma(f2_fma(part(2), s2, part(1)), s1, part(0));
+                float a, b;
+                if (P.splits == 1) {
+                    f2_unpack(f2_mul(x2, f2_pack(l2.x, l2.y)), a, b);
+                    if (one) out[(size_t)row.x * D + mh * 128] = __float2bfloat16_rn(a);
+                    if (two) out[(size_t)row.y * D + mh * 128] = __float2bfloat16_rn(b);
+                } else {
+                    f2_unpack(x2, a, b);
+                    float *acc = P.part_acc + (prow0 + c + e) * D + mh * 128 + t;
+                    if (one) acc[0] = a;
+                    if (two) acc[D] = b;
+                }
             }
         }
     }
