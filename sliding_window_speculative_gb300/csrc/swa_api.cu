@@ -845,14 +845,6 @@ swa_status swa::api_verify_rows(const void *q, const void *k, const void *v,
                        nullptr, nullptr, /*noalloc=*/false, /*sinks=*/0, parts);
 }
 
-bool swa::api_tc_plan(const swa_dims *dims, int32_t window, int dev, TcPlan *t) {
-    const Plan p = make_plan_with(dims, window, device_sms(dev), 2, false);
-    if (p.kernel != 2) return false;
-    *t = TcPlan{p.rows_per_tile, p.q_rows_per_tile, p.row_tiles, p.tc_n, p.splits, p.chunk,
-                (int)p.grid, p.sms, p.items, p.workspace};
-    return true;
-}
-
 cudaError_t swa::api_merge(const AttnParams &P, int head_dim, cudaStream_t s) {
     switch (head_dim) {
         case 64: return launch_merge<64>(P, s);

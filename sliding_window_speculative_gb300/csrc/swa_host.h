@@ -34,13 +34,6 @@ swa_status api_verify_rows(const void *q, const void *k, const void *v, const in
                            const int32_t *q_pos, int32_t window, float scale, void *out, float *lse,
                            const swa_dims *dims, void *parts, swa_stream_t stream);
 
-// The key-major tensor-core plan of an attention call; false if the shape has
-// none.
-struct TcPlan {
-    int rows_per_tile, q_rows_per_tile, row_tiles, n, splits, chunk, grid, sms;
-    long long items, workspace;
-};
-bool api_tc_plan(const swa_dims *dims, int32_t window, int dev, TcPlan *plan);
 // The merge of split partials (P.splits > 1).
 struct AttnParams;
 cudaError_t api_merge(const AttnParams &P, int head_dim, cudaStream_t s);

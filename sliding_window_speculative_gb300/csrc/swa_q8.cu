@@ -197,10 +197,23 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
 
 // Whether a call runs on the fp8 tensor cores straight from the cache, unless a
 // kernel is forced (2: that one; others: bf16 rows and that kernel over them).
-bool direct(const swa_dims *d, int32_t window, int sms, Plan *plan) {
+// An item's draft rows read their window for themselves; the other path reads and
+// writes a sequence's window once, in bf16, whatever the number of rows.  Up to two
+// items per window, or while every SM has at most one item, the first is faster
+// (us, first / second, 8 query heads on 2, head_dim 256; 128): 512 sequences of 8
+// rows, window 188, 41.7 / 107.6; 37.8 / 72.5; of 16 rows 89.9 / 119.2; 80.8 / 76.6;
+// 8 of 64 rows 12.2 / 14.8; 12.1 / 12.4; one of 512 rows 12.5 / 13.9; 11.9 / 11.7.
+// Past that it is not: 64 sequences of 32 rows 26.0 / 21.8; 23.9 / 19.1; 8 chunks of
+// 512 rows, window 600, 128: 82.2 / 33.9.
+bool direct(const swa_dims *d, int32_t window, int sms, const swa_paged *paged, Plan *plan) {
     const int force = swa::api_forced_kernel();
     if (force != 0 && force != 2) return false;
-    return plan_direct(d, window, sms, plan);
+    if (!plan_direct(d, window, sms, plan)) return false;
+    // (rows of a cache tensor are counted in 32 bits there)
+    if (paged != nullptr &&
+        (long long)paged->num_pages * d->num_kv_heads * paged->page_size >= (1LL << 31))
+        return false;
+    return force == 2 || plan->row_tiles <= 2 || plan->items <= sms;
 }
 
 swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
@@ -342,6 +355,10 @@ swa_status swa_q8_read(const swa_q8_cache *cache, const swa_paged *paged, const 
 
 size_t swa_q8_workspace_bytes(const swa_dims *dims, int32_t window) {
     if (swa::api_check_dims(dims, window) != SWA_OK) return 0;
+    // up to two items of 32 rows per window the cache is read in place on any device
+    Plan p;
+    if (plan_direct(dims, window, 1, &p) && p.row_tiles <= 2)
+        return swa_workspace_bytes(dims, window);
     const RowsLayout l = rows_layout(dims, window);
     swa_dims d = *dims;
     d.max_len = l.span;
@@ -372,7 +389,7 @@ swa_status swa_q8_verify_attn(const void *q, const swa_q8_cache *cache, const sw
     if (st != SWA_OK) return st;
 
     Plan plan;
-    if (direct(dims, window, swa::api_device_sms(dev), &plan))
+    if (direct(dims, window, swa::api_device_sms(dev), paged, &plan))
         return attend_direct(q, cache, paged, seq_lens, q_pos, window, scale, out, lse, dims, plan,
                              dev, fault, reinterpret_cast<cudaStream_t>(stream));
 

@@ -476,8 +476,8 @@ __device__ __forceinline__ int early_fills(const TcParams &T, const TcItem &it) 
 // fill table must be initialised and a CTA barrier passed beforehand; no
 // other thread writes the bytes these copies land in (the Q rows TMA writes
 // are never zeroed).  A withheld fill (tests of the bounded waits) is
-// posted on its barrier but not copied.  Without QT the Q rows are left out.
-template <class C, int NT, bool AP, bool SK = false, bool QT = true>
+// posted on its barrier but not copied.
+template <class C, int NT, bool AP, bool SK = false>
 __device__ __forceinline__ void issue_early_fills(const TcParams &T, const TcMaps &M,
                                                   volatile uint32_t *ftab, uint8_t *ring,
                                                   uint8_t *qs, uint64_t *bars, int warp) {
@@ -488,7 +488,6 @@ __device__ __forceinline__ void issue_early_fills(const TcParams &T, const TcMap
     const int n = early_fills<NT, AP>(T, it);
     if (n == 0) return;
     if (warp == NT) {
-        if constexpr (!QT) return;
         mbar_arrive_expect_tx(&bars[C::B_QFULL], C::SLABS * T.rows_per_tile * 128);
         for (int s = 0; s < C::SLABS; ++s)
             tma_load_3d(qs + s * C::Q_SLAB, &M.q, 64 * s, it.h * P.G, it.b * P.q_len + it.i0,
@@ -515,10 +514,10 @@ __device__ __forceinline__ void issue_early_fills(const TcParams &T, const TcMap
 // the item's first K tile so a single Q buffer does not hold back the K
 // stream.  With a fused append, the atoms of a tile from the first new row
 // on (a mixed atom from the cache, new-row atoms from k_new / v_new) land on
-// B_MIX, for the append worker to complete the fill.  Without QT the Q rows are
-// another warp's.  With `early`, the first item's first early_fills() fills and its Q rows were issued already
+// B_MIX, for the append worker to complete the fill.  With `early`, the
+// first item's first early_fills() fills and its Q rows were issued already
 // (issue_early_fills).  Waits for every copy it issued before returning.
-template <class C, int NT, int QB, bool AP, bool SK = false, bool QT = true>
+template <class C, int NT, int QB, bool AP, bool SK = false>
 __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M,
                                               const TcItem *meta, volatile uint32_t *ftab,
                                               uint8_t *ring, uint8_t *qs, uint64_t *bars,
@@ -554,7 +553,6 @@ __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M
         if (it.n_tiles == 0) continue;
         const uint32_t qb = k % QB, quse = k / QB;
         auto load_q = [&]() -> bool {
-            if constexpr (!QT) return true;
             if (!mbar_wait_bounded(&bars[C::B_QEMPTY + qb], (quse & 1) ^ 1, P.fault,
                                    kFaultCopyTimeout, P.wait_limit))
                 return false;
@@ -658,13 +656,11 @@ __device__ __forceinline__ void tile_producer(const TcParams &T, const TcMaps &M
             mbar_wait_bounded(&bars[C::B_MIX + s2], ((mix_n >> s2) & 1u) ^ 1u, P.fault,
                               kFaultCopyTimeout, P.wait_limit);
     }
-    if constexpr (QT) {
-        const uint32_t nq = k < (uint32_t)QB ? k : (uint32_t)QB;
-        for (uint32_t q = 0; q < nq; ++q) {
-            const uint32_t kq = k - 1 - q;
-            mbar_wait_bounded(&bars[C::B_QFULL + kq % QB], (kq / QB) & 1, P.fault,
-                              kFaultCopyTimeout, P.wait_limit);
-        }
+    const uint32_t nq = k < (uint32_t)QB ? k : (uint32_t)QB;
+    for (uint32_t q = 0; q < nq; ++q) {
+        const uint32_t kq = k - 1 - q;
+        mbar_wait_bounded(&bars[C::B_QFULL + kq % QB], (kq / QB) & 1, P.fault,
+                          kFaultCopyTimeout, P.wait_limit);
     }
 }
 

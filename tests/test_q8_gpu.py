@@ -8,10 +8,10 @@ u = 2^-24, w_j the row's weights and s_j = scale q.k_j:
                d = (D + 16) u scale sum |q||k| (+ 2^-20 for the exponential),
                which also covers what a query row split into two e4m3 numbers
                loses (2^-22 of its largest element, per element)
-  a weight     e^d off, then rounded to 8 bits or more (two e4m3 numbers of 4
-               significant bits behind one fp16 number: 2^-9 + 2^-11 < 2^-8),
+  a weight     e^d off, then rounded to 8 bits or more (bf16 over rows read back;
+               straight from the cache 11, in three e4m3 numbers: 2^-8 covers both),
                or, where that is more, by 2^-21 of the largest w_j |v_j|'s scale
-               (the smallest steps of the two numbers): n keys add n 2^-21 of it
+               (the smallest step of the three numbers): n keys add n 2^-21 of it
   the result   rounded to bf16: 2^-8 of itself
   lse          d + 2^-20, 2^-22 of itself
 The largest w_j 448 2^e_j is at most 2 max w_j max|v_j|."""
