@@ -140,7 +140,7 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     const int G = d->num_q_heads / d->num_kv_heads, D = d->head_dim;
     const int R = d->q_len * G;
-    if ((D != 128 && D != 256) || G > 32 ||
+    if (G > 32 ||
         (long long)d->batch * d->num_kv_heads * d->max_len >= (1LL << 31) ||
         (long long)d->batch * d->q_len * d->num_q_heads >= (1LL << 31) ||
         (long long)d->batch * d->num_kv_heads * d->q_len * kMaxSplits >= (1LL << 31))
@@ -204,7 +204,8 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
 // rows, window 188, 41.7 / 107.6; 37.8 / 72.5; of 16 rows 89.9 / 119.2; 80.8 / 76.6;
 // 8 of 64 rows 12.2 / 14.8; 12.1 / 12.4; one of 512 rows 12.5 / 13.9; 11.9 / 11.7.
 // Past that it is not: 64 sequences of 32 rows 26.0 / 21.8; 23.9 / 19.1; 8 chunks of
-// 512 rows, window 600, 128: 82.2 / 33.9.
+// 512 rows, window 600, 128: 82.2 / 33.9.  Heads of 64 always take it: the bf16
+// kernel for them has no tensor cores (64 sequences of 32 rows 24.5 / 106.6).
 bool direct(const swa_dims *d, int32_t window, int sms, const swa_paged *paged, Plan *plan) {
     const int force = swa::api_forced_kernel();
     if (force != 0 && force != 2) return false;
@@ -213,7 +214,7 @@ bool direct(const swa_dims *d, int32_t window, int sms, const swa_paged *paged, 
     if (paged != nullptr &&
         (long long)paged->num_pages * d->num_kv_heads * paged->page_size >= (1LL << 31))
         return false;
-    return force == 2 || plan->row_tiles <= 2 || plan->items <= sms;
+    return force == 2 || d->head_dim == 64 || plan->row_tiles <= 2 || plan->items <= sms;
 }
 
 swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
@@ -355,9 +356,10 @@ swa_status swa_q8_read(const swa_q8_cache *cache, const swa_paged *paged, const 
 
 size_t swa_q8_workspace_bytes(const swa_dims *dims, int32_t window) {
     if (swa::api_check_dims(dims, window) != SWA_OK) return 0;
-    // up to two items of 32 rows per window the cache is read in place on any device
+    // up to two items of 32 rows per window, or with heads of 64, the cache is read in
+    // place on any device
     Plan p;
-    if (plan_direct(dims, window, 1, &p) && p.row_tiles <= 2)
+    if (plan_direct(dims, window, 1, &p) && (p.row_tiles <= 2 || dims->head_dim == 64))
         return swa_workspace_bytes(dims, window);
     const RowsLayout l = rows_layout(dims, window);
     swa_dims d = *dims;

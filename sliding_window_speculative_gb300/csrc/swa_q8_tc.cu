@@ -13,11 +13,12 @@
 namespace swa {
 namespace {
 
-template <int D, int N>
+template <int HD, int N>
 cudaError_t launch(const Q8TcParams &A, const TcMaps &maps, int grid, cudaStream_t stream) {
+    constexpr int D = HD < 128 ? 128 : HD;
     constexpr int NT = D == 256 ? 5 : 10;  // ring slots within 227 KB of shared memory
     using C = Q8Cfg<D, N, NT>;
-    auto kern = swa_q8_tc_kernel<D, N, NT>;
+    auto kern = swa_q8_tc_kernel<HD, N, NT>;
     static std::atomic<bool> attr_done[kMaxDevices];
     const cudaError_t e = raise_smem_limit(kern, C::SMEM_BYTES, attr_done);
     if (e != cudaSuccess) return e;
@@ -43,16 +44,17 @@ cudaError_t q8_tc_launch(const Q8TcLaunch &L, cudaStream_t stream, char *err, si
     }
     const int D = L.head_dim;
     // the cache as rows of D bytes: maps as for the bf16 cache, with 128-byte
-    // slabs of 128 elements
+    // slabs of 128 elements; of rows of 64 the box's other half is past the end, which
+    // fills it with zeros
     TcMaps maps{};
     const cuuint64_t rows = (cuuint64_t)L.cache_rows;
-    const cuuint32_t slabs = (cuuint32_t)(D / 128);
+    const cuuint32_t slabs = D == 256 ? 2 : 1;
     for (int kv = 0; kv < 2; ++kv) {
         CUtensorMap *m4 = kv ? maps.v_atoms : maps.k_atoms;
         for (int bi = 0; bi < 5; ++bi) {
             const bool atom = bi == 4;
             const cuuint32_t boxes = atom ? 1u : (16u >> bi);
-            cuuint64_t dims[4] = {128, rows, slabs, 16};
+            cuuint64_t dims[4] = {(cuuint64_t)(D < 128 ? D : 128), rows, slabs, 16};
             cuuint64_t strides[3] = {(cuuint64_t)D, 128, (cuuint64_t)D * 8};
             cuuint32_t box[4] = {128, 8, slabs, boxes};
             cuuint32_t es[4] = {1, 1, 1, 1};
@@ -70,8 +72,9 @@ cudaError_t q8_tc_launch(const Q8TcLaunch &L, cudaStream_t stream, char *err, si
         }
     }
     const Q8TcParams A{L.T, L.k_exp, L.v_exp};
-    return D == 256 ? launch_n<256>(A, maps, L.n, L.grid, stream)
-                    : launch_n<128>(A, maps, L.n, L.grid, stream);
+    return D == 256   ? launch_n<256>(A, maps, L.n, L.grid, stream)
+           : D == 128 ? launch_n<128>(A, maps, L.n, L.grid, stream)
+                      : launch_n<64>(A, maps, L.n, L.grid, stream);
 }
 
 }  // namespace swa

@@ -510,19 +510,19 @@ __device__ __forceinline__ uint32_t q8_query_at(int r, int l) {
 }
 
 // The k-th item with keys, once the buffer's previous rows are done with.
-template <class C, int D, int N>
+template <class C, int HD, int N>
 __device__ __forceinline__ void q8_fetch_queries(const AttnParams &P, const TcItem &it, uint32_t k,
                                                  uint8_t *qs, uint64_t *bars,
                                                  volatile uint32_t *failed, int w,
                                                  uint32_t inv_g) {
-    constexpr int LPR = D / 8, RP = 32 / LPR;  // lanes per row, rows per pass
+    constexpr int LPR = HD / 8, RP = 32 / LPR;  // lanes per row, rows per pass
     const int lane = (int)(threadIdx.x & 31);
     const int l = lane % LPR;
     uint8_t *q = qs + (k & 1) * C::Q_BUF;
     q8_wait(&bars[C::B_QEMPTY + (k & 1)], ((k >> 1) & 1) ^ 1, P, failed);
 #pragma unroll 1
     for (int r = w + 4 * (lane / LPR); r < it.rows; r += 4 * RP) {
-        const __nv_bfloat16 *src = P.q + q8_row(P, it, inv_g, r) * D + l * 8;
+        const __nv_bfloat16 *src = P.q + q8_row(P, it, inv_g, r) * HD + l * 8;
         const uint32_t dst = smem_u32(q + q8_query_at<C>(r, l));
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + N * 128), "l"(src + 4)
@@ -530,10 +530,10 @@ __device__ __forceinline__ void q8_fetch_queries(const AttnParams &P, const TcIt
     }
 }
 
-template <class C, int D, int N>
+template <class C, int HD, int N>
 __device__ __forceinline__ void q8_queries(const TcItem &it, uint32_t k, uint8_t *qs, float *qsc,
                                            uint64_t *bars, int w) {
-    constexpr int LPR = D / 8, RP = 32 / LPR;
+    constexpr int LPR = HD / 8, RP = 32 / LPR;
     const int lane = (int)(threadIdx.x & 31);
     const int sub = lane / LPR, l = lane % LPR;
     uint8_t *q = qs + (k & 1) * C::Q_BUF;
@@ -576,7 +576,7 @@ __device__ __forceinline__ void q8_queries(const TcItem &it, uint32_t k, uint8_t
 
 // Warps 12..15, second job: the k-th item's O through 1 / l to the output (or to
 // the split partials), and the rows of an item without keys.
-template <class C, int D, int N, int OB>
+template <class C, int HD, int D, int N, int OB>
 __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &it, uint32_t k,
                                             uint32_t tmem, const float *sums, float *linv,
                                             uint32_t *rowidx, uint64_t *bars,
@@ -589,14 +589,14 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
     const size_t bh = (size_t)it.b * P.Hkv + it.h;
     const size_t prow0 = (bh * P.splits + it.split) * P.R + it.row0;
     if (it.n_tiles == 0) {
-        for (int idx = t; idx < it.rows * D; idx += 128) {
-            const int r = idx / D, d = idx % D;
+        for (int idx = t; idx < it.rows * HD; idx += 128) {
+            const int r = idx / HD, d = idx % HD;
             if (P.splits == 1) {
                 const size_t orow = q8_row(P, it, inv_g, r);
-                P.out[orow * D + d] = __float2bfloat16_rn(0.f);
+                P.out[orow * HD + d] = __float2bfloat16_rn(0.f);
                 if (d == 0 && P.lse != nullptr) P.lse[orow] = NEG_INF;
             } else {
-                P.part_acc[(prow0 + r) * D + d] = 0.f;
+                P.part_acc[(prow0 + r) * HD + d] = 0.f;
                 if (d == 0) {
                     P.part_ml[(prow0 + r) * 2] = NEG_INF;
                     P.part_ml[(prow0 + r) * 2 + 1] = 0.f;
@@ -644,7 +644,7 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
         for (int e = 0; e < 8; e += 2) {
             const uint2 row = *reinterpret_cast<const uint2 *>(rows + c + e);
             const float2 l2 = *reinterpret_cast<const float2 *>(li + c + e);
-            const bool one = c + e < it.rows, two = c + e + 1 < it.rows;
+            const bool one = t < HD && c + e < it.rows, two = t < HD && c + e + 1 < it.rows;
 #pragma unroll
             for (int mh = 0; mh < MH; ++mh) {
                 auto part = [&](int p) {
@@ -654,13 +654,13 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
                 float a, b;
                 if (P.splits == 1) {
                     f2_unpack(f2_mul(x2, f2_pack(l2.x, l2.y)), a, b);
-                    if (one) out[(size_t)row.x * D + mh * 128] = __float2bfloat16_rn(a);
-                    if (two) out[(size_t)row.y * D + mh * 128] = __float2bfloat16_rn(b);
+                    if (one) out[(size_t)row.x * HD + mh * 128] = __float2bfloat16_rn(a);
+                    if (two) out[(size_t)row.y * HD + mh * 128] = __float2bfloat16_rn(b);
                 } else {
                     f2_unpack(x2, a, b);
-                    float *acc = P.part_acc + (prow0 + c + e) * D + mh * 128 + t;
+                    float *acc = P.part_acc + (prow0 + c + e) * HD + mh * 128 + t;
                     if (one) acc[0] = a;
-                    if (two) acc[D] = b;
+                    if (two) acc[HD] = b;
                 }
             }
         }
@@ -670,9 +670,12 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
     warp_arrive(&bars[C::B_OFREE + ob]);
 }
 
-template <int D, int N, int NT>
+// HD: head_dim.  Rows of 64 lie in tiles of D = 128 dims like rows of 128: the TMA
+// fills what is past their end with zeros.
+template <int HD, int N, int NT>
 __global__ void __launch_bounds__(kQ8TcThreads, 1)
     swa_q8_tc_kernel(const __grid_constant__ Q8TcParams A, const __grid_constant__ TcMaps M) {
+    constexpr int D = HD < 128 ? 128 : HD;
     using C = Q8Cfg<D, N, NT>;
     using namespace tc;
     constexpr int MH = D / 128, OB = 2;
@@ -956,6 +959,15 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                     if (lane < (t == 0 ? 4 : 3)) q8_wait_here(bar, par, P, failed);
                     __syncwarp();
                 }
+                if (r0 >= it.rows) {
+                    // none of this group's rows exists (their columns are never
+                    // looked at): only the barriers are kept going
+                    if (lane < 3)
+                        mbar_arrive(&bars[lane == 0   ? C::B_SFREE + h
+                                          : lane == 1 ? C::B_TEMPTY + slot
+                                                      : C::B_PFULL + h]);
+                    continue;
+                }
                 const float2 key = tabs[slot * kTcTileKeys + lk];
                 fence_after_sync();
                 // u = (S_hi + S_lo / 16) * row scale * key factor + e_v
@@ -1116,7 +1128,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
         auto fetch = [&]() {
             for (next.n_tiles = 0; jq < n_items && next.n_tiles == 0; ++jq) next = q8_item(T, jq, meta);
             if (next.n_tiles > 0)
-                q8_fetch_queries<C, D, N>(P, next, kq++, qs, bars, failed, w, inv_g);
+                q8_fetch_queries<C, HD, N>(P, next, kq++, qs, bars, failed, w, inv_g);
         };
         fetch();
         // queries one item ahead of the epilogues
@@ -1126,11 +1138,11 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
             it.n_tiles = 1;
             if (j >= 0) it = q8_item(T, j, meta);
             if (it.n_tiles > 0 && next.n_tiles > 0) {
-                q8_queries<C, D, N>(next, kq - 1, qs, qsc, bars, w);
+                q8_queries<C, HD, N>(next, kq - 1, qs, qsc, bars, w);
                 fetch();
             }
             if (j < 0) continue;
-            q8_epilogue<C, D, N, OB>(P, it, k, tmem, sums, linv, rowidx, bars, failed, inv_g);
+            q8_epilogue<C, HD, D, N, OB>(P, it, k, tmem, sums, linv, rowidx, bars, failed, inv_g);
             if (it.n_tiles > 0) ++k;
         }
     }
