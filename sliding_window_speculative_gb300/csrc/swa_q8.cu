@@ -58,6 +58,11 @@ struct Shape {
     int unroll, chunks;
     dim3 grid;
 };
+// Four rows at once, their loads all in flight, where a unit has that many rows for
+// every group of lanes and every SM still gets two CTAs; otherwise one.  Measured, head
+// dim 256, 2 heads, q tokens written and n read back per sequence, one row / four, us:
+// 512 sequences, 64 and 64: 59.5 / 35.5; 64 of them 10.0 / 9.4; 512 of 8 and 8 (16 and
+// 8 rows per unit) 9.9 / 11.2; 8 of 8 and 64 (64 CTAs) 3.4 / 4.1.
 Shape shape_of(long long units, long long rows, int D, int sms) {
     Shape f;
     for (f.unroll = 4;; f.unroll = 1) {
@@ -65,8 +70,7 @@ Shape shape_of(long long units, long long rows, int D, int sms) {
         f.chunks = (int)((rows + per - 1) / per);
         const long long ctas = units * f.chunks;
         f.grid = dim3((unsigned)(ctas < 0x7fffffffLL ? ctas : 0x7fffffffLL));
-        // four rows at once once that still gives every SM a few CTAs
-        if (f.unroll == 1 || ctas >= 8LL * sms) return f;
+        if (f.unroll == 1 || (rows >= per && ctas >= 2LL * sms)) return f;
     }
 }
 
@@ -161,9 +165,11 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     if (d->num_splits > 0) {
         const int n = d->num_splits < kMaxSplits ? d->num_splits : kMaxSplits;
         chunk = (span + n - 1) / n;
-    } else if (units < sms && item > 3 * kTileKeys) {
-        // as many items as SMs, whole tiles each; up to three tiles a split costs more
-        // (partials, a merge) than it wins
+    } else if (units < sms && item > 8 * kTileKeys) {
+        // as many items as SMs, whole tiles each; up to eight tiles a split costs more
+        // (partials, a merge) than it wins (8 sequences of 8 rows, 8 heads of 256 on 2,
+        // unsplit / split, us: window 188 8.1 / 10.2, 500 10.0 / 11.7, 1000 13.1 / 13.5,
+        // 2000 19.3 / 15.0)
         long long n = sms / units;
         if (n > (item + kTileKeys - 1) / kTileKeys) n = (item + kTileKeys - 1) / kTileKeys;
         chunk = (item + n - 1) / n;
@@ -173,13 +179,17 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     p.chunk = (int)chunk;
     p.splits = ceil_div(span, chunk);
     if (d->num_splits == 0) {
-        // fewer rows per item while many SMs would stay idle
+        // fewer rows per item while many SMs would stay idle: 8 while that gives up to
+        // 2/5 of the SMs an item, 16 up to 3/5 (8 rows of 4 heads per KV head, head_dim
+        // 256, window 188, 8 / 16 / 32 rows per item, us: 1 sequence 7.3 / 7.9 / 10.1, 6
+        // 7.9 / 8.1 / 10.1, 12 10.1 / 8.2 / 10.3, 20 14.8 / 10.1 / 10.3, 48 16.2 / 13.2
+        // / 12.3)
         const long long per_unit = (long long)d->batch * d->num_kv_heads * p.splits;
         for (int r : {8, 16}) {
             const int rows = r < G ? G : r / G * G;
             if (rows >= p.rows) break;
             const long long n = per_unit * ceil_div(d->q_len, rows / G);
-            if (r == 8 ? n * 16 <= sms : n * 5 <= 3LL * sms) {
+            if (n * 5 <= (r == 8 ? 2LL : 3LL) * sms) {
                 rows_of(r);
                 break;
             }
@@ -195,17 +205,29 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     return true;
 }
 
+// Whether reading the windows in place is the faster way whatever the device.  An
+// item's draft rows read their window for themselves; the other path reads and writes
+// a sequence's window once, in bf16, whatever the number of rows.  With one item per
+// window the first is faster, with two as well unless heads are of 128 and windows
+// short; heads of 64 always take it (the bf16 kernel for them has no tensor cores).
+// Measured, 8 query heads on 2, first / second, us:
+//   512 sequences of 8 rows, window 188      256: 41.5 / 107.5  128: 38.8 / 72.6
+//   512 of 16 rows, window 188 (two items)   256: 89.6 / 118.7  128: 82.4 / 76.8
+//   512 of 16 rows, window 1024              256: 230 / 481     128: 211 / 280
+//   64 of 32 rows, window 188 (four)         256: 26.1 / 22.3   128: 24.5 / 16.6
+//                                            64: 24.5 / 106.6
+//   8 of 512 rows, window 600 (64)                              128: 82.2 / 33.6
+bool in_place(const swa_dims *d, int32_t window, const Plan &p) {
+    const long long span = (long long)window + d->q_len - 1;
+    return d->head_dim == 64 || p.row_tiles == 1 ||
+           (p.row_tiles == 2 && (d->head_dim == 256 || span > 4 * kTileKeys));
+}
+
 // Whether a call runs on the fp8 tensor cores straight from the cache, unless a
-// kernel is forced (2: that one; others: bf16 rows and that kernel over them).
-// An item's draft rows read their window for themselves; the other path reads and
-// writes a sequence's window once, in bf16, whatever the number of rows.  Up to two
-// items per window, or while every SM has at most one item, the first is faster
-// (us, first / second, 8 query heads on 2, head_dim 256; 128): 512 sequences of 8
-// rows, window 188, 41.7 / 107.6; 37.8 / 72.5; of 16 rows 89.9 / 119.2; 80.8 / 76.6;
-// 8 of 64 rows 12.2 / 14.8; 12.1 / 12.4; one of 512 rows 12.5 / 13.9; 11.9 / 11.7.
-// Past that it is not: 64 sequences of 32 rows 26.0 / 21.8; 23.9 / 19.1; 8 chunks of
-// 512 rows, window 600, 128: 82.2 / 33.9.  Heads of 64 always take it: the bf16
-// kernel for them has no tensor cores (64 sequences of 32 rows 24.5 / 106.6).
+// kernel is forced (2: that one; others: bf16 rows and that kernel over them).  While
+// every SM has at most one item that is the faster way for any number of rows: one
+// sequence of 512 rows, window 188, 256: 12.6 / 14.0, 128: 12.0 / 11.6; 8 of 64 rows
+// 12.3 / 14.7, 12.2 / 12.6.
 bool direct(const swa_dims *d, int32_t window, int sms, const swa_paged *paged, Plan *plan) {
     const int force = swa::api_forced_kernel();
     if (force != 0 && force != 2) return false;
@@ -214,7 +236,7 @@ bool direct(const swa_dims *d, int32_t window, int sms, const swa_paged *paged, 
     if (paged != nullptr &&
         (long long)paged->num_pages * d->num_kv_heads * paged->page_size >= (1LL << 31))
         return false;
-    return force == 2 || d->head_dim == 64 || plan->row_tiles <= 2 || plan->items <= sms;
+    return force == 2 || in_place(d, window, *plan) || plan->items <= sms;
 }
 
 swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
@@ -356,10 +378,8 @@ swa_status swa_q8_read(const swa_q8_cache *cache, const swa_paged *paged, const 
 
 size_t swa_q8_workspace_bytes(const swa_dims *dims, int32_t window) {
     if (swa::api_check_dims(dims, window) != SWA_OK) return 0;
-    // up to two items of 32 rows per window, or with heads of 64, the cache is read in
-    // place on any device
     Plan p;
-    if (plan_direct(dims, window, 1, &p) && (p.row_tiles <= 2 || dims->head_dim == 64))
+    if (plan_direct(dims, window, 1, &p) && in_place(dims, window, p))
         return swa_workspace_bytes(dims, window);
     const RowsLayout l = rows_layout(dims, window);
     swa_dims d = *dims;

@@ -47,8 +47,8 @@ struct Q8AppendParams {
 // What bounds both kernels is the one read and one write of the rows.  A CTA takes
 // U rows per group of lanes from one sequence (and one of K and V), all loads in
 // flight at once; the sequence is found by one division per CTA.
-// Measured, 512 sequences of 64 tokens and 2 heads of 256 written into pages and read
-// back (202 MB): 58 us with one row at a time and its indices from 64-bit divisions.
+// Measured: 512 sequences of 64 tokens and 2 heads of 256 written into pages of 16 and
+// read back (202 MB) 46 us, 4.4 TB/s; 59 with one row at a time.
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     uint32_t r;

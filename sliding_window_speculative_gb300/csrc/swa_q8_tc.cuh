@@ -28,12 +28,22 @@
 // u: weights are resolved relative to what they contribute to the result, so a
 // heavy key of small values does not push the others below the format's range.
 //
+// Heads of 64 lie in tiles of 128 dims: the TMA fills what is past a row's end with
+// zeros, and the kernel is that of 128.
+//
 // What bounds it beside the cache's bytes is the instruction caches: sixteen warps
 // of five roles run different code, and a warp that runs straight through code that
 // the nearest cache (some hundred instructions for four warps) does not hold waits
 // for every line of it.  Unrolled, the kernel issued an instruction in 30% of its
 // cycles and a single MMA took 100 cycles to issue; so the loops over rows stay
-// rolled, eight rows a turn.
+// rolled, eight rows a turn, and what is rare is out of line (512 sequences of 8
+// rows, 4 heads of 256 to a KV head, window 1024: 125 -> 103 us; of one row 103 -> 82).
+// Tried and not kept: two tiles per softmax turn (125), two independent pipelines of
+// half the ring each (145), a warpgroup to every other tile for up to 8 rows (103).
+// Measured, of the bytes' time at 6.78 TB/s: those calls 83% and 97%, window 188 48%
+// (an item of two tiles costs 6 us from its queries to its output), 4 sequences of
+// 32768 keys, heads of 128 in pages of 64: 47%: at
+// their lengths 124 SMs have keys, at 1.1 us a tile (a tile's bytes take 0.7).
 //
 // Warp roles (512 threads; the registers of the first and last warpgroup that
 // they do not need go to the softmax):
