@@ -84,9 +84,17 @@ cudaError_t read_as(const swa::Q8ReadParams &A, const Shape &f, cudaStream_t s) 
     return swa::launch_kernel(swa::swa_q8_read_kernel<D, U>, f.grid, dim3(swa::kQ8Threads), 0, s, A);
 }
 
+uint32_t page_inv(const swa::AttnParams &P) {
+    return P.page_size > 0 ? 0xffffffffu / (uint32_t)P.page_size : 0;
+}
+
 cudaError_t launch_append(swa::Q8AppendParams &A, int D, int sms, cudaStream_t s) {
     const Shape f = shape_of(2LL * A.cache.B, (long long)A.cache.q_len * A.cache.Hkv, D, sms);
     A.chunks = f.chunks;
+    const int groups = swa::kQ8Threads * 8 / D;
+    A.step_tok = groups / A.cache.Hkv;
+    A.step_h = groups % A.cache.Hkv;
+    A.page_inv = page_inv(A.cache);
     if (f.unroll == 1)
         return D == 64    ? append_as<64, 1>(A, f, s)
                : D == 128 ? append_as<128, 1>(A, f, s)
@@ -99,6 +107,7 @@ cudaError_t launch_append(swa::Q8AppendParams &A, int D, int sms, cudaStream_t s
 cudaError_t launch_read(swa::Q8ReadParams &A, int D, int sms, cudaStream_t s) {
     const Shape f = shape_of(2LL * A.cache.B * A.cache.Hkv, A.n, D, sms);
     A.chunks = f.chunks;
+    A.page_inv = page_inv(A.cache);
     if (f.unroll == 1)
         return D == 64    ? read_as<64, 1>(A, f, s)
                : D == 128 ? read_as<128, 1>(A, f, s)

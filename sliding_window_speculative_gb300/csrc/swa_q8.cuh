@@ -35,6 +35,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// (2^e, 2^e) in bf16 for e in [-126, 127]
+__device__ __forceinline__ uint32_t bf16x2_of_pow2(int e) {
+    return (uint32_t)(e + 127) * 0x00800080u;
+}
+
 struct Q8AppendParams {
     const __nv_bfloat16 *src[2];  // k_new, v_new
     long long row[2];             // elements from one token to the next
@@ -42,13 +52,31 @@ struct Q8AppendParams {
     int8_t *exp[2];
     AttnParams cache;  // seq_lens, q_pos, q_len, Hkv, L, the block table
     int chunks;        // of one sequence's q_len * Hkv rows
+    int step_tok, step_h;  // tokens and heads from one of a thread's rows to the next
+    uint32_t page_inv;
 };
 
 // What bounds both kernels is the one read and one write of the rows.  A CTA takes
 // U rows per group of lanes from one sequence (and one of K and V), all loads in
 // flight at once; the sequence is found by one division per CTA.
 // Measured: 512 sequences of 64 tokens and 2 heads of 256 written into pages of 16 and
-// read back (202 MB) 46 us, 4.4 TB/s; 59 with one row at a time.
+// read back (202 MB) 39.5 us, 5.1 TB/s; 59 with one row at a time and divisions.
+
+// The cache row of position pos of head h, as cache_row, the page found without a
+// division: page_inv = (2^32 - 1) / page_size gives the quotient or one less.
+__device__ __forceinline__ long long q8_cache_row(const AttnParams &P, uint32_t page_inv, int b,
+                                                  int h, uint32_t pos, bool *bad) {
+    if (P.block_table == nullptr) return ((long long)b * P.Hkv + h) * P.L + pos;
+    const uint32_t ps = (uint32_t)P.page_size;
+    uint32_t blk = __umulhi(pos, page_inv), in = pos - blk * ps;
+    if (in >= ps) {
+        ++blk;
+        in -= ps;
+    }
+    const int page =
+        checked_page(P, __ldg(P.block_table + (long long)b * P.max_blocks + blk), bad);
+    return ((long long)page * P.Hkv + h) * ps + in;
+}
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -89,20 +117,26 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_append_kernel(const Q8Appen
         if (end > P.L) end = P.L;
         uint4 w[U];
         long long to[U];  // cache rows, -1: none
+        int tok = r0 / P.Hkv, h = r0 - tok * P.Hkv;
+        const __nv_bfloat16 *src = A.src[kv] + (long long)b * P.q_len * A.row[kv] + l * 8;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int r = r0 + GROUPS * j, tok = r / P.Hkv, h = r - tok * P.Hkv;
             w[j] = make_uint4(0, 0, 0, 0);
-            if (r < n)
-                w[j] = __ldcs(reinterpret_cast<const uint4 *>(
-                    A.src[kv] + ((long long)b * P.q_len + tok) * A.row[kv] + (long long)h * D +
-                    l * 8));
             to[j] = -1;
-            const long long pos = q_pos + tok;
-            if (r < n && pos >= 0 && pos < end) {
-                bool bad = false;
-                const long long row = cache_row(P, b, h, (int)pos, &bad);
-                if (!bad) to[j] = row;
+            if (r0 + GROUPS * j < n) {
+                w[j] = __ldcs(reinterpret_cast<const uint4 *>(src + tok * A.row[kv] + h * D));
+                const long long pos = q_pos + tok;
+                if (pos >= 0 && pos < end) {
+                    bool bad = false;
+                    const long long row = q8_cache_row(P, A.page_inv, b, h, (uint32_t)pos, &bad);
+                    if (!bad) to[j] = row;
+                }
+            }
+            tok += A.step_tok;
+            h += A.step_h;
+            if (h >= P.Hkv) {
+                h -= P.Hkv;
+                ++tok;
             }
         }
 #pragma unroll
@@ -125,14 +159,16 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_append_kernel(const Q8Appen
             // a = 1.f 2^k: 448 = 1.75 2^8 holds it at e = k - 8 up to 1.75, else k - 7
             int e = (int)(a >> 7) - 127 - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
             e = e < kQ8MinExp ? kQ8MinExp : (e > kQ8MaxExp ? kQ8MaxExp : e);
-            const float sc = pow2f(-e);
-            uint32_t y[2];
+            // (the product is exact, or below any e4m3 number)
+            const uint32_t sc = bf16x2_of_pow2(-e);
+            uint32_t y[4];
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                y[p] = (uint32_t)e4m3x2(bf16lo(u[2 * p]) * sc, bf16hi(u[2 * p]) * sc) |
-                       ((uint32_t)e4m3x2(bf16lo(u[2 * p + 1]) * sc, bf16hi(u[2 * p + 1]) * sc) << 16);
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t z = bf16x2_mul(u[p], sc);
+                y[p] = e4m3x2(bf16lo(z), bf16hi(z));
+            }
             if (to[j] < 0) continue;
-            *reinterpret_cast<uint2 *>(A.dst[kv] + to[j] * D + l * 8) = make_uint2(y[0], y[1]);
+            *reinterpret_cast<uint2 *>(A.dst[kv] + to[j] * D + l * 8) = make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
             if (l == 0) A.exp[kv][to[j]] = (int8_t)e;
         }
     }
@@ -146,6 +182,7 @@ struct Q8ReadParams {
     const int32_t *start;   // first position of each sequence; NULL: that of its window
     int32_t *shifted;       // (start NULL) [2][B]: lengths and q_pos counted from there
     int n, chunks;          // positions per sequence; chunks of them
+    uint32_t page_inv;
 };
 
 // First position of a sequence's windows, in [0, L].
@@ -183,6 +220,7 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_read_kernel(const Q8ReadPar
         if constexpr (kDebugChecks)
             if (threadIdx.x == 0 && (end < 0 || end > P.L)) debug_oob(P.fault);
         if (end > P.L) end = P.L;
+        __nv_bfloat16 *dst = A.dst[kv] + unit * A.n * D + l * 8;
         uint2 w[U];
         int e[U];
 #pragma unroll
@@ -192,7 +230,7 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_read_kernel(const Q8ReadPar
             w[j] = make_uint2(0, 0);
             e[j] = 0;
             if (i < A.n && pos >= 0 && pos < end) {
-                const long long row = cache_row(P, b, h, (int)pos);
+                const long long row = q8_cache_row(P, A.page_inv, b, h, (uint32_t)pos, nullptr);
                 w[j] = __ldcs(reinterpret_cast<const uint2 *>(A.src[kv] + row * D + l * 8));
                 e[j] = A.exp[kv][row];
             }
@@ -201,16 +239,16 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_read_kernel(const Q8ReadPar
         for (int j = 0; j < U; ++j) {
             const int i = i0 + GROUPS * j;
             if (i >= A.n) break;
-            const float sc = pow2f(e[j] < -126 ? -126 : e[j]);
+            const uint32_t sc = bf16x2_of_pow2(e[j] < -126 ? -126 : e[j]);
             const uint32_t u[2] = {w[j].x, w[j].y};
             uint32_t o[4];
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const uint32_t f = e4m3x2_to_f16x2((uint16_t)(u[p >> 1] >> (16 * (p & 1))));
                 const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-                o[p] = pack_bf16x2(x.x * sc, x.y * sc);
+                o[p] = bf16x2_mul(pack_bf16x2(x.x, x.y), sc);  // (a bf16 number times a power of two)
             }
-            *reinterpret_cast<uint4 *>(A.dst[kv] + (unit * A.n + i) * D + l * 8) =
+            *reinterpret_cast<uint4 *>(dst + (long long)i * D) =
                 make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
