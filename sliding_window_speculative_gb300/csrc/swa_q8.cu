@@ -56,32 +56,29 @@ void set_cache(swa::AttnParams &P, const swa_paged *paged, const swa_dims *d,
 // CTAs of U rows per group of lanes: chunks of `rows` rows for each of `units`.
 struct Shape {
     int unroll, chunks;
-    dim3 grid;
 };
 // Four rows at once, their loads all in flight, where a unit has that many rows for
 // every group of lanes and every SM still gets two CTAs; otherwise one.  Measured, head
 // dim 256, 2 heads, q tokens written and n read back per sequence, one row / four, us:
-// 512 sequences, 64 and 64: 59.5 / 35.5; 64 of them 10.0 / 9.4; 512 of 8 and 8 (16 and
-// 8 rows per unit) 9.9 / 11.2; 8 of 8 and 64 (64 CTAs) 3.4 / 4.1.
+// 512 sequences, 64 and 64: 57.9 / 33.6; 64 of them 9.8 / 8.8; 512 of 8 and 8 (16 and
+// 8 rows per unit) 9.9 / 10.6; 8 of 8 and 64 (64 CTAs) 3.4 / 4.0.
 Shape shape_of(long long units, long long rows, int D, int sms) {
     Shape f;
     for (f.unroll = 4;; f.unroll = 1) {
         const int per = swa::kQ8Threads * 8 / D * f.unroll;
         f.chunks = (int)((rows + per - 1) / per);
-        const long long ctas = units * f.chunks;
-        f.grid = dim3((unsigned)(ctas < 0x7fffffffLL ? ctas : 0x7fffffffLL));
-        if (f.unroll == 1 || (rows >= per && ctas >= 2LL * sms)) return f;
+        if (f.unroll == 1 || (rows >= per && units * f.chunks >= 2LL * sms)) return f;
     }
 }
 
 template <int D, int U>
-cudaError_t append_as(const swa::Q8AppendParams &A, const Shape &f, cudaStream_t s) {
-    return swa::launch_kernel(swa::swa_q8_append_kernel<D, U>, f.grid, dim3(swa::kQ8Threads), 0, s,
+cudaError_t append_as(const swa::Q8AppendParams &A, dim3 grid, cudaStream_t s) {
+    return swa::launch_kernel(swa::swa_q8_append_kernel<D, U>, grid, dim3(swa::kQ8Threads), 0, s,
                               A);
 }
 template <int D, int U>
-cudaError_t read_as(const swa::Q8ReadParams &A, const Shape &f, cudaStream_t s) {
-    return swa::launch_kernel(swa::swa_q8_read_kernel<D, U>, f.grid, dim3(swa::kQ8Threads), 0, s, A);
+cudaError_t read_as(const swa::Q8ReadParams &A, dim3 grid, cudaStream_t s) {
+    return swa::launch_kernel(swa::swa_q8_read_kernel<D, U>, grid, dim3(swa::kQ8Threads), 0, s, A);
 }
 
 uint32_t page_inv(const swa::AttnParams &P) {
@@ -90,31 +87,32 @@ uint32_t page_inv(const swa::AttnParams &P) {
 
 cudaError_t launch_append(swa::Q8AppendParams &A, int D, int sms, cudaStream_t s) {
     const Shape f = shape_of(2LL * A.cache.B, (long long)A.cache.q_len * A.cache.Hkv, D, sms);
-    A.chunks = f.chunks;
+    const dim3 grid(2u * (unsigned)f.chunks, (unsigned)A.cache.B);  // (at most 65535 sequences)
     const int groups = swa::kQ8Threads * 8 / D;
     A.step_tok = groups / A.cache.Hkv;
     A.step_h = groups % A.cache.Hkv;
     A.page_inv = page_inv(A.cache);
     if (f.unroll == 1)
-        return D == 64    ? append_as<64, 1>(A, f, s)
-               : D == 128 ? append_as<128, 1>(A, f, s)
-                          : append_as<256, 1>(A, f, s);
-    return D == 64    ? append_as<64, 4>(A, f, s)
-           : D == 128 ? append_as<128, 4>(A, f, s)
-                      : append_as<256, 4>(A, f, s);
+        return D == 64    ? append_as<64, 1>(A, grid, s)
+               : D == 128 ? append_as<128, 1>(A, grid, s)
+                          : append_as<256, 1>(A, grid, s);
+    return D == 64    ? append_as<64, 4>(A, grid, s)
+           : D == 128 ? append_as<128, 4>(A, grid, s)
+                      : append_as<256, 4>(A, grid, s);
 }
 
 cudaError_t launch_read(swa::Q8ReadParams &A, int D, int sms, cudaStream_t s) {
     const Shape f = shape_of(2LL * A.cache.B * A.cache.Hkv, A.n, D, sms);
-    A.chunks = f.chunks;
+    const unsigned z = 2u * (unsigned)A.cache.Hkv;
+    const dim3 grid((unsigned)f.chunks, (unsigned)A.cache.B, z < 65535u ? z : 65535u);
     A.page_inv = page_inv(A.cache);
     if (f.unroll == 1)
-        return D == 64    ? read_as<64, 1>(A, f, s)
-               : D == 128 ? read_as<128, 1>(A, f, s)
-                          : read_as<256, 1>(A, f, s);
-    return D == 64    ? read_as<64, 4>(A, f, s)
-           : D == 128 ? read_as<128, 4>(A, f, s)
-                      : read_as<256, 4>(A, f, s);
+        return D == 64    ? read_as<64, 1>(A, grid, s)
+               : D == 128 ? read_as<128, 1>(A, grid, s)
+                          : read_as<256, 1>(A, grid, s);
+    return D == 64    ? read_as<64, 4>(A, grid, s)
+           : D == 128 ? read_as<128, 4>(A, grid, s)
+                      : read_as<256, 4>(A, grid, s);
 }
 
 // The bf16 rows of every sequence's windows, [B, Hkv, span, D] for K and for V,

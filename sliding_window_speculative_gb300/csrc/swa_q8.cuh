@@ -51,16 +51,15 @@ struct Q8AppendParams {
     uint8_t *dst[2];
     int8_t *exp[2];
     AttnParams cache;  // seq_lens, q_pos, q_len, Hkv, L, the block table
-    int chunks;        // of one sequence's q_len * Hkv rows
     int step_tok, step_h;  // tokens and heads from one of a thread's rows to the next
     uint32_t page_inv;
 };
 
 // What bounds both kernels is the one read and one write of the rows.  A CTA takes
 // U rows per group of lanes from one sequence (and one of K and V), all loads in
-// flight at once; the sequence is found by one division per CTA.
+// flight at once; the grid is (chunks of rows, sequences).
 // Measured: 512 sequences of 64 tokens and 2 heads of 256 written into pages of 16 and
-// read back (202 MB) 39.5 us, 5.1 TB/s; 59 with one row at a time and divisions.
+// read back (202 MB) 34.2 us, 5.9 TB/s; 59 with one row at a time and divisions.
 
 // The cache row of position pos of head h, as cache_row, the page found without a
 // division: page_inv = (2^32 - 1) / page_size gives the quotient or one less.
@@ -105,72 +104,77 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_append_kernel(const Q8Appen
     const AttnParams &P = A.cache;
     const int l = threadIdx.x % LPR;
     const int n = P.q_len * P.Hkv;  // rows of a sequence: token, then head
-    for (long long c = blockIdx.x; c < 2LL * P.B * A.chunks; c += gridDim.x) {
-        // (K's and V's rows of a token are neighbours in a fused projection)
-        const int kv = (int)(c & 1);
-        const int b = (int)((c >> 1) / A.chunks);
-        const int r0 = (int)((c >> 1) - (long long)b * A.chunks) * (GROUPS * U) + threadIdx.x / LPR;
-        const long long q_pos = P.q_pos[b];
-        long long end = P.seq_lens[b];
-        if constexpr (kDebugChecks)
-            if (threadIdx.x == 0 && (end < 0 || end > P.L)) debug_oob(P.fault);
-        if (end > P.L) end = P.L;
-        uint4 w[U];
-        long long to[U];  // cache rows, -1: none
-        int tok = r0 / P.Hkv, h = r0 - tok * P.Hkv;
-        const __nv_bfloat16 *src = A.src[kv] + (long long)b * P.q_len * A.row[kv] + l * 8;
+    // (K's and V's rows of a token are neighbours in a fused projection)
+    const int kv = (int)(blockIdx.x & 1);
+    const int r0 = (int)(blockIdx.x >> 1) * (GROUPS * U) + threadIdx.x / LPR;
+    const int b = (int)blockIdx.y;
+    uint4 w[U];
+    long long to[U];  // cache rows, -1: none
+    int tok[U], h[U];
+    tok[0] = r0 / P.Hkv;
+    h[0] = r0 - tok[0] * P.Hkv;
+    const __nv_bfloat16 *src = A.src[kv] + (long long)b * P.q_len * A.row[kv] + l * 8;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            w[j] = make_uint4(0, 0, 0, 0);
-            to[j] = -1;
-            if (r0 + GROUPS * j < n) {
-                w[j] = __ldcs(reinterpret_cast<const uint4 *>(src + tok * A.row[kv] + h * D));
-                const long long pos = q_pos + tok;
-                if (pos >= 0 && pos < end) {
-                    bool bad = false;
-                    const long long row = q8_cache_row(P, A.page_inv, b, h, (uint32_t)pos, &bad);
-                    if (!bad) to[j] = row;
-                }
-            }
-            tok += A.step_tok;
-            h += A.step_h;
-            if (h >= P.Hkv) {
-                h -= P.Hkv;
-                ++tok;
+    for (int j = 0; j < U; ++j) {
+        if (j > 0) {
+            tok[j] = tok[j - 1] + A.step_tok;
+            h[j] = h[j - 1] + A.step_h;
+            if (h[j] >= P.Hkv) {
+                h[j] -= P.Hkv;
+                ++tok[j];
             }
         }
+        w[j] = make_uint4(0, 0, 0, 0);
+        if (r0 + GROUPS * j < n)
+            w[j] = __ldcs(reinterpret_cast<const uint4 *>(src + tok[j] * A.row[kv] + h[j] * D));
+    }
+    const long long q_pos = P.q_pos[b];
+    long long end = P.seq_lens[b];
+    if constexpr (kDebugChecks)
+        if (threadIdx.x == 0 && (end < 0 || end > P.L)) debug_oob(P.fault);
+    if (end > P.L) end = P.L;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-            // the largest magnitude: a bf16's bits without the sign rise with it
-            uint32_t a = row_max<LPR>(max_u16x2(max_u16x2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu),
-                                                max_u16x2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu)));
-            if (a >= 0x7f80u) {
-                // infinities or NaN: NaN all, the largest of the others
-                uint32_t fin = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t v = (u[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
-                    if (v >= 0x7f80u) u[e >> 1] |= 0x7fffu << (16 * (e & 1));
-                    else fin = max(fin, v);
-                }
-                a = row_max<LPR>(fin);
-            }
-            // a = 1.f 2^k: 448 = 1.75 2^8 holds it at e = k - 8 up to 1.75, else k - 7
-            int e = (int)(a >> 7) - 127 - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
-            e = e < kQ8MinExp ? kQ8MinExp : (e > kQ8MaxExp ? kQ8MaxExp : e);
-            // (the product is exact, or below any e4m3 number)
-            const uint32_t sc = bf16x2_of_pow2(-e);
-            uint32_t y[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const uint32_t z = bf16x2_mul(u[p], sc);
-                y[p] = e4m3x2(bf16lo(z), bf16hi(z));
-            }
-            if (to[j] < 0) continue;
-            *reinterpret_cast<uint2 *>(A.dst[kv] + to[j] * D + l * 8) = make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
-            if (l == 0) A.exp[kv][to[j]] = (int8_t)e;
+    for (int j = 0; j < U; ++j) {
+        to[j] = -1;
+        const long long pos = q_pos + tok[j];
+        if (r0 + GROUPS * j < n && pos >= 0 && pos < end) {
+            bool bad = false;
+            const long long row = q8_cache_row(P, A.page_inv, b, h[j], (uint32_t)pos, &bad);
+            if (!bad) to[j] = row;
         }
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        // the largest magnitude: a bf16's bits without the sign rise with it
+        uint32_t a = row_max<LPR>(max_u16x2(max_u16x2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu),
+                                            max_u16x2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu)));
+        if (a >= 0x7f80u) {
+            // infinities or NaN: NaN all, the largest of the others
+            uint32_t fin = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t v = (u[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+                if (v >= 0x7f80u) u[e >> 1] |= 0x7fffu << (16 * (e & 1));
+                else fin = max(fin, v);
+            }
+            a = row_max<LPR>(fin);
+        }
+        // a = 1.f 2^k: 448 = 1.75 2^8 holds it at e = k - 8 up to 1.75, else k - 7
+        int e = (int)(a >> 7) - 127 - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
+        e = e < kQ8MinExp ? kQ8MinExp : (e > kQ8MaxExp ? kQ8MaxExp : e);
+        // (the product is exact, or below any e4m3 number)
+        const uint32_t sc = bf16x2_of_pow2(-e);
+        uint32_t y[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t z = bf16x2_mul(u[p], sc);
+            y[p] = e4m3x2(bf16lo(z), bf16hi(z));
+        }
+        if (to[j] < 0) continue;
+        *reinterpret_cast<uint2 *>(A.dst[kv] + to[j] * D + l * 8) =
+            make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
+        if (l == 0) A.exp[kv][to[j]] = (int8_t)e;
     }
 }
 
@@ -181,7 +185,7 @@ struct Q8ReadParams {
     AttnParams cache;       // seq_lens, Hkv, L, the block table
     const int32_t *start;   // first position of each sequence; NULL: that of its window
     int32_t *shifted;       // (start NULL) [2][B]: lengths and q_pos counted from there
-    int n, chunks;          // positions per sequence; chunks of them
+    int n;                  // positions per sequence
     uint32_t page_inv;
 };
 
@@ -199,22 +203,17 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_read_kernel(const Q8ReadPar
     grid_dep_trigger();
     const AttnParams &P = A.cache;
     const int l = threadIdx.x % LPR;
-    if (A.start == nullptr) {
-        for (long long b = (long long)blockIdx.x * kQ8Threads + threadIdx.x; b < P.B;
-             b += (long long)gridDim.x * kQ8Threads) {
-            const int lo = q8_window_start(P, (int)b);
-            const long long len = min((long long)P.seq_lens[b], (long long)P.L) - lo;
-            A.shifted[b] = (int)(len < 0 ? 0 : (len > A.n ? A.n : len));
-            A.shifted[P.B + b] = (int)max((long long)P.q_pos[b] - lo, -(1LL << 31));
-        }
+    const int b = (int)blockIdx.y;
+    if (A.start == nullptr && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
+        const int lo = q8_window_start(P, b);
+        const long long len = min((long long)P.seq_lens[b], (long long)P.L) - lo;
+        A.shifted[b] = (int)(len < 0 ? 0 : (len > A.n ? A.n : len));
+        A.shifted[P.B + b] = (int)max((long long)P.q_pos[b] - lo, -(1LL << 31));
     }
-    const long long units = (long long)P.B * P.Hkv;
-    for (long long c = blockIdx.x; c < 2 * units * A.chunks; c += gridDim.x) {
-        const long long uk = c / A.chunks;
-        const int i0 = (int)(c - uk * A.chunks) * (GROUPS * U) + threadIdx.x / LPR;
-        const int kv = uk >= units;
-        const long long unit = uk - (kv ? units : 0);
-        const int b = (int)(unit / P.Hkv), h = (int)(unit - (long long)b * P.Hkv);
+    const int i0 = (int)blockIdx.x * (GROUPS * U) + threadIdx.x / LPR;
+    for (int z = (int)blockIdx.z; z < 2 * P.Hkv; z += (int)gridDim.z) {
+        const int kv = z & 1, h = z >> 1;
+        const long long unit = (long long)b * P.Hkv + h;
         const long long first = A.start ? (long long)A.start[b] : q8_window_start(P, b);
         long long end = P.seq_lens[b];
         if constexpr (kDebugChecks)
@@ -246,10 +245,9 @@ __global__ void __launch_bounds__(kQ8Threads) swa_q8_read_kernel(const Q8ReadPar
             for (int p = 0; p < 4; ++p) {
                 const uint32_t f = e4m3x2_to_f16x2((uint16_t)(u[p >> 1] >> (16 * (p & 1))));
                 const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-                o[p] = bf16x2_mul(pack_bf16x2(x.x, x.y), sc);  // (a bf16 number times a power of two)
+                o[p] = bf16x2_mul(pack_bf16x2(x.x, x.y), sc);  // (bf16 times a power of two)
             }
-            *reinterpret_cast<uint4 *>(dst + (long long)i * D) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(dst + (long long)i * D) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
