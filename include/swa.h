@@ -280,7 +280,7 @@ typedef struct {
  * [0, min(seq_lens[b], max_len)); other rows are dropped and no other byte of
  * the cache changes.  k_new / v_new must not overlap the cache.  Asynchronous on
  * `stream`, no workspace, no state; errors as for swa_verify_attn. */
-swa_status swa_q8_append(const void *k_new, const void *v_new, int64_t k_row, int64_t v_row,
+swa_status swa_q8_append(const void *k_new, const void *v_new, size_t k_row, size_t v_row,
                          const swa_q8_cache *cache, const swa_paged *paged,
                          const int32_t *seq_lens, const int32_t *q_pos, const swa_dims *dims,
                          swa_stream_t stream);

@@ -134,8 +134,7 @@ def load_library(path=LIB_PATH):
                                       i32, i32, i32, vp]
     lib.swa_sample_accept.restype = ctypes.c_int
     pd, pp, pc = ctypes.POINTER(SwaDims), ctypes.POINTER(SwaPaged), ctypes.POINTER(SwaQ8Cache)
-    i64 = ctypes.c_int64
-    lib.swa_q8_append.argtypes = [vp, vp, i64, i64, pc, pp, vp, vp, pd, vp]
+    lib.swa_q8_append.argtypes = [vp, vp, sz, sz, pc, pp, vp, vp, pd, vp]
     lib.swa_q8_append.restype = ctypes.c_int
     lib.swa_q8_read.argtypes = [pc, pp, vp, vp, i32, vp, vp, pd, vp]
     lib.swa_q8_read.restype = ctypes.c_int

@@ -60,8 +60,8 @@ struct Shape {
 // Four rows at once, their loads all in flight, where a unit has that many rows for
 // every group of lanes and every SM still gets two CTAs; otherwise one.  Measured, head
 // dim 256, 2 heads, q tokens written and n read back per sequence, one row / four, us:
-// 512 sequences, 64 and 64: 57.9 / 33.6; 64 of them 9.8 / 8.8; 512 of 8 and 8 (16 and
-// 8 rows per unit) 9.9 / 10.6; 8 of 8 and 64 (64 CTAs) 3.4 / 4.0.
+// 512 sequences, 64 and 64: 42.6 / 29.7; 64 of them 7.7 / 6.4; 512 of 8 and 8 (16 and
+// 8 rows per unit) 7.5 / 8.5; 8 of 8 and 64 (64 CTAs) 3.0 / 3.5.
 Shape shape_of(long long units, long long rows, int D, int sms) {
     Shape f;
     for (f.unroll = 4;; f.unroll = 1) {
@@ -308,7 +308,7 @@ swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_pag
 
 extern "C" {
 
-swa_status swa_q8_append(const void *k_new, const void *v_new, int64_t k_row, int64_t v_row,
+swa_status swa_q8_append(const void *k_new, const void *v_new, size_t k_row, size_t v_row,
                          const swa_q8_cache *cache, const swa_paged *paged,
                          const int32_t *seq_lens, const int32_t *q_pos, const swa_dims *dims,
                          swa_stream_t stream) {
@@ -322,11 +322,12 @@ swa_status swa_q8_append(const void *k_new, const void *v_new, int64_t k_row, in
         return api_fail(SWA_ERR_INVALID_ARG, "seq_lens and q_pos must be 4-byte aligned");
     st = check_cache(cache, paged, dims);
     if (st != SWA_OK) return st;
-    const int64_t need = (int64_t)dims->num_kv_heads * dims->head_dim;
-    for (int64_t row : {k_row, v_row})
-        if (row < need || row % 8 != 0 || row > ((int64_t)1 << 36))
-            return api_fail(SWA_ERR_INVALID_ARG, "token stride %lld elements is not a multiple of 8 "
-                            "of at least %lld", (long long)row, (long long)need);
+    const size_t need = (size_t)dims->num_kv_heads * dims->head_dim;
+    for (size_t row : {k_row, v_row})
+        if (row < need || row % 8 != 0 || row > ((size_t)1 << 36))
+            return api_fail(SWA_ERR_INVALID_ARG,
+                            "token stride %zu elements is not a multiple of 8 of at least %zu", row,
+                            need);
     int dev = 0;
     uint32_t *fault = nullptr;
     st = swa::api_device(&dev, &fault);
@@ -334,8 +335,8 @@ swa_status swa_q8_append(const void *k_new, const void *v_new, int64_t k_row, in
     swa::Q8AppendParams A{};
     A.src[0] = static_cast<const __nv_bfloat16 *>(k_new);
     A.src[1] = static_cast<const __nv_bfloat16 *>(v_new);
-    A.row[0] = k_row;
-    A.row[1] = v_row;
+    A.row[0] = (long long)k_row;
+    A.row[1] = (long long)v_row;
     A.dst[0] = static_cast<uint8_t *>(cache->k);
     A.dst[1] = static_cast<uint8_t *>(cache->v);
     A.exp[0] = cache->k_exp;
