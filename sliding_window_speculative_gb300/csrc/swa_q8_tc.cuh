@@ -42,8 +42,8 @@
 // half the ring each (145), a warpgroup to every other tile for up to 8 rows (103).
 // Measured, of the bytes' time at 6.78 TB/s: those calls 83% and 97%, window 188 48%
 // (an item of two tiles costs 6 us from its queries to its output), 4 sequences of
-// 32768 keys, heads of 128 in pages of 64: 47%: at
-// their lengths 124 SMs have keys, at 1.1 us a tile (a tile's bytes take 0.7).
+// 32768 keys, heads of 128 in pages of 64: 50% (at their lengths 124 SMs have keys, at
+// 1 us a tile, whose bytes take 0.7).
 //
 // Warp roles (512 threads; the registers of the first and last warpgroup that
 // they do not need go to the softmax):
@@ -304,10 +304,17 @@ __device__ __forceinline__ void q8_early_fills(const TcParams &T, const TcMaps &
 }
 
 // The TMA producer (warp 0): every item's K and V tiles in order into the first free
-// ring slots.  Lane s looks after slot s, so that one test finds a free one, and
-// issues the slot's copy (a paged tile's runs of pages go to a lane each, the page
+// ring slots.  Lane s looks after slot s, so that one test finds the free ones, and
+// issues its slot's copy (a paged tile's runs of pages go to a lane each, the page
 // ids read a tile ahead).  Waits for every copy it issued before returning.
-template <class C, int NT>
+//
+// A turn takes some 1000 cycles.  With PAIRS a tile's K and V share one where two
+// slots are free: for tiles of 128 dims (1350 cycles of bytes) and 16 rows, where the
+// turns are what bounds.  Elsewhere it is the softmax or the bytes, and turns apart
+// are better (one turn / two, us: 512 sequences, window 1024, heads of 128, 1 row 52.1
+// / 56.8, of 256 83.5 / 82.3; 8 rows of 128 93.0 / 92.2, of 256 104.5 / 101.4; 4
+// sequences of 32768 keys 32.2 / 34.6).
+template <class C, int NT, bool PAIRS>
 __device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, const TcItem *meta,
                                             volatile uint32_t *ftab, uint8_t *ring, uint64_t *bars,
                                             volatile uint32_t *failed) {
@@ -358,9 +365,10 @@ __device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, 
                 y = checked_page(P, page, nullptr) * P.Hkv * ps + y0 + (lane == 0 ? in0 : 0);
             }
             const int whole = min(max((n >> 3) - a, 0), run);
+            // fills of the tile issued so far
+            int done = j == 0 ? min(max(n_early - 2 * t, 0), 2) : 0;
 #pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-                if (j == 0 && 2 * t + kv < n_early) continue;
+            while (done < 2) {
                 uint32_t free;
                 int idle = 0;
                 long long since = 0;
@@ -382,27 +390,38 @@ __device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, 
                     }
                 }
                 if (!free) goto drain;
-                const int slot = __ffs((int)free) - 1;
-                if (lane == slot) {
-                    ftab[f % kFillTab] = (f << 8) | ((uses & 1) << 4) | (uint32_t)slot;
-                    mbar_arrive_expect_tx(&bars[C::B_FULL + slot], (uint32_t)natoms * C::ATOM_BYTES);
+                const uint32_t rest = free & (free - 1);
+                const bool both = PAIRS && done == 0 && rest != 0;
+                const int s0 = __ffs((int)free) - 1, s1 = both ? __ffs((int)rest) - 1 : -1;
+                const bool mine = lane == s0 || lane == s1;
+                const uint32_t fill = lane == s1 ? f + 1 : f;
+                if (mine) {
+                    ftab[fill % kFillTab] = (fill << 8) | ((uses & 1) << 4) | (uint32_t)lane;
+                    mbar_arrive_expect_tx(&bars[C::B_FULL + lane], (uint32_t)natoms * C::ATOM_BYTES);
                     ++uses;
                 }
                 __syncwarp();
-                // (tests of the bounded waits: this fill's copies are never issued)
-                if (run > 0 && (paged || lane == slot) &&
-                    !(P.withhold_fill == (int)f && blockIdx.x == 0)) {
-                    uint8_t *dst = ring + slot * C::TILE_BYTES;
-                    const CUtensorMap *m4 = kv ? M.v_atoms : M.k_atoms;
-                    // (16, 8, 4 or 2 whole atoms are one copy)
-                    if (run == whole && whole > 1 && (whole & (whole - 1)) == 0)
-                        tma_load_4d_hint(dst + a * C::ATOM_BYTES, m4 + (__clz(whole) - 27), 0, y, 0,
-                                         0, &bars[C::B_FULL + slot], policy);
-                    else
-                        q8_copy<C>(m4, kv ? &M.v_atom : &M.k_atom, y, whole, run > whole,
-                                   dst + a * C::ATOM_BYTES, &bars[C::B_FULL + slot], policy);
+                // (tests of the bounded waits: one fill's copies are never issued)
+                const int held = blockIdx.x == 0 ? P.withhold_fill : -1;
+                const int turns = paged && both ? 2 : 1;
+#pragma unroll 1
+                for (int x = 0; x < turns; ++x) {
+                    const int slot = !paged ? lane : (x ? s1 : s0);
+                    const int kv = !paged ? (lane == s1 ? 1 : done) : done + x;
+                    if ((paged ? run > 0 : mine) && held != (int)(paged ? f + x : fill)) {
+                        uint8_t *dst = ring + slot * C::TILE_BYTES + a * C::ATOM_BYTES;
+                        const CUtensorMap *m4 = kv ? M.v_atoms : M.k_atoms;
+                        // (16, 8, 4 or 2 whole atoms are one copy)
+                        if (run == whole && whole > 1 && (whole & (whole - 1)) == 0)
+                            tma_load_4d_hint(dst, m4 + (__clz(whole) - 27), 0, y, 0, 0,
+                                             &bars[C::B_FULL + slot], policy);
+                        else
+                            q8_copy<C>(m4, kv ? &M.v_atom : &M.k_atom, y, whole, run > whole, dst,
+                                       &bars[C::B_FULL + slot], policy);
+                    }
                 }
-                ++f;
+                f += both ? 2 : 1;
+                done += both ? 2 : 1;
             }
         }
     }
@@ -764,7 +783,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
     }
     if (warp == 0) {
         // ======================================================= producer
-        q8_producer<C, NT>(T, M, meta, ftab, ring, bars, failed);
+        q8_producer<C, NT, D == 128 && N == 16>(T, M, meta, ftab, ring, bars, failed);
     } else if (warp <= 2) {
         // ============================================================ MMA
         // Warp 1 issues S = K8 Q^T of every tile, warp 2 O += V8^T P^T, each as
