@@ -319,6 +319,12 @@ SHAPES = {
     "small_heads": (3, 4, 8, 4, 64, 333, 400, [400, 37, 1], [396, 33, 0], 8),
     "small_heads_block": (1, 64, 8, 2, 64, 100, 256, [256], [192], 0),
     "prefill": (1, 200, 4, 2, 128, 130, 512, [512], [312], 64),
+    # more items than SMs, many of them per window: the plan reads bf16 rows
+    "prefill_batch": (6, 130, 8, 2, 128, 100, 256, [256, 200, 130, 0, 7, 256],
+                      [126, 70, 0, 0, 3, 120], 16),
+    "prefill_batch_of_256": (3, 257, 8, 2, 256, 70, 320, [320, 257, 300], [63, 0, 40], 0),
+    "prefill_batch_of_64": (6, 130, 8, 2, 64, 100, 256, [256, 200, 130, 0, 7, 256],
+                            [126, 70, 0, 0, 3, 120], 0),
 }
 
 

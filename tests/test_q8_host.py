@@ -123,6 +123,18 @@ def test_workspace_bound(lib):
     assert swa.swa_q8_workspace_bytes(swa.make_dims(*DIMS), 188) > 0
     assert swa.swa_q8_workspace_bytes(swa.make_dims(0, 8, 8, 2, 256, 4096), 188) == 0
     assert swa.swa_q8_workspace_bytes(swa.make_dims(*DIMS), 0) == 0
+    # heads of 64, or one item of 32 packed rows per window: partials at most; otherwise
+    # the windows' bf16 rows as well
+    for D, q_len, rows in ((64, 512, False), (128, 8, False), (256, 8, False), (256, 16, False),
+                           (128, 64, True), (256, 64, True), (128, 16, True)):
+        dims = swa.make_dims(16, q_len, 8, 2, D, 4096)
+        window = 188
+        need, parts = swa.swa_q8_workspace_bytes(dims, window), swa.swa_workspace_bytes(dims, window)
+        span = 2 * 16 * 2 * (window + q_len - 1) * D * 2
+        assert need == parts if not rows else need >= span + parts, (D, q_len)
+    # a long window at two items reads in place
+    dims = swa.make_dims(16, 16, 8, 2, 128, 4096)
+    assert swa.swa_q8_workspace_bytes(dims, 1024) == swa.swa_workspace_bytes(dims, 1024)
 
 
 LOGP = dict(logits=2, keep_ids=None, tokens=16, temperature=None, logprobs=32, ranks=48, entropy=64,
