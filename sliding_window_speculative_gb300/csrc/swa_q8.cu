@@ -147,6 +147,23 @@ constexpr int kMaxSplits = 64;
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
+// Key tiles per item for `units` windows of `tiles` each: the fewest steps, of an SM's
+// items one after another, where an item costs two tiles beside its own and a split
+// six (its partials and the merge's launch) and a quarter for every part.  Measured,
+// unsplit / split: 8 sequences of 8 rows, 8 heads of 256 on 2 (16 units), window 500
+// 10.0 / 11.7 us, 1000 13.1 / 13.5, 2000 19.3 / 15.0.
+long long split_tiles(long long units, long long tiles, int sms) {
+    long long best = tiles, least = 0;
+    for (long long n = 1; n <= kMaxSplits && n <= tiles; ++n) {
+        const long long per = (tiles + n - 1) / n, parts = (tiles + per - 1) / per;
+        if (parts < n) continue;  // (no fewer tiles than with fewer parts)
+        const long long turns = (units * parts + sms - 1) / sms;
+        const long long cost = 4 * turns * (per + 2) + (n > 1 ? 24 + n : 0);
+        if (n == 1 || cost < least) least = cost, best = per;
+    }
+    return best;
+}
+
 // False where that kernel does not take the shape.
 bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     const int G = d->num_q_heads / d->num_kv_heads, D = d->head_dim;
@@ -172,15 +189,9 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     if (d->num_splits > 0) {
         const int n = d->num_splits < kMaxSplits ? d->num_splits : kMaxSplits;
         chunk = (span + n - 1) / n;
-    } else if (units < sms && item > 8 * kTileKeys) {
-        // as many items as SMs, whole tiles each; up to eight tiles a split costs more
-        // (partials, a merge) than it wins (8 sequences of 8 rows, 8 heads of 256 on 2,
-        // unsplit / split, us: window 188 8.1 / 10.2, 500 10.0 / 11.7, 1000 13.1 / 13.5,
-        // 2000 19.3 / 15.0)
-        long long n = sms / units;
-        if (n > (item + kTileKeys - 1) / kTileKeys) n = (item + kTileKeys - 1) / kTileKeys;
-        chunk = (item + n - 1) / n;
-        chunk = (chunk + kTileKeys - 1) / kTileKeys * kTileKeys;
+    } else {
+        chunk = split_tiles(units, (item + kTileKeys - 1) / kTileKeys, sms) * kTileKeys;
+        if (chunk >= item) chunk = span;
         if ((span + chunk - 1) / chunk > kMaxSplits) chunk = (span + kMaxSplits - 1) / kMaxSplits;
     }
     p.chunk = (int)chunk;
@@ -214,20 +225,26 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
 
 // Whether reading the windows in place is the faster way whatever the device.  An
 // item's draft rows read their window for themselves; the other path reads and writes
-// a sequence's window once, in bf16, whatever the number of rows.  With one item per
-// window the first is faster, with two as well unless heads are of 128 and windows
-// short; heads of 64 always take it (the bf16 kernel for them has no tensor cores).
-// Measured, 8 query heads on 2, first / second, us:
-//   512 sequences of 8 rows, window 188      256: 41.5 / 107.5  128: 38.8 / 72.6
-//   512 of 16 rows, window 188 (two items)   256: 89.6 / 118.7  128: 82.4 / 76.8
-//   512 of 16 rows, window 1024              256: 230 / 481     128: 211 / 280
-//   64 of 32 rows, window 188 (four)         256: 26.1 / 22.3   128: 24.5 / 16.6
-//                                            64: 24.5 / 106.6
-//   8 of 512 rows, window 600 (64)                              128: 82.2 / 33.6
+// a sequence's window once, in bf16, whatever the number of rows, and its kernel takes
+// more rows at a time.  So it is for one item per window, and for more of them where
+// windows are long; heads of 64 always take it (the bf16 kernel for them has no tensor
+// cores).  Measured, 8 query heads on 2, in place / over bf16 rows, us:
+//   rows x sequences, items per window      window 188     600        1024      1900
+//   8 x 512, 1        256                   41.5 / 107.5
+//   16 x 512, 2       256                   89.6 / 118.7              230 / 481
+//                     128                   82.4 / 76.8               211 / 280
+//   24 x 64, 3        256                   21.4 / 19.4  32.5 / 42.3  47.8 / 70.6  71 / 121
+//                     128                   20.4 / 15.0  31.2 / 24.0  44.0 / 37.8  66 / 70
+//   32 x 48, 4        256                   21.3 / 18.7  33.9 / 33.9  47.0 / 59.7  70 / 103
+//                     128                   20.4 / 15.1  31.4 / 22.6  44.4 / 33.5  65 / 61
+//   64 x 24, 8        256                   21.5 / 18.5  33.0 / 28.2               70 / 78
+//   128 x 12, 16      256                                33.0 / 26.5               69 / 61
+//   32 x 64, 4        64                    24.5 / 106.6
 bool in_place(const swa_dims *d, int32_t window, const Plan &p) {
-    const long long span = (long long)window + d->q_len - 1;
-    return d->head_dim == 64 || p.row_tiles == 1 ||
-           (p.row_tiles == 2 && (d->head_dim == 256 || span > 4 * kTileKeys));
+    const long long all = (long long)window + d->q_len - 1;
+    const long long span = all < d->max_len ? all : d->max_len;
+    return d->head_dim == 64 ||
+           span >= (d->head_dim == 256 ? 200LL : 800LL) * (p.row_tiles - 1);
 }
 
 // Whether a call runs on the fp8 tensor cores straight from the cache, unless a
