@@ -11,8 +11,8 @@ using swa::api_fail;
 
 namespace {
 
-template <int NT>
-cudaError_t launch(const swa::LogpParams &A, long long rows, int c, cudaStream_t s) {
+template <int NT, bool TOP>
+cudaError_t launch_as(const swa::LogpParams &A, long long rows, int c, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(rows * c));
     cfg.blockDim = dim3(NT);
@@ -27,8 +27,13 @@ cudaError_t launch(const swa::LogpParams &A, long long rows, int c, cudaStream_t
     cfg.attrs = attr;
     cfg.numAttrs = swa::pdl_enabled() ? 2 : 1;
     if (swa::launch_fault_due()) return cudaErrorLaunchOutOfResources;
-    return cudaLaunchKernelEx(&cfg, swa::swa_logprobs_kernel<NT>, A,
+    return cudaLaunchKernelEx(&cfg, swa::swa_logprobs_kernel<NT, TOP>, A,
                               c == 8 ? 3 : c >> 1);
+}
+
+template <int NT>
+cudaError_t launch(const swa::LogpParams &A, long long rows, int c, cudaStream_t s) {
+    return A.top > 0 ? launch_as<NT, true>(A, rows, c, s) : launch_as<NT, false>(A, rows, c, s);
 }
 
 cudaError_t launch_rows(const swa::LogpParams &A, long long rows, int sms, cudaStream_t s) {
@@ -46,11 +51,14 @@ cudaError_t launch_rows(const swa::LogpParams &A, long long rows, int sms, cudaS
     //   240 x 12001, 20    1 of 256 7.7, 1 of 128 9.4, 1 of 512 9.7
     //   100 x 32000, 5     2 of 256 9.2, 4 of 256 11.3, 1 of 256 10.2
     //   4000 x 1000, 5     1 of 128 24.3, 1 of 256 43.0
+    //   40880 x 3120, 0    1 of 128 153, 1 of 256 232, 1 of 32 157
+    //   20000 x 12001, 0   1 of 128 136, 1 of 256 177, 1 of 32 224
+    //   400 x 1000, 0      1 of 128 2.6, 1 of 256 3.5
     const long long nvec = ((long long)A.V + 14) / 8;
     int c = 1;
     while (c < swa::kLogpMaxCluster && rows * c * 2 <= 3LL * sms && nvec > 2048LL * c) c *= 2;
     if (c == swa::kLogpMaxCluster) return launch<512>(A, rows, c, s);
-    if (c == 1 && rows > 3LL * sms && nvec <= 8192) return launch<128>(A, rows, c, s);
+    if (c == 1 && rows > (A.top > 0 ? 3LL : 2LL) * sms && nvec <= 8192) return launch<128>(A, rows, c, s);
     return launch<256>(A, rows, c, s);
 }
 

@@ -50,11 +50,18 @@ struct LogpStats {
     int before;
 };
 
-struct LogpShared {
+struct LogpSums {
+    LogpStats warp[16];
+    LogpStats cta;                    // read by the cluster's first CTA
+    int col, infs, n_cand, n_list;
+    uint32_t least, kth[16];
+};
+
+struct LogpShared : LogpSums {
     uint32_t block[kLogpBlocks];      // a block's largest logit as a rising key
     union {
         struct {
-            uint32_t list[kLogpBlocks - 512];  // the CTA's blocks that may be among the first
+            alignas(16) uint32_t list[kLogpBlocks - 512];  // the CTA's blocks that may be first
             uint32_t lane[512];                // per thread its first block of the CTA
         };
         unsigned long long cand[kLogpMaxTop * kLogpPerBlock];
@@ -62,10 +69,6 @@ struct LogpShared {
     uint32_t best[kLogpMaxCluster * kLogpMaxTop];
     uint32_t first[kLogpMaxTop];      // the CTA's first blocks, in order
     uint32_t pick[kLogpMaxTop];       // the row's
-    LogpStats warp[16];
-    LogpStats cta;                    // read by the cluster's first CTA
-    int col, infs, n_cand, n_list;
-    uint32_t least, kth[16];
 };
 
 // Rising with the value; -0 counts as 0.
@@ -126,16 +129,16 @@ struct LogpRow {
     }
 };
 
-// C CTAs of NT threads (a cluster) per row.
-template <int NT>
-__global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1024 / NT)
+// C CTAs of NT threads (a cluster) per row; with TOP the likeliest tokens too.
+template <int NT, bool TOP>
+__global__ void __launch_bounds__(NT, NT == 128 && TOP ? 7 : 1024 / NT)
     swa_logprobs_kernel(const LogpParams A, const int log_c) {
     namespace cg = cooperative_groups;
     using namespace tc;
     constexpr int NW = NT / 32, U = 4;
     const float INF = __int_as_float(0x7f800000);
     constexpr uint32_t kNegInf2 = 0xff80ff80u, kLow2 = 0xf180f180u;  // -2^100
-    __shared__ LogpShared S;
+    __shared__ std::conditional_t<TOP, LogpShared, LogpSums> S;
     cg::cluster_group cluster = cg::this_cluster();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int C = 1 << log_c;
@@ -177,8 +180,9 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1024 / NT)
         S.infs = S.n_cand = S.n_list = 0;
         S.least = 0;
     }
-    if (A.top > 0 && !fine)
-        for (int i = t; i < n_blocks; i += NT) S.block[i] = 0;
+    if constexpr (TOP)
+        if (!fine)
+            for (int i = t; i < n_blocks; i += NT) S.block[i] = 0;
     __syncthreads();
     if (A.keep && tok >= 0) {
         const int j0 = (int)(((long long)A.V * rank) >> log_c);
@@ -231,9 +235,11 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1024 / NT)
             const float mu = logp_warp_max(own);
             n = fmaxf(n, mu);
             if (lane == k) mine = mu;
-            if (fine && A.top > 0) {
-                const long long b = (u + NW * k) * 32 + lane - b0;
-                if (b < n_blocks) S.block[b] = logp_key16(own);
+            if constexpr (TOP) {
+                if (fine) {
+                    const long long b = (u + NW * k) * 32 + lane - b0;
+                    if (b < n_blocks) S.block[b] = logp_key16(own);
+                }
             }
             uint32_t thr = u + NW * k < (tv >> 5) ? thr_before : thr_behind;
             if (exact) {
@@ -252,8 +258,9 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1024 / NT)
             for (int e = 0; e < 4; ++e) count = bf16x2_add(count, bf16x2_gt(y[e], thr));
         }
         before += (int)(bf16lo(count) + bf16hi(count));
-        if (A.top > 0 && !fine && lane < N)
-            atomicMax(&S.block[(int)(((u + NW * lane) >> (bshift - 5)) - b0)], logp_key16(mine));
+        if constexpr (TOP)
+            if (!fine && lane < N)
+                atomicMax(&S.block[(int)(((u + NW * lane) >> (bshift - 5)) - b0)], logp_key16(mine));
         if (n > m) {  // (the warp's)
             float sa, sb, wa, wb;
             f2_unpack(s2, sa, sb);
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1024 / NT)
     if (lane == 0) S.warp[warp] = LogpStats{m, s, w, before};
     __syncthreads();
     const int top = A.top;
-    if (top > 0) {
+    if constexpr (TOP) {
         // This CTA's first blocks.  A key holds a block's logit and, equal logits
         // falling, its place: all differ.  Threads' own largest keys bound the
         // top-th largest key from below: `per` of them in each warp are at least the
@@ -473,7 +480,8 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1024 / NT)
     }
 
     // -------------------------------------------------------- the first n columns
-    if (top > 0 && rank == 0) {
+    if constexpr (TOP)
+    if (rank == 0) {
         // the row's first blocks among the CTAs' by counting
         for (int i = t; i < C * top; i += NT)
             S.best[i] = C > 1 ? *cluster.map_shared_rank(&S.first[i % top], i / top) : S.first[i];
