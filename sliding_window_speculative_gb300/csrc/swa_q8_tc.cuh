@@ -126,8 +126,8 @@ struct Q8Cfg {
     // registers per thread: the launch's 128, shifted to the softmax
     static constexpr int SOFT_REGS = 160, OTHER_REGS = 256 - SOFT_REGS;
     static_assert(N == 16 || N == 32, "rows per item");
-    // (K tiles are multiplied up to four ahead of the oldest V tile: their fills
-    // entries are behind it in the table, their slots refilled)
+    // (K tiles are multiplied up to four ahead of the oldest V tile and their slots
+    // refilled, while the table still has to hold that V tile's entry)
     static_assert(NT >= 2 && NT + 5 <= kFillTab, "ring slots");
     static_assert(TMEM_USED <= 512, "TMEM");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
