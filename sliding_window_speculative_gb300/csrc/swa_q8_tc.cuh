@@ -1092,6 +1092,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                             }
                         }
                         tmem_wait_st();
+                        fence_before_sync();  // (the arrival below orders it for the next PV)
                     }
                 }
                 // P = 2^(u - ref) in e4m3 numbers; the row sum adds P 2^-e_v
