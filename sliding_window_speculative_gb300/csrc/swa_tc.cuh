@@ -1382,6 +1382,7 @@ __global__ void __launch_bounds__(AP ? kTcThreads + 32 : kTcThreads, 1)
                             }
                         }
                         tmem_wait_st();
+                        fence_before_sync();  // (the arrival below orders it for the next PV)
                     }
                 }
                 // P buffer free: its previous PV has completed

@@ -1,6 +1,6 @@
 """Attention rows whose scores rise from tile to tile, so that nearly every tile raises
 the rows' reference maxima and the accumulators in tensor memory are scaled between two
-MMAs into them.
+MMAs into them: the key-major kernels over the bf16 and the 8-bit cache.
 
 Bounds, u = 2^-24, w_j the row's weights: a score is off by d = (D + 16) u scale
 sum |q||k| + 2^-20 (products summed in fp32, the exponential), a weight by e^d and its
@@ -96,4 +96,29 @@ def test_the_8_bit_cache(B, q_len, Hq, Hkv, D, L, W, page, shape):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, again))
             _check(got, q, k8, v8, ke, ve, lens, pos, W)
+    assert swa.swa_read_device_errors() == 0
+
+
+@pytest.mark.parametrize("shape", ["rising", "zigzag", "falling"])
+@pytest.mark.parametrize("B,q_len,Hq,Hkv,D,L,W", [
+    (2, 8, 8, 2, 256, 1400, 1300), (3, 1, 4, 2, 128, 1400, 5000), (1, 24, 8, 2, 128, 1400, 1200)])
+def test_the_bf16_cache(B, q_len, Hq, Hkv, D, L, W, shape):
+    """The same of swa_verify_attn, on rows that are e4m3 numbers times 2^-6 already."""
+    import sliding_window_speculative_gb300 as swa
+    q, k, v = _rising(B, q_len, Hq, Hkv, D, L, shape, D + B)
+    k8, v8 = ((x.float() * 64).clamp(-448, 448).to(E4M3) for x in (k, v))
+    kd, vd = ((x.float() / 64).to(torch.bfloat16).cuda() for x in (k8, v8))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens = [L - 37 * b for b in range(B)]
+    pos = [n - q_len for n in lens]
+    ex = np.full((B, Hkv, L), -6)
+    codes = [x.view(torch.uint8).numpy() for x in (k8, v8)]
+    for kernel in ("tc", "rows"):
+        with forced_kernel(kernel):
+            call = lambda: swa.swa_verify_attn(q.cuda(), kd, vd, i32(lens), i32(pos), W,  # noqa: E731
+                                               D ** -0.5, num_splits=1)
+            got, again = call(), call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+        _check(got, q, *codes, ex, ex, lens, pos, W)
     assert swa.swa_read_device_errors() == 0
