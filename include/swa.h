@@ -301,7 +301,18 @@ swa_status swa_q8_read(const swa_q8_cache *cache, const swa_paged *paged, const 
 /* swa_verify_attn (paged == NULL) or swa_verify_attn_paged over an 8-bit cache:
  * the same definition with the values that the rows stand for.  Arguments,
  * preconditions, limits, the workspace rules and errors are those of these
- * calls; the workspace is bounded by swa_q8_workspace_bytes. */
+ * calls; the workspace is bounded by swa_q8_workspace_bytes.
+ *
+ * Rounding beside that of these calls: blocks of few rows, long windows and heads
+ * of 64 are attended straight from the e4m3 rows, where
+ *   - a q element is exact, or within 2^-21 of its row's largest where it is below
+ *     2^-14 of that;
+ *   - a weight w_j = exp(s_j - lse) is within 2^-14 of itself, or w_j 2^e_j (e_j:
+ *     the exponent of V's row j) within 2^-21 of the largest such product where that
+ *     is more, with offsets that cancel from key to key.  The largest is that of a
+ *     chunk of at most 8192 keys, whose outputs are joined in fp32: the bound does
+ *     not grow with the window.  num_splits forces no larger chunks.
+ * lse has no part in either. */
 swa_status swa_q8_verify_attn(const void *q, const swa_q8_cache *cache, const swa_paged *paged,
                               const int32_t *seq_lens, const int32_t *q_pos, int32_t window,
                               float scale, void *out, float *lse, const swa_dims *dims,

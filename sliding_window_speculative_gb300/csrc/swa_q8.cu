@@ -164,6 +164,13 @@ long long split_tiles(long long units, long long tiles, int sms) {
     return best;
 }
 
+// Splits that a call takes at least: an item's weights are resolved relative to the
+// largest of them, and so many keys may share one (see swa_q8_tc.cuh).  Without rows
+// that see more than that, any number will do.
+int least_splits(long long span, long long item) {
+    return item > swa::kQ8ItemKeys ? ceil_div(span, swa::kQ8ItemKeys) : 1;
+}
+
 // False where that kernel does not take the shape.
 bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     const int G = d->num_q_heads / d->num_kv_heads, D = d->head_dim;
@@ -184,14 +191,18 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
     if (span > d->max_len) span = d->max_len;
     long long item = (long long)window + p.q_rows - 1;  // keys of an item without a split
     if (item > span) item = span;
+    const int least = least_splits(span, item);
+    if (least > kMaxSplits) return false;
     const long long units = (long long)d->batch * d->num_kv_heads * p.row_tiles;
     long long chunk = span;
     if (d->num_splits > 0) {
-        const int n = d->num_splits < kMaxSplits ? d->num_splits : kMaxSplits;
+        int n = d->num_splits < kMaxSplits ? d->num_splits : kMaxSplits;
+        if (n < least) n = least;
         chunk = (span + n - 1) / n;
     } else {
         chunk = split_tiles(units, (item + kTileKeys - 1) / kTileKeys, sms) * kTileKeys;
         if (chunk >= item) chunk = span;
+        if (least > 1 && chunk > swa::kQ8ItemKeys) chunk = swa::kQ8ItemKeys;
         if ((span + chunk - 1) / chunk > kMaxSplits) chunk = (span + kMaxSplits - 1) / kMaxSplits;
     }
     p.chunk = (int)chunk;
@@ -404,13 +415,16 @@ swa_status swa_q8_read(const swa_q8_cache *cache, const swa_paged *paged, const 
 size_t swa_q8_workspace_bytes(const swa_dims *dims, int32_t window) {
     if (swa::api_check_dims(dims, window) != SWA_OK) return 0;
     Plan p;
-    if (plan_direct(dims, window, 1, &p) && in_place(dims, window, p))
-        return swa_workspace_bytes(dims, window);
-    const RowsLayout l = rows_layout(dims, window);
+    const bool can = plan_direct(dims, window, 1, &p);
+    // (a plan may have more splits than were asked for)
     swa_dims d = *dims;
+    if (can && d.num_splits > 0 && d.num_splits < p.splits) d.num_splits = p.splits;
+    const size_t split = can ? swa_workspace_bytes(&d, window) : 0;
+    if (can && in_place(dims, window, p)) return split;
+    const RowsLayout l = rows_layout(dims, window);
+    d = *dims;
     d.max_len = l.span;
     const size_t rows = l.parts + swa_workspace_bytes(&d, window);
-    const size_t split = swa_workspace_bytes(dims, window);
     return rows > split ? rows : split;
 }
 

@@ -6,6 +6,12 @@
 
 namespace swa {
 
+// Keys that an item of that kernel takes at most: small weights may be off by 2^-21 of
+// the item's largest each (see swa_q8_tc.cuh), by 2^-8 of it together if all are off the
+// same way.  Shorter items cost time: 152 windows of 8000 keys, 8 rows, 4 heads of 128
+// to a KV head, 82 us in one item each, 97 in two.
+constexpr int kQ8ItemKeys = 8192;
+
 struct Q8TcLaunch {
     TcParams T;
     const int8_t *k_exp, *v_exp;

@@ -11,13 +11,20 @@
 // bits each:
 //   q = 2^eq (q_hi + q_lo / 16), eq per query row.  A bf16 number has eight
 //     significant bits, so this is exact down to 2^-14 of the row's largest
-//     element and off by at most 2^-22 of it below.
-//   P = P_0 + (P_1 + P_2 / 16) / 56: that holds an fp16 number's eleven bits, so P
-//     is within 2^-11, or within 2^-21 of the row's largest P where that is more.
-//     (56 is the largest 2^i m, m odd and at most 7, that keeps what P_0 leaves of
-//     a P up to 256 within 448; times 7 that is still exact in fp16.)  An M = 128
-//     MMA takes 45 cycles with 32 columns, 49 with 64, 57 with 96 (measured), so
-//     neither the second half of Q nor the second and third of P cost much.
+//     element and off by at most 2^-21 of it below.
+//   P = P_0 + (P_1 + P_2 / 32) / 32: what a number leaves is signed and at most half
+//     a step of its four bits, so each further one adds five: P is within 2^-14 of
+//     itself, or a smallest step of P_2 (2^-9 / 1024 = 2^-19) where that is more.  (P
+//     is at most 256, of which P_0 leaves at most 8: 32 is the largest power of two
+//     that keeps that within 448.)  The row's largest P is at least 2^2 (kQ8RefBelow),
+//     so that step is 2^-21 of it.  Weights that small count by their number: alike
+//     ones, rounded alike, would be off together.  So P_2 is rounded with an offset,
+//     of up to half that step, that runs evenly through it from key to key (multiples
+//     of the golden ratio): the offsets cancel, and n such weights are off by some
+//     sqrt(n) 2^-22 of the largest.  That no choice of weights is off without limit, an
+//     item takes at most kQ8ItemKeys.  An M = 128 MMA takes 45 cycles with 32 columns,
+//     49 with 64, 57 with 96 (measured), so neither the second half of Q nor the second
+//     and third of P cost much.
 // Products of e4m3 numbers are exact and summed in fp32 (measured: within 2^-21
 // of the summed magnitudes).
 //
@@ -68,13 +75,12 @@ namespace swa {
 constexpr int kQ8TcThreads = 512;
 constexpr int kQ8Tabs = 4;          // tables of key factors
 constexpr float kQ8QLo = 16.f;      // scale of Q_lo
-constexpr float kQ8P1 = 56.f;       // scale of P_1, and of P_2 beside it
-constexpr float kQ8P2 = 16.f;
+constexpr float kQ8PStep = 32.f;    // scale of P_1 to P_0, and of P_2 to P_1
 // The reference maximum of a row sits this far (log2) below the largest u of the
 // tiles that set it, and P stays at most 2^8: a later tile may exceed that u by 2^6
 // before the references are raised.  A lower one would cost the small weights'
-// resolution: half a smallest step of P_2, 2^-10 / 56 / 16, is to be within 2^-21 of
-// the largest weight.
+// resolution, a higher one time (512 sequences of 8 rows, 8 heads of 256 on 2, window
+// 1024: 2 104 us, 4 116, 5 125).
 constexpr float kQ8RefBelow = 2.f;
 constexpr float kQ8RaiseAt = 8.f;
 
@@ -190,6 +196,20 @@ __device__ __forceinline__ void mma_commit_by(bool lead, uint64_t *bar) {
 // 2^e for any int8 e, kept finite and normal.
 __device__ __forceinline__ float q8_pow2(int e) { return pow2f(e < -126 ? -126 : e); }
 
+// The e4m3 pair nearest to a pair of weights, the weights becoming what is left times
+// kQ8PStep (exact: a difference of two numbers so near, and a power of two), plus `more`.
+__device__ __forceinline__ uint16_t take_e4m3(uint64_t &p2, uint64_t more) {
+    constexpr uint16_t MINUS_STEP = 0xd000;  // -kQ8PStep in fp16
+    float a, b;
+    tc::f2_unpack(p2, a, b);
+    const uint16_t c = e4m3x2(a, b);
+    const uint32_t h = e4m3x2_to_f16x2(c);
+    tc::f2_unpack(tc::f2_fma(p2, tc::f2_pack(kQ8PStep, kQ8PStep), more), a, b);
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(a) : "h"((uint16_t)h), "h"(MINUS_STEP));
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(b) : "h"((uint16_t)(h >> 16)), "h"(MINUS_STEP));
+    p2 = tc::f2_pack(a, b);
+    return c;
+}
 // The e4m3 pair nearest to an fp16 pair (at most 448), the fp16 pair becoming
 // what is left times `scale`: exact if that has at most 11 bits.
 __device__ __forceinline__ uint16_t take_e4m3(__half2 &p, float scale) {
@@ -658,7 +678,7 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
     q8_wait(&bars[C::B_OFULL + ob], (k / OB) & 1, P, failed);
     fence_after_sync();
     const uint32_t o0 = tmem + ((uint32_t)(quad * 32) << 16) + C::O_COL + ob * C::O_COLS;
-    const uint64_t s1 = f2_pack(1.f / kQ8P1, 1.f / kQ8P1), s2 = f2_pack(1.f / kQ8P2, 1.f / kQ8P2);
+    const uint64_t sp = f2_pack(1.f / kQ8PStep, 1.f / kQ8PStep);
     // (a warp stores 64 bytes of a row at a time: whole sectors)
     __nv_bfloat16 *out = P.out + t;
 #pragma unroll 1
@@ -679,7 +699,7 @@ __device__ __forceinline__ void q8_epilogue(const AttnParams &P, const TcItem &i
                 auto part = [&](int p) {
                     return f2_pack(__uint_as_float(o[mh][p][e]), __uint_as_float(o[mh][p][e + 1]));
                 };
-                const uint64_t x2 = f2_fma(f2_fma(part(2), s2, part(1)), s1, part(0));
+                const uint64_t x2 = f2_fma(f2_fma(part(2), sp, part(1)), sp, part(0));
                 float a, b;
                 if (P.splits == 1) {
                     f2_unpack(f2_mul(x2, f2_pack(l2.x, l2.y)), a, b);
@@ -1099,6 +1119,9 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                 const int ev = (int)key.y;
                 const float ive = pow2f(ev > 126 ? -126 : (ev < -127 ? 127 : -ev));
                 const uint64_t iv2 = f2_pack(ive, ive);
+                // P_2's offset: the fraction of key * 0.618.., in [-2^-10, 2^-10)
+                const float offset = (float)(int)((uint32_t)(j0 + lk) * 0x9e3779b9u) * 0x1p-41f;
+                const uint64_t offset2 = f2_pack(offset, offset);
                 uint8_t *pt = ps + h * C::P_BUF + lk * 32;
 #pragma unroll 1
                 for (int c = 0; c < CH; ++c) {
@@ -1113,12 +1136,13 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                             float d0, d1;
                             f2_unpack(f2_sub(f2_pack(v[r], v[r + 1]), m2[q]), d0, d1);
                             const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
-                            f2_unpack(f2_fma(f2_pack(p0, p1), iv2, f2_pack(lrow[r], lrow[r + 1])),
-                                      lrow[r], lrow[r + 1]);
-                            __half2 x = __floats2half2_rn(p0, p1);
-                            pk[0][r / 2] = take_e4m3(x, kQ8P1);
-                            pk[1][r / 2] = take_e4m3(x, kQ8P2);
-                            pk[2][r / 2] = last_e4m3(x);
+                            uint64_t p2 = f2_pack(p0, p1);
+                            f2_unpack(f2_fma(p2, iv2, f2_pack(lrow[r], lrow[r + 1])), lrow[r],
+                                      lrow[r + 1]);
+                            pk[0][r / 2] = take_e4m3(p2, 0);
+                            pk[1][r / 2] = take_e4m3(p2, offset2);
+                            f2_unpack(p2, d0, d1);
+                            pk[2][r / 2] = e4m3x2(d0, d1);
                         }
                     }
                     // columns i N + r0 + 8 c .. of part i, in key lk's 32-byte rows
