@@ -363,11 +363,11 @@ swa_status ensure_workspace(int dev, size_t need, cudaStream_t stream, void **ou
     return SWA_OK;
 }
 
-template <int D>
+template <int D, bool NAN_LSE>
 cudaError_t launch_merge(const swa::AttnParams &P, cudaStream_t s) {
     const long long blocks = (long long)P.B * P.Hkv * P.R;  // one per packed row
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return swa::launch_kernel(swa::swa_merge_kernel<D>, dim3((unsigned)blocks),
+    return swa::launch_kernel(swa::swa_merge_kernel<D, NAN_LSE>, dim3((unsigned)blocks),
                               dim3(swa::kMergeThreads), 0, s, P);
 }
 
@@ -418,7 +418,7 @@ swa_status launch_plan(const Plan &pl, const swa_dims *dims, const swa::AttnPara
         if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
     }
     if (pl.splits > 1) {
-        e = swa::api_merge(P, dims->head_dim, s);
+        e = swa::api_merge(P, dims->head_dim, /*nan_lse=*/false, s);
         if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
     }
     return SWA_OK;
@@ -845,11 +845,11 @@ swa_status swa::api_verify_rows(const void *q, const void *k, const void *v,
                        nullptr, nullptr, /*noalloc=*/false, /*sinks=*/0, parts);
 }
 
-cudaError_t swa::api_merge(const AttnParams &P, int head_dim, cudaStream_t s) {
+cudaError_t swa::api_merge(const AttnParams &P, int head_dim, bool nan_lse, cudaStream_t s) {
     switch (head_dim) {
-        case 64: return launch_merge<64>(P, s);
-        case 128: return launch_merge<128>(P, s);
-        default: return launch_merge<256>(P, s);
+        case 64: return nan_lse ? launch_merge<64, true>(P, s) : launch_merge<64, false>(P, s);
+        case 128: return nan_lse ? launch_merge<128, true>(P, s) : launch_merge<128, false>(P, s);
+        default: return nan_lse ? launch_merge<256, true>(P, s) : launch_merge<256, false>(P, s);
     }
 }
 

@@ -34,9 +34,9 @@ swa_status api_verify_rows(const void *q, const void *k, const void *v, const in
                            const int32_t *q_pos, int32_t window, float scale, void *out, float *lse,
                            const swa_dims *dims, void *parts, swa_stream_t stream);
 
-// The merge of split partials (P.splits > 1).
+// The merge of split partials (P.splits > 1); nan_lse: rows of NaN get that lse too.
 struct AttnParams;
-cudaError_t api_merge(const AttnParams &P, int head_dim, cudaStream_t s);
+cudaError_t api_merge(const AttnParams &P, int head_dim, bool nan_lse, cudaStream_t s);
 // swa_debug_options in effect: the kernel override, the bounded waits' limit in
 // SM cycles, the withheld fill.
 int api_forced_kernel();

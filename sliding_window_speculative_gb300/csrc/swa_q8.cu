@@ -326,7 +326,7 @@ swa_status attend_direct(const void *q, const swa_q8_cache *cache, const swa_pag
         return msg[0] ? api_fail(SWA_ERR_CUDA, "%s", msg)
                       : swa::api_cuda_fail(e, "8-bit attention kernel launch");
     if (pl.splits > 1) {
-        e = swa::api_merge(P, d->head_dim, s);
+        e = swa::api_merge(P, d->head_dim, /*nan_lse=*/true, s);
         if (e != cudaSuccess) return swa::api_cuda_fail(e, "merge kernel launch");
     }
     return swa::api_ok();

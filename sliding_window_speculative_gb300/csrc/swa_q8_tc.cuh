@@ -616,7 +616,9 @@ __device__ __forceinline__ void q8_queries(const TcItem &it, uint32_t k, uint8_t
         if (r < it.rows) {
             at[0] = make_uint2(hi[0], hi[1]);
             at[N * 16] = make_uint2(lo[0], lo[1]);
-            if (l == 0) qsc[(k & 1) * N + r] = pow2f(e);
+            // (a row with an infinity or a NaN has scores of NaN: its two numbers are
+            // finite where the conversion bounds them)
+            if (l == 0) qsc[(k & 1) * N + r] = a < 0x7f80u ? pow2f(e) : __int_as_float(0x7fffffff);
         }
     }
     fence_proxy_async_smem();

@@ -554,7 +554,9 @@ __global__ void __launch_bounds__(kSimtThreads) swa_simt_kernel(const AttnParams
 constexpr int kMergeThreads = 256;
 constexpr int kMergeMaxSplits = 64;
 
-template <int D>
+// NAN_LSE: a row with a NaN among its sums gets an lse of NaN (its output is NaN either
+// way); otherwise -inf, as where nothing is split.
+template <int D, bool NAN_LSE>
 __global__ void __launch_bounds__(kMergeThreads) swa_merge_kernel(const AttnParams P) {
     const float NEG_INF = -__int_as_float(0x7f800000);
     constexpr int CPR = D / 8;                    // 8-dim chunks per row
@@ -631,7 +633,8 @@ __global__ void __launch_bounds__(kMergeThreads) swa_merge_kernel(const AttnPara
         wv.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
         *reinterpret_cast<uint4 *>(P.out + orow * D + tid * 8) = wv;
         if (tid == 0 && P.lse != nullptr)
-            P.lse[orow] = Lam > 0.f ? (red[0] + __log2f(Lam)) * kLn2 : NEG_INF;
+            P.lse[orow] = Lam > 0.f || (NAN_LSE && Lam != Lam) ? (red[0] + __log2f(Lam)) * kLn2
+                                                               : NEG_INF;
     }
 }
 

@@ -1,0 +1,70 @@
+"""Attention straight from the 8-bit cache with infinities, NaN and values at the ends of
+the range in what it reads: rows that see them become NaN, all others keep their bits."""
+import numpy as np
+import pytest
+import torch
+
+from tests.helpers import forced_kernel
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sliding_window_speculative_gb300 import build
+    build.build()
+    yield
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def inputs(B, q_len, Hq, Hkv, D, L, seed=0):
+    """q on the host, the cache on the device (codes of normal values, exponents -9..-7)."""
+    rng = np.random.default_rng(seed)
+    q = torch.from_numpy(rng.standard_normal((B, q_len, Hq, D))).to(torch.bfloat16)
+    cache = [torch.from_numpy(rng.standard_normal((B, Hkv, L, D)) * 110).float().clamp(-448, 448)
+             .to(E4M3).view(torch.uint8).cuda() for _ in range(2)]
+    cache += [torch.from_numpy(rng.integers(-9, -6, (B, Hkv, L)).astype(np.int8)).cuda()
+              for _ in range(2)]
+    return q, cache
+
+
+def call(q, cache, lens, pos, W, scale, **kw):
+    import sliding_window_speculative_gb300 as swa
+    with forced_kernel("tc"):
+        out, lse = swa.swa_q8_verify_attn(q.cuda(), cache[0].view(E4M3), cache[1].view(E4M3),
+                                          cache[2], cache[3], i32(lens), i32(pos), W, scale, **kw)
+    torch.cuda.synchronize()
+    assert swa.swa_read_device_errors() == 0
+    return out.cpu(), lse.cpu()
+
+
+SHAPES = [(2, 8, 8, 2, 256, 300, 188), (2, 3, 4, 2, 128, 300, 400), (1, 24, 4, 4, 64, 200, 90)]
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("B,q_len,Hq,Hkv,D,L,W", SHAPES)
+def test_infinities_and_nan_in_a_query_row(B, q_len, Hq, Hkv, D, L, W, splits, value):
+    """0 times infinity is NaN, and so is a softmax of infinities."""
+    q, cache = inputs(B, q_len, Hq, Hkv, D, L, seed=D)
+    for t in cache[:2]:
+        t[..., 5] = 0                             # (a dim that is zero in every key)
+    lens, pos = [L - 13 * b for b in range(B)], [L - 13 * b - q_len for b in range(B)]
+    want = call(q, cache, lens, pos, W, D ** -0.5, num_splits=splits)
+    bad = torch.zeros((B, q_len, Hq), dtype=torch.bool)
+    for b, i, h, d in ((0, 0, 0, 5), (0, q_len - 1, Hq - 1, 7), (B - 1, q_len // 2, 1, D - 1)):
+        q[b, i, h, d] = value
+        bad[b, i, h] = True
+    out, lse = call(q, cache, lens, pos, W, D ** -0.5, num_splits=splits)
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(out[~bad], want[0][~bad]) and torch.equal(lse[~bad], want[1][~bad])
+    # a row that sees no key looks at nothing
+    out, lse = call(q, cache, [0] * B, [0] * B, W, D ** -0.5, num_splits=splits)
+    assert not out.any() and (lse == -float("inf")).all()
