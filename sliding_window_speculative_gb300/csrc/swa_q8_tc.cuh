@@ -1021,7 +1021,7 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                 }
                 const float2 key = tabs[slot * kTcTileKeys + lk];
                 fence_after_sync();
-                // u = (S_hi + S_lo / 16) * row scale * key factor + e_v
+                // u = (S_hi + S_lo / 16) * (row scale * key factor) + e_v
                 float v[HN], over = NEG_INF;
                 const uint64_t lo2 = f2_pack(1.f / kQ8QLo, 1.f / kQ8QLo);
                 const uint64_t ks2 = f2_pack(key.x, key.x), ve2 = f2_pack(key.y, key.y);
@@ -1042,7 +1042,9 @@ __global__ void __launch_bounds__(kQ8TcThreads, 1)
                                 f2_fma(f2_pack(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])),
                                        lo2,
                                        f2_pack(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
-                            f2_unpack(f2_fma(f2_mul(s2, rs2[p]), ks2, ve2), v[r], v[r + 1]);
+                            // (the two scales first: a row's alone may take the score past
+                            // the range, where the key's brings it back)
+                            f2_unpack(f2_fma(s2, f2_mul(rs2[p], ks2), ve2), v[r], v[r + 1]);
                         }
                     }
                     if (sees != ALL) {

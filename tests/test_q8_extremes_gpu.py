@@ -68,3 +68,22 @@ def test_infinities_and_nan_in_a_query_row(B, q_len, Hq, Hkv, D, L, W, splits, v
     # a row that sees no key looks at nothing
     out, lse = call(q, cache, [0] * B, [0] * B, W, D ** -0.5, num_splits=splits)
     assert not out.any() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("m", [-100, -60, 60, 110, 119])
+@pytest.mark.parametrize("B,q_len,Hq,Hkv,D,L,W", SHAPES)
+def test_queries_of_every_magnitude(B, q_len, Hq, Hkv, D, L, W, m):
+    """Queries times 2^m under a scale of 2^-m: no step between them may leave the range,
+    and every product with a power of two is exact, so the bits are the same."""
+    q, cache = inputs(B, q_len, Hq, Hkv, D, L, seed=D + 1)
+    cache[2] += 10
+    # (a whole number of steps, so that 2^m times it is a bf16 number, at most 8)
+    q = (q.float() * 16).round().clamp(-128, 128) / 16
+    lens, pos = [L] * B, [L - q_len] * B
+    want = call(q.to(torch.bfloat16), cache, lens, pos, W, 2.0 ** -4)
+    big = (q.double() * 2.0 ** m).to(torch.bfloat16)
+    assert torch.equal(big.double(), q.double() * 2.0 ** m)
+    got = call(big, cache, lens, pos, W, 2.0 ** (-4 - m))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert want[0].isfinite().all() and want[1].isfinite().all()
