@@ -37,13 +37,14 @@ cudaError_t launch(const swa::LogpParams &A, long long rows, int c, cudaStream_t
 }
 
 cudaError_t launch_rows(const swa::LogpParams &A, long long rows, int sms, cudaStream_t s) {
-    // One CTA per row, four to an SM; clusters share a row while that leaves at most
-    // three CTAs to an SM and each CTA eight vectors per thread.  Many rows that are
-    // not long get CTAs of 128 threads: the steps behind the pass are a larger share
+    // One CTA per row, four to an SM; clusters of up to four share a row while that
+    // leaves at most three CTAs to an SM and each CTA over 1024 vectors (four per
+    // thread), of eight while that leaves at most three CTAs to two SMs.  The eight have
+    // 512 threads where every thread has eight vectors and half the SMs stay without a
+    // CTA: with fewer vectors a row's loads are no longer four at a time.  Many rows that
+    // are not long get CTAs of 128 threads: the steps behind the pass are a larger share
     // of theirs.  Measured on GB300, calls behind one another in a replayed graph, us
     // (rows x columns, alternatives):
-    //   8 x 262144, 5      8 CTAs of 512 threads 10.0, of 256 10.2, 4 of 512 12.1, 2 of
-    //                      512 14.1
     //   64 x 262144, 5     4 of 256 13.9, 2 of 512 14.6, 8 of 256 17.2, 1 of 512 21.2
     //   200 x 262144, 5    4 of 256 34.9, 2 of 256 36.4, 1 of 512 35.0, 1 of 256 43.0
     //   512 x 262144, 20   1 of 256 65.7, 1 of 512 70.7, 2 of 128 70.9, 2 of 256 75.0
@@ -54,10 +55,21 @@ cudaError_t launch_rows(const swa::LogpParams &A, long long rows, int sms, cudaS
     //   40880 x 3120, 0    1 of 128 153, 1 of 256 232, 1 of 32 157
     //   20000 x 12001, 0   1 of 128 136, 1 of 256 177, 1 of 32 224
     //   400 x 1000, 0      1 of 128 2.6, 1 of 256 3.5
+    // and with other logits from one call to the next, so that they come from memory:
+    //   8 x 262144, 5      8 of 512 10.5, 8 of 256 11.3, 4 of 512 13.1, 2 of 512 15.8
+    //   16 x 262144, 5     8 of 256 12.6, 8 of 512 13.0, 4 of 512 13.8, 4 of 256 14.7
+    //   8 x 100352, 5      8 of 256 8.3, 8 of 512 9.2, 4 of 256 9.3, 2 of 512 11.0
+    //   28 x 100352, 5     8 of 256 10.8, 4 of 256 10.9, 8 of 512 13.4, 2 of 512 12.4
+    //   28 x 262144, 5     8 of 256 13.5, 4 of 512 14.2, 8 of 512 15.0, 4 of 256 15.0
+    //   57 x 100352, 5     4 of 256 11.9, 2 of 512 12.8, 8 of 256 14.2, 8 of 512 24.4
+    //   40 x 66000, 0      4 of 256 6.4, 2 of 512 6.8, 4 of 512 6.9, 8 of 512 14.2
     const long long nvec = ((long long)A.V + 14) / 8;
     int c = 1;
-    while (c < swa::kLogpMaxCluster && rows * c * 2 <= 3LL * sms && nvec > 2048LL * c) c *= 2;
-    if (c == swa::kLogpMaxCluster) return launch<512>(A, rows, c, s);
+    while (c < swa::kLogpMaxCluster && rows * c * 2 <= (c == 4 ? 3LL * sms / 2 : 3LL * sms) &&
+           nvec > 2048LL * c)
+        c *= 2;
+    if (c == swa::kLogpMaxCluster && rows * c * 2 <= sms && nvec >= 4096LL * c)
+        return launch<512>(A, rows, c, s);
     if (c == 1 && rows > (A.top > 0 ? 3LL : 2LL) * sms && nvec <= 8192) return launch<128>(A, rows, c, s);
     return launch<256>(A, rows, c, s);
 }
