@@ -10,7 +10,9 @@ def attention(q, k8, v8, ke, ve, seq_len, q_pos, window, scale):
     ve [Hkv, L] exponents.
 
     Returns out [q_len, Hq, D], lse [q_len, Hq] and per row
-      mag   the largest scale * sum |q||k| of a visible key
+      mag   the largest scale * sum |q||k| of a visible key; (D + 16) 2^-24 of it bounds
+            a score's error, so that of q elements below 2^-14 of their row's largest
+            (2^-21 of that largest, times |k|) is added as that many times as much
       wv    sum_j w_j |v_j| per dim
       top   the largest w_j * 448 * 2^e_j
       seen  the keys it sees."""
@@ -22,15 +24,14 @@ def attention(q, k8, v8, ke, ve, seq_len, q_pos, window, scale):
     first, end = max(0, q_pos - window + 1), min(seq_len, L, q_pos + q_len)
     if end <= first:
         return out, lse, mag, wv, top, seen
-    js = np.arange(first, end)
     for g in range(Hkv):
         k = kv8.row_values(k8[g, first:end], ke[g, first:end])
         v = kv8.row_values(v8[g, first:end], ve[g, first:end])
         row = 448.0 * 2.0 ** ve[g, first:end].astype(np.float64)
         for i in range(q_len):
             p = q_pos + i
-            see = (js <= p) & (js > p - window)
-            if not see.any():
+            see = slice(max(p - window + 1 - first, 0), max(min(p + 1, end) - first, 0))
+            if see.stop <= see.start:
                 continue
             for h in range(g * (Hq // Hkv), (g + 1) * (Hq // Hkv)):
                 s = scale * (k[see] @ q[i, h])
@@ -39,6 +40,9 @@ def attention(q, k8, v8, ke, ve, seq_len, q_pos, window, scale):
                 lse[i, h] = m + np.log(w.sum())
                 w /= w.sum()
                 out[i, h], wv[i, h] = w @ v[see], w @ np.abs(v[see])
-                mag[i, h] = abs(scale) * (np.abs(k[see]) @ np.abs(q[i, h])).max()
-                top[i, h], seen[i, h] = (w * row[see]).max(), see.sum()
+                big = np.abs(q[i, h]).max()
+                off = np.where(np.abs(q[i, h]) < 2.0 ** -14 * big, 2.0 ** -21 * big, 0.0)
+                mag[i, h] = abs(scale) * (np.abs(k[see]) @ (np.abs(q[i, h]) +
+                                                            off * 2.0 ** 24 / (D + 16))).max()
+                top[i, h], seen[i, h] = (w * row[see]).max(), see.stop - see.start
     return out, lse, mag, wv, top, seen

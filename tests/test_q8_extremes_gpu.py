@@ -87,3 +87,41 @@ def test_queries_of_every_magnitude(B, q_len, Hq, Hkv, D, L, W, m):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert want[0].isfinite().all() and want[1].isfinite().all()
+
+
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+@pytest.mark.parametrize("kernel", ["tc", "rows"])
+@pytest.mark.parametrize("B,q_len,Hq,Hkv,D,L,W", SHAPES)
+def test_nan_in_a_visible_key(B, q_len, Hq, Hkv, D, L, W, code, kernel):
+    """A NaN in K makes the rows NaN that see it, in V their dim; rows of the block that do
+    not see it keep theirs (of V, the other dims: weights of 0 are multiplied too)."""
+    import sliding_window_speculative_gb300 as swa
+    if D == 64 and kernel == "rows":
+        pytest.skip("heads of 64 have no such kernel")
+    q, cache = inputs(B, q_len, Hq, Hkv, D, L, seed=D + 2)
+    lens, pos = [L] * B, [L - q_len] * B
+    G, last, d = Hq // Hkv, L - 1, 3                 # (only the block's last row sees L - 1)
+
+    def run(cache):
+        with forced_kernel(kernel):
+            out, lse = swa.swa_q8_verify_attn(q.cuda(), cache[0].view(E4M3), cache[1].view(E4M3),
+                                              cache[2], cache[3], i32(lens), i32(pos), W, D ** -0.5)
+        torch.cuda.synchronize()
+        assert swa.swa_read_device_errors() == 0
+        return out.cpu(), lse.cpu()
+
+    want = run(cache)
+    bad = [t.clone() for t in cache]
+    bad[0][0, 0, last, d] = code
+    out, lse = run(bad)
+    sees = torch.zeros((B, q_len, Hq), dtype=torch.bool)
+    sees[0, q_len - 1, :G] = True
+    assert out[sees].isnan().all()
+    assert torch.equal(out[~sees], want[0][~sees]) and torch.equal(lse[~sees], want[1][~sees])
+    bad = [t.clone() for t in cache]
+    bad[1][0, 0, last, d] = code
+    out, lse = run(bad)
+    assert out[sees][:, d].isnan().all() and torch.equal(lse, want[1])
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[0, :, :G, d] = False                        # (may be NaN in the block's other rows)
+    assert torch.equal(out[same], want[0][same])
