@@ -239,7 +239,8 @@ bool plan_direct(const swa_dims *d, int32_t window, int sms, Plan *out) {
 // a sequence's window once, in bf16, whatever the number of rows, and its kernel takes
 // more rows at a time.  So it is for one item per window, and for more of them where
 // windows are long; heads of 64 always take it (the bf16 kernel for them has no tensor
-// cores).  Measured, 8 query heads on 2, in place / over bf16 rows, us:
+// cores).  Measured, 8 query heads on 2, in place / over bf16 rows, us (in place with
+// weights of 11 bits; of 14 it takes 1 to 3% more):
 //   rows x sequences, items per window      window 188     600        1024      1900
 //   8 x 512, 1        256                   41.5 / 107.5
 //   16 x 512, 2       256                   89.6 / 118.7              230 / 481

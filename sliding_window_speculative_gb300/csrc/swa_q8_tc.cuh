@@ -44,13 +44,15 @@
 // for every line of it.  Unrolled, the kernel issued an instruction in 30% of its
 // cycles and a single MMA took 100 cycles to issue; so the loops over rows stay
 // rolled, eight rows a turn, and what is rare is out of line (512 sequences of 8
-// rows, 4 heads of 256 to a KV head, window 1024: 125 -> 103 us; of one row 103 -> 82).
-// Tried and not kept: two tiles per softmax turn (125), two independent pipelines of
-// half the ring each (145), a warpgroup to every other tile for up to 8 rows (103).
-// Measured, of the bytes' time at 6.78 TB/s: those calls 83% and 97%, window 188 48%
-// (an item of two tiles costs 6 us from its queries to its output), 4 sequences of
-// 32768 keys, heads of 128 in pages of 64: 50% (at their lengths 124 SMs have keys, at
-// 1 us a tile, whose bytes take 0.7).
+// rows, 4 heads of 256 to a KV head, window 1024: 125 us unrolled, 116 rolled, 103 with
+// less code in the other roles too).  Tried and not kept: two tiles per softmax turn
+// (125), two independent pipelines of half the ring each (145), a warpgroup to every
+// other tile for up to 8 rows (103).
+// Measured, of the bytes' time at 6.78 TB/s: those calls 82% (103 us), of one row 97%
+// (82.6), window 188 48% and 46% (an item of two tiles costs 6 us from its queries to
+// its output), 4 sequences of 32768 keys, heads of 128 in pages of 64: 50% (32.4 us: at
+// their lengths 124 SMs have keys, up to 29 tiles each at 0.8 us, whose bytes take 0.7;
+// the first and last steps, the merge).
 //
 // Warp roles (512 threads; the registers of the first and last warpgroup that
 // they do not need go to the softmax):
@@ -80,7 +82,7 @@ constexpr float kQ8PStep = 32.f;    // scale of P_1 to P_0, and of P_2 to P_1
 // tiles that set it, and P stays at most 2^8: a later tile may exceed that u by 2^6
 // before the references are raised.  A lower one would cost the small weights'
 // resolution, a higher one time (512 sequences of 8 rows, 8 heads of 256 on 2, window
-// 1024: 2 104 us, 4 116, 5 125).
+// 1024: 2 103 us, 4 116, 5 125).
 constexpr float kQ8RefBelow = 2.f;
 constexpr float kQ8RaiseAt = 8.f;
 
@@ -331,9 +333,9 @@ __device__ __forceinline__ void q8_early_fills(const TcParams &T, const TcMaps &
 // A turn takes some 1000 cycles.  With PAIRS a tile's K and V share one where two
 // slots are free: for tiles of 128 dims (1350 cycles of bytes) and 16 rows, where the
 // turns are what bounds.  Elsewhere it is the softmax or the bytes, and turns apart
-// are better (one turn / two, us: 512 sequences, window 1024, heads of 128, 1 row 52.1
-// / 56.8, of 256 83.5 / 82.3; 8 rows of 128 93.0 / 92.2, of 256 104.5 / 101.4; 4
-// sequences of 32768 keys 32.2 / 34.6).
+// are better (one turn / two, us: 512 sequences, window 1024, heads of 128, 1 row 52.3
+// / 57.6, of 256 84.5 / 82.6; 8 rows of 128 96.3 / 94.8, of 256 105.8 / 102.9; 4
+// sequences of 32768 keys 32.3 / 35.1).
 template <class C, int NT, bool PAIRS>
 __device__ __forceinline__ void q8_producer(const TcParams &T, const TcMaps &M, const TcItem *meta,
                                             volatile uint32_t *ftab, uint8_t *ring, uint64_t *bars,
